@@ -1,7 +1,8 @@
 /*
  * kvdecode.h -- C ABI of libkvdecode.so: single-token decode attention over a
- * long KV cache that reads only part of it (Quest-style block selection),
- * for NVIDIA GB300 (sm_103a), one GPU.
+ * long KV cache that reads only part of it (Quest-style block selection), and
+ * what a server needs around it (positions and norms, a cache in pages, chunks
+ * of new tokens), for NVIDIA GB300 (sm_103a), one GPU.
  *
  * Sources, by page title and section:
  *  [QUEST]  "Sparse Attention -- Quest-style block-selector for long-context
@@ -46,7 +47,7 @@
 extern "C" {
 #endif
 
-#define KVD_ABI_VERSION 3
+#define KVD_ABI_VERSION 4
 
 /* Exported symbols (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -66,7 +67,14 @@ typedef enum {
     KVD_ERR_WORKSPACE = 6     /* workspace NULL, misaligned or too small */
 } kvd_status;
 
-typedef enum { KVD_F16 = 0, KVD_INT8 = 1, KVD_Q8_0 = 2, KVD_Q4_0 = 3 } kvd_kv_dtype;
+/* KVD_BF16: paged caches only. */
+typedef enum {
+    KVD_F16 = 0,
+    KVD_INT8 = 1,
+    KVD_Q8_0 = 2,
+    KVD_Q4_0 = 3,
+    KVD_BF16 = 4
+} kvd_kv_dtype;
 
 /*
  * The cache: a plain descriptor of caller-owned device memory.
@@ -418,6 +426,185 @@ KVD_API size_t kvd_workspace_bytes(const kvd_cache *cache, int32_t n_heads);
 /* invalid arguments.  Host only.                                          */
 KVD_API int32_t kvd_selected_count(int32_t len, int32_t block, int32_t k_sel,
                            int32_t sink_tokens, int32_t recent_tokens);
+
+/* ====================================================================== */
+/* Around the decode: positions, per-head norms, a cache in pages, and     */
+/* attention of a chunk of new tokens.  The pages have no counterpart:     */
+/* they start from queries and keys that are normed and rotated already,   */
+/* and their caches are contiguous.                                        */
+/* ====================================================================== */
+
+/* Element type of activations (the cache has kvd_kv_dtype). */
+typedef enum { KVD_X_F16 = 0, KVD_X_BF16 = 1, KVD_X_F32 = 2 } kvd_x_dtype;
+
+/*
+ * Rows of heads: [n_tokens, n_heads, head_dim] with the heads of one token
+ * dense and `stride` elements from one token to the next, so that the query,
+ * key and value parts of one fused projection can be passed as they lie.
+ * x is 16-byte aligned, stride >= n_heads * head_dim, and stride times the
+ * element size a multiple of 16.
+ */
+typedef struct kvd_heads {
+    void *x;
+    int64_t stride;
+    int32_t dtype;        /* kvd_x_dtype */
+    int32_t n_heads;
+} kvd_heads;
+
+/* How the angles per position are stretched for contexts longer than the
+ * one a model was trained on; f_i = base^(-2i / rot_dim), i < rot_dim / 2. */
+typedef enum {
+    KVD_ROPE_NONE = 0,
+    KVD_ROPE_LINEAR = 1,  /* f_i / factor */
+    KVD_ROPE_NTK = 2,     /* base * factor^(rot_dim / (rot_dim - 2)) for base */
+    KVD_ROPE_YARN = 3,    /* f_i for channels that turn more than `high` times in orig_len
+                             positions, f_i / factor below `low` turns, a linear ramp over
+                             the channels between (their whole numbers, as floor and ceil
+                             give them); the rotated channels times 0.1 ln(factor) + 1 */
+    KVD_ROPE_BANDS = 4    /* the same two ends, the ramp linear in the number of turns */
+} kvd_rope_scaling;
+
+/*
+ * Position rotation of the first rot_dim channels of a head.  Pair i is
+ * channels (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved; at position
+ * p it turns by p * f_i, and both channels are scaled by mscale.
+ * freqs: device, [rot_dim / 2] words: f_i / (2 pi) turns per position, times
+ * 2^64 (kvd_rope_freqs).  A position times such a word, modulo 2^64, is the
+ * angle's fraction of a turn to 2^-33 at any int32 position; an f32 angle has
+ * lost it after some thousand positions.
+ */
+typedef struct kvd_rope {
+    const uint64_t *freqs;
+    int32_t rot_dim;      /* a multiple of 16 in [16, head_dim] */
+    int32_t interleaved;  /* 0 or 1 */
+    float mscale;
+    int32_t reserved;     /* must be 0 */
+} kvd_rope;
+
+/* The words of kvd_rope.freqs for a host to copy to the device, and mscale.
+ * factor >= 1 (ignored by NONE); orig_len, low < high: YARN (1 and 32 turns
+ * where both are 0) and BANDS (1 and 4).  Host only.
+ * Errors: INVALID (NULL, rot_dim not a positive multiple of 16 up to 1024,
+ * base <= 1 or not finite, factor < 1, orig_len < 1, low < 0, low >= high). */
+KVD_API kvd_status kvd_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
+                                  double orig_len, double low, double high, uint64_t *freqs,
+                                  float *mscale);
+
+/* ---------------------------------------------------------------------- */
+/* Per-head RMS norm and position rotation of queries and keys, one pass.  */
+/*   y = R(p) (x * w / sqrt(mean(x^2) + eps)), rounded once to the output    */
+/*   type; w is q_weight or k_weight ([head_dim] f32, device), and without  */
+/*   one there is no norm; rope NULL leaves the rotation out.               */
+/*   q, q_out, k, k_out: [n_tokens, .., head_dim]; k and k_out may be NULL.  */
+/*   An output may be its own input (same address, stride and type), and    */
+/*   must not overlap the inputs otherwise.                                  */
+/*   positions: device int32 [n_tokens] (NULL when rope is NULL).            */
+/* The outputs feed kvd_decode_attn and kvd_select_blocks (f32 queries) and */
+/* kvd_kv_append (f16 or f32 keys).  n_tokens == 0 is a no-op.               */
+/* Errors: INVALID; UNSUPPORTED (head_dim not a multiple of 16 in           */
+/* [16, 1024], rot_dim not a multiple of 16); CUDA.                          */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_qk_norm_rope(const kvd_heads *q, const kvd_heads *q_out,
+                                    const kvd_heads *k, const kvd_heads *k_out, int32_t n_tokens,
+                                    int32_t head_dim, const int32_t *positions,
+                                    const kvd_rope *rope, const float *q_weight,
+                                    const float *k_weight, float eps, void *stream);
+
+/*
+ * A cache in pages: page j of every sequence is a page of one pool, found by
+ * the sequence's row of page_table.
+ *   k, v        [n_pages, n_kv_heads, page_size, head_dim]  f16, bf16 or int8 codes
+ *   k_scale,    [n_pages, n_kv_heads, page_size] f32 (int8: absmax / 127 of the
+ *   v_scale     token's row, as in kvd_cache; NULL otherwise)
+ *   page_table  device int32 [batch, max_pages]: the page of tokens
+ *               [j * page_size, (j + 1) * page_size).  Entries of pages that no
+ *               token below the sequence's length needs are not read.
+ *   seq_lens    device int32 [batch]: the tokens of each sequence, the new ones
+ *               of the current call counted (both calls below take the same)
+ *   len         host: at least the largest of seq_lens; it sizes the grids
+ * An f16 or int8 kvd_cache is such a cache with one page a sequence: page_size =
+ * max_seq, n_pages = batch, page_table[b][0] = b.
+ * Rows at or beyond a sequence's length may hold anything, NaN too.
+ * The int32s on the device are checked there: a page outside [0, n_pages), a
+ * length outside [0, len], or starts that fall or leave [0, n_tokens] write
+ * KVD_ERR_INVALID to dev_status.  Such a page is neither read nor written (its
+ * keys are left out), and a length or a start is moved into its range.  So does
+ * a sequence with more new tokens than its length: those before position 0 are
+ * not appended, and see no key.
+ */
+typedef struct kvd_paged_cache {
+    int32_t dtype;        /* KVD_F16, KVD_BF16 or KVD_INT8 */
+    int32_t batch;        /* sequences >= 1 */
+    int32_t n_kv_heads;
+    int32_t head_dim;     /* 64 or 128 */
+    int32_t n_pages;      /* pages of the pool */
+    int32_t page_size;    /* tokens, a multiple of 16 */
+    int32_t max_pages;    /* columns of page_table */
+    int32_t len;          /* at least the largest of seq_lens, <= max_pages * page_size */
+    void *k;
+    void *v;
+    void *k_scale;
+    void *v_scale;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    int32_t *dev_status;  /* may be NULL */
+} kvd_paged_cache;
+
+/* ---------------------------------------------------------------------- */
+/* Append new tokens of a ragged batch to their pages, with the norm and    */
+/* the rotation of kvd_qk_norm_rope on the way.                              */
+/*   starts: device int32 [batch + 1]: sequence b's new tokens are rows      */
+/*   [starts[b], starts[b + 1]) of k, v and q, and stand at positions        */
+/*   seq_lens[b] - n_b .. seq_lens[b] - 1.  Rows at or behind starts[batch]  */
+/*   (a padded batch) count for nothing, and their q_out is not written.     */
+/*   k, v: [n_tokens, n_kv_heads, head_dim] of one type.  Keys are normed    */
+/*   (k_weight) and rotated (rope) in f32; then keys and values are rounded  */
+/*   to the cache's type, or quantized as by kvd_kv_append.  Only the rows   */
+/*   of new tokens are written.                                               */
+/*   q, q_out (both NULL, or both given): normed and rotated as the keys are. */
+/* No bounds are kept: the selection works on kvd_cache.                     */
+/* Two sequences must not share a page that this call writes.                */
+/* n_tokens == 0 is a no-op.                                                  */
+/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, rot_dim); CUDA.         */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_heads *k,
+                                    const kvd_heads *v, int32_t n_tokens, const int32_t *starts,
+                                    const kvd_rope *rope, const float *k_weight,
+                                    const kvd_heads *q, const kvd_heads *q_out,
+                                    const float *q_weight, float eps, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Attention of a ragged batch's new tokens over their sequences' pages:    */
+/* a prefill chunk, single decode tokens, or both in one batch.              */
+/*   starts as for kvd_paged_append (the new tokens are in the cache).       */
+/*   For token i of sequence b's n_b and query head h of KV head             */
+/*   h / (n_heads / n_kv_heads), with p = seq_lens[b] - n_b + i:              */
+/*     out = sum_t softmax(softmax_scale * q . k_t)_t v_t  over the cached    */
+/*     tokens t <= p, and p - window < t when window > 0                      */
+/*   (int8: k_t = scale_t * code_t, and q stays as it is).  A token that sees */
+/*   no key gets a zero row.  Rows at or behind starts[batch] are not written. */
+/*   A non-finite value row spoils the outputs of its own sequence's tokens   */
+/*   in this call, those before it included.                                   */
+/*   q, out: [n_tokens, n_heads, head_dim] of one type: the cache's, or f16 or */
+/*   bf16 over an int8 cache.  softmax_scale > 0.                               */
+/*   max_new: at least the largest n_b (it sizes the grid; the tokens of a     */
+/*   larger n_b are left out, and INVALID is reported to dev_status).          */
+/*   workspace: kvd_paged_workspace_bytes; need not be zeroed.  Calls that     */
+/*   may overlap on the GPU need a workspace each.                              */
+/* n_tokens == 0 is a no-op.                                                    */
+/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, more than 16 query heads  */
+/* a KV head); WORKSPACE; CUDA.                                                  */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q,
+                                  int32_t n_tokens, const int32_t *starts, int32_t max_new,
+                                  float softmax_scale, int32_t window, const kvd_heads *out,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of kvd_paged_attn for n_heads query heads, up to n_tokens new
+ * tokens with up to max_new in one sequence, and any len the page table can hold.
+ * Asked with the device current that will run the call.  0 on invalid arguments. */
+KVD_API size_t kvd_paged_workspace_bytes(const kvd_paged_cache *cache, int32_t n_heads,
+                                         int32_t n_tokens, int32_t max_new);
 
 /* Static description of a status code.  Host only. */
 KVD_API const char *kvd_status_string(kvd_status status);

@@ -9,7 +9,8 @@ fallback: if the library is not built, loading it raises.
 Entry points (same names as the C ABI, without the ``kvd_`` prefix):
   kv_append, select_blocks, decode_attn, decode_attn_dense, decode_step,
   decode_step_host, workspace_bytes, selected_count, status_string,
-  debug_qk_int8, debug_scores, decode_attn_static.
+  debug_qk_int8, debug_scores, decode_attn_static; and around the decode
+  rope_table (kvd_rope_freqs), qk_norm_rope, paged_append, paged_attn.
 """
 from __future__ import annotations
 
@@ -28,6 +29,7 @@ F16 = 0
 INT8 = 1
 Q8_0 = 2
 Q4_0 = 3
+BF16 = 4  # paged caches only
 BLOCK = 64
 HEAD_DIM = 128
 
@@ -39,7 +41,9 @@ EXPORTS = ("kvd_kv_append", "kvd_select_blocks", "kvd_decode_attn", "kvd_decode_
            "kvd_selected_count", "kvd_status_string", "kvd_abi_version", "kvd_debug_qk_int8",
            "kvd_debug_scores", "kvd_decode_attn_static", "kvd_decode_attn_sv",
            "kvd_decode_attn_tail", "kvd_kv_append_f32", "kvd_select_blocks_per_head",
-           "kvd_decode_attn_per_head", "kvd_debug_wait_timeout", "kvd_debug_stage_marks")
+           "kvd_decode_attn_per_head", "kvd_debug_wait_timeout", "kvd_debug_stage_marks",
+           "kvd_rope_freqs", "kvd_qk_norm_rope", "kvd_paged_append", "kvd_paged_attn",
+           "kvd_paged_workspace_bytes")
 
 
 class KvdError(RuntimeError):
@@ -56,6 +60,28 @@ class CacheStruct(C.Structure):
                 ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p), ("kbounds", C.c_void_p), ("dev_status", C.c_void_p),
                 ("moments", C.c_void_p), ("seq_lens", C.c_void_p)]
+
+
+class PagedCacheStruct(C.Structure):
+    """Mirror of ``kvd_paged_cache``."""
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("n_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages", C.c_int32), ("len", C.c_int32),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("page_table", C.c_void_p), ("seq_lens", C.c_void_p),
+                ("dev_status", C.c_void_p)]
+
+
+class HeadsStruct(C.Structure):
+    """Mirror of ``kvd_heads``."""
+    _fields_ = [("x", C.c_void_p), ("stride", C.c_int64), ("dtype", C.c_int32),
+                ("n_heads", C.c_int32)]
+
+
+class RopeStruct(C.Structure):
+    """Mirror of ``kvd_rope``."""
+    _fields_ = [("freqs", C.c_void_p), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("mscale", C.c_float), ("reserved", C.c_int32)]
 
 
 _lib = None
@@ -97,6 +123,14 @@ def lib():
         L.kvd_debug_scores.argtypes = [cp, p, i32, p, p]
         L.kvd_debug_wait_timeout.argtypes = [p, i32, p]
         L.kvd_debug_stage_marks.argtypes = [p, sz]
+        pc, hp, rp, f64 = C.POINTER(PagedCacheStruct), C.POINTER(HeadsStruct), \
+            C.POINTER(RopeStruct), C.c_double
+        L.kvd_rope_freqs.argtypes = [i32, f64, i32, f64, f64, f64, f64, p, C.POINTER(C.c_float)]
+        L.kvd_qk_norm_rope.argtypes = [hp, hp, hp, hp, i32, i32, p, rp, p, p, C.c_float, p]
+        L.kvd_paged_append.argtypes = [pc, hp, hp, i32, p, rp, p, hp, hp, p, C.c_float, p]
+        L.kvd_paged_attn.argtypes = [pc, hp, i32, p, i32, C.c_float, i32, hp, p, sz, p]
+        L.kvd_paged_workspace_bytes.argtypes = [pc, i32, i32, i32]
+        L.kvd_paged_workspace_bytes.restype = sz
         _lib = L
     return _lib
 
@@ -387,10 +421,251 @@ def debug_scores(cache: KVCache, q: torch.Tensor, ub: torch.Tensor, stream=None)
         cache.ref(), _ptr(q), int(q.shape[1]), _ptr(ub), _stream(q, stream)))
 
 
-__all__ = ["F16", "INT8", "Q8_0", "Q4_0", "BLOCK", "HEAD_DIM", "KVCache", "KvdError", "CacheStruct", "lib",
+# ------------------------------------------- positions, norms, paged cache ---
+_X = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "bands": 4}
+
+
+def _heads(t: Optional[torch.Tensor]):
+    """kvd_heads of rows [n_tokens, n_heads, head_dim]; only the token stride is free."""
+    if t is None:
+        return None
+    if t.dim() != 3 or t.dtype not in _X:
+        raise ValueError("rows are [n_tokens, n_heads, head_dim] of float16, bfloat16 or float32")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d != 1) or (s1 != d and h != 1):
+        raise ValueError("the heads of a token must be dense")
+    return HeadsStruct(t.data_ptr(), s0 if n > 1 else h * d, _X[t.dtype], h)
+
+
+def _int32(t: torch.Tensor, shape, name: str):
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} is an int32 tensor of shape {tuple(shape)}")
+    return _ptr(t)
+
+
+def _weight(t: Optional[torch.Tensor], d: int):
+    if t is not None and (t.dtype != torch.float32 or t.shape != (d,)):
+        raise ValueError("a norm weight is a float32 tensor [head_dim]")
+    return _ptr(t)
+
+
+def _same_device(first: torch.Tensor, *others):
+    """The device all tensors of a call live on (other, absent ones are None)."""
+    d = first.device
+    if d.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError("the tensors of a call must be on one device")
+    return d
+
+
+class _On:
+    """The call's device current, as the library launches on the current device."""
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else \
+            torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class RopeTable:
+    """Rotation of the first rot_dim channels: frequencies on the device and the
+    descriptor that points at them.  See rope_table."""
+
+    def __init__(self, freqs: torch.Tensor, rot_dim: int, interleaved: bool, mscale: float):
+        self.freqs, self.rot_dim, self.interleaved, self.mscale = freqs, rot_dim, interleaved, mscale
+        self.s = RopeStruct(freqs.data_ptr(), rot_dim, int(interleaved), mscale, 0)
+
+    def ref(self):
+        return C.byref(self.s)
+
+
+def rope_table(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
+               scaling: str = "none", factor: float = 1.0, orig_len: float = 0.0,
+               low: float = 0.0, high: float = 0.0, device="cuda") -> RopeTable:
+    """The angles per position of a model's rotation, made once.
+
+    interleaved: pairs (2i, 2i+1), else (i, i + rot_dim/2).  scaling: "none",
+    "linear", "ntk", "yarn" or "bands" (kvd_rope_scaling), with the context's
+    stretch `factor`, the trained length orig_len and, for the last two, the
+    turns in orig_len below which a channel is stretched in full (low) and above
+    which it is kept (high); 0 and 0 take the usual ones."""
+    if scaling not in SCALINGS:
+        raise ValueError(f"scaling is one of {sorted(SCALINGS)}")
+    words = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    m = C.c_float()
+    _check("kvd_rope_freqs", lib().kvd_rope_freqs(
+        int(rot_dim), float(base), SCALINGS[scaling], float(factor), float(orig_len), float(low),
+        float(high), _ptr(words), C.byref(m)))
+    return RopeTable(words.to(device), int(rot_dim), bool(interleaved), m.value)
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional[torch.Tensor],
+                 rope: Optional[RopeTable], q_out: torch.Tensor, k_out: Optional[torch.Tensor],
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, stream=None):
+    """Per-head RMS norm (with a weight) and rotation (with a table) of
+    q [T, H, D] and k [T, Hkv, D] into q_out and k_out; positions int32 [T].
+    Any of float16, bfloat16 and float32 in, and out; in place too."""
+    T, _, D = q.shape
+    if q_out.shape != q.shape or (k is not None and (k_out is None or k_out.shape != k.shape or
+                                                     k.shape[0] != T or k.shape[2] != D)):
+        raise ValueError("outputs have their inputs' shapes, and q and k as many tokens and channels")
+    d = _same_device(q, k, positions, q_out, k_out, q_weight, k_weight,
+                     None if rope is None else rope.freqs)
+    with _On(d):
+        _check("kvd_qk_norm_rope", lib().kvd_qk_norm_rope(
+            _heads(q), _heads(q_out), _heads(k), _heads(k_out), T, D,
+            None if positions is None else _int32(positions, (T,), "positions"),
+            None if rope is None else rope.ref(), _weight(q_weight, D), _weight(k_weight, D),
+            float(eps), _stream(q, stream)))
+
+
+class PagedKVCache:
+    """A pool of pages, each sequence's table of them, and the C descriptor.
+
+    k, v        [n_pages, Hkv, page_size, D] float16, bfloat16 or int8 codes; D 64 or 128
+    k_scale     [n_pages, Hkv, page_size] float32 (int8); same for v_scale
+    page_table  [batch, max_pages] int32: the page of each run of page_size tokens
+    seq_lens    [batch] int32: tokens of each sequence, those of the current call
+                counted; the caller advances it (once a step, for all layers)
+    status      [1] int32 device word for values out of range
+    len         at least the largest of seq_lens (host; sizes the grids)
+    """
+
+    def __init__(self, dtype: int, batch: int, n_pages: int, n_kv_heads: int, page_size: int,
+                 max_pages: int, head_dim: int = HEAD_DIM, device="cuda",
+                 tensors: Optional[dict] = None):
+        self.dtype, self.batch, self.n_pages, self.n_kv_heads = dtype, batch, n_pages, n_kv_heads
+        self.page_size, self.max_pages, self.head_dim = page_size, max_pages, head_dim
+        dev = torch.device(device)
+        t = dict(tensors) if tensors is not None else {}
+        kvt = {F16: torch.float16, BF16: torch.bfloat16}.get(dtype, torch.int8)
+        rows = (n_pages, n_kv_heads, page_size)
+        want = {"k": (rows + (head_dim,), kvt), "v": (rows + (head_dim,), kvt),
+                "page_table": ((batch, max_pages), torch.int32),
+                "seq_lens": ((batch,), torch.int32), "status": ((1,), torch.int32)}
+        if dtype == INT8:
+            want["k_scale"] = want["v_scale"] = (rows, torch.float32)
+        for name, (shape, kind) in want.items():
+            if name not in t:
+                zero = name in ("page_table", "seq_lens", "status")
+                t[name] = (torch.zeros if zero else torch.empty)(shape, dtype=kind, device=dev)
+            elif tuple(t[name].shape) != shape or t[name].dtype != kind:
+                raise ValueError(f"{name} is {kind} of shape {shape}")
+        self.device = _same_device(*t.values())
+        self.t = t
+        self.s = PagedCacheStruct(dtype, batch, n_kv_heads, head_dim, n_pages, page_size,
+                                  max_pages, 0, *(_ptr(t.get(n)) for n in (
+                                      "k", "v", "k_scale", "v_scale", "page_table", "seq_lens",
+                                      "status")))
+
+    @classmethod
+    def over(cls, cache: KVCache, seq_lens: Optional[torch.Tensor] = None) -> "PagedKVCache":
+        """A float16 or int8 KVCache as a paged one, one page a sequence, over the
+        same memory: seq_lens (default: len for each) counts the tokens to attend."""
+        if cache.dtype not in (F16, INT8):
+            raise KvdError("PagedKVCache.over", 2)
+        dev = cache.t["k"].device
+        t = {n: cache.t[n] for n in ("k", "v", "k_scale", "v_scale", "status") if n in cache.t}
+        t["page_table"] = torch.arange(cache.batch, dtype=torch.int32, device=dev).view(-1, 1)
+        t["seq_lens"] = seq_lens if seq_lens is not None else torch.full(
+            (cache.batch,), cache.len, dtype=torch.int32, device=dev)
+        p = cls(cache.dtype, cache.batch, cache.batch, cache.n_kv_heads, cache.max_seq, 1,
+                head_dim=cache.head_dim, device=dev, tensors=t)
+        p.len = cache.len
+        return p
+
+    @property
+    def len(self) -> int:
+        return self.s.len
+
+    @len.setter
+    def len(self, n: int):
+        self.s.len = int(n)
+
+    def __getattr__(self, name):
+        t = self.__dict__.get("t")
+        if t is not None and name in t:
+            return t[name]
+        raise AttributeError(name)
+
+    def ref(self):
+        return C.byref(self.s)
+
+    def device_status(self) -> int:
+        return int(self.t["status"].item())
+
+
+def paged_workspace_bytes(cache: PagedKVCache, n_heads: int, n_tokens: int, max_new: int) -> int:
+    with _On(cache.device):
+        return int(lib().kvd_paged_workspace_bytes(cache.ref(), n_heads, n_tokens, max_new))
+
+
+def make_paged_workspace(cache: PagedKVCache, n_heads: int, n_tokens: int,
+                         max_new: int) -> torch.Tensor:
+    """A workspace for paged_attn calls of up to n_tokens new tokens, up to max_new a sequence."""
+    n = paged_workspace_bytes(cache, n_heads, n_tokens, max_new)
+    if n == 0:
+        raise KvdError("kvd_paged_workspace_bytes", 1)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def paged_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                 rope: Optional[RopeTable] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 stream=None):
+    """Rows [starts[b], starts[b+1]) of k, v [T, Hkv, D] to sequence b's last positions,
+    the keys normed and rotated on the way, and q [T, H, D] with them into q_out."""
+    T, _, D = k.shape
+    if v.shape != k.shape or D != cache.head_dim:
+        raise ValueError("k and v are [n_tokens, n_kv_heads, head_dim]")
+    if q is not None and (q_out is None or q_out.shape != q.shape or q.shape[0] != T or
+                          q.shape[2] != D):
+        raise ValueError("q and q_out are [n_tokens, n_heads, head_dim]")
+    _same_device(cache.t["k"], k, v, starts, k_weight, q, q_out, q_weight,
+                 None if rope is None else rope.freqs)
+    with _On(cache.device):
+        _check("kvd_paged_append", lib().kvd_paged_append(
+            cache.ref(), _heads(k), _heads(v), T, _int32(starts, (cache.batch + 1,), "starts"),
+            None if rope is None else rope.ref(), _weight(k_weight, D), _heads(q), _heads(q_out),
+            _weight(q_weight, D), float(eps), _stream(k, stream)))
+
+
+def paged_attn(cache: PagedKVCache, q: torch.Tensor, starts: torch.Tensor, max_new: int,
+               softmax_scale: float, out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+               stream=None):
+    """Causal attention of rows [starts[b], starts[b+1]) of q [T, H, D], sequence b's last
+    tokens, over its pages (with a window: the last `window` keys), into out [T, H, D]."""
+    T, _, D = q.shape
+    if out.shape != q.shape or D != cache.head_dim:
+        raise ValueError("q and out are [n_tokens, n_heads, head_dim]")
+    _same_device(cache.t["k"], q, starts, out, workspace)
+    with _On(cache.device):
+        _check("kvd_paged_attn", lib().kvd_paged_attn(
+            cache.ref(), _heads(q), T, _int32(starts, (cache.batch + 1,), "starts"), int(max_new),
+            float(softmax_scale), int(window), _heads(out), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(q, stream)))
+
+
+__all__ = ["F16", "INT8", "Q8_0", "Q4_0", "BF16", "BLOCK", "HEAD_DIM", "KVCache", "KvdError", "CacheStruct", "lib",
            "debug_stage_marks", "MARK_SLOTS", "MARK_CTAS", "MARK_KINDS",
            "workspace_bytes", "make_workspace", "selected_count", "status_string", "kv_append",
            "kv_append_f32", "select_blocks", "decode_attn", "decode_attn_dense", "decode_attn_static",
            "decode_attn_sv", "decode_attn_tail", "select_blocks_per_head",
            "decode_attn_per_head", "decode_step",
-           "decode_step_host", "debug_qk_int8", "debug_scores", "debug_wait_timeout", "synth", "EXPORTS"]
+           "decode_step_host", "debug_qk_int8", "debug_scores", "debug_wait_timeout", "synth", "EXPORTS",
+           "PagedCacheStruct", "HeadsStruct", "RopeStruct", "RopeTable", "rope_table",
+           "qk_norm_rope", "PagedKVCache", "paged_workspace_bytes", "make_paged_workspace",
+           "paged_append", "paged_attn", "SCALINGS"]

@@ -1,0 +1,55 @@
+// paged.h -- launchers of the norm/rotation, paged append and paged attention
+// kernels (rope.cu, paged_attn.cu) for their C-ABI front end (paged_api.cu).
+// Arguments are already validated by the caller.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "kvdecode.h"
+
+namespace kvd {
+
+// One launch of the norm/rotation kernel.  Heads of a token are numbered
+// q, then k, then v; an absent part has zero heads.
+struct RowsIn {
+    const void *x;
+    int64_t stride;
+    int n_heads;
+};
+struct RowsOut {
+    void *x;
+    int64_t stride;
+    int dtype;  // kvd_x_dtype
+};
+struct RopeArgs {
+    RowsIn q, k, v;
+    RowsOut q_out, k_out;  // k_out: unused with a cache
+    const float *q_weight, *k_weight;
+    float eps;
+    int head_dim, n_tokens;
+    const int32_t *positions;  // without a cache
+    kvd_rope rope;             // rot_dim 0: no rotation
+    const int32_t *starts;     // with a cache
+    kvd_paged_cache cache;     // page_table NULL: no cache
+};
+
+cudaError_t launch_rope(const RopeArgs &a, int x_dtype, cudaStream_t st);
+
+// One attention call.
+struct PagedAttnArgs {
+    kvd_paged_cache c;
+    const void *q;
+    void *out;
+    int64_t q_stride, out_stride;
+    bool bf16;  // q and out: bf16, else f16
+    int H, G, n_tokens, max_new, window;
+    const int32_t *starts;
+    float scale_log2;  // softmax_scale * log2(e)
+};
+
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st);
+size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new);
+
+}  // namespace kvd
