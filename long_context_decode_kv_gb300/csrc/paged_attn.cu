@@ -2,123 +2,949 @@
 //
 //   out = sum_t softmax(scale q . k_t)_t v_t,   p - window < t <= p
 //
-// One warp per (token, query head): 32 keys at a time, a lane per key for the
-// scores and a lane per channel pair for the values, with the running maximum
-// and sum of the softmax.
+// One CTA per SM, persistent.  An item is one sequence's run of new tokens and
+// one KV head: the rows are the tokens' query heads of that KV head, up to 128
+// a tensor-core tile, over the key tiles of 128 tokens that any row sees.  All
+// items' key tiles form one line, cut into equal lengths for the CTAs: a long
+// decode spreads over all SMs, a causal chunk's short and long rows balance,
+// and an item that a cut divides is joined from f32 partials by merge_kernel.
+//
+// A CTA runs two softmax streams so that one's exponentials hide behind the
+// other's products.  PAIR (sequences with more rows than a tile): two row tiles
+// over the same keys, each key tile loaded once for 256 rows.  Otherwise (decode
+// and short chunks): one row tile, its key tiles taken in turn by the streams,
+// which are joined at the item's end.
+//
+// Roles: warps 0-3 and 4-7 the streams' softmax, one row a thread (the row's
+// logits sit in one tensor-memory lane, so no shuffles); warp 8 loads by TMA
+// (pages land as they lie, 16 to 128 rows a box); warp 9 issues the products
+//   S = Q K^T   shared x shared      O += P V   P from tensor memory
+// S of one tile is overwritten in place by P, so two streams' S and O fill the
+// 512 columns.  The maximum that scales a row's exponentials is raised only when
+// a logit passes it by 2^8, which leaves the sums exact to f32 and makes the
+// rescaling of O rare; P stays below 2^8, far inside f16.
+// P is rounded to the input type (the tensor core's operand): a relative error
+// of half a step in each weight, which sums and statistics in f32 do not add to.
+#include <cuda.h>
+
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
 #include "paged_dev.cuh"
+#include "tcgen05.cuh"
 
 namespace kvd {
 namespace {
 
-template <bool BF16, int DT>
-__device__ __forceinline__ float2 cache2(const void *base, size_t at) {
-    if constexpr (DT == KVD_INT8) {
-        const char2 c = *reinterpret_cast<const char2 *>(static_cast<const int8_t *>(base) + at);
-        return make_float2(static_cast<float>(c.x), static_cast<float>(c.y));
-    } else {
-        return unpack2<DT == KVD_BF16>(
-            *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + at));
-    }
+constexpr int kTile = 128;       // keys a tile, rows a tile
+constexpr int kThreads = 384;
+constexpr int kProducer = 8, kIssuer = 9;  // warps; 10 and 11 idle
+// Registers a thread: 168 at launch (64,512 for 384 threads), moved to the
+// softmax warps, which hold a row's 128 logits: 256 * 208 + 128 * 88 = 64,512.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr float kRaise = 8.0f;   // log2 by which a logit may pass the running maximum
+
+struct Dev {  // a launch's arguments
+    kvd_paged_cache c;
+    uint16_t *out;
+    int64_t out_stride;
+    int H, G, n_tokens, max_new, window;
+    const int32_t *starts;
+    float scale_log2;
+    int q_tokens;       // tokens of a row tile: 128 / G
+    int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
+    int dead_row;       // a cache row outside the pool
+    int min_tiles;      // least key tiles a CTA takes
+    float *acc;         // partial sums [2 * CTAs][rows / 32][D / 4][32][4]
+    float2 *ml;         // their maxima and sums [2 * CTAs][rows]
+    int4 *merge;        // [CTAs][2]: what merge_kernel joins
+    int ws_rows;        // rows of a partial: 256 (PAIR) or fewer, a multiple of 32
+};
+
+// ---------------------------------------------------------------- items ---
+struct Seq {
+    int s0, n, len;  // first token, new tokens (at most max_new), length
+    int first;       // position of the first new token
+};
+
+__device__ __forceinline__ Seq seq_of(const Dev &a, int b, bool report) {
+    const int r0 = a.starts[b], r1 = a.starts[b + 1];
+    int len = a.c.seq_lens[b];
+    const int s0 = min(max(r0, 0), a.n_tokens);
+    const int s1 = min(max(r1, s0), a.n_tokens);
+    const int l = min(max(len, 0), a.c.len);
+    Seq s{s0, min(s1 - s0, a.max_new), l, l - (s1 - s0)};
+    if (report && (r0 != s0 || r1 != s1 || l != len || s1 - s0 > a.max_new || s.first < 0))
+        report_status(a.c.dev_status, KVD_ERR_INVALID);
+    return s;
 }
 
-template <bool BF16, int DT, int D>
-__global__ void __launch_bounds__(128) attn_kernel(const __grid_constant__ PagedAttnArgs a) {
-    __shared__ float2 qs[4][D / 2];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x, h = blockIdx.y * 4 + warp;
+struct Item {
+    int i0, cnt;   // tokens of the sequence's new ones
+    int lo, hi;    // keys [lo, hi) that any of them sees
+    int j0, tiles; // key tiles: one at least, so that rows that see nothing are written
+};
+
+__device__ __forceinline__ Item item_of(const Dev &a, const Seq &s, int tile, int width) {
+    Item it;
+    it.i0 = tile * width;
+    it.cnt = min(width, s.n - it.i0);
+    const int p0 = s.first + it.i0;
+    it.hi = max(p0 + it.cnt, 0);
+    it.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), it.hi) : 0;
+    it.j0 = it.lo / kTile;
+    it.tiles = max((it.hi + kTile - 1) / kTile - it.j0, 1);
+    return it;
+}
+
+// A CTA's walk along the line of items' key tiles, the same in every role.
+struct Walk {
+    int b, head, tile, off;
+    long left;
+    int k;  // segments taken
+    Seq s;
+};
+struct Segment {
+    Item it;
+    int b, s0, first_pos, head;
+    int j0, j1;        // key tiles
+    bool starts, ends; // whether it holds its item's first and last tile
+    int k;
+};
+
+__device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, Segment &g) {
+    if (w.left <= 0) return false;
+    g.it = item_of(a, w.s, w.tile, width);
+    const int take = static_cast<int>(min(static_cast<long>(g.it.tiles - w.off), w.left));
+    g.b = w.b;
+    g.s0 = w.s.s0;
+    g.first_pos = w.s.first;
+    g.head = w.head;
+    g.j0 = g.it.j0 + w.off;
+    g.j1 = g.j0 + take;
+    g.starts = w.off == 0;
+    g.ends = w.off + take == g.it.tiles;
+    g.k = w.k++;
+    w.left -= take;
+    w.off = 0;
+    if (w.left > 0) {
+        if ((w.tile + 1) * width < w.s.n) {
+            ++w.tile;
+        } else {
+            w.tile = 0;
+            if (++w.head == a.c.n_kv_heads) {
+                w.head = 0;
+                do {
+                    ++w.b;
+                    if (w.b >= a.c.batch) {  // the line has no more items
+                        w.left = 0;
+                        break;
+                    }
+                    w.s = seq_of(a, w.b, false);
+                } while (w.s.n == 0);
+            }
+        }
+    }
+    return true;
+}
+
+// ------------------------------------------------------------ the kernel ---
+template <int D, bool PAIR>
+struct Shape {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
+    static constexpr int kJoinBytes = PAIR ? 0 : kTile * 64 * 4;  // 64 channels of a stream's O
+    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kAhead = PAIR ? 1 : 2;  // key tiles whose S is issued ahead of PV
+    // +1024: the tiles start on a 1024-byte boundary
+    static constexpr int kSmem = 1024 + kQBytes + kJoinBytes + kStages * kTileBytes;
+};
+
+struct Bars {
+    uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], done,
+        join_full, join_empty;
+};
+
+template <bool BF16, int D, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q_map,
+            const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    using Sh = Shape<D, PAIR>;
+    constexpr int kHalves = D / 64;
+    constexpr int kHalfBytes = kTile * 128;
+    constexpr int kStages = Sh::kStages;
+    constexpr int kAhead = Sh::kAhead;
+
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ Bars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ uint32_t dead_groups[8];  // per key tile: its 16-key groups on bad pages
+    __shared__ float2 join_ml[kTile];
+    __shared__ long scan_total[kThreads / 32];
+    __shared__ Walk start;
+
+    uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    uint8_t *q_smem = smem;
+    float *join = reinterpret_cast<float *>(smem + Sh::kQBytes);
+    uint8_t *ring = smem + Sh::kQBytes + Sh::kJoinBytes;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int width = PAIR ? 2 * a.q_tokens : a.q_tokens;  // tokens of an item
+
+    if (warp == kIssuer) tmem_alloc(&tmem_slot, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_full[i], 1);
+        }
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_empty[i], 1);
+        }
+        mbar_init(&bar.q_empty, 1);
+        mbar_init(&bar.done, 1);
+        mbar_init(&bar.join_full, 4);
+        mbar_init(&bar.join_empty, 4);
+        fence_barrier_init();
+        abort_flag = 0;
+        start.left = 0;
+    }
     pdl_wait();
     pdl_launch_dependents();
-    if (h >= a.H) return;
-    const int b = sequence_of(a.starts, a.c.batch, t, lane);
-    const int s0 = a.starts[b], s1 = a.starts[b + 1];
-    if (t < s0 || t >= s1 || t - s0 >= a.max_new) {
-        if (t < a.starts[a.c.batch]) report_status(a.c.dev_status, KVD_ERR_INVALID);
-        return;
+
+    // ---- this CTA's piece of the line of key tiles
+    auto cost_of = [&](int b, bool report) -> long {
+        if (b >= a.c.batch) return 0;
+        const Seq s = seq_of(a, b, report);
+        long n = 0;
+        for (int t = 0; t * width < s.n; ++t) n += item_of(a, s, t, width).tiles;
+        return n * a.c.n_kv_heads;
+    };
+    auto scan = [&](long cost, long &before) -> long {  // exclusive prefix, and the sum
+        long v = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) scan_total[warp] = v;
+        __syncthreads();
+        long sum = 0;
+        before = v - cost;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += scan_total[i];
+            sum += scan_total[i];
+        }
+        __syncthreads();
+        return sum;
+    };
+    long before = 0;
+    long cost = cost_of(tid, blockIdx.x == 0);
+    long total = scan(cost, before);
+    const bool one_pass = a.c.batch <= kThreads;
+    for (int b0 = kThreads; b0 < a.c.batch; b0 += kThreads) {
+        long skip;
+        total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
     }
-    const long pos = static_cast<long>(checked_len(a.c, b)) - (s1 - t);
-    if (pos < 0) report_status(a.c.dev_status, KVD_ERR_INVALID);
-    const long first = a.window > 0 && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    const uint16_t *q = static_cast<const uint16_t *>(a.q) + t * a.q_stride + h * D;
-    for (int i = lane; i < D / 2; i += 32)
-        qs[warp][i] = unpack2<BF16>(reinterpret_cast<const uint32_t *>(q)[i]);
-    __syncwarp();
-    float m = -INFINITY, l = 0.0f;
-    float2 acc[D / 64] = {};
-    const int ps = a.c.page_size;
-    for (long k0 = first / 32 * 32; k0 <= pos; k0 += 32) {
-        const long kt = k0 + lane;
-        int page = -1;
-        size_t row = 0;
-        if (kt >= first && kt <= pos) {
-            const int j = static_cast<int>(kt / ps);
-            page = checked_page(a.c, b, j);
-            row = (static_cast<size_t>(page) * a.c.n_kv_heads + h / a.G) * ps + (kt - static_cast<long>(j) * ps);
-        }
-        float s = -INFINITY;
-        if (page >= 0) {
-            float dot = 0.0f;
-            for (int i = 0; i < D / 2; ++i) {
-                const float2 k = cache2<BF16, DT>(a.c.k, row * D + 2 * i);
-                dot = fmaf(qs[warp][i].x, k.x, fmaf(qs[warp][i].y, k.y, dot));
+    const long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long>(a.min_tiles));
+    const long ctas = min(static_cast<long>(gridDim.x), (total + per - 1) / per);
+    const long x0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    const long x1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    if (x0 < x1) {
+        long base = 0;
+        for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
+            if (!one_pass) {
+                cost = cost_of(b0 + tid, false);
+                const long sum = scan(cost, before);
+                before += base;
+                base += sum;
             }
-            if (DT == KVD_INT8) dot *= static_cast<const float *>(a.c.k_scale)[row];
-            s = dot * a.scale_log2;
-        }
-        float mx = s;
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (mx == -INFINITY) continue;
-        const float mn = fmaxf(m, mx);
-        const float alpha = exp2f(m - mn);
-        float p = exp2f(s - mn);
-        float sum = p;
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        l = l * alpha + sum;
-        m = mn;
-        if (DT == KVD_INT8 && page >= 0) p *= static_cast<const float *>(a.c.v_scale)[row];
-        for (int d = 0; d < D / 64; ++d) {
-            acc[d].x *= alpha;
-            acc[d].y *= alpha;
-        }
-        for (int u = 0; u < 32; ++u) {
-            const int pg = __shfl_sync(0xffffffffu, page, u);
-            const size_t r = __shfl_sync(0xffffffffu, row, u);
-            const float pu = __shfl_sync(0xffffffffu, p, u);
-            if (pg < 0) continue;
-            for (int d = 0; d < D / 64; ++d) {
-                const float2 v = cache2<BF16, DT>(a.c.v, r * D + 2 * (lane + 32 * d));
-                acc[d].x = fmaf(pu, v.x, acc[d].x);
-                acc[d].y = fmaf(pu, v.y, acc[d].y);
+            if (before <= x0 && x0 < before + cost) {
+                Walk w;
+                w.b = b0 + tid;
+                w.s = seq_of(a, w.b, false);
+                const long per_head = cost / a.c.n_kv_heads;
+                long r = x0 - before;
+                w.head = static_cast<int>(r / per_head);
+                r -= w.head * per_head;
+                w.tile = 0;
+                for (;;) {
+                    const int n = item_of(a, w.s, w.tile, width).tiles;
+                    if (r < n) break;
+                    r -= n;
+                    ++w.tile;
+                }
+                w.off = static_cast<int>(r);
+                w.left = x1 - x0;
+                w.k = 0;
+                start = w;
             }
         }
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    uint32_t *o = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + t * a.out_stride + h * D);
-    for (int d = 0; d < D / 64; ++d) o[lane + 32 * d] = pack2<BF16>(acc[d].x * inv, acc[d].y * inv);
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Walk w = start;
+    Segment g;
+    volatile int *abort = &abort_flag;
+    auto fail = [&] {
+        *abort = 1;
+        report_status(a.c.dev_status, KVD_ERR_TIMEOUT);
+    };
+
+    // rows and key tiles of stream t in a segment
+    struct Part {
+        int cnt, p0, j0, j1;  // tokens, first position, key tiles (PAIR: its own; else the segment's)
+    };
+    auto part_of = [&](const Segment &g, int t) -> Part {
+        Part p;
+        const int i = g.it.i0 + (PAIR ? t * a.q_tokens : 0);
+        p.cnt = min(a.q_tokens, g.it.i0 + g.it.cnt - i);
+        p.p0 = g.first_pos + i;
+        p.j0 = g.j0;
+        p.j1 = g.j1;
+        if constexpr (PAIR) {
+            if (p.cnt <= 0) {
+                p.cnt = 0;
+                p.j1 = p.j0;
+                return p;
+            }
+            const int hi = max(p.p0 + p.cnt, 0);
+            const int lo = a.window > 0 ? min(max(p.p0 - a.window + 1, 0), hi) : 0;
+            p.j0 = max(p.j0, lo / kTile);
+            p.j1 = min(p.j1, (hi + kTile - 1) / kTile);
+            if (p.j1 < p.j0) p.j1 = p.j0;
+        }
+        return p;
+    };
+    // the key tiles a segment loads: those some stream takes
+    auto span_of = [&](const Segment &g, int &j0, int &j1) {
+        j0 = g.j0;
+        j1 = g.j1;
+        if constexpr (PAIR) {
+            const Part p0 = part_of(g, 0), p1 = part_of(g, 1);
+            const bool e0 = p0.j0 == p0.j1, e1 = p1.j0 == p1.j1;
+            if (e0 && e1) {
+                j1 = j0;
+            } else {
+                j0 = e0 ? p1.j0 : e1 ? p0.j0 : min(p0.j0, p1.j0);
+                j1 = e0 ? p1.j1 : e1 ? p0.j1 : max(p0.j1, p1.j1);
+            }
+        }
+    };
+
+    if (warp >= kProducer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kProducer) {
+        // ------------------------------------------------------- loads ---
+        const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
+        const int boxes = kTile / a.box;
+        const int ps = a.c.page_size;
+        uint32_t it = 0, keys = 0;  // ring places filled, key tiles loaded
+        uint32_t q_phase = 0;
+        bool ok = true;
+        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
+        while (ok && next_segment(a, width, w, g)) {
+            int j0, j1;
+            span_of(g, j0, j1);
+            if (g.k > 0) {
+                ok = mbar_wait(&bar.q_empty, q_phase, abort);
+                q_phase ^= 1;
+                if (!ok) break;
+            }
+            if (lane == 0 && j1 > j0) {
+                const int rows = a.q_tokens * a.G;
+                for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
+                    const Part p = part_of(g, t);
+                    if (p.j0 == p.j1) continue;
+                    mbar_arrive_expect_tx(&bar.q_full[t], rows * 128 * kHalves);
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_4d(q_smem + t * Sh::kTileBytes + h * kHalfBytes, &q_map, h * 64, 0,
+                                    g.head, g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0),
+                                    &bar.q_full[t]);
+                }
+            }
+            // the cache row of this lane's box of tile j (dead_row: not needed, or a bad page)
+            uint32_t bad = 0;
+            auto row_of = [&](int j, bool &is_bad) -> int {
+                is_bad = false;
+                const int t0 = j * kTile + lane * a.box;
+                if (lane >= boxes || j >= j1 || t0 >= g.it.hi || t0 + a.box <= g.it.lo)
+                    return a.dead_row;
+                const int col = t0 / ps;
+                const int page = checked_page(a.c, g.b, col);
+                is_bad = page < 0;
+                return is_bad ? a.dead_row
+                              : (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
+            };
+            auto load = [&](int row, const CUtensorMap *map) -> bool {
+                const uint32_t st = it % kStages;
+                if (!mbar_wait(&bar.kv_empty[st], ((it / kStages) & 1) ^ 1, abort)) return false;
+                if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[st], Sh::kTileBytes);
+                __syncwarp();
+                if (lane < boxes) {
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_2d(ring + st * Sh::kTileBytes + h * kHalfBytes +
+                                        lane * a.box * 128,
+                                    map, h * 64, row, &bar.kv_full[st], policy);
+                }
+                ++it;
+                return true;
+            };
+            auto load_keys = [&](int row, bool is_bad) -> bool {
+                bad = __reduce_or_sync(0xffffffffu,
+                                       is_bad ? ((1u << (a.box / 16)) - 1) << (lane * (a.box / 16))
+                                              : 0u);
+                if (lane == 0) dead_groups[keys & 7] = bad;
+                __syncwarp();
+                ++keys;
+                return load(row, &k_map);
+            };
+            // rows of the next tiles, read ahead of their use
+            int row[kAhead + 2];
+            bool is_bad[kAhead + 2];
+#pragma unroll
+            for (int i = 0; i < kAhead + 2; ++i) row[i] = row_of(j0 + i, is_bad[i]);
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (ok && j0 + i < j1) ok = load_keys(row[i], is_bad[i]);
+            for (int j = j0; ok && j < j1; ++j) {
+                ok = load(row[0], &v_map);
+                if (ok && j + kAhead < j1) ok = load_keys(row[kAhead], is_bad[kAhead]);
+#pragma unroll
+                for (int i = 0; i < kAhead + 1; ++i) {
+                    row[i] = row[i + 1];
+                    is_bad[i] = is_bad[i + 1];
+                }
+                row[kAhead + 1] = row_of(j + kAhead + 2, is_bad[kAhead + 1]);
+            }
+            if (g.starts && !g.ends) {
+                // the item goes on in the next CTAs: leave word for merge_kernel
+                const long rest = g.it.tiles - (g.j1 - g.it.j0);
+                int pieces = 1;
+                while (total * (blockIdx.x + pieces + 1) / ctas - x1 < rest) ++pieces;
+                rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
+                rec1 = make_int4(g.head, 0, 0, 0);
+            }
+        }
+        if (!ok) fail();
+        if (lane == 0) {
+            a.merge[2 * blockIdx.x] = rec0;
+            a.merge[2 * blockIdx.x + 1] = rec1;
+        }
+        if (*abort) {
+            // nothing may land in shared memory after the CTA has gone
+            volatile int none = 0;
+            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+                mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, &none);
+        }
+        } else if (warp == kIssuer) {
+        // ---------------------------------------------------- products ---
+        constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kTile, false);
+        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, D, true);
+        const uint32_t q_addr = smem_addr(q_smem), ring_addr = smem_addr(ring);
+        uint32_t it = 0;
+        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        bool ok = true;
+        auto wait_tile = [&]() -> bool {  // the next place of the ring is full
+            const bool r = mbar_wait(&bar.kv_full[it % kStages], (it / kStages) & 1, abort);
+            tmem_fence_after();
+            return r;
+        };
+        auto issue_s = [&](int t) {  // the tile at `it` against row tile t
+            if (lane == 0) {
+                const uint32_t q = q_addr + (PAIR ? t * Sh::kTileBytes : 0);
+                const uint32_t k = ring_addr + (it % kStages) * Sh::kTileBytes;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint32_t at = (i / 4) * kHalfBytes + (i % 4) * 32;
+                    mma_ss(tmem + t * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024),
+                           kIdS, i > 0);
+                }
+                mma_commit(&bar.s_full[t]);
+            }
+            __syncwarp();
+        };
+        while (ok && next_segment(a, width, w, g)) {
+            int j0, j1;
+            span_of(g, j0, j1);
+            Part part[2] = {part_of(g, 0), part_of(g, 1)};
+#pragma unroll
+            for (int t = 0; t < (PAIR ? 2 : 1); ++t)
+                if (ok && part[t].j0 < part[t].j1) {
+                    ok = mbar_wait(&bar.q_full[t], q_phase[t], abort);
+                    q_phase[t] ^= 1;
+                }
+            // stream t takes key tile j
+            auto takes = [&](int t, int j) {
+                return PAIR ? (j >= part[t].j0 && j < part[t].j1) : ((j - j0) & 1) == t && j < j1;
+            };
+            // S of key tile j for the streams that take it, then its place is free
+            auto scores = [&](int j, int t) {
+                if (takes(t, j)) issue_s(t);
+            };
+            auto release = [&]() {
+                if (lane == 0) mma_commit(&bar.kv_empty[it % kStages]);
+                __syncwarp();
+                ++it;
+            };
+            // the segment's last S is issued: its queries can be replaced
+            auto release_q = [&]() {
+                if (lane == 0) mma_commit(&bar.q_empty);
+                __syncwarp();
+            };
+            for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i) {
+                if (!(ok = wait_tile())) break;
+                scores(j0 + i, 0);
+                scores(j0 + i, 1);
+                release();
+            }
+            if (j1 - j0 <= kAhead) release_q();
+            for (int j = j0; ok && j < j1; ++j) {
+                if (!(ok = wait_tile())) break;
+                const uint32_t v_st = it % kStages;
+                uint8_t *vs = ring + v_st * Sh::kTileBytes;
+                // value rows that no token of the item sees may hold NaN: clear them
+                const int from = max(g.it.lo - j * kTile, 0), to = min(g.it.hi - j * kTile, kTile);
+                if (from > 0 || to < kTile) {
+                    const int n = (from + (kTile - max(to, 0))) * 8 * kHalves;
+                    for (int i = lane; i < n; i += 32) {
+                        const int c = i % 8, h = (i / 8) % kHalves;
+                        int r = i / (8 * kHalves);
+                        if (r >= from) r += max(to, 0) - from;
+                        *reinterpret_cast<uint4 *>(vs + h * kHalfBytes + r * 128 + c * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                ++it;  // from here on the key tile ahead
+                const int ahead = j + kAhead;
+                bool have = false;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (takes(t, j)) {
+                        if (!(ok = mbar_wait(&bar.p_full[t], p_phase[t], abort))) break;
+                        p_phase[t] ^= 1;
+                        tmem_fence_after();
+                        if (lane == 0) {
+                            const bool fresh = PAIR ? j == part[t].j0 : j - j0 < 2;
+                            const uint32_t v = ring_addr + v_st * Sh::kTileBytes;
+#pragma unroll
+                            for (int i = 0; i < kTile / 16; ++i)
+                                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
+                                       smem_desc(v + i * 2048, kHalfBytes, 1024), kIdO,
+                                       !fresh || i > 0);
+                            if (PAIR && j + 1 == part[t].j1) mma_commit(&bar.o_full[t]);
+                        }
+                        __syncwarp();
+                    }
+                    if (ahead < j1 && takes(t, ahead)) {
+                        if (!have && !(ok = wait_tile())) break;
+                        have = true;
+                        issue_s(t);
+                    }
+                }
+                if (!ok) break;
+                if (lane == 0) mma_commit(&bar.kv_empty[v_st]);
+                __syncwarp();
+                if (ahead < j1) {
+                    if (!have && !(ok = wait_tile())) break;
+                    release();
+                    if (ahead + 1 == j1) release_q();
+                }
+            }
+            if (!PAIR && ok && lane == 0) {
+                mma_commit(&bar.o_full[0]);
+                mma_commit(&bar.o_full[1]);
+            }
+            __syncwarp();
+        }
+        if (!ok) fail();
+        // every product and every barrier arrival is done before the CTA goes
+        if (lane == 0) mma_commit(&bar.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&bar.done, 0, &none)) fail();
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        // ------------------------------------------------------ softmax ---
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tmem + ((warp & 3) << 21);  // this warp's 32 lanes
+        const uint32_t s_addr = lanes + t * 128, o_addr = lanes + 256 + t * 128;
+        uint32_t s_phase = 0, o_phase = 0, join_phase = 0, keys = 0;
+        bool ok = true;
+        while (ok && next_segment(a, width, w, g)) {
+            int j0, j1;
+            span_of(g, j0, j1);
+            const Part part = part_of(g, t);
+            const int rows = part.cnt * a.G;
+            const bool warp_live = (warp & 3) * 32 < rows;
+            const int tok = row / a.G;
+            const int pos = part.p0 + tok;
+            // keys [lo, hi) of this row
+            const int hi = row < rows ? max(pos + 1, 0) : 0x7fffffff;
+            const int lo = row < rows && a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+            float m = -INFINITY;
+            float2 l2 = make_float2(0.0f, 0.0f);
+            const int first = PAIR ? part.j0 : j0 + t;
+            for (int j = first; j < part.j1; j += PAIR ? 1 : 2) {
+                if (!(ok = mbar_wait(&bar.s_full[t], s_phase, abort))) break;
+                s_phase ^= 1;
+                if (warp_live) {
+                    tmem_fence_after();
+                    float s[128];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, s + 32 * i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) pin32(s + 32 * i);
+                    const int rh = hi - j * kTile, rl = lo - j * kTile;
+                    const uint32_t dead = dead_groups[(keys + (j - j0)) & 7];
+                    if (__any_sync(0xffffffffu, rh < kTile || rl > 0) || dead) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c >= rh || c < rl || (dead >> (c / 16) & 1)) s[c] = -INFINITY;
+                    }
+                    float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+                    const float top =
+                        fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+                    if (__any_sync(0xffffffffu, top > m + kRaise && m != -INFINITY)) {
+                        // the maximum has outgrown the sums' scale
+                        const float mn = fmaxf(m, top);
+                        const float f = m == -INFINITY ? 1.0f : exp2_approx(m - mn);
+                        m = mn;
+                        l2.x *= f;
+                        l2.y *= f;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            float o[32];
+                            tmem_ld32(o_addr + 32 * i, o);
+                            tmem_wait_ld();
+                            pin32(o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] *= f;
+                            tmem_st32(o_addr + 32 * i, o);
+                        }
+                    } else if (m == -INFINITY) {
+                        m = top;
+                    }
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+                    const float2 off = make_float2(-base, -base);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            const int at = 32 * i + 2 * c;
+                            float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc, off);
+                            x.x = exp2_approx(x.x);
+                            x.y = exp2_approx(x.y);
+                            l2 = __fadd2_rn(l2, x);
+                            p[c] = pack2<BF16>(x.x, x.y);
+                        }
+                        tmem_st16(s_addr + 16 * i, p);
+                    }
+                    tmem_wait_st();
+                    tmem_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[t]);
+            }
+            if (!ok) break;
+            keys += j1 - j0;
+            // ---- the segment's result
+            float l = l2.x + l2.y;
+            const bool some = first < part.j1;
+            if (PAIR ? some : j1 > j0) {
+                if (!(ok = mbar_wait(&bar.o_full[t], o_phase, abort))) break;
+                o_phase ^= 1;
+                tmem_fence_after();
+            }
+            const bool whole = g.starts && g.ends;
+            const int prow = (PAIR ? t * 128 : 0) + row;
+            const size_t slot = 2 * blockIdx.x + (g.k == 0 ? 0 : 1);
+            float mine = 1.0f, other = 0.0f;  // scale of this stream's O and of the joined one's
+            if constexpr (!PAIR) {
+                if (t == 1) {
+                    // the halves of the segment before have been read
+                    if (!(ok = mbar_wait(&bar.join_empty, join_phase ^ 1, abort))) break;
+                    join_ml[row] = make_float2(m, l);
+                }
+                if (t == 0) {
+                    if (!(ok = mbar_wait(&bar.join_full, join_phase, abort))) break;
+                    const float2 o = join_ml[row];
+                    const float mn = fmaxf(m, o.x);
+                    mine = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
+                    other = o.x == -INFINITY ? 0.0f : exp2_approx(o.x - mn);
+                    l = l * mine + o.y * other;
+                    m = mn;
+                }
+            }
+            const bool live = row < rows;
+            if (whole) {
+                const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                mine = some ? mine * inv : 0.0f;
+                other *= inv;
+            }
+            if ((PAIR || t == 0) && live && !whole) a.ml[slot * a.ws_rows + prow] = make_float2(m, l);
+            uint16_t *dst = a.out;
+            if (live)
+                dst += static_cast<int64_t>(g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0) + tok) *
+                           a.out_stride +
+                       static_cast<int64_t>(g.head * a.G + row % a.G) * D;
+            float4 *part_dst = reinterpret_cast<float4 *>(a.acc) +
+                               ((slot * (a.ws_rows / 32) + prow / 32) * (D / 4)) * 32 + lane;
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+                if (!PAIR && h > 0) {
+                    ok = t == 1 ? mbar_wait(&bar.join_empty, join_phase ^ 1, abort)
+                                : mbar_wait(&bar.join_full, join_phase, abort);
+                    if (!ok) break;
+                }
+#pragma unroll
+                for (int i = 2 * h; i < 2 * h + 2; ++i) {
+                    float o[32];
+                    if (warp_live && some) {
+                        tmem_ld32(o_addr + 32 * i, o);
+                        tmem_wait_ld();
+                        pin32(o);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = 0.0f;
+                    }
+                    if constexpr (!PAIR) {
+                        if (t == 1) {
+                            if (warp_live)
+#pragma unroll
+                                for (int c = 0; c < 32; ++c)
+                                    join[((i & 1) * 32 + c) * kTile + row] = o[c];
+                            continue;
+                        }
+                        if (warp_live)
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float u = join[((i & 1) * 32 + c) * kTile + row];
+                                o[c] = (mine != 0.0f ? o[c] * mine : 0.0f) +
+                                       (other != 0.0f ? u * other : 0.0f);
+                            }
+                    } else if (whole) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] *= mine;
+                    }
+                    if (live && whole) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            *reinterpret_cast<uint4 *>(dst + 32 * i + c) =
+                                make_uint4(pack2<BF16>(o[c], o[c + 1]), pack2<BF16>(o[c + 2], o[c + 3]),
+                                           pack2<BF16>(o[c + 4], o[c + 5]),
+                                           pack2<BF16>(o[c + 6], o[c + 7]));
+                    } else if (live) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            part_dst[(8 * i + c / 4) * 32] =
+                                make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                    __syncwarp();
+                }
+                if constexpr (!PAIR) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(t == 1 ? &bar.join_full : &bar.join_empty);
+                    join_phase ^= 1;
+                }
+            }
+        }
+        if (!ok) fail();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kIssuer) {
+        tmem_fence_after();
+        tmem_free(tmem, 512);
+    }
 }
 
-template <bool BF16, int DT>
-cudaError_t launch_d(const PagedAttnArgs &a, cudaStream_t st) {
-    const dim3 grid(a.n_tokens, (a.H + 3) / 4);
-    if (a.c.head_dim == 64)
-        return launch_ex(attn_kernel<BF16, DT, 64>, grid, dim3(128), 0, st, true, a);
-    return launch_ex(attn_kernel<BF16, DT, 128>, grid, dim3(128), 0, st, true, a);
+// Joins the items that a cut between CTAs divided: CTA (c, y) serves the item
+// whose first piece is CTA c's last segment and goes on in the CTAs after it.
+//   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
+// A warp takes 32 rows and 8 channels at a time, a lane a row.
+template <bool BF16, int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Dev a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 rec = a.merge[2 * blockIdx.x];
+    if (rec.x == 0) return;
+    const int head = a.merge[2 * blockIdx.x + 1].x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int blocks = a.ws_rows / 32;
+    const size_t first = 2 * blockIdx.x + rec.y, next = 2 * blockIdx.x;
+    for (int u = blockIdx.y * 8 + warp; u < blocks * (D / 8); u += gridDim.y * 8) {
+        const int prow = u / (D / 8) * 32 + lane, c8 = u % (D / 8);
+        const int r = prow % kTile;
+        const int tok = prow / kTile * a.q_tokens + r / a.G;
+        if (r >= a.q_tokens * a.G || tok >= rec.w) continue;
+        float m = -INFINITY;
+        for (int i = 0; i < rec.x; ++i)
+            m = fmaxf(m, a.ml[(i == 0 ? first : next + 2 * i) * a.ws_rows + prow].x);
+        float o[8] = {};
+        float l = 0.0f;
+        for (int i = 0; i < rec.x; ++i) {
+            const size_t slot = i == 0 ? first : next + 2 * i;
+            const float2 ml = a.ml[slot * a.ws_rows + prow];
+            if (ml.x == -INFINITY) continue;
+            const float f = exp2_approx(ml.x - m);
+            l += f * ml.y;
+            const float4 *p = reinterpret_cast<const float4 *>(a.acc) +
+                              ((slot * blocks + prow / 32) * (D / 4) + 2 * c8) * 32 + lane;
+            const float4 u0 = p[0], u1 = p[32];
+            o[0] = fmaf(f, u0.x, o[0]);
+            o[1] = fmaf(f, u0.y, o[1]);
+            o[2] = fmaf(f, u0.z, o[2]);
+            o[3] = fmaf(f, u0.w, o[3]);
+            o[4] = fmaf(f, u1.x, o[4]);
+            o[5] = fmaf(f, u1.y, o[5]);
+            o[6] = fmaf(f, u1.z, o[6]);
+            o[7] = fmaf(f, u1.w, o[7]);
+        }
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        *reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(rec.z + tok) * a.out_stride +
+                                   static_cast<int64_t>(head * a.G + r % a.G) * D + 8 * c8) =
+            make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),
+                       pack2<BF16>(o[4] * inv, o[5] * inv), pack2<BF16>(o[6] * inv, o[7] * inv));
+    }
+}
+
+// ----------------------------------------------------------------- launch ---
+using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
+
+// The driver's encoder of tensor maps, asked of the runtime once.
+EncodeTiled encoder() {
+    static std::atomic<void *> fn{nullptr};
+    void *p = fn.load(std::memory_order_relaxed);
+    if (!p) {
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            return nullptr;
+        fn.store(p, std::memory_order_relaxed);
+    }
+    return reinterpret_cast<EncodeTiled>(p);
+}
+
+bool make_map(CUtensorMap *m, bool bf16, const void *base, int rank, const cuuint64_t *dims,
+              const cuuint64_t *strides, const cuuint32_t *box) {
+    const EncodeTiled enc = encoder();
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                      rank, const_cast<void *>(base), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct WsPlan {
+    int ctas, rows;
+    bool pair;
+    size_t merge, ml, acc, total;
+};
+
+WsPlan ws_plan(int G, int D, int max_new) {
+    WsPlan w;
+    w.ctas = device_sm_count();
+    w.pair = max_new > kTile / G;
+    w.rows = w.pair ? 2 * kTile : (max_new * G + 31) / 32 * 32;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.merge = 0;
+    w.ml = up(static_cast<size_t>(w.ctas) * 2 * sizeof(int4));
+    w.acc = w.ml + up(static_cast<size_t>(w.ctas) * 2 * w.rows * sizeof(float2));
+    w.total = w.acc + up(static_cast<size_t>(w.ctas) * 2 * w.rows * D * sizeof(float));
+    return w;
+}
+
+template <bool BF16, int D, bool PAIR>
+cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
+    const kvd_paged_cache &c = p.c;
+    Dev a = {};
+    a.c = c;
+    a.out = static_cast<uint16_t *>(p.out);
+    a.out_stride = p.out_stride;
+    a.H = p.H;
+    a.G = p.G;
+    a.n_tokens = p.n_tokens;
+    a.max_new = p.max_new;
+    a.window = p.window;
+    a.starts = p.starts;
+    a.scale_log2 = p.scale_log2;
+    a.q_tokens = kTile / p.G;
+    a.box = 16;
+    while (a.box < kTile && c.page_size % (2 * a.box) == 0) a.box *= 2;
+    const int64_t rows = static_cast<int64_t>(c.n_pages) * c.n_kv_heads * c.page_size;
+    a.dead_row = static_cast<int>(rows);
+    a.min_tiles = 2;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    a.merge = reinterpret_cast<int4 *>(base + w.merge);
+    a.ml = reinterpret_cast<float2 *>(base + w.ml);
+    a.acc = reinterpret_cast<float *>(base + w.acc);
+    a.ws_rows = w.rows;
+
+    CUtensorMap q_map, k_map, v_map;
+    const cuuint64_t qd[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.G),
+                              static_cast<cuuint64_t>(c.n_kv_heads),
+                              static_cast<cuuint64_t>(p.n_tokens)};
+    const cuuint64_t qs[3] = {static_cast<cuuint64_t>(D) * 2,
+                              static_cast<cuuint64_t>(D) * 2 * p.G,
+                              static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), 1,
+                              static_cast<cuuint32_t>(a.q_tokens)};
+    const cuuint64_t kd[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t ks[1] = {static_cast<cuuint64_t>(D) * 2};
+    const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(a.box)};
+    if (!make_map(&q_map, BF16, p.q, 4, qd, qs, qb) || !make_map(&k_map, BF16, c.k, 2, kd, ks, kb) ||
+        !make_map(&v_map, BF16, c.v, 2, kd, ks, kb))
+        return cudaErrorInvalidValue;
+
+    constexpr size_t smem = Shape<D, PAIR>::kSmem;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(attn_kernel<BF16, D, PAIR>),
+                                   kThreads, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_ex(attn_kernel<BF16, D, PAIR>, dim3(w.ctas), dim3(kThreads), smem, st, true, a, q_map,
+                  k_map, v_map);
+    if (e != cudaSuccess) return e;
+    return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, PAIR ? 4 : 1), dim3(256), 0, st, true, a);
+}
+
+template <bool BF16>
+cudaError_t launch_type(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
+    const WsPlan w = ws_plan(p.G, p.c.head_dim, p.max_new);
+    if (p.c.head_dim == 64)
+        return w.pair ? launch_shape<BF16, 64, true>(p, w, ws, st)
+                      : launch_shape<BF16, 64, false>(p, w, ws, st);
+    return w.pair ? launch_shape<BF16, 128, true>(p, w, ws, st)
+                  : launch_shape<BF16, 128, false>(p, w, ws, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st) {
-    (void)ws;
-    if (a.c.dtype == KVD_F16) return launch_d<false, KVD_F16>(a, st);
-    if (a.c.dtype == KVD_BF16) return launch_d<true, KVD_BF16>(a, st);
-    return a.bf16 ? launch_d<true, KVD_INT8>(a, st) : launch_d<false, KVD_INT8>(a, st);
+    if (a.c.dtype == KVD_INT8) return launch_paged_attn_simple(a, st);
+    return a.bf16 ? launch_type<true>(a, ws, st) : launch_type<false>(a, ws, st);
 }
 
 size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new) {
-    (void)c, (void)H, (void)n_tokens, (void)max_new;
-    return 256;
+    (void)n_tokens;
+    return ws_plan(H / c.n_kv_heads, c.head_dim, max_new).total;
 }
 
 }  // namespace kvd
