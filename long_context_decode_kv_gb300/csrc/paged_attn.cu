@@ -20,9 +20,10 @@
 // (pages land as they lie, 16 to 128 rows a box); warp 9 issues the products
 //   S = Q K^T   shared x shared      O += P V   P from tensor memory
 // S of one tile is overwritten in place by P, so two streams' S and O fill the
-// 512 columns.  The maximum that scales a row's exponentials is raised only when
-// a logit passes it by 2^8, which leaves the sums exact to f32 and makes the
-// rescaling of O rare; P stays below 2^8, far inside f16.
+// 512 columns.  The reference m of a row's weights 2^(logit - m) follows its
+// maximum loosely, within a factor that f16 and f32 hold with the same relative
+// error; that spares the search for each tile's maximum and makes the rescaling
+// of O rare.
 // P is rounded to the input type (the tensor core's operand): a relative error
 // of half a step in each weight, which sums and statistics in f32 do not add to.
 #include <cuda.h>
@@ -44,7 +45,10 @@ constexpr int kProducer = 8, kIssuer = 9;  // warps; 10 and 11 idle
 // Registers a thread: 168 at launch (64,512 for 384 threads), moved to the
 // softmax warps, which hold a row's 128 logits: 256 * 208 + 128 * 88 = 64,512.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
-constexpr float kRaise = 8.0f;   // log2 by which a logit may pass the running maximum
+// A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
+// weights add up to more than kRaise raises m for the next one, and one above
+// kRedo is computed again (f16 holds weights up to 65,504).
+constexpr float kRaise = 256.0f, kRedo = 8192.0f;
 
 struct Dev {  // a launch's arguments
     kvd_paged_cache c;
@@ -62,6 +66,22 @@ struct Dev {  // a launch's arguments
     int4 *merge;        // [CTAs][2]: what merge_kernel joins
     int ws_rows;        // rows of a partial: 256 (PAIR) or fewer, a multiple of 32
 };
+
+// mbar_wait in few instructions, for the waits between the roles: most find the
+// phase complete, and the issuing warp, which runs a few lines between the
+// softmax warps' long ones, pays for each line fetched.  Warps call it whole,
+// and all lanes get the same answer.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((n & 63u) == 0) {
+            const uint64_t t = global_timer_ns();
+            if (t0 == 0) t0 = t;
+            if (__any_sync(0xffffffffu, *abort || t - t0 > kWaitLimitNs)) return false;
+        }
+    }
+}
 
 // ---------------------------------------------------------------- items ---
 struct Seq {
@@ -347,6 +367,11 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         const int boxes = kTile / a.box;
         const int ps = a.c.page_size;
         uint32_t it = 0, keys = 0;  // ring places filled, key tiles loaded
+        // Bits of the ring's places: whether what lies there is freed by its own
+        // arrival (a key tile behind a value tile is freed by that one's), and
+        // the parity of the next arrival.
+        uint32_t own = 0, phase = 0;
+        uint32_t filled = 0, fills = 0;  // places whose full barrier was used; its next parity
         uint32_t q_phase = 0;
         bool ok = true;
         int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
@@ -354,7 +379,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             int j0, j1;
             span_of(g, j0, j1);
             if (g.k > 0) {
-                ok = mbar_wait(&bar.q_empty, q_phase, abort);
+                ok = wait_for(&bar.q_empty, q_phase, abort);
                 q_phase ^= 1;
                 if (!ok) break;
             }
@@ -371,7 +396,6 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
             }
             // the cache row of this lane's box of tile j (dead_row: not needed, or a bad page)
-            uint32_t bad = 0;
             auto row_of = [&](int j, bool &is_bad) -> int {
                 is_bad = false;
                 const int t0 = j * kTile + lane * a.box;
@@ -383,29 +407,40 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 return is_bad ? a.dead_row
                               : (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
             };
-            auto load = [&](int row, const CUtensorMap *map) -> bool {
+            // The next place of the ring, free: a value tile, and the key tile
+            // that follows it in the same iteration of the products, complete on
+            // the value tile's barrier; the first key tiles on their own.
+            auto place = [&](bool frees) -> bool {
                 const uint32_t st = it % kStages;
-                if (!mbar_wait(&bar.kv_empty[st], ((it / kStages) & 1) ^ 1, abort)) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&bar.kv_full[st], Sh::kTileBytes);
+                if (own >> st & 1) {
+                    if (!wait_for(&bar.kv_empty[st], phase >> st & 1, abort)) return false;
+                    phase ^= 1u << st;
+                }
+                own = (own & ~(1u << st)) | (frees ? 1u << st : 0u);
+                return true;
+            };
+            auto expect = [&](uint64_t *full, int tiles) {
+                filled |= 1u << (it % kStages);
+                fills ^= 1u << (it % kStages);
+                if (lane == 0) mbar_arrive_expect_tx(full, tiles * Sh::kTileBytes);
                 __syncwarp();
+            };
+            auto load = [&](int row, const CUtensorMap *map, uint64_t *full) {
                 if (lane < boxes) {
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h)
-                        tma_load_2d(ring + st * Sh::kTileBytes + h * kHalfBytes +
+                        tma_load_2d(ring + (it % kStages) * Sh::kTileBytes + h * kHalfBytes +
                                         lane * a.box * 128,
-                                    map, h * 64, row, &bar.kv_full[st], policy);
+                                    map, h * 64, row, full, policy);
                 }
                 ++it;
-                return true;
             };
-            auto load_keys = [&](int row, bool is_bad) -> bool {
-                bad = __reduce_or_sync(0xffffffffu,
-                                       is_bad ? ((1u << (a.box / 16)) - 1) << (lane * (a.box / 16))
-                                              : 0u);
+            auto mark_dead = [&](bool is_bad) {
+                const int n = a.box / 16;
+                const uint32_t bad =
+                    __reduce_or_sync(0xffffffffu, is_bad ? ((1u << n) - 1) << (lane * n) : 0u);
                 if (lane == 0) dead_groups[keys & 7] = bad;
-                __syncwarp();
                 ++keys;
-                return load(row, &k_map);
             };
             // rows of the next tiles, read ahead of their use
             int row[kAhead + 2];
@@ -414,10 +449,21 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             for (int i = 0; i < kAhead + 2; ++i) row[i] = row_of(j0 + i, is_bad[i]);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (ok && j0 + i < j1) ok = load_keys(row[i], is_bad[i]);
+                if (ok && j0 + i < j1 && (ok = place(true))) {
+                    mark_dead(is_bad[i]);
+                    uint64_t *full = &bar.kv_full[it % kStages];
+                    expect(full, 1);
+                    load(row[i], &k_map, full);
+                }
             for (int j = j0; ok && j < j1; ++j) {
-                ok = load(row[0], &v_map);
-                if (ok && j + kAhead < j1) ok = load_keys(row[kAhead], is_bad[kAhead]);
+                if (!(ok = place(true))) break;
+                const bool more = j + kAhead < j1;
+                uint64_t *full = &bar.kv_full[it % kStages];
+                if (more) mark_dead(is_bad[kAhead]);
+                expect(full, more ? 2 : 1);
+                load(row[0], &v_map, full);
+                // the value tile's arrivals are due even if the key tile's place never comes
+                if (more && (ok = place(false))) load(row[kAhead], &k_map, full);
 #pragma unroll
                 for (int i = 0; i < kAhead + 1; ++i) {
                     row[i] = row[i + 1];
@@ -442,31 +488,33 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         if (*abort) {
             // nothing may land in shared memory after the CTA has gone
             volatile int none = 0;
-            for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
-                mbar_wait(&bar.kv_full[i % kStages], (i / kStages) & 1, &none);
+            for (uint32_t st = 0; st < kStages; ++st)
+                if (filled >> st & 1) mbar_wait(&bar.kv_full[st], ~(fills >> st) & 1, &none);
         }
         } else if (warp == kIssuer) {
         // ---------------------------------------------------- products ---
         constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kTile, false);
         constexpr uint32_t kIdO = mma_idesc(BF16, kTile, D, true);
-        const uint32_t q_addr = smem_addr(q_smem), ring_addr = smem_addr(ring);
-        uint32_t it = 0;
-        uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+        const uint32_t ring_addr = smem_addr(ring);
+        const uint32_t q_desc = warp_uniform(desc_low(smem_addr(q_smem), 16));
+        const uint32_t tmem_u = warp_uniform(tmem);
+        uint32_t st = 0;  // place of the ring
+        uint32_t full_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
         bool ok = true;
-        auto wait_tile = [&]() -> bool {  // the next place of the ring is full
-            const bool r = mbar_wait(&bar.kv_full[it % kStages], (it / kStages) & 1, abort);
-            tmem_fence_after();
+        auto wait_tile = [&]() -> bool {  // what this place's barrier announces is there
+            const bool r = wait_for(&bar.kv_full[st], full_phase >> st & 1, abort);
+            full_phase ^= 1u << st;
             return r;
         };
-        auto issue_s = [&](int t) {  // the tile at `it` against row tile t
-            if (lane == 0) {
-                const uint32_t q = q_addr + (PAIR ? t * Sh::kTileBytes : 0);
-                const uint32_t k = ring_addr + (it % kStages) * Sh::kTileBytes;
+        auto next_place = [&] { st = st + 1 == kStages ? 0 : st + 1; };
+        auto issue_s = [&](int t) {  // the key tile at this place against row tile t
+            const uint32_t k = warp_uniform(desc_low(ring_addr + st * Sh::kTileBytes, 16));
+            const uint32_t q = q_desc + (PAIR ? t * (Sh::kTileBytes / 16) : 0);
+            if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t at = (i / 4) * kHalfBytes + (i % 4) * 32;
-                    mma_ss(tmem + t * 128, smem_desc(q + at, 16, 1024), smem_desc(k + at, 16, 1024),
-                           kIdS, i > 0);
+                    const uint32_t at = ((i / 4) * kHalfBytes + (i % 4) * 32) / 16;
+                    mma_ss(tmem_u + t * 128, smem_desc(q + at), smem_desc(k + at), kIdS, i > 0);
                 }
                 mma_commit(&bar.s_full[t]);
             }
@@ -479,41 +527,38 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 #pragma unroll
             for (int t = 0; t < (PAIR ? 2 : 1); ++t)
                 if (ok && part[t].j0 < part[t].j1) {
-                    ok = mbar_wait(&bar.q_full[t], q_phase[t], abort);
+                    ok = wait_for(&bar.q_full[t], q_phase[t], abort);
                     q_phase[t] ^= 1;
                 }
             // stream t takes key tile j
             auto takes = [&](int t, int j) {
                 return PAIR ? (j >= part[t].j0 && j < part[t].j1) : ((j - j0) & 1) == t && j < j1;
             };
-            // S of key tile j for the streams that take it, then its place is free
-            auto scores = [&](int j, int t) {
-                if (takes(t, j)) issue_s(t);
-            };
-            auto release = [&]() {
-                if (lane == 0) mma_commit(&bar.kv_empty[it % kStages]);
-                __syncwarp();
-                ++it;
-            };
             // the segment's last S is issued: its queries can be replaced
             auto release_q = [&]() {
-                if (lane == 0) mma_commit(&bar.q_empty);
+                if (elect_one()) mma_commit(&bar.q_empty);
                 __syncwarp();
             };
             for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i) {
                 if (!(ok = wait_tile())) break;
-                scores(j0 + i, 0);
-                scores(j0 + i, 1);
-                release();
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (takes(t, j0 + i)) issue_s(t);
+                if (elect_one()) mma_commit(&bar.kv_empty[st]);
+                __syncwarp();
+                next_place();
             }
             if (j1 - j0 <= kAhead) release_q();
             for (int j = j0; ok && j < j1; ++j) {
+                // the value tile, and the key tile ahead at the next place
                 if (!(ok = wait_tile())) break;
-                const uint32_t v_st = it % kStages;
-                uint8_t *vs = ring + v_st * Sh::kTileBytes;
+                const uint32_t v_st = st;
+                const uint32_t v =
+                    warp_uniform(desc_low(ring_addr + v_st * Sh::kTileBytes, kHalfBytes));
                 // value rows that no token of the item sees may hold NaN: clear them
                 const int from = max(g.it.lo - j * kTile, 0), to = min(g.it.hi - j * kTile, kTile);
                 if (from > 0 || to < kTile) {
+                    uint8_t *vs = ring + v_st * Sh::kTileBytes;
                     const int n = (from + (kTile - max(to, 0))) * 8 * kHalves;
                     for (int i = lane; i < n; i += 32) {
                         const int c = i % 8, h = (i / 8) % kHalves;
@@ -525,43 +570,37 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     fence_proxy_async();
                     __syncwarp();
                 }
-                ++it;  // from here on the key tile ahead
+                next_place();
                 const int ahead = j + kAhead;
-                bool have = false;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (takes(t, j)) {
-                        if (!(ok = mbar_wait(&bar.p_full[t], p_phase[t], abort))) break;
+                        const uint32_t add =
+                            warp_uniform(PAIR ? j != part[t].j0 : j - j0 >= 2);
+                        if (!(ok = wait_for(&bar.p_full[t], p_phase[t], abort))) break;
                         p_phase[t] ^= 1;
                         tmem_fence_after();
-                        if (lane == 0) {
-                            const bool fresh = PAIR ? j == part[t].j0 : j - j0 < 2;
-                            const uint32_t v = ring_addr + v_st * Sh::kTileBytes;
+                        if (elect_one()) {
 #pragma unroll
                             for (int i = 0; i < kTile / 16; ++i)
-                                mma_ts(tmem + 256 + t * 128, tmem + t * 128 + i * 8,
-                                       smem_desc(v + i * 2048, kHalfBytes, 1024), kIdO,
-                                       !fresh || i > 0);
+                                mma_ts(tmem_u + 256 + t * 128, tmem_u + t * 128 + i * 8,
+                                       smem_desc(v + i * (2048 / 16)), kIdO, i > 0 ? 1 : add);
                             if (PAIR && j + 1 == part[t].j1) mma_commit(&bar.o_full[t]);
                         }
                         __syncwarp();
                     }
-                    if (ahead < j1 && takes(t, ahead)) {
-                        if (!have && !(ok = wait_tile())) break;
-                        have = true;
-                        issue_s(t);
-                    }
+                    if (ahead < j1 && takes(t, ahead)) issue_s(t);
                 }
                 if (!ok) break;
-                if (lane == 0) mma_commit(&bar.kv_empty[v_st]);
+                // both tiles are used up
+                if (elect_one()) mma_commit(&bar.kv_empty[v_st]);
                 __syncwarp();
                 if (ahead < j1) {
-                    if (!have && !(ok = wait_tile())) break;
-                    release();
+                    next_place();
                     if (ahead + 1 == j1) release_q();
                 }
             }
-            if (!PAIR && ok && lane == 0) {
+            if (!PAIR && ok && elect_one()) {
                 mma_commit(&bar.o_full[0]);
                 mma_commit(&bar.o_full[1]);
             }
@@ -569,10 +608,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         }
         if (!ok) fail();
         // every product and every barrier arrival is done before the CTA goes
-        if (lane == 0) mma_commit(&bar.done);
+        if (elect_one()) mma_commit(&bar.done);
         __syncwarp();
         volatile int none = 0;
-        if (!mbar_wait(&bar.done, 0, &none)) fail();
+        if (!wait_for(&bar.done, 0, &none)) fail();
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -593,11 +632,12 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             // keys [lo, hi) of this row
             const int hi = row < rows ? max(pos + 1, 0) : 0x7fffffff;
             const int lo = row < rows && a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-            float m = -INFINITY;
-            float2 l2 = make_float2(0.0f, 0.0f);
+            float m = row < rows ? -INFINITY : 0.0f;
+            // rows that are none keep a scale of their own
+            float l = 0.0f, last = 0.0f;
             const int first = PAIR ? part.j0 : j0 + t;
             for (int j = first; j < part.j1; j += PAIR ? 1 : 2) {
-                if (!(ok = mbar_wait(&bar.s_full[t], s_phase, abort))) break;
+                if (!(ok = wait_for(&bar.s_full[t], s_phase, abort))) break;
                 s_phase ^= 1;
                 if (warp_live) {
                     tmem_fence_after();
@@ -614,48 +654,71 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         for (int c = 0; c < 128; ++c)
                             if (c >= rh || c < rl || (dead >> (c / 16) & 1)) s[c] = -INFINITY;
                     }
-                    float mx[4] = {s[0], s[1], s[2], s[3]};
+                    // The exponentials take the scale of the tiles before, and the
+                    // tile's own sum tells whether it still fits: one above kRaise
+                    // raises the scale for the next tile, one above kRedo (or a row's
+                    // first tile) finds the maximum and computes the tile again.
+                    // In between no pass over the row looks for a maximum.
+                    bool fix = __any_sync(0xffffffffu, m == -INFINITY || last > kRaise);
+                    float2 sum[2];
+                    for (;;) {
+                        if (fix) {
+                            float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                    for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-                    const float top =
-                        fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
-                    if (__any_sync(0xffffffffu, top > m + kRaise && m != -INFINITY)) {
-                        // the maximum has outgrown the sums' scale
-                        const float mn = fmaxf(m, top);
-                        const float f = m == -INFINITY ? 1.0f : exp2_approx(m - mn);
-                        m = mn;
-                        l2.x *= f;
-                        l2.y *= f;
+                            for (int c = 4; c < 124; c += 8)
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            float o[32];
-                            tmem_ld32(o_addr + 32 * i, o);
-                            tmem_wait_ld();
-                            pin32(o);
+                                for (int i = 0; i < 4; ++i)
+                                    mx[i] = fmax3(mx[i], s[c + i], s[c + 4 + i]);
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] *= f;
-                            tmem_st32(o_addr + 32 * i, o);
+                            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[124 + i]);
+                            const float top =
+                                fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                            const float mn = fmaxf(last > kRaise ? m + __log2f(last) - 7.0f : m, top);
+                            const float f = m == -INFINITY || mn == -INFINITY
+                                                ? 1.0f
+                                                : exp2_approx(m - mn);
+                            m = mn;
+                            last = 0.0f;
+                            l *= f;
+                            if (j > first) {
+#pragma unroll
+                                for (int i = 0; i < D / 16; ++i) {
+                                    float o[16];
+                                    tmem_ld16(o_addr + 16 * i, o);
+                                    tmem_wait_ld();
+                                    pin16(o);
+#pragma unroll
+                                    for (int c = 0; c < 16; ++c) o[c] *= f;
+                                    tmem_st16(o_addr + 16 * i, reinterpret_cast<uint32_t *>(o));
+                                }
+                            }
                         }
-                    } else if (m == -INFINITY) {
-                        m = top;
-                    }
-                    const float base = m == -INFINITY ? 0.0f : m;
-                    const float2 sc = make_float2(a.scale_log2, a.scale_log2);
-                    const float2 off = make_float2(-base, -base);
+                        const float base = m == -INFINITY ? 0.0f : m;
+                        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+                        const float2 off = make_float2(-base, -base);
+                        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t p[16];
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t p[16];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const int at = 32 * i + 2 * c;
-                            float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc, off);
-                            x.x = exp2_approx(x.x);
-                            x.y = exp2_approx(x.y);
-                            l2 = __fadd2_rn(l2, x);
-                            p[c] = pack2<BF16>(x.x, x.y);
+                            for (int c = 0; c < 16; ++c) {
+                                const int at = 32 * i + 2 * c;
+                                float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc, off);
+                                x.x = exp2_approx(x.x);
+                                x.y = exp2_approx(x.y);
+                                sum[c & 1] = __fadd2_rn(sum[c & 1], x);
+                                p[c] = pack2<BF16>(x.x, x.y);
+                            }
+                            tmem_st16(s_addr + 16 * i, p);
                         }
-                        tmem_st16(s_addr + 16 * i, p);
+                        sum[0] = __fadd2_rn(sum[0], sum[1]);
+                        last = sum[0].x + sum[0].y;
+                        // after a fix no weight passes 1
+                        if (fix || !__any_sync(0xffffffffu, last > kRedo)) break;
+                        fix = true;
+                        last = 0.0f;
                     }
+                    l += last;
                     tmem_wait_st();
                     tmem_fence_before();
                 }
@@ -665,10 +728,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             if (!ok) break;
             keys += j1 - j0;
             // ---- the segment's result
-            float l = l2.x + l2.y;
             const bool some = first < part.j1;
             if (PAIR ? some : j1 > j0) {
-                if (!(ok = mbar_wait(&bar.o_full[t], o_phase, abort))) break;
+                if (!(ok = wait_for(&bar.o_full[t], o_phase, abort))) break;
                 o_phase ^= 1;
                 tmem_fence_after();
             }
@@ -679,11 +741,11 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             if constexpr (!PAIR) {
                 if (t == 1) {
                     // the halves of the segment before have been read
-                    if (!(ok = mbar_wait(&bar.join_empty, join_phase ^ 1, abort))) break;
+                    if (!(ok = wait_for(&bar.join_empty, join_phase ^ 1, abort))) break;
                     join_ml[row] = make_float2(m, l);
                 }
                 if (t == 0) {
-                    if (!(ok = mbar_wait(&bar.join_full, join_phase, abort))) break;
+                    if (!(ok = wait_for(&bar.join_full, join_phase, abort))) break;
                     const float2 o = join_ml[row];
                     const float mn = fmaxf(m, o.x);
                     mine = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
@@ -709,8 +771,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 #pragma unroll
             for (int h = 0; h < kHalves; ++h) {
                 if (!PAIR && h > 0) {
-                    ok = t == 1 ? mbar_wait(&bar.join_empty, join_phase ^ 1, abort)
-                                : mbar_wait(&bar.join_full, join_phase, abort);
+                    ok = t == 1 ? wait_for(&bar.join_empty, join_phase ^ 1, abort)
+                                : wait_for(&bar.join_full, join_phase, abort);
                     if (!ok) break;
                 }
 #pragma unroll

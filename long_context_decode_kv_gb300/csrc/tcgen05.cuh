@@ -54,10 +54,29 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
 // bytes.  K-major operands (rows are M or N): sbo = 1024, from 8 rows to the
 // next 8; lbo unused.  MN-major operands (rows are K): lbo from one 64-element
 // column block to the next, sbo = 1024 from 8 rows to the next 8.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) |
-           (static_cast<uint64_t>(lbo >> 4) << 16) | (static_cast<uint64_t>(sbo >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+// The two halves: kDescHigh is the same for all, and the low one moves along a
+// tile by adding bytes / 16.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lbo) {
+    return ((addr & 0x3ffffu) >> 4) | ((lbo >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t smem_desc(uint32_t low) {
+    return (static_cast<uint64_t>(kDescHigh) << 32) | low;
+}
+
+// One lane of the warp, the same each time.  Products issued under it take
+// their descriptors from uniform registers when those come from warp_uniform;
+// from ordinary ones each product costs several moves, more than it takes to
+// compute (measured: 90 cycles a 128x128x16 product against 64).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ uint32_t warp_uniform(uint32_t v) {
+    return __shfl_sync(0xffffffffu, v, 0);
 }
 
 // Instruction descriptor: f32 accumulator, A and B both f16 or both bf16,
@@ -69,20 +88,20 @@ constexpr uint32_t mma_idesc(bool bf16, int m, int n, bool b_mn) {
 
 // D (tensor memory) = A (shared) * B (shared) + (acc ? D : 0), K = 16.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+                                       uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 // The same with A in tensor memory (two elements a column).
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                       bool acc) {
+                                       uint32_t acc) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(acc))
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
 
@@ -108,18 +127,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v) {
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float *v) {
-    const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+__device__ __forceinline__ void pin16(float *v) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]),
+                          "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float *v) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
-        "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
-        "%28, %29, %30, %31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
-        "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
-        "r"(r[30]), "r"(r[31]), "r"(addr)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
     asm volatile(
@@ -163,9 +185,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// A barrier over `threads` threads of the block (warps call it whole).
-__device__ __forceinline__ void named_barrier(int id, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 }  // namespace kvd
