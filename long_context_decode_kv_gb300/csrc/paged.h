@@ -50,7 +50,6 @@ struct PagedAttnArgs {
 };
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st);
-cudaError_t launch_paged_attn_simple(const PagedAttnArgs &a, cudaStream_t st);
 size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new);
 
 }  // namespace kvd

@@ -40,11 +40,14 @@ namespace kvd {
 namespace {
 
 constexpr int kTile = 128;       // keys a tile, rows a tile
-constexpr int kThreads = 384;
 constexpr int kProducer = 8, kIssuer = 9;  // warps; 10 and 11 idle
-// Registers a thread: 168 at launch (64,512 for 384 threads), moved to the
-// softmax warps, which hold a row's 128 logits: 256 * 208 + 128 * 88 = 64,512.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kConverter = 12;             // to 15: int8 caches only
+// Registers a thread: 168 at launch (64,512 for 384 threads), or 128 (65,536 for
+// 512), moved to the softmax warps, which hold a row's 128 logits:
+// 256 * 208 + 128 * 88 = 64,512, or 256 * 184 + 256 * 72 = 65,536.
+constexpr int threads_of(bool i8) { return i8 ? 512 : 384; }
+constexpr int softmax_regs(bool i8) { return i8 ? 184 : 208; }
+constexpr int other_regs(bool i8) { return i8 ? 72 : 88; }
 // A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
 // weights add up to more than kRaise raises m for the next one, and one above
 // kRedo is computed again (f16 holds weights up to 65,504).
@@ -170,28 +173,65 @@ __device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, S
     return true;
 }
 
+// Four int8 codes as two words of f16 or bf16, exactly.  f16: code + 128 in the
+// low bits of 1024 + x, less 1152.  bf16: 128 + (code's low 7 bits), less 128 or,
+// for a negative code, 256.
+template <bool BF16>
+__device__ __forceinline__ void codes_to(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (BF16) {
+        const uint32_t t0 = __byte_perm(w, 0, 0x4140), t1 = __byte_perm(w, 0, 0x4342);
+        auto sub = [](uint32_t t) {
+            const uint32_t x = (t & 0x007f007fu) | 0x43004300u, y = (t & 0x00800080u) | 0x43004300u;
+            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&y));
+            return *reinterpret_cast<const uint32_t *>(&d);
+        };
+        lo = sub(t0);
+        hi = sub(t1);
+    } else {
+        const uint32_t u = w ^ 0x80808080u;
+        const uint32_t k1152 = 0x64806480u;
+        auto sub = [&](uint32_t x) {
+            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x),
+                                      *reinterpret_cast<const __half2 *>(&k1152));
+            return *reinterpret_cast<const uint32_t *>(&d);
+        };
+        lo = sub(__byte_perm(u, 0x64646464u, 0x4140));
+        hi = sub(__byte_perm(u, 0x64646464u, 0x4342));
+    }
+}
+
 // ------------------------------------------------------------ the kernel ---
-template <int D, bool PAIR>
+template <int D, bool PAIR, bool I8>
 struct Shape {
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
     static constexpr int kJoinBytes = PAIR ? 0 : kTile * 64 * 4;  // 64 channels of a stream's O
-    static constexpr int kStages = D == 128 ? 5 : 8;
+    static constexpr int kStages = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    // int8: tiles as loaded (codes, then the rows' key and value scales with a key
+    // tile), and the scales the softmax takes, for more key tiles than the ring
+    // lets the loads run ahead of it
+    static constexpr int kRaw = I8 ? (D == 128 ? 3 : 6) : 0;
+    static constexpr int kRawBytes = kTile * D + 2 * kTile * 4;
+    static constexpr int kScales = D == 128 ? 4 : 8;
+    static constexpr int kScaleBytes = I8 ? kScales * 2 * kTile * 4 : 0;
     static constexpr int kAhead = PAIR ? 1 : 2;  // key tiles whose S is issued ahead of PV
     // +1024: the tiles start on a 1024-byte boundary
-    static constexpr int kSmem = 1024 + kQBytes + kJoinBytes + kStages * kTileBytes;
+    static constexpr int kSmem = 1024 + kQBytes + kJoinBytes + kStages * kTileBytes +
+                                 kRaw * kRawBytes + kScaleBytes;
 };
 
 struct Bars {
     uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], done,
-        join_full, join_empty;
+        join_full, join_empty, raw_full[6], raw_empty[6];
 };
 
-template <bool BF16, int D, bool PAIR>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool BF16, int D, bool PAIR, bool I8>
+__global__ void __launch_bounds__(threads_of(I8), 1)
 attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q_map,
             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using Sh = Shape<D, PAIR>;
+    using Sh = Shape<D, PAIR, I8>;
+    constexpr int kThreads = threads_of(I8);
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
     constexpr int kStages = Sh::kStages;
@@ -203,6 +243,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     __shared__ int abort_flag;
     __shared__ uint32_t dead_groups[8];  // per key tile: its 16-key groups on bad pages
     __shared__ float2 join_ml[kTile];
+    __shared__ int value_exp[8];            // int8: per key tile, see Scales
+    __shared__ __align__(16) float ones[I8 ? kTile : 1];
     __shared__ long scan_total[kThreads / 32];
     __shared__ Walk start;
 
@@ -210,6 +252,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     uint8_t *q_smem = smem;
     float *join = reinterpret_cast<float *>(smem + Sh::kQBytes);
     uint8_t *ring = smem + Sh::kQBytes + Sh::kJoinBytes;
+    uint8_t *raw = ring + kStages * Sh::kTileBytes;
+    // Scales: [kScales][2][128], a key tile's key scales times the softmax scale, and
+    // its value scales times 2^-value_exp
+    float *scales = reinterpret_cast<float *>(raw + Sh::kRaw * Sh::kRawBytes);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int width = PAIR ? 2 * a.q_tokens : a.q_tokens;  // tokens of an item
@@ -223,8 +269,12 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             mbar_init(&bar.o_full[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.kv_full[i], 1);
+            mbar_init(&bar.kv_full[i], I8 ? 4 : 1);
             mbar_init(&bar.kv_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kRaw; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 4);
         }
         mbar_init(&bar.q_empty, 1);
         mbar_init(&bar.done, 1);
@@ -234,6 +284,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         abort_flag = 0;
         start.left = 0;
     }
+    if (I8 && tid < kTile) ones[tid] = 1.0f;
     pdl_wait();
     pdl_launch_dependents();
 
@@ -360,7 +411,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     };
 
     if (warp >= kProducer) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
         if (warp == kProducer) {
         // ------------------------------------------------------- loads ---
         const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
@@ -435,6 +486,32 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 ++it;
             };
+            // int8: the tile's codes as they lie, and with keys both rows' scales
+            auto load_raw = [&](int row, const CUtensorMap *map, bool keys_too) -> bool {
+                constexpr int kRaw = I8 ? Sh::kRaw : 1;
+                const uint32_t st = it % kRaw;
+                if (it >= kRaw && !wait_for(&bar.raw_empty[st], (it / kRaw - 1) & 1, abort))
+                    return false;
+                const bool live = lane < boxes && row != a.dead_row;
+                const int n = keys_too ? __popc(__ballot_sync(0xffffffffu, live)) : 0;
+                filled |= 1u << st;
+                fills ^= 1u << st;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&bar.raw_full[st], kTile * D + n * a.box * 8);
+                __syncwarp();
+                uint8_t *dst = raw + st * Sh::kRawBytes;
+                if (lane < boxes)
+                    tma_load_2d(dst + lane * a.box * D, map, 0, row, &bar.raw_full[st], policy);
+                if (keys_too && live) {
+                    float *sc = reinterpret_cast<float *>(dst + kTile * D) + lane * a.box;
+                    tma_load_1d(sc, static_cast<const float *>(a.c.k_scale) + row, a.box * 4,
+                                &bar.raw_full[st], policy);
+                    tma_load_1d(sc + kTile, static_cast<const float *>(a.c.v_scale) + row,
+                                a.box * 4, &bar.raw_full[st], policy);
+                }
+                ++it;
+                return true;
+            };
             auto mark_dead = [&](bool is_bad) {
                 const int n = a.box / 16;
                 const uint32_t bad =
@@ -449,21 +526,30 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             for (int i = 0; i < kAhead + 2; ++i) row[i] = row_of(j0 + i, is_bad[i]);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i)
-                if (ok && j0 + i < j1 && (ok = place(true))) {
+                if (ok && j0 + i < j1) {
                     mark_dead(is_bad[i]);
-                    uint64_t *full = &bar.kv_full[it % kStages];
-                    expect(full, 1);
-                    load(row[i], &k_map, full);
+                    if constexpr (I8) {
+                        ok = load_raw(row[i], &k_map, true);
+                    } else if ((ok = place(true))) {
+                        uint64_t *full = &bar.kv_full[it % kStages];
+                        expect(full, 1);
+                        load(row[i], &k_map, full);
+                    }
                 }
             for (int j = j0; ok && j < j1; ++j) {
-                if (!(ok = place(true))) break;
                 const bool more = j + kAhead < j1;
-                uint64_t *full = &bar.kv_full[it % kStages];
                 if (more) mark_dead(is_bad[kAhead]);
-                expect(full, more ? 2 : 1);
-                load(row[0], &v_map, full);
-                // the value tile's arrivals are due even if the key tile's place never comes
-                if (more && (ok = place(false))) load(row[kAhead], &k_map, full);
+                if constexpr (I8) {
+                    ok = load_raw(row[0], &v_map, false) &&
+                         (!more || load_raw(row[kAhead], &k_map, true));
+                } else {
+                    if (!(ok = place(true))) break;
+                    uint64_t *full = &bar.kv_full[it % kStages];
+                    expect(full, more ? 2 : 1);
+                    load(row[0], &v_map, full);
+                    // the value tile's bytes are due even if the key tile's place never comes
+                    if (more && (ok = place(false))) load(row[kAhead], &k_map, full);
+                }
 #pragma unroll
                 for (int i = 0; i < kAhead + 1; ++i) {
                     row[i] = row[i + 1];
@@ -488,8 +574,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         if (*abort) {
             // nothing may land in shared memory after the CTA has gone
             volatile int none = 0;
-            for (uint32_t st = 0; st < kStages; ++st)
-                if (filled >> st & 1) mbar_wait(&bar.kv_full[st], ~(fills >> st) & 1, &none);
+            uint64_t *full = I8 ? bar.raw_full : bar.kv_full;
+            for (uint32_t st = 0; st < 8; ++st)
+                if (filled >> st & 1) mbar_wait(&full[st], ~(fills >> st) & 1, &none);
         }
         } else if (warp == kIssuer) {
         // ---------------------------------------------------- products ---
@@ -557,7 +644,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     warp_uniform(desc_low(ring_addr + v_st * Sh::kTileBytes, kHalfBytes));
                 // value rows that no token of the item sees may hold NaN: clear them
                 const int from = max(g.it.lo - j * kTile, 0), to = min(g.it.hi - j * kTile, kTile);
-                if (from > 0 || to < kTile) {
+                if (!I8 && (from > 0 || to < kTile)) {
                     uint8_t *vs = ring + v_st * Sh::kTileBytes;
                     const int n = (from + (kTile - max(to, 0))) * 8 * kHalves;
                     for (int i = lane; i < n; i += 32) {
@@ -572,6 +659,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 next_place();
                 const int ahead = j + kAhead;
+                if (I8 && ahead < j1 && !(ok = wait_tile())) break;  // a barrier of its own
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (takes(t, j)) {
@@ -613,8 +701,103 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         volatile int none = 0;
         if (!wait_for(&bar.done, 0, &none)) fail();
         }
+        if constexpr (I8) {
+            if (warp >= kConverter) {
+                // ----------------------------------------- int8 to f16 or bf16 ---
+                // Codes are whole numbers up to 127, exact in either type; the
+                // scales go to the softmax, so the products lose nothing.
+                const int ct = tid - kConverter * 32;
+                uint32_t it = 0, out = 0, keys = 0, own = 0, phase = 0;
+                int exp_now = 0;
+                bool ok = true;
+                // One tile.  16 codes a step: 8 lanes read a row, and write its
+                // chunks so that the 8 lanes of a store hit different banks.
+                auto convert = [&](bool is_k, bool frees, int j, bool first) -> bool {
+                    const uint32_t st = out;
+                    if (own >> st & 1) {
+                        if (!wait_for(&bar.kv_empty[st], phase >> st & 1, abort)) return false;
+                        phase ^= 1u << st;
+                    }
+                    own = (own & ~(1u << st)) | (frees ? 1u << st : 0u);
+                    const uint32_t rs = it % Sh::kRaw;
+                    if (!wait_for(&bar.raw_full[rs], (it / Sh::kRaw) & 1, abort)) return false;
+                    const uint8_t *src = raw + rs * Sh::kRawBytes;
+                    uint8_t *dst = ring + st * Sh::kTileBytes;
+                    constexpr int kUnits = D / 16;  // 16-code steps a row
+                    if (is_k) {
+                        const float *sc = reinterpret_cast<const float *>(src + kTile * D);
+                        const int tok = j * kTile + ct;
+                        const bool dead = tok < g.it.lo || tok >= g.it.hi ||
+                                          (dead_groups[keys & 7] >> (ct / 16) & 1);
+                        const float ks = dead ? 0.0f : sc[ct];
+                        const float vs = dead ? 0.0f : sc[kTile + ct];
+                        // the exponent of the tile's largest value scale: each warp
+                        // looks at all 128 (NaN counts for nothing)
+                        float top = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = i * 32 + lane, tk = j * kTile + at;
+                            const bool d = tk < g.it.lo || tk >= g.it.hi ||
+                                           (dead_groups[keys & 7] >> (at / 16) & 1);
+                            top = fmaxf(top, d ? 0.0f : sc[kTile + at]);
+                        }
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                        const int e =
+                            min(max((__float_as_int(top) >> 23 & 255) - 126, -100), 100);
+                        // kept while the scales stay below 4: weights up to kRedo fit f16
+                        if (first || e > exp_now + 2) exp_now = e;
+                        float *to = scales + keys % Sh::kScales * (2 * kTile);
+                        to[ct] = ks * a.scale_log2;
+                        to[kTile + ct] = vs * __int_as_float((127 - exp_now) << 23);
+                        if (ct == 0) value_exp[keys % Sh::kScales] = exp_now;
+                        ++keys;
+                    }
+#pragma unroll 2
+                    for (int i = 0; i < kUnits; ++i) {
+                        const int unit = ct + i * 128;
+                        const int row = unit / kUnits, u = unit % kUnits;
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + row * D + 16 * u);
+                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) codes_to<BF16>(in[c], o[2 * c], o[2 * c + 1]);
+                        uint8_t *line = dst + (u / 4) * kHalfBytes + row * 128;
+                        const int odd = kUnits == 8 ? u / 4 : 0;
+                        const int c0 = ((u % 4) * 2 + odd) ^ (row & 7);
+                        const int c1 = ((u % 4) * 2 + 1 - odd) ^ (row & 7);
+                        *reinterpret_cast<uint4 *>(line + 16 * c0) =
+                            odd ? make_uint4(o[4], o[5], o[6], o[7])
+                                : make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4 *>(line + 16 * c1) =
+                            odd ? make_uint4(o[0], o[1], o[2], o[3])
+                                : make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(&bar.kv_full[st]);
+                        mbar_arrive(&bar.raw_empty[rs]);
+                    }
+                    ++it;
+                    out = st + 1 == kStages ? 0 : st + 1;
+                    return true;
+                };
+                while (ok && next_segment(a, width, w, g)) {
+                    int j0, j1;
+                    span_of(g, j0, j1);
+                    for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i)
+                        ok = convert(true, true, j0 + i, i == 0);
+                    for (int j = j0; ok && j < j1; ++j)
+                        ok = convert(false, true, j, false) &&
+                             (j + kAhead >= j1 || convert(true, false, j + kAhead, false));
+                }
+                if (!ok) fail();
+            }
+        }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(softmax_regs(I8)));
         // ------------------------------------------------------ softmax ---
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((warp & 3) << 21);  // this warp's 32 lanes
@@ -636,6 +819,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             // rows that are none keep a scale of their own
             float l = 0.0f, last = 0.0f;
             const int first = PAIR ? part.j0 : j0 + t;
+            int exp_now = 0;  // int8: O is in units of 2^exp_now
             for (int j = first; j < part.j1; j += PAIR ? 1 : 2) {
                 if (!(ok = wait_for(&bar.s_full[t], s_phase, abort))) break;
                 s_phase ^= 1;
@@ -649,30 +833,41 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     for (int i = 0; i < 4; ++i) pin32(s + 32 * i);
                     const int rh = hi - j * kTile, rl = lo - j * kTile;
                     const uint32_t dead = dead_groups[(keys + (j - j0)) & 7];
+                    const float *tile_sc = scales + (keys + (j - j0)) % Sh::kScales * (2 * kTile);
+                    const float *k_sc = tile_sc;
                     if (__any_sync(0xffffffffu, rh < kTile || rl > 0) || dead) {
 #pragma unroll
-                        for (int c = 0; c < 128; ++c)
+                        for (int c = 0; c < 128; ++c) {
+                            if (I8) s[c] *= k_sc[c];
                             if (c >= rh || c < rl || (dead >> (c / 16) & 1)) s[c] = -INFINITY;
+                        }
+                        if (I8) k_sc = ones;  // the logits are scaled already
+                    }
+                    int new_exp = 0;
+                    if constexpr (I8) {
+                        new_exp = value_exp[(keys + (j - j0)) % Sh::kScales];
+                        if (j == first) exp_now = new_exp;
                     }
                     // The exponentials take the scale of the tiles before, and the
                     // tile's own sum tells whether it still fits: one above kRaise
                     // raises the scale for the next tile, one above kRedo (or a row's
                     // first tile) finds the maximum and computes the tile again.
                     // In between no pass over the row looks for a maximum.
-                    bool fix = __any_sync(0xffffffffu, m == -INFINITY || last > kRaise);
+                    bool fix = __any_sync(0xffffffffu, m == -INFINITY || last > kRaise) ||
+                               (I8 && new_exp != exp_now);
                     float2 sum[2];
                     for (;;) {
                         if (fix) {
-                            float mx[4] = {s[0], s[1], s[2], s[3]};
+                            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                            for (int c = 4; c < 124; c += 8)
+                            for (int c = 0; c < 128; c += 8)
 #pragma unroll
                                 for (int i = 0; i < 4; ++i)
-                                    mx[i] = fmax3(mx[i], s[c + i], s[c + 4 + i]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[124 + i]);
-                            const float top =
-                                fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
+                                    mx[i] = I8 ? fmax3(mx[i], s[c + i] * k_sc[c + i],
+                                                       s[c + 4 + i] * k_sc[c + 4 + i])
+                                               : fmax3(mx[i], s[c + i], s[c + 4 + i]);
+                            const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) *
+                                              (I8 ? 1.0f : a.scale_log2);
                             const float mn = fmaxf(last > kRaise ? m + __log2f(last) - 7.0f : m, top);
                             const float f = m == -INFINITY || mn == -INFINITY
                                                 ? 1.0f
@@ -681,6 +876,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                             last = 0.0f;
                             l *= f;
                             if (j > first) {
+                                // by at most 2^-200 in one step: 0 where it matters
+                                const float fo =
+                                    I8 ? f * exp2_approx(static_cast<float>(exp_now - new_exp)) : f;
 #pragma unroll
                                 for (int i = 0; i < D / 16; ++i) {
                                     float o[16];
@@ -688,11 +886,12 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                     tmem_wait_ld();
                                     pin16(o);
 #pragma unroll
-                                    for (int c = 0; c < 16; ++c) o[c] *= f;
+                                    for (int c = 0; c < 16; ++c) o[c] *= fo;
                                     tmem_st16(o_addr + 16 * i, reinterpret_cast<uint32_t *>(o));
                                 }
                             }
                         }
+                        exp_now = new_exp;
                         const float base = m == -INFINITY ? 0.0f : m;
                         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
                         const float2 off = make_float2(-base, -base);
@@ -703,10 +902,15 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 const int at = 32 * i + 2 * c;
-                                float2 x = __ffma2_rn(make_float2(s[at], s[at + 1]), sc, off);
+                                float2 x = __ffma2_rn(
+                                    make_float2(s[at], s[at + 1]),
+                                    I8 ? *reinterpret_cast<const float2 *>(k_sc + at) : sc, off);
                                 x.x = exp2_approx(x.x);
                                 x.y = exp2_approx(x.y);
                                 sum[c & 1] = __fadd2_rn(sum[c & 1], x);
+                                if (I8)
+                                    x = __fmul2_rn(x, *reinterpret_cast<const float2 *>(
+                                                          tile_sc + kTile + at));
                                 p[c] = pack2<BF16>(x.x, x.y);
                             }
                             tmem_st16(s_addr + 16 * i, p);
@@ -737,7 +941,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             const bool whole = g.starts && g.ends;
             const int prow = (PAIR ? t * 128 : 0) + row;
             const size_t slot = 2 * blockIdx.x + (g.k == 0 ? 0 : 1);
-            float mine = 1.0f, other = 0.0f;  // scale of this stream's O and of the joined one's
+            // scale of this stream's O and of the joined one's
+            const float unit = I8 ? __int_as_float((127 + exp_now) << 23) : 1.0f;
+            float mine = unit, other = 0.0f;
             if constexpr (!PAIR) {
                 if (t == 1) {
                     // the halves of the segment before have been read
@@ -751,6 +957,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     mine = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
                     other = o.x == -INFINITY ? 0.0f : exp2_approx(o.x - mn);
                     l = l * mine + o.y * other;
+                    mine *= unit;
                     m = mn;
                 }
             }
@@ -791,7 +998,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                             if (warp_live)
 #pragma unroll
                                 for (int c = 0; c < 32; ++c)
-                                    join[((i & 1) * 32 + c) * kTile + row] = o[c];
+                                    join[((i & 1) * 32 + c) * kTile + row] =
+                                        I8 ? o[c] * unit : o[c];
                             continue;
                         }
                         if (warp_live)
@@ -801,7 +1009,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 o[c] = (mine != 0.0f ? o[c] * mine : 0.0f) +
                                        (other != 0.0f ? u * other : 0.0f);
                             }
-                    } else if (whole) {
+                    } else if (whole || I8) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) o[c] *= mine;
                     }
@@ -905,13 +1113,17 @@ EncodeTiled encoder() {
     return reinterpret_cast<EncodeTiled>(p);
 }
 
-bool make_map(CUtensorMap *m, bool bf16, const void *base, int rank, const cuuint64_t *dims,
+bool make_map(CUtensorMap *m, int kv_dtype, const void *base, int rank, const cuuint64_t *dims,
               const cuuint64_t *strides, const cuuint32_t *box) {
     const EncodeTiled enc = encoder();
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    return enc && enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-                      rank, const_cast<void *>(base), dims, strides, box, ones,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const CUtensorMapDataType type = kv_dtype == KVD_INT8   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : kv_dtype == KVD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return enc && enc(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE,
+                      kv_dtype == KVD_INT8 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                           : CU_TENSOR_MAP_SWIZZLE_128B,
                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -935,7 +1147,7 @@ WsPlan ws_plan(int G, int D, int max_new) {
     return w;
 }
 
-template <bool BF16, int D, bool PAIR>
+template <bool BF16, int D, bool PAIR, bool I8>
 cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
     const kvd_paged_cache &c = p.c;
     Dev a = {};
@@ -971,37 +1183,39 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
     const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), 1,
                               static_cast<cuuint32_t>(a.q_tokens)};
     const cuuint64_t kd[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t ks[1] = {static_cast<cuuint64_t>(D) * 2};
-    const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(a.box)};
-    if (!make_map(&q_map, BF16, p.q, 4, qd, qs, qb) || !make_map(&k_map, BF16, c.k, 2, kd, ks, kb) ||
-        !make_map(&v_map, BF16, c.v, 2, kd, ks, kb))
+    const cuuint64_t ks[1] = {static_cast<cuuint64_t>(D) * (I8 ? 1 : 2)};
+    const cuuint32_t kb[2] = {I8 ? D : 64, static_cast<cuuint32_t>(a.box)};
+    if (!make_map(&q_map, BF16 ? KVD_BF16 : KVD_F16, p.q, 4, qd, qs, qb) ||
+        !make_map(&k_map, c.dtype, c.k, 2, kd, ks, kb) ||
+        !make_map(&v_map, c.dtype, c.v, 2, kd, ks, kb))
         return cudaErrorInvalidValue;
 
-    constexpr size_t smem = Shape<D, PAIR>::kSmem;
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(attn_kernel<BF16, D, PAIR>),
-                                   kThreads, smem);
+    constexpr size_t smem = Shape<D, PAIR, I8>::kSmem;
+    auto *kernel = attn_kernel<BF16, D, PAIR, I8>;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads_of(I8), smem);
     if (e != cudaSuccess) return e;
-    e = launch_ex(attn_kernel<BF16, D, PAIR>, dim3(w.ctas), dim3(kThreads), smem, st, true, a, q_map,
-                  k_map, v_map);
+    e = launch_ex(kernel, dim3(w.ctas), dim3(threads_of(I8)), smem, st, true, a, q_map, k_map,
+                  v_map);
     if (e != cudaSuccess) return e;
     return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, PAIR ? 4 : 1), dim3(256), 0, st, true, a);
 }
 
-template <bool BF16>
+template <bool BF16, bool I8>
 cudaError_t launch_type(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
     const WsPlan w = ws_plan(p.G, p.c.head_dim, p.max_new);
     if (p.c.head_dim == 64)
-        return w.pair ? launch_shape<BF16, 64, true>(p, w, ws, st)
-                      : launch_shape<BF16, 64, false>(p, w, ws, st);
-    return w.pair ? launch_shape<BF16, 128, true>(p, w, ws, st)
-                  : launch_shape<BF16, 128, false>(p, w, ws, st);
+        return w.pair ? launch_shape<BF16, 64, true, I8>(p, w, ws, st)
+                      : launch_shape<BF16, 64, false, I8>(p, w, ws, st);
+    return w.pair ? launch_shape<BF16, 128, true, I8>(p, w, ws, st)
+                  : launch_shape<BF16, 128, false, I8>(p, w, ws, st);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st) {
-    if (a.c.dtype == KVD_INT8) return launch_paged_attn_simple(a, st);
-    return a.bf16 ? launch_type<true>(a, ws, st) : launch_type<false>(a, ws, st);
+    if (a.c.dtype == KVD_INT8)
+        return a.bf16 ? launch_type<true, true>(a, ws, st) : launch_type<false, true>(a, ws, st);
+    return a.bf16 ? launch_type<true, false>(a, ws, st) : launch_type<false, false>(a, ws, st);
 }
 
 size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new) {
