@@ -40,14 +40,31 @@ namespace kvd {
 namespace {
 
 constexpr int kTile = 128;       // keys a tile, rows a tile
-constexpr int kProducer = 8, kIssuer = 9;  // warps; 10 and 11 idle
-constexpr int kConverter = 12;             // to 15: int8 caches only
+constexpr int kProducer = 8, kIssuer = 9;  // warps
+// How a call's rows lie on the tiles (see above).  kFew: kOne with at most 32
+// rows over an int8 cache: the warps whose rows are none turn codes instead.
+enum Mode { kPair, kOne, kFew };
 // Registers a thread: 168 at launch (64,512 for 384 threads), or 128 (65,536 for
 // 512), moved to the softmax warps, which hold a row's 128 logits:
 // 256 * 208 + 128 * 88 = 64,512, or 256 * 184 + 256 * 72 = 65,536.
-constexpr int threads_of(bool i8) { return i8 ? 512 : 384; }
+constexpr int threads_of(bool i8, Mode mode) { return i8 && mode != kFew ? 512 : 384; }
 constexpr int softmax_regs(bool i8) { return i8 ? 184 : 208; }
 constexpr int other_regs(bool i8) { return i8 ? 72 : 88; }
+// Warps that turn int8 codes: two teams, one for the key tiles and one for the
+// value tiles.  The team of a warp (0 keys, 1 values, -1 none) and its place there.
+constexpr int team_warps(Mode mode) { return mode == kFew ? 4 : 2; }
+__device__ __forceinline__ int team_of(Mode mode, int warp, int &place) {
+    if (mode == kFew) {  // 1, 2, 3 and 10; 5, 6, 7 and 11
+        if (warp == 10 || warp == 11) {
+            place = 3;
+            return warp - 10;
+        }
+        place = (warp & 3) - 1;
+        return warp < 8 && place >= 0 ? warp >> 2 : -1;
+    }
+    place = warp & 1;
+    return warp >= 12 ? (warp - 12) >> 1 : -1;
+}
 // A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
 // weights add up to more than kRaise raises m for the next one, and one above
 // kRedo is computed again (f16 holds weights up to 65,504).
@@ -202,8 +219,9 @@ __device__ __forceinline__ void codes_to(uint32_t w, uint32_t &lo, uint32_t &hi)
 }
 
 // ------------------------------------------------------------ the kernel ---
-template <int D, bool PAIR, bool I8>
+template <int D, Mode MODE, bool I8>
 struct Shape {
+    static constexpr bool PAIR = MODE == kPair;
     static constexpr int kTileBytes = kTile * D * 2;
     static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
     static constexpr int kJoinBytes = PAIR ? 0 : kTile * 64 * 4;  // 64 channels of a stream's O
@@ -226,12 +244,14 @@ struct Bars {
         join_full, join_empty, raw_full[6], raw_empty[6];
 };
 
-template <bool BF16, int D, bool PAIR, bool I8>
-__global__ void __launch_bounds__(threads_of(I8), 1)
+template <bool BF16, int D, Mode MODE, bool I8>
+__global__ void __launch_bounds__(threads_of(I8, MODE), 1)
 attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q_map,
             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    using Sh = Shape<D, PAIR, I8>;
-    constexpr int kThreads = threads_of(I8);
+    using Sh = Shape<D, MODE, I8>;
+    constexpr bool PAIR = MODE == kPair, FEW = MODE == kFew;
+    constexpr int kThreads = threads_of(I8, MODE);
+    constexpr int kRowWarps = FEW ? 1 : 4;  // softmax warps of a stream
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
     constexpr int kStages = Sh::kStages;
@@ -265,21 +285,21 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.p_full[i], kRowWarps);
             mbar_init(&bar.o_full[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.kv_full[i], I8 ? 4 : 1);
+            mbar_init(&bar.kv_full[i], I8 ? team_warps(MODE) : 1);
             mbar_init(&bar.kv_empty[i], 1);
         }
         for (int i = 0; i < Sh::kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 4);
+            mbar_init(&bar.raw_empty[i], team_warps(MODE));
         }
         mbar_init(&bar.q_empty, 1);
         mbar_init(&bar.done, 1);
-        mbar_init(&bar.join_full, 4);
-        mbar_init(&bar.join_empty, 4);
+        mbar_init(&bar.join_full, kRowWarps);
+        mbar_init(&bar.join_empty, kRowWarps);
         fence_barrier_init();
         abort_flag = 0;
         start.left = 0;
@@ -410,8 +430,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         }
     };
 
-    if (warp >= kProducer) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
+    if (FEW ? warp != 0 && warp != 4 : warp >= kProducer) {
+        if constexpr (!FEW)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
         if (warp == kProducer) {
         // ------------------------------------------------------- loads ---
         const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
@@ -681,7 +702,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 if (!ok) break;
                 // both tiles are used up
-                if (elect_one()) mma_commit(&bar.kv_empty[v_st]);
+                if (elect_one()) {
+                    mma_commit(&bar.kv_empty[v_st]);
+                    if (I8 && ahead < j1) mma_commit(&bar.kv_empty[st]);
+                }
                 __syncwarp();
                 if (ahead < j1) {
                     next_place();
@@ -701,103 +725,118 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         volatile int none = 0;
         if (!wait_for(&bar.done, 0, &none)) fail();
         }
-        if constexpr (I8) {
-            if (warp >= kConverter) {
-                // ----------------------------------------- int8 to f16 or bf16 ---
-                // Codes are whole numbers up to 127, exact in either type; the
-                // scales go to the softmax, so the products lose nothing.
-                const int ct = tid - kConverter * 32;
-                uint32_t it = 0, out = 0, keys = 0, own = 0, phase = 0;
-                int exp_now = 0;
-                bool ok = true;
-                // One tile.  16 codes a step: 8 lanes read a row, and write its
-                // chunks so that the 8 lanes of a store hit different banks.
-                auto convert = [&](bool is_k, bool frees, int j, bool first) -> bool {
-                    const uint32_t st = out;
-                    if (own >> st & 1) {
-                        if (!wait_for(&bar.kv_empty[st], phase >> st & 1, abort)) return false;
-                        phase ^= 1u << st;
-                    }
-                    own = (own & ~(1u << st)) | (frees ? 1u << st : 0u);
-                    const uint32_t rs = it % Sh::kRaw;
-                    if (!wait_for(&bar.raw_full[rs], (it / Sh::kRaw) & 1, abort)) return false;
-                    const uint8_t *src = raw + rs * Sh::kRawBytes;
-                    uint8_t *dst = ring + st * Sh::kTileBytes;
-                    constexpr int kUnits = D / 16;  // 16-code steps a row
-                    if (is_k) {
-                        const float *sc = reinterpret_cast<const float *>(src + kTile * D);
-                        const int tok = j * kTile + ct;
-                        const bool dead = tok < g.it.lo || tok >= g.it.hi ||
-                                          (dead_groups[keys & 7] >> (ct / 16) & 1);
-                        const float ks = dead ? 0.0f : sc[ct];
-                        const float vs = dead ? 0.0f : sc[kTile + ct];
-                        // the exponent of the tile's largest value scale: each warp
-                        // looks at all 128 (NaN counts for nothing)
-                        float top = 0.0f;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = i * 32 + lane, tk = j * kTile + at;
-                            const bool d = tk < g.it.lo || tk >= g.it.hi ||
-                                           (dead_groups[keys & 7] >> (at / 16) & 1);
-                            top = fmaxf(top, d ? 0.0f : sc[kTile + at]);
-                        }
-#pragma unroll
-                        for (int o = 16; o > 0; o >>= 1)
-                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                        const int e =
-                            min(max((__float_as_int(top) >> 23 & 255) - 126, -100), 100);
-                        // kept while the scales stay below 4: weights up to kRedo fit f16
-                        if (first || e > exp_now + 2) exp_now = e;
-                        float *to = scales + keys % Sh::kScales * (2 * kTile);
-                        to[ct] = ks * a.scale_log2;
-                        to[kTile + ct] = vs * __int_as_float((127 - exp_now) << 23);
-                        if (ct == 0) value_exp[keys % Sh::kScales] = exp_now;
-                        ++keys;
-                    }
-#pragma unroll 2
-                    for (int i = 0; i < kUnits; ++i) {
-                        const int unit = ct + i * 128;
-                        const int row = unit / kUnits, u = unit % kUnits;
-                        const uint4 w = *reinterpret_cast<const uint4 *>(src + row * D + 16 * u);
-                        const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) codes_to<BF16>(in[c], o[2 * c], o[2 * c + 1]);
-                        uint8_t *line = dst + (u / 4) * kHalfBytes + row * 128;
-                        const int odd = kUnits == 8 ? u / 4 : 0;
-                        const int c0 = ((u % 4) * 2 + odd) ^ (row & 7);
-                        const int c1 = ((u % 4) * 2 + 1 - odd) ^ (row & 7);
-                        *reinterpret_cast<uint4 *>(line + 16 * c0) =
-                            odd ? make_uint4(o[4], o[5], o[6], o[7])
-                                : make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(line + 16 * c1) =
-                            odd ? make_uint4(o[0], o[1], o[2], o[3])
-                                : make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(&bar.kv_full[st]);
-                        mbar_arrive(&bar.raw_empty[rs]);
-                    }
-                    ++it;
-                    out = st + 1 == kStages ? 0 : st + 1;
-                    return true;
+        int place = 0;
+        const int team = I8 ? team_of(MODE, warp, place) : -1;
+        if (I8 && team >= 0) {
+            // --------------------------------------------- int8 to f16 or bf16 ---
+            // Codes are whole numbers up to 127, exact in either type; the scales
+            // go to the softmax, so the products lose nothing.
+            constexpr int kTeam = 32 * team_warps(MODE);
+            constexpr int kRaw = I8 ? Sh::kRaw : 1;
+            constexpr int kUnits = D / 16;                  // 16-code steps a row
+            constexpr int kWarpRows = 32 / kUnits;          // rows a warp's step takes
+            constexpr int kSteps = kTile / (kWarpRows * team_warps(MODE));
+            // This lane's row and 16 codes of a step.  The 8 lanes of a load or a
+            // store lie on two rows: at D = 128 on the one's first half and the
+            // other's second, so that the codes come from all banks; and as the
+            // swizzle turns even chunks of an odd row into odd ones, the chunks go
+            // to all banks too.
+            const int q8 = lane >> 3, k8 = lane & 7;
+            const int my_row = place * kWarpRows +
+                               (D == 128 ? 2 * (q8 >> 1) + (k8 >> 2) : lane >> 2);
+            const int my_u = D == 128 ? (k8 & 3) + 4 * ((q8 & 1) ^ (k8 >> 2)) : lane & 3;
+            const int src_at = my_row * D + 16 * my_u;
+            const int dst_row = (my_u / 4) * kHalfBytes + my_row * 128;
+            const int dst0 = dst_row + 16 * (((my_u % 4) * 2) ^ (my_row & 7));
+            const int dst1 = dst_row + 16 * (((my_u % 4) * 2 + 1) ^ (my_row & 7));
+            constexpr int kStepRows = kWarpRows * team_warps(MODE);  // a multiple of 8
+            static_assert(kStepRows % 8 == 0, "the swizzle of a lane's row stays");
+            const int ct = place * 32 + lane;
+            uint32_t n = 0, keys = 0;  // tiles and key tiles so far, the other team's too
+            int exp_now = 0;
+            bool ok = true;
+            // The scales of key tile j for the softmax.
+            auto turn_scales = [&](const float *sc, int j, bool first) {
+                const uint32_t bad = dead_groups[keys & 7];
+                const bool edge = j * kTile < g.it.lo || (j + 1) * kTile > g.it.hi || bad;
+                auto dead = [&](int at) {
+                    const int tok = j * kTile + at;
+                    return edge && (tok < g.it.lo || tok >= g.it.hi || (bad >> (at / 16) & 1));
                 };
-                while (ok && next_segment(a, width, w, g)) {
-                    int j0, j1;
-                    span_of(g, j0, j1);
-                    for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i)
-                        ok = convert(true, true, j0 + i, i == 0);
-                    for (int j = j0; ok && j < j1; ++j)
-                        ok = convert(false, true, j, false) &&
-                             (j + kAhead >= j1 || convert(true, false, j + kAhead, false));
+                // the exponent of the tile's largest value scale (infinities and NaN
+                // count for nothing); each warp looks at all 128
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int at = i * 32 + lane;
+                    const uint32_t v = __float_as_uint(sc[kTile + at]);
+                    if (!dead(at) && v < 0x7f800000u) top = max(top, v);
                 }
-                if (!ok) fail();
+                top = __reduce_max_sync(0xffffffffu, top);
+                const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 100);
+                // kept while the scales stay below 4: weights up to kRedo fit f16
+                if (first || e > exp_now + 2) exp_now = e;
+                const float unit = __int_as_float((127 - exp_now) << 23);
+                float *to = scales + keys % Sh::kScales * (2 * kTile);
+#pragma unroll
+                for (int at = ct; at < kTile; at += kTeam) {
+                    const bool d = dead(at);
+                    to[at] = d ? 0.0f : sc[at] * a.scale_log2;
+                    to[kTile + at] = d ? 0.0f : sc[kTile + at] * unit;
+                }
+                if (ct == 0) value_exp[keys % Sh::kScales] = exp_now;
+            };
+            // Tile n.
+            auto turn = [&](bool is_k, int j, bool first) -> bool {
+                const uint32_t rs = n % kRaw, st = n % kStages;
+                if (!wait_for(&bar.raw_full[rs], (n / kRaw) & 1, abort)) return false;
+                const uint8_t *src = raw + rs * Sh::kRawBytes;
+                uint8_t *dst = ring + st * Sh::kTileBytes;
+                if (n >= kStages && !wait_for(&bar.kv_empty[st], (n / kStages - 1) & 1, abort))
+                    return false;
+                if (is_k) turn_scales(reinterpret_cast<const float *>(src + kTile * D), j, first);
+                // rolled: the roles' hot lines have to stay in the instruction cache
+                // together (fully unrolled, a tile takes 1.4 times as long)
+#pragma unroll 2
+                for (int i = 0; i < kSteps; ++i) {
+                    const uint4 w =
+                        *reinterpret_cast<const uint4 *>(src + src_at + i * (kStepRows * D));
+                    uint4 lo, hi;
+                    codes_to<BF16>(w.x, lo.x, lo.y);
+                    codes_to<BF16>(w.y, lo.z, lo.w);
+                    codes_to<BF16>(w.z, hi.x, hi.y);
+                    codes_to<BF16>(w.w, hi.z, hi.w);
+                    *reinterpret_cast<uint4 *>(dst + dst0 + i * (kStepRows * 128)) = lo;
+                    *reinterpret_cast<uint4 *>(dst + dst1 + i * (kStepRows * 128)) = hi;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.kv_full[st]);
+                    mbar_arrive(&bar.raw_empty[rs]);
+                }
+                return true;
+            };
+            auto tile = [&](bool is_k, int j, bool first) -> bool {
+                const bool r = is_k != (team == 0) || turn(is_k, j, first);
+                ++n;
+                keys += is_k;
+                return r;
+            };
+            while (ok && next_segment(a, width, w, g)) {
+                int j0, j1;
+                span_of(g, j0, j1);
+                for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i)
+                    ok = tile(true, j0 + i, i == 0);
+                for (int j = j0; ok && j < j1; ++j)
+                    ok = tile(false, j, false) &&
+                         (j + kAhead >= j1 || tile(true, j + kAhead, false));
             }
+            if (!ok) fail();
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(softmax_regs(I8)));
+        if constexpr (!FEW)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(softmax_regs(I8)));
         // ------------------------------------------------------ softmax ---
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((warp & 3) << 21);  // this warp's 32 lanes
@@ -900,18 +939,34 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         for (int i = 0; i < 4; ++i) {
                             uint32_t p[16];
 #pragma unroll
-                            for (int c = 0; c < 16; ++c) {
-                                const int at = 32 * i + 2 * c;
-                                float2 x = __ffma2_rn(
-                                    make_float2(s[at], s[at + 1]),
-                                    I8 ? *reinterpret_cast<const float2 *>(k_sc + at) : sc, off);
-                                x.x = exp2_approx(x.x);
-                                x.y = exp2_approx(x.y);
-                                sum[c & 1] = __fadd2_rn(sum[c & 1], x);
-                                if (I8)
-                                    x = __fmul2_rn(x, *reinterpret_cast<const float2 *>(
-                                                          tile_sc + kTile + at));
-                                p[c] = pack2<BF16>(x.x, x.y);
+                            for (int h = 0; h < 2; ++h) {
+                                float4 kc[4], vc[4];  // int8: the scales of 16 keys
+                                if constexpr (I8) {
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) {
+                                        const int at = 32 * i + 16 * h + 4 * c;
+                                        kc[c] = *reinterpret_cast<const float4 *>(k_sc + at);
+                                        vc[c] = *reinterpret_cast<const float4 *>(tile_sc + kTile + at);
+                                    }
+                                }
+#pragma unroll
+                                for (int c = 0; c < 8; ++c) {
+                                    const int at = 32 * i + 16 * h + 2 * c;
+                                    const float4 k4 = kc[c / 2], v4 = vc[c / 2];
+                                    float2 x = __ffma2_rn(
+                                        make_float2(s[at], s[at + 1]),
+                                        !I8          ? sc
+                                        : c % 2 == 0 ? make_float2(k4.x, k4.y)
+                                                     : make_float2(k4.z, k4.w),
+                                        off);
+                                    x.x = exp2_approx(x.x);
+                                    x.y = exp2_approx(x.y);
+                                    sum[c & 1] = __fadd2_rn(sum[c & 1], x);
+                                    if (I8)
+                                        x = __fmul2_rn(x, c % 2 == 0 ? make_float2(v4.x, v4.y)
+                                                                     : make_float2(v4.z, v4.w));
+                                    p[8 * h + c] = pack2<BF16>(x.x, x.y);
+                                }
                             }
                             tmem_st16(s_addr + 16 * i, p);
                         }
@@ -1147,7 +1202,7 @@ WsPlan ws_plan(int G, int D, int max_new) {
     return w;
 }
 
-template <bool BF16, int D, bool PAIR, bool I8>
+template <bool BF16, int D, Mode MODE, bool I8>
 cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
     const kvd_paged_cache &c = p.c;
     Dev a = {};
@@ -1190,24 +1245,30 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
         !make_map(&v_map, c.dtype, c.v, 2, kd, ks, kb))
         return cudaErrorInvalidValue;
 
-    constexpr size_t smem = Shape<D, PAIR, I8>::kSmem;
-    auto *kernel = attn_kernel<BF16, D, PAIR, I8>;
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads_of(I8), smem);
+    constexpr size_t smem = Shape<D, MODE, I8>::kSmem;
+    constexpr int threads = threads_of(I8, MODE);
+    auto *kernel = attn_kernel<BF16, D, MODE, I8>;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads, smem);
     if (e != cudaSuccess) return e;
-    e = launch_ex(kernel, dim3(w.ctas), dim3(threads_of(I8)), smem, st, true, a, q_map, k_map,
+    e = launch_ex(kernel, dim3(w.ctas), dim3(threads), smem, st, true, a, q_map, k_map,
                   v_map);
     if (e != cudaSuccess) return e;
-    return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, PAIR ? 4 : 1), dim3(256), 0, st, true, a);
+    return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, MODE == kPair ? 4 : 1), dim3(256), 0, st, true, a);
+}
+
+template <bool BF16, int D, bool I8>
+cudaError_t launch_mode(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
+    if (w.pair) return launch_shape<BF16, D, kPair, I8>(p, w, ws, st);
+    if constexpr (I8)
+        if (w.rows <= 32) return launch_shape<BF16, D, kFew, I8>(p, w, ws, st);
+    return launch_shape<BF16, D, kOne, I8>(p, w, ws, st);
 }
 
 template <bool BF16, bool I8>
 cudaError_t launch_type(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
     const WsPlan w = ws_plan(p.G, p.c.head_dim, p.max_new);
-    if (p.c.head_dim == 64)
-        return w.pair ? launch_shape<BF16, 64, true, I8>(p, w, ws, st)
-                      : launch_shape<BF16, 64, false, I8>(p, w, ws, st);
-    return w.pair ? launch_shape<BF16, 128, true, I8>(p, w, ws, st)
-                  : launch_shape<BF16, 128, false, I8>(p, w, ws, st);
+    return p.c.head_dim == 64 ? launch_mode<BF16, 64, I8>(p, w, ws, st)
+                              : launch_mode<BF16, 128, I8>(p, w, ws, st);
 }
 
 }  // namespace
