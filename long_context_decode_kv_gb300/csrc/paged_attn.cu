@@ -40,7 +40,7 @@ namespace kvd {
 namespace {
 
 constexpr int kTile = 128;       // keys a tile, rows a tile
-constexpr int kProducer = 8, kIssuer = 9;  // warps
+constexpr int kProducer = 8, kIssuer = 9;  // warps; the issuer of stream 1: 10
 // How a call's rows lie on the tiles (see above).  kFew: kOne with at most 32
 // rows over an int8 cache: the warps whose rows are none turn codes instead.
 enum Mode { kPair, kOne, kFew };
@@ -77,7 +77,7 @@ struct Dev {  // a launch's arguments
     int H, G, n_tokens, max_new, window;
     const int32_t *starts;
     float scale_log2;
-    int q_tokens;       // tokens of a row tile: 128 / G
+    int q_tokens;       // tokens of a row tile: 128 / G (kPair), or max_new
     int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
     int dead_row;       // a cache row outside the pool
     int min_tiles;      // least key tiles a CTA takes
@@ -87,20 +87,21 @@ struct Dev {  // a launch's arguments
     int ws_rows;        // rows of a partial: 256 (PAIR) or fewer, a multiple of 32
 };
 
-// mbar_wait in few instructions, for the waits between the roles: most find the
-// phase complete, and the issuing warp, which runs a few lines between the
-// softmax warps' long ones, pays for each line fetched.  Warps call it whole,
-// and all lanes get the same answer.
+// mbar_wait for the waits between the roles, in few instructions: the roles' hot
+// lines have to fit the instruction cache together, and a wait mostly ends in its
+// first try.  Warps call it whole, and all lanes get the same answer.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    uint64_t t0 = 0;
-    for (uint32_t n = 1;; ++n) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((n & 63u) == 0) {
-            const uint64_t t = global_timer_ns();
-            if (t0 == 0) t0 = t;
-            if (__any_sync(0xffffffffu, *abort || t - t0 > kWaitLimitNs)) return false;
+    uint32_t n = 0, t0 = 0;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
+        if ((++n & 63u) == 0) {
+            const uint32_t t = static_cast<uint32_t>(global_timer_ns());
+            if (n == 64) t0 = t;
+            if (__any_sync(0xffffffffu, *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs)))
+                return false;
         }
     }
+    return true;
 }
 
 // ---------------------------------------------------------------- items ---
@@ -223,14 +224,20 @@ template <int D, Mode MODE, bool I8>
 struct Shape {
     static constexpr bool PAIR = MODE == kPair;
     static constexpr int kTileBytes = kTile * D * 2;
-    static constexpr int kQBytes = (PAIR ? 2 : 1) * kTileBytes;
-    static constexpr int kJoinBytes = PAIR ? 0 : kTile * 64 * 4;  // 64 channels of a stream's O
-    static constexpr int kStages = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-    // int8: tiles as loaded (codes, then the rows' key and value scales with a key
-    // tile), and the scales the softmax takes, for more key tiles than the ring
-    // lets the loads run ahead of it
-    static constexpr int kRaw = I8 ? (D == 128 ? 3 : 6) : 0;
-    static constexpr int kRawBytes = kTile * D + 2 * kTile * 4;
+    // Rows kept of a row tile and its join buffer.  kFew: the tensor core still
+    // reads 128 rows, the others from whatever lies behind: rows that are none.
+    static constexpr int kRows = MODE == kFew ? 32 : kTile;
+    static constexpr int kQHalf = kRows * 128;
+    static constexpr int kQTile = kQHalf * (D / 64);
+    static constexpr int kQBytes = (PAIR ? 2 : 1) * kQTile;
+    static constexpr int kJoinBytes = PAIR ? 0 : kRows * 64 * 4;  // 64 channels of a stream's O
+    static constexpr int kStages =
+        I8 ? (D == 128 ? (MODE == kFew ? 4 : 3) : 6) : (D == 128 ? 5 : 8);
+    // int8: tiles as loaded (codes, then the rows' key and value scales with keys),
+    // and the scales the softmax takes, for more key tiles than the ring lets the
+    // loads run ahead of it
+    static constexpr int kRaw = !I8 ? 0 : D == 128 ? (MODE == kFew ? 4 : 3) : 6;
+    static constexpr int kRawBytes = kTile * (D + 8);
     static constexpr int kScales = D == 128 ? 4 : 8;
     static constexpr int kScaleBytes = I8 ? kScales * 2 * kTile * 4 : 0;
     static constexpr int kAhead = PAIR ? 1 : 2;  // key tiles whose S is issued ahead of PV
@@ -240,8 +247,8 @@ struct Shape {
 };
 
 struct Bars {
-    uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], done,
-        join_full, join_empty, raw_full[6], raw_empty[6];
+    uint64_t q_full[2], q_empty, kv_full[8], kv_empty[8], s_full[2], p_full[2], o_full[2], turn[2], done,
+        join_full, join_empty, raw_full[8], raw_empty[8];
 };
 
 template <bool BF16, int D, Mode MODE, bool I8>
@@ -287,17 +294,18 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], kRowWarps);
             mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.turn[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&bar.kv_full[i], I8 ? team_warps(MODE) : 1);
-            mbar_init(&bar.kv_empty[i], 1);
+            mbar_init(&bar.kv_empty[i], PAIR ? 2 : 1);  // the streams that use a tile
         }
         for (int i = 0; i < Sh::kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], team_warps(MODE));
         }
-        mbar_init(&bar.q_empty, 1);
-        mbar_init(&bar.done, 1);
+        mbar_init(&bar.q_empty, PAIR ? 2 : 1);  // the warps that issue products
+        mbar_init(&bar.done, PAIR ? 2 : 1);
         mbar_init(&bar.join_full, kRowWarps);
         mbar_init(&bar.join_empty, kRowWarps);
         fence_barrier_init();
@@ -313,6 +321,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         if (b >= a.c.batch) return 0;
         const Seq s = seq_of(a, b, report);
         long n = 0;
+#pragma unroll 1
         for (int t = 0; t * width < s.n; ++t) n += item_of(a, s, t, width).tiles;
         return n * a.c.n_kv_heads;
     };
@@ -338,16 +347,20 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     long cost = cost_of(tid, blockIdx.x == 0);
     long total = scan(cost, before);
     const bool one_pass = a.c.batch <= kThreads;
+#pragma unroll 1
     for (int b0 = kThreads; b0 < a.c.batch; b0 += kThreads) {
         long skip;
         total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
     }
     const long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long>(a.min_tiles));
-    const long ctas = min(static_cast<long>(gridDim.x), (total + per - 1) / per);
-    const long x0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-    const long x1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    const long ctas = max(min(static_cast<long>(gridDim.x), (total + per - 1) / per), 1l);
+    const long share = total / ctas, spare = total % ctas;
+    auto cut = [&](long c) { return c * share + min(c, spare); };  // where CTA c begins
+    const long x0 = blockIdx.x < ctas ? cut(blockIdx.x) : total;
+    const long x1 = blockIdx.x < ctas ? cut(blockIdx.x + 1) : total;
     if (x0 < x1) {
         long base = 0;
+#pragma unroll 1
         for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
             if (!one_pass) {
                 cost = cost_of(b0 + tid, false);
@@ -364,6 +377,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 w.head = static_cast<int>(r / per_head);
                 r -= w.head * per_head;
                 w.tile = 0;
+#pragma unroll 1
                 for (;;) {
                     const int n = item_of(a, w.s, w.tile, width).tiles;
                     if (r < n) break;
@@ -437,8 +451,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         // ------------------------------------------------------- loads ---
         const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
         const int boxes = kTile / a.box;
+        const int ahead_tiles = 32 / boxes;  // whose rows one read of the page table gives
         const int ps = a.c.page_size;
-        uint32_t it = 0, keys = 0;  // ring places filled, key tiles loaded
+        uint32_t st = 0, keys = 0;  // the next place (int8: of the raw ring), key tiles loaded
+        uint32_t it = 0;            // int8: tiles loaded
         // Bits of the ring's places: whether what lies there is freed by its own
         // arrival (a key tile behind a value tile is freed by that one's), and
         // the parity of the next arrival.
@@ -447,6 +463,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         uint32_t q_phase = 0;
         bool ok = true;
         int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
+#pragma unroll 1
         while (ok && next_segment(a, width, w, g)) {
             int j0, j1;
             span_of(g, j0, j1);
@@ -457,64 +474,36 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             }
             if (lane == 0 && j1 > j0) {
                 const int rows = a.q_tokens * a.G;
+#pragma unroll 1
                 for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
                     const Part p = part_of(g, t);
                     if (p.j0 == p.j1) continue;
                     mbar_arrive_expect_tx(&bar.q_full[t], rows * 128 * kHalves);
+#pragma unroll 1
                     for (int h = 0; h < kHalves; ++h)
-                        tma_load_4d(q_smem + t * Sh::kTileBytes + h * kHalfBytes, &q_map, h * 64, 0,
+                        tma_load_4d(q_smem + t * Sh::kQTile + h * Sh::kQHalf, &q_map, h * 64, 0,
                                     g.head, g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0),
                                     &bar.q_full[t]);
                 }
             }
-            // the cache row of this lane's box of tile j (dead_row: not needed, or a bad page)
-            auto row_of = [&](int j, bool &is_bad) -> int {
-                is_bad = false;
-                const int t0 = j * kTile + lane * a.box;
-                if (lane >= boxes || j >= j1 || t0 >= g.it.hi || t0 + a.box <= g.it.lo)
+            // The cache rows of the boxes of tiles j, j + 1, .., a lane a box: dead_row
+            // where none is needed, -1 on a bad page.
+            auto rows_of = [&](int j) -> int {
+                const int t0 = (j + lane / boxes) * kTile + lane % boxes * a.box;
+                if (t0 >= j1 * kTile || t0 >= g.it.hi || t0 + a.box <= g.it.lo)
                     return a.dead_row;
                 const int col = t0 / ps;
                 const int page = checked_page(a.c, g.b, col);
-                is_bad = page < 0;
-                return is_bad ? a.dead_row
-                              : (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
-            };
-            // The next place of the ring, free: a value tile, and the key tile
-            // that follows it in the same iteration of the products, complete on
-            // the value tile's barrier; the first key tiles on their own.
-            auto place = [&](bool frees) -> bool {
-                const uint32_t st = it % kStages;
-                if (own >> st & 1) {
-                    if (!wait_for(&bar.kv_empty[st], phase >> st & 1, abort)) return false;
-                    phase ^= 1u << st;
-                }
-                own = (own & ~(1u << st)) | (frees ? 1u << st : 0u);
-                return true;
-            };
-            auto expect = [&](uint64_t *full, int tiles) {
-                filled |= 1u << (it % kStages);
-                fills ^= 1u << (it % kStages);
-                if (lane == 0) mbar_arrive_expect_tx(full, tiles * Sh::kTileBytes);
-                __syncwarp();
-            };
-            auto load = [&](int row, const CUtensorMap *map, uint64_t *full) {
-                if (lane < boxes) {
-#pragma unroll
-                    for (int h = 0; h < kHalves; ++h)
-                        tma_load_2d(ring + (it % kStages) * Sh::kTileBytes + h * kHalfBytes +
-                                        lane * a.box * 128,
-                                    map, h * 64, row, full, policy);
-                }
-                ++it;
+                return page < 0 ? -1 : (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
             };
             // int8: the tile's codes as they lie, and with keys both rows' scales
             auto load_raw = [&](int row, const CUtensorMap *map, bool keys_too) -> bool {
-                constexpr int kRaw = I8 ? Sh::kRaw : 1;
-                const uint32_t st = it % kRaw;
-                if (it >= kRaw && !wait_for(&bar.raw_empty[st], (it / kRaw - 1) & 1, abort))
-                    return false;
-                const bool live = lane < boxes && row != a.dead_row;
-                const int n = keys_too ? __popc(__ballot_sync(0xffffffffu, live)) : 0;
+                if (it >= Sh::kRaw) {
+                    if (!wait_for(&bar.raw_empty[st], phase >> st & 1, abort)) return false;
+                    phase ^= 1u << st;
+                }
+                const bool live = keys_too && lane < boxes && row != a.dead_row;
+                const int n = __popc(__ballot_sync(0xffffffffu, live));
                 filled |= 1u << st;
                 fills ^= 1u << st;
                 if (lane == 0)
@@ -523,7 +512,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 uint8_t *dst = raw + st * Sh::kRawBytes;
                 if (lane < boxes)
                     tma_load_2d(dst + lane * a.box * D, map, 0, row, &bar.raw_full[st], policy);
-                if (keys_too && live) {
+                if (live) {
                     float *sc = reinterpret_cast<float *>(dst + kTile * D) + lane * a.box;
                     tma_load_1d(sc, static_cast<const float *>(a.c.k_scale) + row, a.box * 4,
                                 &bar.raw_full[st], policy);
@@ -531,58 +520,76 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 a.box * 4, &bar.raw_full[st], policy);
                 }
                 ++it;
+                st = st + 1 == (I8 ? Sh::kRaw : 1) ? 0 : st + 1;
                 return true;
             };
-            auto mark_dead = [&](bool is_bad) {
-                const int n = a.box / 16;
-                const uint32_t bad =
-                    __reduce_or_sync(0xffffffffu, is_bad ? ((1u << n) - 1) << (lane * n) : 0u);
-                if (lane == 0) dead_groups[keys & 7] = bad;
-                ++keys;
-            };
-            // rows of the next tiles, read ahead of their use
-            int row[kAhead + 2];
-            bool is_bad[kAhead + 2];
-#pragma unroll
-            for (int i = 0; i < kAhead + 2; ++i) row[i] = row_of(j0 + i, is_bad[i]);
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)
-                if (ok && j0 + i < j1) {
-                    mark_dead(is_bad[i]);
-                    if constexpr (I8) {
-                        ok = load_raw(row[i], &k_map, true);
-                    } else if ((ok = place(true))) {
-                        uint64_t *full = &bar.kv_full[it % kStages];
-                        expect(full, 1);
-                        load(row[i], &k_map, full);
+            // The tiles in the order of the products: kAhead key tiles, then value
+            // and key tiles in turn.  Rows are read ahead of their use.
+            int kj = j0, vj = j0;
+            int rows_k = 0, rows_v = 0, rows_next = rows_of(j0);
+            uint64_t *full = nullptr;
+#pragma unroll 1
+            while (ok && vj < j1) {
+                const bool is_k = kj < min(j1, vj + kAhead);
+                const bool pre = vj == j0;  // a key tile before any value tile
+                const int in = ((is_k ? kj : vj) - j0) % ahead_tiles;
+                if (in == 0) {
+                    if (is_k) {
+                        rows_k = rows_next;
+                        rows_next = rows_of(kj + ahead_tiles);
+                    } else {
+                        rows_v = rows_k;
                     }
                 }
-            for (int j = j0; ok && j < j1; ++j) {
-                const bool more = j + kAhead < j1;
-                if (more) mark_dead(is_bad[kAhead]);
-                if constexpr (I8) {
-                    ok = load_raw(row[0], &v_map, false) &&
-                         (!more || load_raw(row[kAhead], &k_map, true));
+                int row = __shfl_sync(0xffffffffu, is_k ? rows_k : rows_v,
+                                      in * boxes + lane % boxes);
+                const bool bad = row < 0;
+                if (bad) row = a.dead_row;
+                if (is_k) {
+                    const int n = a.box / 16;
+                    const uint32_t groups = __reduce_or_sync(
+                        0xffffffffu, bad ? ((1u << n) - 1) << (lane % boxes * n) : 0u);
+                    if (lane == 0) dead_groups[keys & 7] = groups;
+                    ++keys;
+                    ++kj;
                 } else {
-                    if (!(ok = place(true))) break;
-                    uint64_t *full = &bar.kv_full[it % kStages];
-                    expect(full, more ? 2 : 1);
-                    load(row[0], &v_map, full);
-                    // the value tile's bytes are due even if the key tile's place never comes
-                    if (more && (ok = place(false))) load(row[kAhead], &k_map, full);
+                    ++vj;
                 }
+                const CUtensorMap *map = is_k ? &k_map : &v_map;
+                if constexpr (I8) {
+                    ok = load_raw(row, map, is_k);
+                } else {
+                    // The next place of the ring, free.  A value tile, and the key
+                    // tile that follows it in the same step of the products, complete
+                    // on the value tile's barrier; the first key tiles on their own.
+                    if (own >> st & 1) {
+                        if (!(ok = wait_for(&bar.kv_empty[st], phase >> st & 1, abort))) break;
+                        phase ^= 1u << st;
+                    }
+                    own = (own & ~(1u << st)) | (!is_k || pre ? 1u << st : 0u);
+                    if (!is_k || pre) {
+                        full = &bar.kv_full[st];
+                        filled |= 1u << st;
+                        fills ^= 1u << st;
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(full,
+                                                  (!is_k && kj < j1 ? 2 : 1) * Sh::kTileBytes);
+                        __syncwarp();
+                    }
+                    if (lane < boxes)
 #pragma unroll
-                for (int i = 0; i < kAhead + 1; ++i) {
-                    row[i] = row[i + 1];
-                    is_bad[i] = is_bad[i + 1];
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_2d(ring + st * Sh::kTileBytes + h * kHalfBytes +
+                                            lane * a.box * 128,
+                                        map, h * 64, row, full, policy);
+                    st = st + 1 == kStages ? 0 : st + 1;
                 }
-                row[kAhead + 1] = row_of(j + kAhead + 2, is_bad[kAhead + 1]);
             }
             if (g.starts && !g.ends) {
                 // the item goes on in the next CTAs: leave word for merge_kernel
                 const long rest = g.it.tiles - (g.j1 - g.it.j0);
                 int pieces = 1;
-                while (total * (blockIdx.x + pieces + 1) / ctas - x1 < rest) ++pieces;
+                while (cut(blockIdx.x + pieces + 1) - x1 < rest) ++pieces;
                 rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
                 rec1 = make_int4(g.head, 0, 0, 0);
             }
@@ -599,131 +606,128 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             for (uint32_t st = 0; st < 8; ++st)
                 if (filled >> st & 1) mbar_wait(&full[st], ~(fills >> st) & 1, &none);
         }
-        } else if (warp == kIssuer) {
-        // ---------------------------------------------------- products ---
-        constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kTile, false);
-        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, D, true);
-        const uint32_t ring_addr = smem_addr(ring);
-        const uint32_t q_desc = warp_uniform(desc_low(smem_addr(q_smem), 16));
-        const uint32_t tmem_u = warp_uniform(tmem);
-        uint32_t st = 0;  // place of the ring
-        uint32_t full_phase = 0, q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
-        bool ok = true;
-        auto wait_tile = [&]() -> bool {  // what this place's barrier announces is there
-            const bool r = wait_for(&bar.kv_full[st], full_phase >> st & 1, abort);
-            full_phase ^= 1u << st;
-            return r;
-        };
-        auto next_place = [&] { st = st + 1 == kStages ? 0 : st + 1; };
-        auto issue_s = [&](int t) {  // the key tile at this place against row tile t
-            const uint32_t k = warp_uniform(desc_low(ring_addr + st * Sh::kTileBytes, 16));
-            const uint32_t q = q_desc + (PAIR ? t * (Sh::kTileBytes / 16) : 0);
-            if (elect_one()) {
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t at = ((i / 4) * kHalfBytes + (i % 4) * 32) / 16;
-                    mma_ss(tmem_u + t * 128, smem_desc(q + at), smem_desc(k + at), kIdS, i > 0);
-                }
-                mma_commit(&bar.s_full[t]);
-            }
-            __syncwarp();
-        };
-        while (ok && next_segment(a, width, w, g)) {
-            int j0, j1;
-            span_of(g, j0, j1);
-            Part part[2] = {part_of(g, 0), part_of(g, 1)};
-#pragma unroll
-            for (int t = 0; t < (PAIR ? 2 : 1); ++t)
-                if (ok && part[t].j0 < part[t].j1) {
-                    ok = wait_for(&bar.q_full[t], q_phase[t], abort);
-                    q_phase[t] ^= 1;
-                }
-            // stream t takes key tile j
-            auto takes = [&](int t, int j) {
-                return PAIR ? (j >= part[t].j0 && j < part[t].j1) : ((j - j0) & 1) == t && j < j1;
+        } else if (warp == kIssuer || (PAIR && warp == kIssuer + 1)) {
+            // ------------------------------------------------ products ---
+            // An issued product waits until the tensor pipe has room, so a warp that
+            // issues both streams' leaves the pipe idle through its own waits.  In
+            // kPair, where the products are the bound, each stream has its warp, one
+            // waiting behind the other's products; they take turns, which keeps one
+            // stream's softmax beside the other's products.  Otherwise one warp
+            // serves the streams' key tiles in turn.
+            constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kTile, false);
+            constexpr uint32_t kIdO = mma_idesc(BF16, kTile, D, true);
+            const int who = warp - kIssuer;  // kPair: the stream
+            const uint32_t ring_addr = smem_addr(ring);
+            const uint32_t q =
+                warp_uniform(desc_low(smem_addr(q_smem + (PAIR ? who * Sh::kQTile : 0)), 16));
+            uint32_t st = 0;          // place of the ring
+            uint32_t full_phase = 0;  // bits of its places
+            uint32_t q_phase = 0, p_phase = 0 /* bits: streams */, turn_phase = who ^ 1;
+            bool ok = true;
+            auto wait_tile = [&]() -> bool {  // what this place's barrier announces is there
+                const bool r = wait_for(&bar.kv_full[st], full_phase >> st & 1, abort);
+                full_phase ^= 1u << st;
+                return r;
             };
-            // the segment's last S is issued: its queries can be replaced
-            auto release_q = [&]() {
-                if (elect_one()) mma_commit(&bar.q_empty);
-                __syncwarp();
-            };
-            for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i) {
-                if (!(ok = wait_tile())) break;
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (takes(t, j0 + i)) issue_s(t);
-                if (elect_one()) mma_commit(&bar.kv_empty[st]);
-                __syncwarp();
-                next_place();
-            }
-            if (j1 - j0 <= kAhead) release_q();
-            for (int j = j0; ok && j < j1; ++j) {
-                // the value tile, and the key tile ahead at the next place
-                if (!(ok = wait_tile())) break;
-                const uint32_t v_st = st;
-                const uint32_t v =
-                    warp_uniform(desc_low(ring_addr + v_st * Sh::kTileBytes, kHalfBytes));
-                // value rows that no token of the item sees may hold NaN: clear them
-                const int from = max(g.it.lo - j * kTile, 0), to = min(g.it.hi - j * kTile, kTile);
-                if (!I8 && (from > 0 || to < kTile)) {
-                    uint8_t *vs = ring + v_st * Sh::kTileBytes;
-                    const int n = (from + (kTile - max(to, 0))) * 8 * kHalves;
-                    for (int i = lane; i < n; i += 32) {
-                        const int c = i % 8, h = (i / 8) % kHalves;
-                        int r = i / (8 * kHalves);
-                        if (r >= from) r += max(to, 0) - from;
-                        *reinterpret_cast<uint4 *>(vs + h * kHalfBytes + r * 128 + c * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async();
+            auto next_place = [&] { st = st + 1 == kStages ? 0 : st + 1; };
+#pragma unroll 1
+            while (ok && next_segment(a, width, w, g)) {
+                int j0, j1;
+                span_of(g, j0, j1);
+                const Part part = part_of(g, who);
+                // the warp's key tiles
+                const int mine = PAIR ? part.j0 : j0, end = part.j1;
+                auto takes = [&](int j) { return j >= mine && j < end; };
+                constexpr int kStep = PAIR ? 1 : 2;  // to a stream's next tile
+                if (mine < end) {
+                    ok = wait_for(&bar.q_full[who], q_phase, abort);
+                    q_phase ^= 1;
+                } else {
+                    if (elect_one()) mma_commit(&bar.q_empty);  // not read at all
                     __syncwarp();
                 }
-                next_place();
-                const int ahead = j + kAhead;
-                if (I8 && ahead < j1 && !(ok = wait_tile())) break;  // a barrier of its own
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (takes(t, j)) {
-                        const uint32_t add =
-                            warp_uniform(PAIR ? j != part[t].j0 : j - j0 >= 2);
-                        if (!(ok = wait_for(&bar.p_full[t], p_phase[t], abort))) break;
-                        p_phase[t] ^= 1;
+                // Step j: O of key tile j, and S of the one kAhead tiles on.
+#pragma unroll 1
+                for (int j = j0 - kAhead; ok && j < j1; ++j) {
+                    const int ahead = j + kAhead;
+                    const bool has_o = j >= j0, has_s = ahead < j1;
+                    if (!has_o && !has_s) continue;
+                    const int t = PAIR ? who : (j - j0) & 1;
+                    const uint32_t s_at = warp_uniform(tmem + t * 128);
+                    const bool do_o = has_o && takes(j), do_s = has_s && takes(ahead);
+                    const uint32_t v_st = st;
+                    const uint32_t v =
+                        warp_uniform(desc_low(ring_addr + st * Sh::kTileBytes, kHalfBytes));
+                    if (has_o) {
+                        // the value tile, and the key tile ahead at the next place
+                        if (!(ok = wait_tile())) break;
+                        // value rows that no token of the item sees may hold NaN: clear them
+                        // (each stream's warp, before its own product)
+                        const int from = max(g.it.lo - j * kTile, 0);
+                        const int to = min(g.it.hi - j * kTile, kTile);
+                        if (!I8 && do_o && (from > 0 || to < kTile)) {
+                            uint8_t *vs = ring + v_st * Sh::kTileBytes;
+                            const int n = (from + (kTile - max(to, 0))) * 8 * kHalves;
+#pragma unroll 1
+                            for (int i = lane; i < n; i += 32) {
+                                const int c = i % 8, h = (i / 8) % kHalves;
+                                int r = i / (8 * kHalves);
+                                if (r >= from) r += max(to, 0) - from;
+                                *reinterpret_cast<uint4 *>(vs + h * kHalfBytes + r * 128 + c * 16) =
+                                    make_uint4(0, 0, 0, 0);
+                            }
+                            fence_proxy_async();
+                            __syncwarp();
+                        }
+                        next_place();
+                    }
+                    const bool own_k = has_s && (I8 || !has_o);  // a barrier and release of its own
+                    if (own_k && !(ok = wait_tile())) break;
+                    const uint32_t k = warp_uniform(desc_low(ring_addr + st * Sh::kTileBytes, 16));
+                    const uint32_t add = warp_uniform(j >= mine + kStep);
+                    if (do_o) {
+                        if (!(ok = wait_for(&bar.p_full[t], p_phase >> t & 1, abort))) break;
+                        p_phase ^= 1u << t;
                         tmem_fence_after();
-                        if (elect_one()) {
+                    }
+                    if (PAIR) {
+                        if (!(ok = wait_for(&bar.turn[t], turn_phase, abort))) break;
+                        turn_phase ^= 1;
+                    }
+                    if (elect_one()) {
+                        if (do_o) {
 #pragma unroll
                             for (int i = 0; i < kTile / 16; ++i)
-                                mma_ts(tmem_u + 256 + t * 128, tmem_u + t * 128 + i * 8,
-                                       smem_desc(v + i * (2048 / 16)), kIdO, i > 0 ? 1 : add);
-                            if (PAIR && j + 1 == part[t].j1) mma_commit(&bar.o_full[t]);
+                                mma_ts(s_at + 256, s_at + i * 8, smem_desc(v + i * (2048 / 16)),
+                                       kIdO, i > 0 ? 1 : add);
+                            if (j + kStep >= end) mma_commit(&bar.o_full[t]);
                         }
-                        __syncwarp();
+                        if (do_s) {
+#pragma unroll
+                            for (int i = 0; i < D / 16; ++i) {
+                                const uint32_t in = (i % 4) * 32;
+                                mma_ss(s_at, smem_desc(q + ((i / 4) * Sh::kQHalf + in) / 16),
+                                       smem_desc(k + ((i / 4) * kHalfBytes + in) / 16), kIdS,
+                                       i > 0);
+                            }
+                            mma_commit(&bar.s_full[t]);
+                        }
+                        if (PAIR) mbar_arrive(&bar.turn[t ^ 1]);
+                        // the tiles are used up, and with the last S the queries
+                        if (has_o) mma_commit(&bar.kv_empty[v_st]);
+                        if (own_k) mma_commit(&bar.kv_empty[st]);
+                        if (do_s && ahead + 1 == end) mma_commit(&bar.q_empty);
                     }
-                    if (ahead < j1 && takes(t, ahead)) issue_s(t);
-                }
-                if (!ok) break;
-                // both tiles are used up
-                if (elect_one()) {
-                    mma_commit(&bar.kv_empty[v_st]);
-                    if (I8 && ahead < j1) mma_commit(&bar.kv_empty[st]);
-                }
-                __syncwarp();
-                if (ahead < j1) {
-                    next_place();
-                    if (ahead + 1 == j1) release_q();
+                    __syncwarp();
+                    if (has_s) next_place();
                 }
             }
-            if (!PAIR && ok && elect_one()) {
-                mma_commit(&bar.o_full[0]);
-                mma_commit(&bar.o_full[1]);
-            }
+            if (!ok) fail();
+            // every product and every barrier arrival is done before the CTA goes
+            if (elect_one()) mma_commit(&bar.done);
             __syncwarp();
-        }
-        if (!ok) fail();
-        // every product and every barrier arrival is done before the CTA goes
-        if (elect_one()) mma_commit(&bar.done);
-        __syncwarp();
-        volatile int none = 0;
-        if (!wait_for(&bar.done, 0, &none)) fail();
+            volatile int none = 0;
+            if (!mbar_wait(&bar.done, 0, &none)) fail();
         }
         int place = 0;
         const int team = I8 ? team_of(MODE, warp, place) : -1;
@@ -732,7 +736,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             // Codes are whole numbers up to 127, exact in either type; the scales
             // go to the softmax, so the products lose nothing.
             constexpr int kTeam = 32 * team_warps(MODE);
-            constexpr int kRaw = I8 ? Sh::kRaw : 1;
+            constexpr uint32_t kRaw = I8 ? Sh::kRaw : 1;
             constexpr int kUnits = D / 16;                  // 16-code steps a row
             constexpr int kWarpRows = 32 / kUnits;          // rows a warp's step takes
             constexpr int kSteps = kTile / (kWarpRows * team_warps(MODE));
@@ -761,16 +765,15 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 const bool edge = j * kTile < g.it.lo || (j + 1) * kTile > g.it.hi || bad;
                 auto dead = [&](int at) {
                     const int tok = j * kTile + at;
-                    return edge && (tok < g.it.lo || tok >= g.it.hi || (bad >> (at / 16) & 1));
+                    return tok < g.it.lo || tok >= g.it.hi || (bad >> (at / 16) & 1);
                 };
                 // the exponent of the tile's largest value scale (infinities and NaN
                 // count for nothing); each warp looks at all 128
                 uint32_t top = 0;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int at = i * 32 + lane;
-                    const uint32_t v = __float_as_uint(sc[kTile + at]);
-                    if (!dead(at) && v < 0x7f800000u) top = max(top, v);
+                    const uint32_t v = __float_as_uint(sc[kTile + i * 32 + lane]);
+                    if (v < 0x7f800000u && !(edge && dead(i * 32 + lane))) top = max(top, v);
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
                 const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 100);
@@ -780,27 +783,28 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 float *to = scales + keys % Sh::kScales * (2 * kTile);
 #pragma unroll
                 for (int at = ct; at < kTile; at += kTeam) {
-                    const bool d = dead(at);
-                    to[at] = d ? 0.0f : sc[at] * a.scale_log2;
-                    to[kTile + at] = d ? 0.0f : sc[kTile + at] * unit;
+                    float ks = sc[at] * a.scale_log2, vs = sc[kTile + at] * unit;
+                    if (edge && dead(at)) ks = vs = 0.0f;
+                    to[at] = ks;
+                    to[kTile + at] = vs;
                 }
                 if (ct == 0) value_exp[keys % Sh::kScales] = exp_now;
             };
             // Tile n.
             auto turn = [&](bool is_k, int j, bool first) -> bool {
-                const uint32_t rs = n % kRaw, st = n % kStages;
+                const uint32_t st = n % kStages, rs = n % kRaw;
                 if (!wait_for(&bar.raw_full[rs], (n / kRaw) & 1, abort)) return false;
-                const uint8_t *src = raw + rs * Sh::kRawBytes;
-                uint8_t *dst = ring + st * Sh::kTileBytes;
                 if (n >= kStages && !wait_for(&bar.kv_empty[st], (n / kStages - 1) & 1, abort))
                     return false;
+                const uint8_t *src = raw + rs * Sh::kRawBytes;
                 if (is_k) turn_scales(reinterpret_cast<const float *>(src + kTile * D), j, first);
+                src += src_at;
+                uint8_t *dst = ring + st * Sh::kTileBytes;
                 // rolled: the roles' hot lines have to stay in the instruction cache
-                // together (fully unrolled, a tile takes 1.4 times as long)
-#pragma unroll 2
+                // together (unrolled 8 times a tile took 1.4 times as long)
+#pragma unroll 4
                 for (int i = 0; i < kSteps; ++i) {
-                    const uint4 w =
-                        *reinterpret_cast<const uint4 *>(src + src_at + i * (kStepRows * D));
+                    const uint4 w = *reinterpret_cast<const uint4 *>(src + i * (kStepRows * D));
                     uint4 lo, hi;
                     codes_to<BF16>(w.x, lo.x, lo.y);
                     codes_to<BF16>(w.y, lo.z, lo.w);
@@ -817,20 +821,19 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 return true;
             };
-            auto tile = [&](bool is_k, int j, bool first) -> bool {
-                const bool r = is_k != (team == 0) || turn(is_k, j, first);
-                ++n;
-                keys += is_k;
-                return r;
-            };
+#pragma unroll 1
             while (ok && next_segment(a, width, w, g)) {
                 int j0, j1;
                 span_of(g, j0, j1);
-                for (int i = 0; ok && i < kAhead && j0 + i < j1; ++i)
-                    ok = tile(true, j0 + i, i == 0);
-                for (int j = j0; ok && j < j1; ++j)
-                    ok = tile(false, j, false) &&
-                         (j + kAhead >= j1 || tile(true, j + kAhead, false));
+                int kj = j0, vj = j0;
+#pragma unroll 1
+                while (ok && vj < j1) {  // the order of the loads
+                    const bool is_k = kj < min(j1, vj + kAhead);
+                    if (is_k == (team == 0)) ok = turn(is_k, kj, kj == j0);
+                    ++n;
+                    keys += is_k;
+                    ++(is_k ? kj : vj);
+                }
             }
             if (!ok) fail();
         }
@@ -843,6 +846,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         const uint32_t s_addr = lanes + t * 128, o_addr = lanes + 256 + t * 128;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, keys = 0;
         bool ok = true;
+#pragma unroll 1
         while (ok && next_segment(a, width, w, g)) {
             int j0, j1;
             span_of(g, j0, j1);
@@ -859,29 +863,45 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             float l = 0.0f, last = 0.0f;
             const int first = PAIR ? part.j0 : j0 + t;
             int exp_now = 0;  // int8: O is in units of 2^exp_now
+#pragma unroll 1
             for (int j = first; j < part.j1; j += PAIR ? 1 : 2) {
                 if (!(ok = wait_for(&bar.s_full[t], s_phase, abort))) break;
                 s_phase ^= 1;
                 if (warp_live) {
                     tmem_fence_after();
-                    float s[128];
+                    // int8 holds half the row's logits, and reads the others from
+                    // tensor memory again where they are used (P overwrites the
+                    // first half only): the scales take registers too
+                    constexpr int kHeld = I8 ? 2 : 4;
+                    float s[32 * kHeld];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(s_addr + 32 * i, s + 32 * i);
+                    for (int i = 0; i < kHeld; ++i) tmem_ld32(s_addr + 32 * i, s + 32 * i);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) pin32(s + 32 * i);
+                    for (int i = 0; i < kHeld; ++i) pin32(s + 32 * i);
                     const int rh = hi - j * kTile, rl = lo - j * kTile;
                     const uint32_t dead = dead_groups[(keys + (j - j0)) & 7];
                     const float *tile_sc = scales + (keys + (j - j0)) % Sh::kScales * (2 * kTile);
-                    const float *k_sc = tile_sc;
-                    if (__any_sync(0xffffffffu, rh < kTile || rl > 0) || dead) {
+                    // in a tile that hides keys from a row the logits are scaled
+                    // before they are hidden (0 * infinity is none)
+                    const bool hides = __any_sync(0xffffffffu, rh < kTile || rl > 0) || dead;
+                    const float *k_sc = I8 && hides ? ones : tile_sc;
+                    auto hide = [&](float *v, int c0) {
+                        auto below = [](int n) {  // n low bits
+                            return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+                        };
+                        uint32_t seen = below(rh - c0) & ~below(rl - c0);
+                        if (dead >> (c0 / 16) & 1) seen &= 0xffff0000u;
+                        if (dead >> (c0 / 16) & 2) seen &= 0x0000ffffu;
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) {
-                            if (I8) s[c] *= k_sc[c];
-                            if (c >= rh || c < rl || (dead >> (c / 16) & 1)) s[c] = -INFINITY;
+                        for (int c = 0; c < 32; ++c) {
+                            if (I8) v[c] *= tile_sc[c0 + c];
+                            if (!(seen >> c & 1)) v[c] = -INFINITY;
                         }
-                        if (I8) k_sc = ones;  // the logits are scaled already
-                    }
+                    };
+                    if (hides)
+#pragma unroll
+                        for (int i = 0; i < kHeld; ++i) hide(s + 32 * i, 32 * i);
                     int new_exp = 0;
                     if constexpr (I8) {
                         new_exp = value_exp[(keys + (j - j0)) % Sh::kScales];
@@ -895,16 +915,31 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     bool fix = __any_sync(0xffffffffu, m == -INFINITY || last > kRaise) ||
                                (I8 && new_exp != exp_now);
                     float2 sum[2];
+#pragma unroll 1
                     for (;;) {
                         if (fix) {
                             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                            auto top_of = [&](const float *v, int c0, int n) {
 #pragma unroll
-                            for (int c = 0; c < 128; c += 8)
+                                for (int c = 0; c < n; c += 8)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    mx[i] = I8 ? fmax3(mx[i], s[c + i] * k_sc[c + i],
-                                                       s[c + 4 + i] * k_sc[c + 4 + i])
-                                               : fmax3(mx[i], s[c + i], s[c + 4 + i]);
+                                    for (int i = 0; i < 4; ++i)
+                                        mx[i] = I8 ? fmax3(mx[i], v[c + i] * k_sc[c0 + c + i],
+                                                           v[c + 4 + i] * k_sc[c0 + c + 4 + i])
+                                                   : fmax3(mx[i], v[c + i], v[c + 4 + i]);
+                            };
+                            top_of(s, 0, 32 * kHeld);
+                            if constexpr (I8) {
+#pragma unroll 1
+                                for (int i = kHeld; i < 4; ++i) {
+                                    float v[32];
+                                    tmem_ld32(s_addr + 32 * i, v);
+                                    tmem_wait_ld();
+                                    pin32(v);
+                                    if (hides) hide(v, 32 * i);
+                                    top_of(v, 32 * i, 32);
+                                }
+                            }
                             const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) *
                                               (I8 ? 1.0f : a.scale_log2);
                             const float mn = fmaxf(last > kRaise ? m + __log2f(last) - 7.0f : m, top);
@@ -918,7 +953,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 // by at most 2^-200 in one step: 0 where it matters
                                 const float fo =
                                     I8 ? f * exp2_approx(static_cast<float>(exp_now - new_exp)) : f;
-#pragma unroll
+#pragma unroll 1
                                 for (int i = 0; i < D / 16; ++i) {
                                     float o[16];
                                     tmem_ld16(o_addr + 16 * i, o);
@@ -935,8 +970,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
                         const float2 off = make_float2(-base, -base);
                         sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        // the weights of 32 keys, and P
+                        auto weights = [&](const float *v, int c0) {
                             uint32_t p[16];
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
@@ -944,17 +979,18 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 if constexpr (I8) {
 #pragma unroll
                                     for (int c = 0; c < 4; ++c) {
-                                        const int at = 32 * i + 16 * h + 4 * c;
+                                        const int at = c0 + 16 * h + 4 * c;
                                         kc[c] = *reinterpret_cast<const float4 *>(k_sc + at);
-                                        vc[c] = *reinterpret_cast<const float4 *>(tile_sc + kTile + at);
+                                        vc[c] =
+                                            *reinterpret_cast<const float4 *>(tile_sc + kTile + at);
                                     }
                                 }
 #pragma unroll
                                 for (int c = 0; c < 8; ++c) {
-                                    const int at = 32 * i + 16 * h + 2 * c;
+                                    const int at = 16 * h + 2 * c;
                                     const float4 k4 = kc[c / 2], v4 = vc[c / 2];
                                     float2 x = __ffma2_rn(
-                                        make_float2(s[at], s[at + 1]),
+                                        make_float2(v[at], v[at + 1]),
                                         !I8          ? sc
                                         : c % 2 == 0 ? make_float2(k4.x, k4.y)
                                                      : make_float2(k4.z, k4.w),
@@ -968,7 +1004,26 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                     p[8 * h + c] = pack2<BF16>(x.x, x.y);
                                 }
                             }
-                            tmem_st16(s_addr + 16 * i, p);
+                            tmem_st16(s_addr + c0 / 2, p);
+                        };
+                        if constexpr (I8) {
+                            float v[2][32];
+                            tmem_ld32(s_addr + 64, v[0]);
+                            weights(s, 0);
+                            tmem_ld32(s_addr + 96, v[1]);
+                            weights(s + 32, 32);
+                            tmem_wait_ld();
+                            pin32(v[0]);
+                            pin32(v[1]);
+                            if (hides) {
+                                hide(v[0], 64);
+                                hide(v[1], 96);
+                            }
+                            weights(v[0], 64);
+                            weights(v[1], 96);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) weights(s + 32 * i, 32 * i);
                         }
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         last = sum[0].x + sum[0].y;
@@ -988,7 +1043,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             keys += j1 - j0;
             // ---- the segment's result
             const bool some = first < part.j1;
-            if (PAIR ? some : j1 > j0) {
+            if (some) {
                 if (!(ok = wait_for(&bar.o_full[t], o_phase, abort))) break;
                 o_phase ^= 1;
                 tmem_fence_after();
@@ -1030,14 +1085,14 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                        static_cast<int64_t>(g.head * a.G + row % a.G) * D;
             float4 *part_dst = reinterpret_cast<float4 *>(a.acc) +
                                ((slot * (a.ws_rows / 32) + prow / 32) * (D / 4)) * 32 + lane;
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < kHalves; ++h) {
                 if (!PAIR && h > 0) {
                     ok = t == 1 ? wait_for(&bar.join_empty, join_phase ^ 1, abort)
                                 : wait_for(&bar.join_full, join_phase, abort);
                     if (!ok) break;
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int i = 2 * h; i < 2 * h + 2; ++i) {
                     float o[32];
                     if (warp_live && some) {
@@ -1053,14 +1108,14 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                             if (warp_live)
 #pragma unroll
                                 for (int c = 0; c < 32; ++c)
-                                    join[((i & 1) * 32 + c) * kTile + row] =
+                                    join[((i & 1) * 32 + c) * Sh::kRows + row] =
                                         I8 ? o[c] * unit : o[c];
                             continue;
                         }
                         if (warp_live)
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
-                                const float u = join[((i & 1) * 32 + c) * kTile + row];
+                                const float u = join[((i & 1) * 32 + c) * Sh::kRows + row];
                                 o[c] = (mine != 0.0f ? o[c] * mine : 0.0f) +
                                        (other != 0.0f ? u * other : 0.0f);
                             }
@@ -1216,7 +1271,7 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
     a.window = p.window;
     a.starts = p.starts;
     a.scale_log2 = p.scale_log2;
-    a.q_tokens = kTile / p.G;
+    a.q_tokens = MODE == kPair ? kTile / p.G : p.max_new;
     a.box = 16;
     while (a.box < kTile && c.page_size % (2 * a.box) == 0) a.box *= 2;
     const int64_t rows = static_cast<int64_t>(c.n_pages) * c.n_kv_heads * c.page_size;

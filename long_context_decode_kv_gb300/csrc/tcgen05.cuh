@@ -149,8 +149,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
         "%10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
-        "r"(addr)
-        : "memory");
+        "r"(addr));
 }
 
 // Tiled TMA loads global -> shared.  x counts elements and x times the element
