@@ -430,52 +430,58 @@ def _heads(t: Optional[torch.Tensor]):
     """kvd_heads of rows [n_tokens, n_heads, head_dim]; only the token stride is free."""
     if t is None:
         return None
-    if t.dim() != 3 or t.dtype not in _X:
+    x = _X.get(t.dtype)
+    shape = t.shape
+    if x is None or len(shape) != 3:
         raise ValueError("rows are [n_tokens, n_heads, head_dim] of float16, bfloat16 or float32")
-    n, h, d = t.shape
+    n, h, d = shape
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d != 1) or (s1 != d and h != 1):
         raise ValueError("the heads of a token must be dense")
-    return HeadsStruct(t.data_ptr(), s0 if n > 1 else h * d, _X[t.dtype], h)
+    return HeadsStruct(t.data_ptr(), s0 if n > 1 else h * d, x, h)
 
 
-def _int32(t: torch.Tensor, shape, name: str):
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} is an int32 tensor of shape {tuple(shape)}")
-    return _ptr(t)
+def _int32(t: torch.Tensor, n: int, name: str):
+    if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} is an int32 tensor [{n}]")
+    if n > 1 and t.stride()[0] != 1:
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
 def _weight(t: Optional[torch.Tensor], d: int):
-    if t is not None and (t.dtype != torch.float32 or t.shape != (d,)):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != d:
         raise ValueError("a norm weight is a float32 tensor [head_dim]")
-    return _ptr(t)
+    if t.stride()[0] != 1:
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _same_device(first: torch.Tensor, *others):
-    """The device all tensors of a call live on (other, absent ones are None)."""
-    d = first.device
-    if d.type != "cuda":
+def _one_device(index: int, *tensors):
+    """All tensors of a call (absent ones None) on CUDA device `index`."""
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    for t in others:
-        if t is not None and t.device != d:
+    for t in tensors:
+        if t is not None and t.get_device() != index:
             raise ValueError("the tensors of a call must be on one device")
-    return d
 
 
-class _On:
-    """The call's device current, as the library launches on the current device."""
-
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else \
-            torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _call(name: str, index: int, stream, fn, *args):
+    """The library's call with its device current (it launches there), on the given
+    stream or the device's current one."""
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        stream = stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, stream)
+    if rc != 0:
+        raise KvdError(name, rc)
 
 
 class RopeTable:
@@ -521,14 +527,13 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], positions: Optional
     if q_out.shape != q.shape or (k is not None and (k_out is None or k_out.shape != k.shape or
                                                      k.shape[0] != T or k.shape[2] != D)):
         raise ValueError("outputs have their inputs' shapes, and q and k as many tokens and channels")
-    d = _same_device(q, k, positions, q_out, k_out, q_weight, k_weight,
-                     None if rope is None else rope.freqs)
-    with _On(d):
-        _check("kvd_qk_norm_rope", lib().kvd_qk_norm_rope(
-            _heads(q), _heads(q_out), _heads(k), _heads(k_out), T, D,
-            None if positions is None else _int32(positions, (T,), "positions"),
-            None if rope is None else rope.ref(), _weight(q_weight, D), _weight(k_weight, D),
-            float(eps), _stream(q, stream)))
+    d = q.get_device()
+    _one_device(d, k, positions, q_out, k_out, q_weight, k_weight,
+                None if rope is None else rope.freqs)
+    _call("kvd_qk_norm_rope", d, stream, lib().kvd_qk_norm_rope, _heads(q), _heads(q_out),
+          _heads(k), _heads(k_out), T, D,
+          None if positions is None else _int32(positions, T, "positions"),
+          None if rope is None else rope.s, _weight(q_weight, D), _weight(k_weight, D), eps)
 
 
 class PagedKVCache:
@@ -563,8 +568,9 @@ class PagedKVCache:
                 t[name] = (torch.zeros if zero else torch.empty)(shape, dtype=kind, device=dev)
             elif tuple(t[name].shape) != shape or t[name].dtype != kind:
                 raise ValueError(f"{name} is {kind} of shape {shape}")
-        self.device = _same_device(*t.values())
         self.t = t
+        self.device = t["k"].device
+        _one_device(t["k"].get_device(), *t.values())
         self.s = PagedCacheStruct(dtype, batch, n_kv_heads, head_dim, n_pages, page_size,
                                   max_pages, 0, *(_ptr(t.get(n)) for n in (
                                       "k", "v", "k_scale", "v_scale", "page_table", "seq_lens",
@@ -608,7 +614,7 @@ class PagedKVCache:
 
 
 def paged_workspace_bytes(cache: PagedKVCache, n_heads: int, n_tokens: int, max_new: int) -> int:
-    with _On(cache.device):
+    with torch.cuda.device(cache.device):
         return int(lib().kvd_paged_workspace_bytes(cache.ref(), n_heads, n_tokens, max_new))
 
 
@@ -634,13 +640,12 @@ def paged_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, starts: 
     if q is not None and (q_out is None or q_out.shape != q.shape or q.shape[0] != T or
                           q.shape[2] != D):
         raise ValueError("q and q_out are [n_tokens, n_heads, head_dim]")
-    _same_device(cache.t["k"], k, v, starts, k_weight, q, q_out, q_weight,
-                 None if rope is None else rope.freqs)
-    with _On(cache.device):
-        _check("kvd_paged_append", lib().kvd_paged_append(
-            cache.ref(), _heads(k), _heads(v), T, _int32(starts, (cache.batch + 1,), "starts"),
-            None if rope is None else rope.ref(), _weight(k_weight, D), _heads(q), _heads(q_out),
-            _weight(q_weight, D), float(eps), _stream(k, stream)))
+    d = k.get_device()
+    _one_device(d, cache.t["k"], v, starts, k_weight, q, q_out, q_weight,
+                None if rope is None else rope.freqs)
+    _call("kvd_paged_append", d, stream, lib().kvd_paged_append, cache.s, _heads(k), _heads(v), T,
+          _int32(starts, cache.batch + 1, "starts"), None if rope is None else rope.s,
+          _weight(k_weight, D), _heads(q), _heads(q_out), _weight(q_weight, D), eps)
 
 
 def paged_attn(cache: PagedKVCache, q: torch.Tensor, starts: torch.Tensor, max_new: int,
@@ -651,12 +656,11 @@ def paged_attn(cache: PagedKVCache, q: torch.Tensor, starts: torch.Tensor, max_n
     T, _, D = q.shape
     if out.shape != q.shape or D != cache.head_dim:
         raise ValueError("q and out are [n_tokens, n_heads, head_dim]")
-    _same_device(cache.t["k"], q, starts, out, workspace)
-    with _On(cache.device):
-        _check("kvd_paged_attn", lib().kvd_paged_attn(
-            cache.ref(), _heads(q), T, _int32(starts, (cache.batch + 1,), "starts"), int(max_new),
-            float(softmax_scale), int(window), _heads(out), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(q, stream)))
+    d = q.get_device()
+    _one_device(d, cache.t["k"], starts, out, workspace)
+    _call("kvd_paged_attn", d, stream, lib().kvd_paged_attn, cache.s, _heads(q), T,
+          _int32(starts, cache.batch + 1, "starts"), max_new, softmax_scale, window, _heads(out),
+          _ptr(workspace), workspace.numel() * workspace.element_size())
 
 
 __all__ = ["F16", "INT8", "Q8_0", "Q4_0", "BF16", "BLOCK", "HEAD_DIM", "KVCache", "KvdError", "CacheStruct", "lib",

@@ -27,7 +27,7 @@ struct RopeArgs {
     RowsIn q, k, v;
     RowsOut q_out, k_out;  // k_out: unused with a cache
     const float *q_weight, *k_weight;
-    float eps;
+    float eps, inv_dim;  // inv_dim: 1 / head_dim
     int head_dim, n_tokens;
     const int32_t *positions;  // without a cache
     kvd_rope rope;             // rot_dim 0: no rotation

@@ -162,6 +162,7 @@ kvd_status kvd_qk_norm_rope(const kvd_heads *q, const kvd_heads *q_out, const kv
     a.k_weight = k ? k_weight : nullptr;
     a.eps = eps;
     a.head_dim = head_dim;
+    a.inv_dim = 1.0f / static_cast<float>(head_dim);
     a.n_tokens = n_tokens;
     a.positions = positions;
     if (rope) a.rope = *rope;
@@ -200,6 +201,7 @@ kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_heads *k, co
     a.k_weight = k_weight;
     a.eps = eps;
     a.head_dim = D;
+    a.inv_dim = 1.0f / static_cast<float>(D);
     a.n_tokens = n_tokens;
     if (rope) a.rope = *rope;
     a.starts = starts;

@@ -4,12 +4,13 @@
 //   y = R(p) (x * w / sqrt(mean(x^2) + eps))
 //   R(p) turns channel pair i of the first rot_dim channels by p * f_i.
 //
-// Bound by HBM: each element is read once and written once.  One CTA serves one
-// token (several share one when a batch has few tokens), so the sines and
-// cosines of the token's rot_dim / 2 angles are computed once, one per thread,
-// and read from shared memory by the token's 10 to 100 heads.  A row of head_dim
-// channels is held by the fewest lanes that take 8 channels each (16 lanes at
-// 128), so a warp moves 512 contiguous bytes of f16 an instruction.
+// Bound by HBM: each element is read once and written once.  A warp serves one
+// token (several share one when a batch has few), so the sines and cosines of a
+// lane's channels and the norms' weights are made once, stay in registers, and
+// serve the token's 10 to 100 heads; no lane waits for another warp.  A row of
+// head_dim channels is held by the fewest lanes that take 8 channels each (16
+// lanes at 128), so a warp moves 512 contiguous bytes of f16 an instruction, with
+// U such loads in flight.
 //
 // The angle: the frequency is a 64-bit fraction of a turn per position, so the
 // product with the position, modulo 2^64, is the angle's fraction of a turn with
@@ -24,7 +25,6 @@ namespace kvd {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kMaxPairs = 512;
 
 template <typename T>
 struct Raw {  // 8 channels as loaded: f16 or bf16
@@ -74,49 +74,47 @@ __device__ __forceinline__ void store8(void *p, int dtype, size_t at, const floa
 }
 
 // LPR lanes hold one row, lane l chunks l, l + LPR, .. (8 channels each, VPL of
-// them); U rows a lane group are loaded before the first is worked on.
+// them); U rows a lane group are in flight.
 template <typename IN, int LPR, int VPL, int U, bool PAGED>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-    __shared__ float2 turn[kMaxPairs];  // (cos, sin) * mscale of the token's angles
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t = blockIdx.x;
+__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeArgs a,
+                                                        int parts) {
+    const int lane = threadIdx.x & 31;
+    const int unit = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int t = unit / parts;
+    constexpr int kRows = 32 / LPR;  // a warp holds at once
     const int sub = lane / LPR, col = lane % LPR;
     const int nrows = a.q.n_heads + a.k.n_heads + a.v.n_heads;
     const int chunks = a.head_dim / 8;
-    constexpr int kRowsPerWarp = 32 / LPR;
-    const int step = gridDim.y * (kThreads / 32) * kRowsPerWarp;
-    const int r0 = (blockIdx.y * (kThreads / 32) + warp) * kRowsPerWarp;
+    const int step = parts * kRows, r0 = unit % parts * kRows;
     pdl_wait();
     pdl_launch_dependents();
+    if (t >= a.n_tokens) return;
 
     Raw<IN> raw[U][VPL];
-    auto load = [&](int base) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            int r = base + u * step + sub;
-            const bool ok = r < nrows;
-            const RowsIn *in = &a.q;
-            if (r >= a.q.n_heads) {
-                r -= a.q.n_heads;
-                in = &a.k;
-                if (r >= a.k.n_heads) {
-                    r -= a.k.n_heads;
-                    in = &a.v;
-                }
-            }
-            const IN *src = static_cast<const IN *>(in->x) + t * in->stride +
-                            static_cast<int64_t>(r) * a.head_dim;
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int c = col + i * LPR;
-                if (ok && c < chunks)
-                    raw[u][i].load(src + 8 * c);
-                else
-                    raw[u][i].zero();
+    auto load = [&](int u, int r) {  // row r into raw[u]
+        const bool ok = r < nrows;
+        const RowsIn *in = &a.q;
+        if (r >= a.q.n_heads) {
+            r -= a.q.n_heads;
+            in = &a.k;
+            if (r >= a.k.n_heads) {
+                r -= a.k.n_heads;
+                in = &a.v;
             }
         }
+        const IN *src = static_cast<const IN *>(in->x) + t * in->stride +
+                        static_cast<int64_t>(r) * a.head_dim;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int c = col + i * LPR;
+            if (ok && c < chunks)
+                raw[u][i].load(src + 8 * c);
+            else
+                raw[u][i].zero();
+        }
     };
-    load(r0);
+#pragma unroll
+    for (int u = 0; u < U; ++u) load(u, r0 + u * step + sub);
 
     // the token's position, and with a cache the place of its rows
     long pos = 0;
@@ -127,7 +125,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         const int s0 = a.starts[b], s1 = a.starts[b + 1], end = a.starts[a.cache.batch];
         if (t < s0 || t >= s1) {
             // behind the last sequence, or starts that are not in order
-            if (t < end && threadIdx.x == 0) report_status(a.cache.dev_status, KVD_ERR_INVALID);
+            if (t < end && lane == 0) report_status(a.cache.dev_status, KVD_ERR_INVALID);
             return;
         }
         pos = static_cast<long>(checked_len(a.cache, b)) - (s1 - t);
@@ -137,28 +135,56 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             const int page = checked_page(a.cache, b, j);
             store_kv = page >= 0;
             row0 = static_cast<size_t>(page) * a.cache.n_kv_heads * ps + (pos - j * ps);
-        } else if (threadIdx.x == 0) {
+        } else if (lane == 0) {
             report_status(a.cache.dev_status, KVD_ERR_INVALID);
         }
     } else if (a.rope.rot_dim) {
         pos = a.positions[t];
     }
 
+    // (cos, sin) * mscale of this lane's channels: for pairs (i, i + rot_dim / 2)
+    // of all 8 of a chunk, with the sign of the other channel's share; interleaved,
+    // of its 4 pairs.  Channels that are not rotated: (1, 0).
     const int half = a.rope.rot_dim / 2;
+    float cs[VPL][8], sn[VPL][8];
     if (half) {
-        for (int i = threadIdx.x; i < half; i += kThreads) {
-            const uint64_t frac = static_cast<uint64_t>(pos) * a.rope.freqs[i];
-            // signed upper half: half turns in [-1, 1)
-            const float x = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
-            float s, c;
-            sincospif(x, &s, &c);
-            turn[i] = make_float2(c * a.rope.mscale, s * a.rope.mscale);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int ch = 8 * (col + i * LPR);
+            const bool turns = ch < 2 * half;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                cs[i][j] = 1.0f;
+                sn[i][j] = 0.0f;
+                if (!turns || (a.rope.interleaved && j >= 4)) continue;
+                const int pair = a.rope.interleaved ? ch / 2 + j : ch < half ? ch + j : ch - half + j;
+                const uint64_t frac = static_cast<uint64_t>(pos) * a.rope.freqs[pair];
+                // signed upper half: half turns in [-1, 1)
+                const float x = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
+                float s, c;
+                sincospif(x, &s, &c);
+                cs[i][j] = c * a.rope.mscale;
+                sn[i][j] = (a.rope.interleaved || ch >= half ? s : -s) * a.rope.mscale;
+            }
         }
-        __syncthreads();
+    }
+    float wq[VPL][8] = {}, wk[VPL][8] = {};
+    const bool norms = a.q_weight || a.k_weight;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int c = col + i * LPR;
+        Raw<float> w;
+        if (a.q_weight && c < chunks) {
+            w.load(a.q_weight + 8 * c);
+            w.get(wq[i]);
+        }
+        if (a.k_weight && c < chunks) {
+            w.load(a.k_weight + 8 * c);
+            w.get(wk[i]);
+        }
     }
 
     for (int base = r0; base < nrows; base += U * step) {
-        if (base != r0) load(base);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (base + u * step >= nrows) break;  // the same for the whole warp
@@ -176,7 +202,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
             float x[VPL][8];
 #pragma unroll
             for (int i = 0; i < VPL; ++i) raw[u][i].get(x[i]);
-            if (a.q_weight || a.k_weight) {
+            if (base + (U + u) * step < nrows) load(u, base + (U + u) * step + sub);
+            if (norms) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int i = 0; i < VPL; ++i)
@@ -184,37 +211,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                     for (int j = 0; j < 8; ++j) ss = fmaf(x[i][j], x[i][j], ss);
 #pragma unroll
                 for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float *w = part == 0 ? a.q_weight : part == 1 ? a.k_weight : nullptr;
-                if (w) {
-                    const float rs =
-                        1.0f / sqrtf(ss / static_cast<float>(a.head_dim) + a.eps);
+                if (part == 0 ? a.q_weight != nullptr : part == 1 && a.k_weight) {
+                    const float rs = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) {
-                        const int c = col + i * LPR;
-                        if (c < chunks) {
-                            const float4 w0 = reinterpret_cast<const float4 *>(w)[2 * c];
-                            const float4 w1 = reinterpret_cast<const float4 *>(w)[2 * c + 1];
-                            const float ww[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+                    for (int i = 0; i < VPL; ++i)
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) x[i][j] *= rs * ww[j];
-                        }
-                    }
+                        for (int j = 0; j < 8; ++j)
+                            x[i][j] *= rs * (part == 0 ? wq[i][j] : wk[i][j]);
                 }
             }
             if (half) {
                 if (a.rope.interleaved) {
+                    if (part < 2) {
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) {
-                        const int ch = 8 * (col + i * LPR);
-                        if (part < 2 && ch < 2 * half) {
+                        for (int i = 0; i < VPL; ++i)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const float2 cs = turn[ch / 2 + j];
                                 const float p = x[i][2 * j], q = x[i][2 * j + 1];
-                                x[i][2 * j] = fmaf(p, cs.x, -q * cs.y);
-                                x[i][2 * j + 1] = fmaf(q, cs.x, p * cs.y);
+                                x[i][2 * j] = fmaf(p, cs[i][j], -q * sn[i][j]);
+                                x[i][2 * j + 1] = fmaf(q, cs[i][j], p * sn[i][j]);
                             }
-                        }
                     }
                 } else {
                     // the other channel of each pair is rot_dim / 2 away: a whole
@@ -239,17 +255,13 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
                             }
                         }
                     }
+                    if (part < 2) {
 #pragma unroll
-                    for (int i = 0; i < VPL; ++i) {
-                        const int ch = 8 * (col + i * LPR);
-                        if (part < 2 && ch < 2 * half) {
-                            const bool low = ch < half;
-                            const float2 *cs = turn + (low ? ch : ch - half);
+                        for (int i = 0; i < VPL; ++i) {
+                            if (8 * (col + i * LPR) >= 2 * half) continue;
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const float m = y[i][j] * cs[j].y;
-                                x[i][j] = fmaf(x[i][j], cs[j].x, low ? -m : m);
-                            }
+                            for (int j = 0; j < 8; ++j)
+                                x[i][j] = fmaf(x[i][j], cs[i][j], y[i][j] * sn[i][j]);
                         }
                     }
                 }
@@ -307,14 +319,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <typename IN, int LPR, int VPL, int U, bool PAGED>
 cudaError_t launch(const RopeArgs &a, cudaStream_t st) {
     const int nrows = a.q.n_heads + a.k.n_heads + a.v.n_heads;
-    const int per_cta = kThreads / LPR;  // rows a CTA holds at once
-    // CTAs a token: one, or as many as fill the SMs a few times over
-    const int most = (nrows + per_cta - 1) / per_cta;
-    int want = (8 * device_sm_count() + a.n_tokens - 1) / a.n_tokens;
-    if (want > most) want = most;
-    if (want < 1) want = 1;
-    return launch_ex(rope_kernel<IN, LPR, VPL, U, PAGED>, dim3(a.n_tokens, want), dim3(kThreads),
-                     0, st, true, a);
+    constexpr int kRows = 32 / LPR;
+    // Warps a token: one, or as many as give every SM 16 warps
+    const int most = (nrows + kRows - 1) / kRows;
+    int parts = (16 * device_sm_count() + a.n_tokens - 1) / a.n_tokens;
+    if (parts > most) parts = most;
+    const int64_t units = static_cast<int64_t>(a.n_tokens) * parts;
+    constexpr int kWarps = kThreads / 32;
+    return launch_ex(rope_kernel<IN, LPR, VPL, U, PAGED>,
+                     dim3(static_cast<unsigned>((units + kWarps - 1) / kWarps)), dim3(kThreads), 0,
+                     st, true, a, parts);
 }
 
 template <typename IN>
