@@ -589,7 +589,8 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*   bf16 over an int8 cache.  softmax_scale > 0.                               */
 /*   max_new: at least the largest n_b (it sizes the grid; the tokens of a     */
 /*   larger n_b are left out, and INVALID is reported to dev_status).          */
-/*   workspace: kvd_paged_workspace_bytes; need not be zeroed.  Calls that     */
+/*   workspace: kvd_paged_workspace_bytes, zero-filled before its first use;   */
+/*   every call that completes leaves its counters at zero again.  Calls that  */
 /*   may overlap on the GPU need a workspace each.                              */
 /* n_tokens == 0 is a no-op.                                                    */
 /* Errors: INVALID; UNSUPPORTED (head_dim, page_size, more than 16 query heads  */

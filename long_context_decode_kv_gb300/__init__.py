@@ -620,11 +620,12 @@ def paged_workspace_bytes(cache: PagedKVCache, n_heads: int, n_tokens: int, max_
 
 def make_paged_workspace(cache: PagedKVCache, n_heads: int, n_tokens: int,
                          max_new: int) -> torch.Tensor:
-    """A workspace for paged_attn calls of up to n_tokens new tokens, up to max_new a sequence."""
+    """A zero-filled workspace for paged_attn calls of up to n_tokens new tokens, up to
+    max_new a sequence."""
     n = paged_workspace_bytes(cache, n_heads, n_tokens, max_new)
     if n == 0:
         raise KvdError("kvd_paged_workspace_bytes", 1)
-    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
 def paged_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,

@@ -211,6 +211,10 @@ __device__ __forceinline__ uint32_t float_to_key(float f) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+__device__ __forceinline__ float key_to_float(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 // q8_0 quantization of one 128-wide row held 4 values per lane by a full
 // warp: the 8 lanes 8g..8g+7 hold group g (channels 32g..32g+31).  The
 // group's scale is d = fl16(absmax/127) (the IEEE f32 quotient rounded to

@@ -49,7 +49,14 @@ struct PagedAttnArgs {
     float scale_log2;  // softmax_scale * log2(e)
 };
 
+// The workspace begins with paged_counter_bytes() of counters, zero between calls,
+// which launch_paged_decode uses and launch_paged_attn leaves alone.
+size_t paged_counter_bytes();
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st);
-size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new);
+size_t paged_attn_ws(const kvd_paged_cache &c, int H, int max_new);
+// At most kDecodeRows rows (new tokens times query heads of a KV head) a sequence.
+constexpr int kDecodeRows = 32;
+cudaError_t launch_paged_decode(const PagedAttnArgs &a, void *ws, cudaStream_t st);
+size_t paged_decode_ws(int rows, int D);
 
 }  // namespace kvd

@@ -65,7 +65,10 @@ kvd_status check_paged(const kvd_paged_cache *c) {
     if (c->page_size % 16 != 0) return KVD_ERR_UNSUPPORTED;
     if (c->len < 0 || c->len > static_cast<int64_t>(c->max_pages) * c->page_size)
         return KVD_ERR_INVALID;
-    // rows of the pool are counted in 31 bits
+    // tokens, key tiles and rows of the pool are counted in 31 bits
+    if (c->len > (1 << 30) ||
+        static_cast<__int128>(c->batch) * c->n_kv_heads * (c->len / 128 + 1) > 0x7fffffff)
+        return KVD_ERR_UNSUPPORTED;
     if (static_cast<__int128>(c->n_pages) * c->n_kv_heads * c->page_size > 0x7fffffff)
         return KVD_ERR_UNSUPPORTED;
     if (!c->k || !aligned(c->k, 16) || !c->v || !aligned(c->v, 16)) return KVD_ERR_INVALID;
@@ -76,6 +79,14 @@ kvd_status check_paged(const kvd_paged_cache *c) {
         return KVD_ERR_INVALID;
     if (c->dev_status && !aligned(c->dev_status, 4)) return KVD_ERR_INVALID;
     return KVD_OK;
+}
+
+bool few_rows(int G, int max_new) { return static_cast<int64_t>(G) * max_new <= kDecodeRows; }
+
+size_t attn_ws(const kvd_paged_cache &c, int H, int max_new) {
+    const int G = H / c.n_kv_heads;
+    return few_rows(G, max_new) ? paged_decode_ws(G * max_new, c.head_dim)
+                                : paged_attn_ws(c, H, max_new);
 }
 
 RowsIn rows_in(const kvd_heads *h) { return RowsIn{h->x, h->stride, h->n_heads}; }
@@ -214,7 +225,7 @@ size_t kvd_paged_workspace_bytes(const kvd_paged_cache *cache, int32_t n_heads, 
     if (check_paged(cache) != KVD_OK || n_tokens < 1 || max_new < 1) return 0;
     if (n_heads < 1 || n_heads % cache->n_kv_heads != 0 || n_heads / cache->n_kv_heads > 16)
         return 0;
-    return paged_attn_ws(*cache, n_heads, n_tokens, max_new);
+    return attn_ws(*cache, n_heads, max_new);
 }
 
 kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int32_t n_tokens,
@@ -237,7 +248,7 @@ kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int3
     if (G > 16) return KVD_ERR_UNSUPPORTED;
     if (!starts || !aligned(starts, 4)) return KVD_ERR_INVALID;
     if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < paged_attn_ws(*cache, q->n_heads, n_tokens, max_new))
+        workspace_bytes < attn_ws(*cache, q->n_heads, max_new))
         return KVD_ERR_WORKSPACE;
     PagedAttnArgs a = {};
     a.c = *cache;
@@ -253,7 +264,9 @@ kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int3
     a.window = window;
     a.starts = starts;
     a.scale_log2 = softmax_scale * kLog2e;
-    return cuda_status(launch_paged_attn(a, workspace, static_cast<cudaStream_t>(stream)));
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(few_rows(G, max_new) ? launch_paged_decode(a, workspace, st)
+                                            : launch_paged_attn(a, workspace, st));
 }
 
 }  // extern "C"

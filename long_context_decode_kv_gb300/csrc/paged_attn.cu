@@ -26,102 +26,36 @@
 // of O rare.
 // P is rounded to the input type (the tensor core's operand): a relative error
 // of half a step in each weight, which sums and statistics in f32 do not add to.
-#include <cuda.h>
-
-#include <atomic>
-
-#include "common.cuh"
-#include "internal.h"
-#include "paged.h"
-#include "paged_dev.cuh"
-#include "tcgen05.cuh"
+#include "paged_attn_dev.cuh"
 
 namespace kvd {
 namespace {
 
-constexpr int kTile = 128;       // keys a tile, rows a tile
+// A tile of rows has kTile of them too.
 constexpr int kProducer = 8, kIssuer = 9;  // warps; the issuer of stream 1: 10
-// How a call's rows lie on the tiles (see above).  kFew: kOne with at most 32
-// rows over an int8 cache: the warps whose rows are none turn codes instead.
-enum Mode { kPair, kOne, kFew };
+enum Mode { kPair, kOne };  // how a call's rows lie on the tiles (see above)
 // Registers a thread: 168 at launch (64,512 for 384 threads), or 128 (65,536 for
 // 512), moved to the softmax warps, which hold a row's 128 logits:
 // 256 * 208 + 128 * 88 = 64,512, or 256 * 184 + 256 * 72 = 65,536.
-constexpr int threads_of(bool i8, Mode mode) { return i8 && mode != kFew ? 512 : 384; }
+constexpr int threads_of(bool i8) { return i8 ? 512 : 384; }
 constexpr int softmax_regs(bool i8) { return i8 ? 184 : 208; }
 constexpr int other_regs(bool i8) { return i8 ? 72 : 88; }
-// Warps that turn int8 codes: two teams, one for the key tiles and one for the
-// value tiles.  The team of a warp (0 keys, 1 values, -1 none) and its place there.
-constexpr int team_warps(Mode mode) { return mode == kFew ? 4 : 2; }
-__device__ __forceinline__ int team_of(Mode mode, int warp, int &place) {
-    if (mode == kFew) {  // 1, 2, 3 and 10; 5, 6, 7 and 11
-        if (warp == 10 || warp == 11) {
-            place = 3;
-            return warp - 10;
-        }
-        place = (warp & 3) - 1;
-        return warp < 8 && place >= 0 ? warp >> 2 : -1;
-    }
-    place = warp & 1;
-    return warp >= 12 ? (warp - 12) >> 1 : -1;
-}
+// Warps that turn int8 codes: 12 and 13 the key tiles, 14 and 15 the value tiles.
+constexpr int kTeam = 12, kTeamWarps = 2;
 // A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
 // weights add up to more than kRaise raises m for the next one, and one above
 // kRedo is computed again (f16 holds weights up to 65,504).
 constexpr float kRaise = 256.0f, kRedo = 8192.0f;
 
-struct Dev {  // a launch's arguments
-    kvd_paged_cache c;
-    uint16_t *out;
-    int64_t out_stride;
-    int H, G, n_tokens, max_new, window;
-    const int32_t *starts;
-    float scale_log2;
+struct Dev : AttnArgs {
     int q_tokens;       // tokens of a row tile: 128 / G (kPair), or max_new
-    int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
-    int dead_row;       // a cache row outside the pool
-    int min_tiles;      // least key tiles a CTA takes
     float *acc;         // partial sums [2 * CTAs][rows / 32][D / 4][32][4]
     float2 *ml;         // their maxima and sums [2 * CTAs][rows]
     int4 *merge;        // [CTAs][2]: what merge_kernel joins
     int ws_rows;        // rows of a partial: 256 (PAIR) or fewer, a multiple of 32
 };
 
-// mbar_wait for the waits between the roles, in few instructions: the roles' hot
-// lines have to fit the instruction cache together, and a wait mostly ends in its
-// first try.  Warps call it whole, and all lanes get the same answer.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
-    uint32_t n = 0, t0 = 0;
-#pragma unroll 1
-    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
-        if ((++n & 63u) == 0) {
-            const uint32_t t = static_cast<uint32_t>(global_timer_ns());
-            if (n == 64) t0 = t;
-            if (__any_sync(0xffffffffu, *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs)))
-                return false;
-        }
-    }
-    return true;
-}
-
 // ---------------------------------------------------------------- items ---
-struct Seq {
-    int s0, n, len;  // first token, new tokens (at most max_new), length
-    int first;       // position of the first new token
-};
-
-__device__ __forceinline__ Seq seq_of(const Dev &a, int b, bool report) {
-    const int r0 = a.starts[b], r1 = a.starts[b + 1];
-    int len = a.c.seq_lens[b];
-    const int s0 = min(max(r0, 0), a.n_tokens);
-    const int s1 = min(max(r1, s0), a.n_tokens);
-    const int l = min(max(len, 0), a.c.len);
-    Seq s{s0, min(s1 - s0, a.max_new), l, l - (s1 - s0)};
-    if (report && (r0 != s0 || r1 != s1 || l != len || s1 - s0 > a.max_new || s.first < 0))
-        report_status(a.c.dev_status, KVD_ERR_INVALID);
-    return s;
-}
-
 struct Item {
     int i0, cnt;   // tokens of the sequence's new ones
     int lo, hi;    // keys [lo, hi) that any of them sees
@@ -191,52 +125,20 @@ __device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, S
     return true;
 }
 
-// Four int8 codes as two words of f16 or bf16, exactly.  f16: code + 128 in the
-// low bits of 1024 + x, less 1152.  bf16: 128 + (code's low 7 bits), less 128 or,
-// for a negative code, 256.
-template <bool BF16>
-__device__ __forceinline__ void codes_to(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (BF16) {
-        const uint32_t t0 = __byte_perm(w, 0, 0x4140), t1 = __byte_perm(w, 0, 0x4342);
-        auto sub = [](uint32_t t) {
-            const uint32_t x = (t & 0x007f007fu) | 0x43004300u, y = (t & 0x00800080u) | 0x43004300u;
-            const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&x),
-                                             *reinterpret_cast<const __nv_bfloat162 *>(&y));
-            return *reinterpret_cast<const uint32_t *>(&d);
-        };
-        lo = sub(t0);
-        hi = sub(t1);
-    } else {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t k1152 = 0x64806480u;
-        auto sub = [&](uint32_t x) {
-            const __half2 d = __hsub2(*reinterpret_cast<const __half2 *>(&x),
-                                      *reinterpret_cast<const __half2 *>(&k1152));
-            return *reinterpret_cast<const uint32_t *>(&d);
-        };
-        lo = sub(__byte_perm(u, 0x64646464u, 0x4140));
-        hi = sub(__byte_perm(u, 0x64646464u, 0x4342));
-    }
-}
-
 // ------------------------------------------------------------ the kernel ---
 template <int D, Mode MODE, bool I8>
 struct Shape {
     static constexpr bool PAIR = MODE == kPair;
     static constexpr int kTileBytes = kTile * D * 2;
-    // Rows kept of a row tile and its join buffer.  kFew: the tensor core still
-    // reads 128 rows, the others from whatever lies behind: rows that are none.
-    static constexpr int kRows = MODE == kFew ? 32 : kTile;
-    static constexpr int kQHalf = kRows * 128;
+    static constexpr int kQHalf = kTile * 128;  // 64 channels of a row tile
     static constexpr int kQTile = kQHalf * (D / 64);
     static constexpr int kQBytes = (PAIR ? 2 : 1) * kQTile;
-    static constexpr int kJoinBytes = PAIR ? 0 : kRows * 64 * 4;  // 64 channels of a stream's O
-    static constexpr int kStages =
-        I8 ? (D == 128 ? (MODE == kFew ? 4 : 3) : 6) : (D == 128 ? 5 : 8);
+    static constexpr int kJoinBytes = PAIR ? 0 : kTile * 64 * 4;  // 64 channels of a stream's O
+    static constexpr int kStages = I8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
     // int8: tiles as loaded (codes, then the rows' key and value scales with keys),
     // and the scales the softmax takes, for more key tiles than the ring lets the
     // loads run ahead of it
-    static constexpr int kRaw = !I8 ? 0 : D == 128 ? (MODE == kFew ? 4 : 3) : 6;
+    static constexpr int kRaw = !I8 ? 0 : D == 128 ? 3 : 6;
     static constexpr int kRawBytes = kTile * (D + 8);
     static constexpr int kScales = D == 128 ? 4 : 8;
     static constexpr int kScaleBytes = I8 ? kScales * 2 * kTile * 4 : 0;
@@ -252,13 +154,12 @@ struct Bars {
 };
 
 template <bool BF16, int D, Mode MODE, bool I8>
-__global__ void __launch_bounds__(threads_of(I8, MODE), 1)
+__global__ void __launch_bounds__(threads_of(I8), 1)
 attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q_map,
             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using Sh = Shape<D, MODE, I8>;
-    constexpr bool PAIR = MODE == kPair, FEW = MODE == kFew;
-    constexpr int kThreads = threads_of(I8, MODE);
-    constexpr int kRowWarps = FEW ? 1 : 4;  // softmax warps of a stream
+    constexpr bool PAIR = MODE == kPair;
+    constexpr int kThreads = threads_of(I8);
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
     constexpr int kStages = Sh::kStages;
@@ -292,22 +193,22 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.q_full[i], 1);
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], kRowWarps);
+            mbar_init(&bar.p_full[i], 4);
             mbar_init(&bar.o_full[i], 1);
             mbar_init(&bar.turn[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.kv_full[i], I8 ? team_warps(MODE) : 1);
+            mbar_init(&bar.kv_full[i], I8 ? kTeamWarps : 1);
             mbar_init(&bar.kv_empty[i], PAIR ? 2 : 1);  // the streams that use a tile
         }
         for (int i = 0; i < Sh::kRaw; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], team_warps(MODE));
+            mbar_init(&bar.raw_empty[i], kTeamWarps);
         }
         mbar_init(&bar.q_empty, PAIR ? 2 : 1);  // the warps that issue products
         mbar_init(&bar.done, PAIR ? 2 : 1);
-        mbar_init(&bar.join_full, kRowWarps);
-        mbar_init(&bar.join_empty, kRowWarps);
+        mbar_init(&bar.join_full, 4);
+        mbar_init(&bar.join_empty, 4);
         fence_barrier_init();
         abort_flag = 0;
         start.left = 0;
@@ -444,9 +345,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         }
     };
 
-    if (FEW ? warp != 0 && warp != 4 : warp >= kProducer) {
-        if constexpr (!FEW)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
+    if (warp >= kProducer) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
         if (warp == kProducer) {
         // ------------------------------------------------------- loads ---
         const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
@@ -729,17 +629,16 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             volatile int none = 0;
             if (!mbar_wait(&bar.done, 0, &none)) fail();
         }
-        int place = 0;
-        const int team = I8 ? team_of(MODE, warp, place) : -1;
-        if (I8 && team >= 0) {
+        if (I8 && warp >= kTeam) {
+            const int team = (warp - kTeam) / kTeamWarps, place = (warp - kTeam) % kTeamWarps;
             // --------------------------------------------- int8 to f16 or bf16 ---
             // Codes are whole numbers up to 127, exact in either type; the scales
             // go to the softmax, so the products lose nothing.
-            constexpr int kTeam = 32 * team_warps(MODE);
+            constexpr int kTeamThreads = 32 * kTeamWarps;
             constexpr uint32_t kRaw = I8 ? Sh::kRaw : 1;
             constexpr int kUnits = D / 16;                  // 16-code steps a row
             constexpr int kWarpRows = 32 / kUnits;          // rows a warp's step takes
-            constexpr int kSteps = kTile / (kWarpRows * team_warps(MODE));
+            constexpr int kSteps = kTile / (kWarpRows * kTeamWarps);
             // This lane's row and 16 codes of a step.  The 8 lanes of a load or a
             // store lie on two rows: at D = 128 on the one's first half and the
             // other's second, so that the codes come from all banks; and as the
@@ -753,7 +652,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             const int dst_row = (my_u / 4) * kHalfBytes + my_row * 128;
             const int dst0 = dst_row + 16 * (((my_u % 4) * 2) ^ (my_row & 7));
             const int dst1 = dst_row + 16 * (((my_u % 4) * 2 + 1) ^ (my_row & 7));
-            constexpr int kStepRows = kWarpRows * team_warps(MODE);  // a multiple of 8
+            constexpr int kStepRows = kWarpRows * kTeamWarps;  // a multiple of 8
             static_assert(kStepRows % 8 == 0, "the swizzle of a lane's row stays");
             const int ct = place * 32 + lane;
             uint32_t n = 0, keys = 0;  // tiles and key tiles so far, the other team's too
@@ -782,7 +681,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 const float unit = __int_as_float((127 - exp_now) << 23);
                 float *to = scales + keys % Sh::kScales * (2 * kTile);
 #pragma unroll
-                for (int at = ct; at < kTile; at += kTeam) {
+                for (int at = ct; at < kTile; at += kTeamThreads) {
                     float ks = sc[at] * a.scale_log2, vs = sc[kTile + at] * unit;
                     if (edge && dead(at)) ks = vs = 0.0f;
                     to[at] = ks;
@@ -838,8 +737,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             if (!ok) fail();
         }
     } else {
-        if constexpr (!FEW)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(softmax_regs(I8)));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(softmax_regs(I8)));
         // ------------------------------------------------------ softmax ---
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = tmem + ((warp & 3) << 21);  // this warp's 32 lanes
@@ -1108,14 +1006,14 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                             if (warp_live)
 #pragma unroll
                                 for (int c = 0; c < 32; ++c)
-                                    join[((i & 1) * 32 + c) * Sh::kRows + row] =
+                                    join[((i & 1) * 32 + c) * kTile + row] =
                                         I8 ? o[c] * unit : o[c];
                             continue;
                         }
                         if (warp_live)
 #pragma unroll
                             for (int c = 0; c < 32; ++c) {
-                                const float u = join[((i & 1) * 32 + c) * Sh::kRows + row];
+                                const float u = join[((i & 1) * 32 + c) * kTile + row];
                                 o[c] = (mine != 0.0f ? o[c] * mine : 0.0f) +
                                        (other != 0.0f ? u * other : 0.0f);
                             }
@@ -1206,38 +1104,6 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Dev 
 }
 
 // ----------------------------------------------------------------- launch ---
-using EncodeTiled = decltype(&cuTensorMapEncodeTiled);
-
-// The driver's encoder of tensor maps, asked of the runtime once.
-EncodeTiled encoder() {
-    static std::atomic<void *> fn{nullptr};
-    void *p = fn.load(std::memory_order_relaxed);
-    if (!p) {
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess)
-            return nullptr;
-        fn.store(p, std::memory_order_relaxed);
-    }
-    return reinterpret_cast<EncodeTiled>(p);
-}
-
-bool make_map(CUtensorMap *m, int kv_dtype, const void *base, int rank, const cuuint64_t *dims,
-              const cuuint64_t *strides, const cuuint32_t *box) {
-    const EncodeTiled enc = encoder();
-    const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const CUtensorMapDataType type = kv_dtype == KVD_INT8   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : kv_dtype == KVD_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    return enc && enc(m, type, rank, const_cast<void *>(base), dims, strides, box, ones,
-                      CU_TENSOR_MAP_INTERLEAVE_NONE,
-                      kv_dtype == KVD_INT8 ? CU_TENSOR_MAP_SWIZZLE_NONE
-                                           : CU_TENSOR_MAP_SWIZZLE_128B,
-                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 struct WsPlan {
     int ctas, rows;
     bool pair;
@@ -1250,8 +1116,8 @@ WsPlan ws_plan(int G, int D, int max_new) {
     w.pair = max_new > kTile / G;
     w.rows = w.pair ? 2 * kTile : (max_new * G + 31) / 32 * 32;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    w.merge = 0;
-    w.ml = up(static_cast<size_t>(w.ctas) * 2 * sizeof(int4));
+    w.merge = paged_counter_bytes();
+    w.ml = w.merge + up(static_cast<size_t>(w.ctas) * 2 * sizeof(int4));
     w.acc = w.ml + up(static_cast<size_t>(w.ctas) * 2 * w.rows * sizeof(float2));
     w.total = w.acc + up(static_cast<size_t>(w.ctas) * 2 * w.rows * D * sizeof(float));
     return w;
@@ -1259,23 +1125,13 @@ WsPlan ws_plan(int G, int D, int max_new) {
 
 template <bool BF16, int D, Mode MODE, bool I8>
 cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
-    const kvd_paged_cache &c = p.c;
     Dev a = {};
-    a.c = c;
-    a.out = static_cast<uint16_t *>(p.out);
-    a.out_stride = p.out_stride;
-    a.H = p.H;
-    a.G = p.G;
-    a.n_tokens = p.n_tokens;
-    a.max_new = p.max_new;
-    a.window = p.window;
-    a.starts = p.starts;
-    a.scale_log2 = p.scale_log2;
     a.q_tokens = MODE == kPair ? kTile / p.G : p.max_new;
-    a.box = 16;
-    while (a.box < kTile && c.page_size % (2 * a.box) == 0) a.box *= 2;
-    const int64_t rows = static_cast<int64_t>(c.n_pages) * c.n_kv_heads * c.page_size;
-    a.dead_row = static_cast<int>(rows);
+    CUtensorMap q_map, k_map, v_map;
+    constexpr CUtensorMapSwizzle kv_swizzle =
+        I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!fill_launch(p, a.q_tokens, kv_swizzle, kv_swizzle, a, q_map, k_map, v_map))
+        return cudaErrorInvalidValue;
     a.min_tiles = 2;
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.merge = reinterpret_cast<int4 *>(base + w.merge);
@@ -1283,25 +1139,8 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
     a.acc = reinterpret_cast<float *>(base + w.acc);
     a.ws_rows = w.rows;
 
-    CUtensorMap q_map, k_map, v_map;
-    const cuuint64_t qd[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(p.G),
-                              static_cast<cuuint64_t>(c.n_kv_heads),
-                              static_cast<cuuint64_t>(p.n_tokens)};
-    const cuuint64_t qs[3] = {static_cast<cuuint64_t>(D) * 2,
-                              static_cast<cuuint64_t>(D) * 2 * p.G,
-                              static_cast<cuuint64_t>(p.q_stride) * 2};
-    const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(p.G), 1,
-                              static_cast<cuuint32_t>(a.q_tokens)};
-    const cuuint64_t kd[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t ks[1] = {static_cast<cuuint64_t>(D) * (I8 ? 1 : 2)};
-    const cuuint32_t kb[2] = {I8 ? D : 64, static_cast<cuuint32_t>(a.box)};
-    if (!make_map(&q_map, BF16 ? KVD_BF16 : KVD_F16, p.q, 4, qd, qs, qb) ||
-        !make_map(&k_map, c.dtype, c.k, 2, kd, ks, kb) ||
-        !make_map(&v_map, c.dtype, c.v, 2, kd, ks, kb))
-        return cudaErrorInvalidValue;
-
     constexpr size_t smem = Shape<D, MODE, I8>::kSmem;
-    constexpr int threads = threads_of(I8, MODE);
+    constexpr int threads = threads_of(I8);
     auto *kernel = attn_kernel<BF16, D, MODE, I8>;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads, smem);
     if (e != cudaSuccess) return e;
@@ -1314,8 +1153,6 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
 template <bool BF16, int D, bool I8>
 cudaError_t launch_mode(const PagedAttnArgs &p, const WsPlan &w, void *ws, cudaStream_t st) {
     if (w.pair) return launch_shape<BF16, D, kPair, I8>(p, w, ws, st);
-    if constexpr (I8)
-        if (w.rows <= 32) return launch_shape<BF16, D, kFew, I8>(p, w, ws, st);
     return launch_shape<BF16, D, kOne, I8>(p, w, ws, st);
 }
 
@@ -1334,8 +1171,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st)
     return a.bf16 ? launch_type<true, false>(a, ws, st) : launch_type<false, false>(a, ws, st);
 }
 
-size_t paged_attn_ws(const kvd_paged_cache &c, int H, int n_tokens, int max_new) {
-    (void)n_tokens;
+size_t paged_attn_ws(const kvd_paged_cache &c, int H, int max_new) {
     return ws_plan(H / c.n_kv_heads, c.head_dim, max_new).total;
 }
 

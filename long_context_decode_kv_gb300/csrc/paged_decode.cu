@@ -1,0 +1,866 @@
+// paged_decode.cu -- attention over a paged cache for few rows: single tokens and
+// short runs of new ones, whose query heads of one KV head number at most 32.
+//
+//   out = sum_t softmax(scale q . k_t)_t v_t,   p - window < t <= p
+//
+// Bound by the cache's bytes, so the keys take the tensor core's 128 lanes and the
+// rows its narrow side: S^T = K Q^T and O^T = V^T P^T cost a quarter to an eighth
+// of what row tiles would, and a thread holds one key's logits.  Its key and value
+// scales (int8) are then two numbers of its own, its exponentials as many as there
+// are rows, and the sums over keys stay apart until the end.
+//
+// One CTA per SM, persistent, the items (sequence, KV head) cut evenly as in
+// paged_attn.cu; an item that a cut divides is joined by the last of its CTAs to
+// arrive, from f32 partials.
+//
+// Roles: warps 0-3 softmax (thread = key); warps 4 and 5 load key and value tiles
+// by TMA, a ring each; warp 6 issues the products.  int8: warps 8-11 turn key
+// codes into f16 or bf16 whole numbers in tensor memory, where the product takes
+// its first operand from, and warps 12-15 value codes in shared memory.  Keys that
+// went through shared memory once more (64 KB of the tile's 200) would cost it
+// more time than HBM takes for the tile.
+//
+// The weights' reference m follows a row's maximum loosely: a weight that passes
+// 2^13 (rarely any; f16 holds 2^16) has the four warps find the maximum and
+// compute the tile again, as the first tile of an item does.
+#include "paged_attn_dev.cuh"
+
+namespace kvd {
+namespace {
+
+constexpr float kRedo = 8192.0f;  // above it a weight asks for a new reference
+
+struct DecodeArgs : AttnArgs {
+    uint32_t *arrived;  // [CTAs], zero between calls: pieces of the item that CTA c's last
+                        // segment begins
+    float2 *ml;         // [2 * CTAs][NR] references and sums of partials
+    float *acc;         // [2 * CTAs][NR][D]
+};
+
+// A CTA's walk along the line of items' key tiles.
+struct Place {
+    int b, head, off;
+    int left;  // tiles
+    Seq s;
+};
+struct Run {  // tiles [j0, j1) of an item, from its tile `off` on
+    int j0, j1, lo, hi, tiles, off;
+    int b, head;
+    Seq s;
+};
+
+__device__ __forceinline__ Run run_of(const AttnArgs &a, const Seq &s) {
+    Run r;
+    r.hi = max(s.first + s.n, 0);
+    r.lo = a.window > 0 ? min(max(s.first - a.window + 1, 0), r.hi) : 0;
+    r.j0 = r.lo / kTile;
+    r.tiles = max((r.hi + kTile - 1) / kTile - r.j0, 1);
+    return r;
+}
+
+// The next run of the walk, or false at its end.
+__device__ __forceinline__ bool next_run(const AttnArgs &a, Place &p, Run &r) {
+    if (p.left <= 0) return false;
+    r = run_of(a, p.s);
+    const int take = min(r.tiles - p.off, p.left);
+    r.off = p.off;
+    r.j0 += p.off;
+    r.j1 = r.j0 + take;
+    r.b = p.b;
+    r.head = p.head;
+    r.s = p.s;
+    p.left -= take;
+    p.off = 0;
+    if (p.left > 0 && ++p.head == a.c.n_kv_heads) {
+        p.head = 0;
+#pragma unroll 1
+        do {
+            if (++p.b >= a.c.batch) {
+                p.left = 0;
+                break;
+            }
+            p.s = seq_of(a, p.b, false);
+        } while (p.s.n == 0);
+    }
+    return true;
+}
+
+template <int D, int NR, bool I8>
+struct DecodeShape {
+    static constexpr int kTileBytes = kTile * D * 2;
+    static constexpr int kQHalf = NR * 128;            // 64 channels of the rows
+    static constexpr int kQBytes = kQHalf * (D / 64);
+    static constexpr int kPBytes = NR * 256;           // weights of a tile
+    // keys: as the product takes them, or (int8) codes and the rows' scales
+    static constexpr int kKeyBytes = I8 ? kTile * (D + 8) : kTileBytes;
+    static constexpr int kKeys = D == 128 ? (I8 ? 4 : 3) : 6;
+    static constexpr int kRawBytes = kTile * D;        // int8: value codes
+    static constexpr int kRaws = !I8 ? 0 : D == 128 ? 4 : 6;
+    static constexpr int kValues = D == 128 ? (I8 ? 2 : 3) : (I8 ? 4 : 6);
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kPBytes + kKeys * kKeyBytes +
+                                 kRaws * kRawBytes + kValues * kTileBytes;
+    static constexpr int kThreads = I8 ? 512 : 256;
+    static constexpr uint32_t kColumns = I8 ? 256 : 128;  // tensor memory: S, S, O; codes
+};
+
+struct DecodeBars {
+    uint64_t q_full, q_empty, key_full[6], key_empty[6], raw_full[6], raw_empty[6], value_full[6],
+        value_empty[6], turned_full[2], turned_empty[2], s_full[2], p_full[2], o_done[2], vote,
+        done;
+};
+
+template <bool BF16, int D, int NR, bool I8>
+__global__ void __launch_bounds__(DecodeShape<D, NR, I8>::kThreads, 1)
+decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant__ CUtensorMap q_map,
+                    const __grid_constant__ CUtensorMap k_map,
+                    const __grid_constant__ CUtensorMap v_map) {
+    using Sh = DecodeShape<D, NR, I8>;
+    constexpr int kHalves = D / 64;
+    constexpr int kHalfBytes = kTile * 128;
+    constexpr int kRaws = I8 ? Sh::kRaws : 1;
+
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ DecodeBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag, flag[2], last_piece;
+    __shared__ uint32_t dead_groups[16];  // per key tile: its 16-key groups on bad pages
+    __shared__ __align__(16) float m_s[NR], f_s[NR];  // references, and the factor to a new one
+    __shared__ float red[4][NR], sums[4][NR], top_scale[4];
+    __shared__ float unit_s[2];  // int8: O in units of unit_s[1]; value scales times unit_s[0]
+
+    uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    uint8_t *q_smem = smem;
+    uint8_t *p_smem = q_smem + Sh::kQBytes;
+    uint8_t *keys = p_smem + 2 * Sh::kPBytes;
+    uint8_t *raws = keys + Sh::kKeys * Sh::kKeyBytes;
+    uint8_t *values = raws + Sh::kRaws * Sh::kRawBytes;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 6) tmem_alloc(&tmem_slot, Sh::kColumns);
+    if (tid == 0) {
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < 6; ++i) {
+            mbar_init(&bar.key_full[i], 1);
+            // freed by the product, or (int8) by who reads codes and who reads scales
+            mbar_init(&bar.key_empty[i], I8 ? 8 : 1);
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 4);
+            mbar_init(&bar.value_full[i], I8 ? 4 : 1);
+            mbar_init(&bar.value_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.turned_full[i], 4);
+            mbar_init(&bar.turned_empty[i], 1);
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4);
+            mbar_init(&bar.o_done[i], 1);
+            flag[i] = 0;
+        }
+        mbar_init(&bar.vote, 4);
+        mbar_init(&bar.done, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+    }
+    // rows that are none: zero queries
+    for (int i = tid; i < Sh::kQBytes / 16; i += Sh::kThreads)
+        reinterpret_cast<uint4 *>(q_smem)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // ---- this CTA's piece of the line of key tiles, found by each warp
+    auto cost_of = [&](int b, bool report) -> int {
+        if (b >= a.c.batch) return 0;
+        const Seq s = seq_of(a, b, report);
+        return s.n > 0 ? run_of(a, s).tiles * a.c.n_kv_heads : 0;
+    };
+    auto scan = [&](int v) -> int {  // inclusive
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        return v;
+    };
+    const bool report = blockIdx.x == 0 && warp == 0;
+    int cost = cost_of(lane, report);
+    int upto = scan(cost);
+    int total = __shfl_sync(0xffffffffu, upto, 31);
+#pragma unroll 1
+    for (int b0 = 32; b0 < a.c.batch; b0 += 32)
+        total += __reduce_add_sync(0xffffffffu, cost_of(b0 + lane, report));
+    const int ctas = max(min(static_cast<int>(gridDim.x), total / a.min_tiles), 1);
+    const int share = total / ctas, spare = total % ctas;
+    auto cut = [&](int c) { return c * share + min(c, spare); };  // where CTA c begins
+    // the CTA that holds tile x
+    auto cta_of = [&](int x) {
+        const int big = spare * (share + 1);
+        return x < big ? x / (share + 1) : spare + (x - big) / max(share, 1);
+    };
+    Place w;
+    w.left = 0;
+    const int x0 = static_cast<int>(blockIdx.x) < ctas ? cut(blockIdx.x) : total;
+    if (static_cast<int>(blockIdx.x) < ctas && total > 0) {
+        int base = 0;
+#pragma unroll 1
+        for (int b0 = 0;; b0 += 32) {
+            if (b0 > 0) {
+                cost = cost_of(b0 + lane, false);
+                upto = scan(cost);
+            }
+            const uint32_t in =
+                __ballot_sync(0xffffffffu, cost > 0 && base + upto - cost <= x0 && x0 < base + upto);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                w.b = b0 + l;
+                const int r = x0 - base - __shfl_sync(0xffffffffu, upto - cost, l);
+                w.s = seq_of(a, w.b, false);
+                const int tiles = run_of(a, w.s).tiles;
+                w.head = r / tiles;
+                w.off = r - w.head * tiles;
+                w.left = cut(blockIdx.x + 1) - x0;
+                break;
+            }
+            base += __shfl_sync(0xffffffffu, upto, 31);
+            if (b0 + 32 >= a.c.batch) break;
+        }
+    }
+    const uint32_t tmem = tmem_slot;
+    volatile int *abort = &abort_flag;
+    auto fail = [&] {
+        *abort = 1;
+        report_status(a.c.dev_status, KVD_ERR_TIMEOUT);
+    };
+    Run g;
+    bool ok = true;
+    constexpr uint32_t kOColumn = 2 * NR, kCodeColumn = 128;
+
+    if (warp == 4 || warp == 5) {
+        // ------------------------------------------------------------ loads ---
+        const bool is_k = warp == 4;
+        const uint64_t policy = l2_policy_evict_first();
+        const int boxes = kTile / a.box, ps = a.c.page_size;
+        const int per_read = 32 / boxes;  // tiles whose rows one read of the page table gives
+        const int places = is_k ? Sh::kKeys : I8 ? kRaws : Sh::kValues;
+        const int place_bytes = is_k ? Sh::kKeyBytes : I8 ? Sh::kRawBytes : Sh::kTileBytes;
+        uint8_t *ring = is_k ? keys : I8 ? raws : values;
+        uint64_t *full = is_k ? bar.key_full : I8 ? bar.raw_full : bar.value_full;
+        uint64_t *empty = is_k ? bar.key_empty : I8 ? bar.raw_empty : bar.value_empty;
+        const CUtensorMap *map = is_k ? &k_map : &v_map;
+        uint32_t n = 0, st = 0, round = 0, q_phase = 0;
+#pragma unroll 1
+        for (bool first = true; ok && next_run(a, w, g); first = false) {
+            if (is_k) {
+                if (!first) {
+                    if (!(ok = wait_for(&bar.q_empty, q_phase, abort))) break;
+                    q_phase ^= 1;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.q_full, a.max_new * a.G * 128 * kHalves);
+                    for (int h = 0; h < kHalves; ++h)
+                        tma_load_4d(q_smem + h * Sh::kQHalf, &q_map, h * 64, 0, g.head, g.s.s0,
+                                    &bar.q_full);
+                }
+                __syncwarp();
+            }
+            // the cache rows of the boxes of tiles j, j + 1, .., a lane a box: dead_row
+            // where none is needed, -1 on a bad page
+            auto rows_of = [&](int j) -> int {
+                const int t0 = (j + lane / boxes) * kTile + lane % boxes * a.box;
+                if (t0 >= g.j1 * kTile || t0 >= g.hi || t0 + a.box <= g.lo) return a.dead_row;
+                const int col = t0 / ps;
+                const int page = checked_page(a.c, g.b, col);
+                return page < 0 ? -1 : (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
+            };
+            int rows = 0, rows_next = rows_of(g.j0);
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j) {
+                const int in = (j - g.j0) % per_read;
+                if (in == 0) {
+                    rows = rows_next;
+                    rows_next = rows_of(j + per_read);
+                }
+                int row = __shfl_sync(0xffffffffu, rows, in * boxes + lane % boxes);
+                const bool bad = row < 0;
+                if (bad) row = a.dead_row;
+                if (round > 0 && !(ok = wait_for(&empty[st], (round - 1) & 1, abort))) break;
+                int bytes = I8 ? kTile * D : Sh::kTileBytes;
+                const bool scales = I8 && is_k && lane < boxes && row != a.dead_row;
+                if (is_k) {
+                    const int k = a.box / 16;
+                    const uint32_t groups = __reduce_or_sync(
+                        0xffffffffu, bad ? ((1u << k) - 1) << (lane % boxes * k) : 0u);
+                    if (lane == 0) dead_groups[n & 15] = groups;
+                    if (I8) bytes += __popc(__ballot_sync(0xffffffffu, scales)) * a.box * 8;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                __syncwarp();
+                uint8_t *dst = ring + st * place_bytes;
+                if (lane < boxes) {
+                    if constexpr (I8) {
+                        tma_load_2d(dst + lane * a.box * D, map, 0, row, &full[st], policy);
+                        if (scales) {
+                            float *sc = reinterpret_cast<float *>(dst + kTile * D) + lane * a.box;
+                            tma_load_1d(sc, static_cast<const float *>(a.c.k_scale) + row,
+                                        a.box * 4, &full[st], policy);
+                            tma_load_1d(sc + kTile, static_cast<const float *>(a.c.v_scale) + row,
+                                        a.box * 4, &full[st], policy);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < kHalves; ++h)
+                            tma_load_2d(dst + h * kHalfBytes + lane * a.box * 128, map, h * 64, row,
+                                        &full[st], policy);
+                    }
+                }
+                ++n;
+                if (++st == static_cast<uint32_t>(places)) {
+                    st = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok) fail();
+        if (*abort) {
+            // nothing may land in shared memory after the CTA has gone
+            volatile int none = 0;
+            for (int i = 0; i < places; ++i) {
+                const uint32_t fills = round + (static_cast<uint32_t>(i) < st ? 1 : 0);
+                if (fills > 0) mbar_wait(&full[i], (fills - 1) & 1, &none);
+            }
+        }
+    } else if (warp == 6) {
+        // --------------------------------------------------------- products ---
+        constexpr uint32_t kIdS = mma_idesc(BF16, kTile, NR, false);
+        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, NR, false, true);
+        const uint32_t key_addr = smem_addr(keys), value_addr = smem_addr(values);
+        const uint32_t tmem_u = warp_uniform(tmem);
+        const uint32_t q = warp_uniform(desc_low(smem_addr(q_smem), 16));
+        uint32_t n = 0;                         // tiles whose O is issued
+        uint32_t k_st = 0, k_round = 0, v_st = 0, v_round = 0, q_phase = 0;
+#pragma unroll 1
+        while (ok && next_run(a, w, g)) {
+            if (!(ok = wait_for(&bar.q_full, q_phase, abort))) break;
+            q_phase ^= 1;
+            // step j: O of tile j, and S of tile j + 2
+#pragma unroll 1
+            for (int j = g.j0 - 2; ok && j < g.j1; ++j) {
+                const bool has_o = j >= g.j0, has_s = j + 2 < g.j1;
+                const uint32_t b = (n + (has_o ? 0 : j + 2 - g.j0)) & 1;  // buffers of j and j + 2
+                if (has_o) {
+                    if (!(ok = wait_for(&bar.value_full[v_st], v_round & 1, abort))) break;
+                    const int from = max(g.lo - j * kTile, 0), to = min(g.hi - j * kTile, kTile);
+                    if (!I8 && (from > 0 || to < kTile)) {
+                        // value rows that no token sees may hold NaN: clear them
+                        uint8_t *vs = values + v_st * Sh::kTileBytes;
+                        const int c = (from + (kTile - max(to, 0))) * 8 * kHalves;
+#pragma unroll 1
+                        for (int i = lane; i < c; i += 32) {
+                            int r = i / (8 * kHalves);
+                            if (r >= from) r += max(to, 0) - from;
+                            *reinterpret_cast<uint4 *>(vs + (i / 8) % kHalves * kHalfBytes +
+                                                       r * 128 + i % 8 * 16) =
+                                make_uint4(0, 0, 0, 0);
+                        }
+                        fence_proxy_async();
+                        __syncwarp();
+                    }
+                    if (!(ok = wait_for(&bar.p_full[b], (n >> 1) & 1, abort))) break;
+                    tmem_fence_after();
+                    const uint32_t v = warp_uniform(
+                        desc_low(value_addr + v_st * Sh::kTileBytes, D == 128 ? kHalfBytes : 0));
+                    const uint32_t p = warp_uniform(desc_low(smem_addr(p_smem) + b * Sh::kPBytes, 16));
+                    const uint32_t add = warp_uniform(j > g.j0);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < kTile / 16; ++i)
+                            mma_ss(tmem_u + kOColumn, smem_desc(v + i * (2048 / 16)),
+                                   smem_desc(p + ((i / 4) * (NR * 128) + (i % 4) * 32) / 16), kIdO,
+                                   i > 0 ? 1 : add);
+                        mma_commit(&bar.value_empty[v_st]);
+                        mma_commit(&bar.o_done[b]);
+                    }
+                    __syncwarp();
+                    ++n;
+                    if (++v_st == Sh::kValues) {
+                        v_st = 0;
+                        ++v_round;
+                    }
+                }
+                if (has_s) {
+                    uint32_t a_at, code = 0;
+                    if constexpr (I8) {
+                        // the codes' buffers alternate as S does
+                        const uint32_t c = n + (has_o ? 1 : j + 2 - g.j0);  // tile number
+                        if (!(ok = wait_for(&bar.turned_full[b], (c >> 1) & 1, abort))) break;
+                        tmem_fence_after();
+                        a_at = 0;
+                        code = warp_uniform(tmem_u + kCodeColumn + b * (D / 2));
+                    } else {
+                        if (!(ok = wait_for(&bar.key_full[k_st], k_round & 1, abort))) break;
+                        a_at = warp_uniform(desc_low(key_addr + k_st * Sh::kKeyBytes, 16));
+                    }
+                    const uint32_t s_at = warp_uniform(tmem_u + b * NR);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t in = (i % 4) * 32;
+                            const uint64_t qd = smem_desc(q + ((i / 4) * Sh::kQHalf + in) / 16);
+                            if constexpr (I8)
+                                mma_ts(s_at, code + i * 8, qd, kIdS, i > 0);
+                            else
+                                mma_ss(s_at, smem_desc(a_at + ((i / 4) * kHalfBytes + in) / 16), qd,
+                                       kIdS, i > 0);
+                        }
+                        mma_commit(&bar.s_full[b]);
+                        mma_commit(I8 ? &bar.turned_empty[b] : &bar.key_empty[k_st]);
+                        if (j + 3 == g.j1) mma_commit(&bar.q_empty);
+                    }
+                    __syncwarp();
+                    if (++k_st == Sh::kKeys) {
+                        k_st = 0;
+                        ++k_round;
+                    }
+                }
+            }
+        }
+        if (!ok) fail();
+        // every product and every barrier arrival is done before the CTA goes
+        if (elect_one()) mma_commit(&bar.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&bar.done, 0, &none)) fail();
+    } else if (I8 && warp >= 8 && warp < 12) {
+        // -------------------------------------- key codes to tensor memory ---
+        const int row = tid - 256;  // the key, and the lane
+        const uint32_t lanes = tmem + ((warp & 3) << 21) + kCodeColumn;
+        const int swizzle = D == 128 ? row & 7 : (row >> 1) & 3;
+        uint32_t n = 0, st = 0, round = 0;
+#pragma unroll 1
+        while (ok && next_run(a, w, g)) {
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j) {
+                if (!(ok = wait_for(&bar.key_full[st], round & 1, abort))) break;
+                if (n >= 2 && !(ok = wait_for(&bar.turned_empty[n & 1], ((n >> 1) - 1) & 1, abort)))
+                    break;
+                tmem_fence_after();
+                const uint8_t *src = keys + st * Sh::kKeyBytes + row * D;
+#pragma unroll 1
+                for (int c = 0; c < D / 16; c += 4) {
+                    uint32_t o[32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 x =
+                            *reinterpret_cast<const uint4 *>(src + ((c + i) ^ swizzle) * 16);
+                        codes_to<BF16>(x.x, o[8 * i], o[8 * i + 1]);
+                        codes_to<BF16>(x.y, o[8 * i + 2], o[8 * i + 3]);
+                        codes_to<BF16>(x.z, o[8 * i + 4], o[8 * i + 5]);
+                        codes_to<BF16>(x.w, o[8 * i + 6], o[8 * i + 7]);
+                    }
+                    tmem_st32(lanes + (n & 1) * (D / 2) + c * 8, o);
+                }
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.turned_full[n & 1]);
+                    mbar_arrive(&bar.key_empty[st]);
+                }
+                ++n;
+                if (++st == Sh::kKeys) {
+                    st = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok) fail();
+    } else if (I8 && warp >= 12) {
+        // ------------------------------------ value codes to shared memory ---
+        // A lane's row and 16 codes of a step: the 8 lanes of a load or a store lie
+        // on two rows, at D = 128 on the one's first half and the other's second, so
+        // that the codes come from all banks; and as the swizzle turns even chunks of
+        // an odd row into odd ones, the chunks go to all banks too.
+        constexpr int kUnits = D / 16;          // 16-code steps a row
+        constexpr int kRows = 32 / kUnits * 4;  // rows of a step of the four warps
+        constexpr int kSteps = kTile / kRows;
+        const int q8 = lane >> 3, k8 = lane & 7;
+        const int row = (warp - 12) * (32 / kUnits) +
+                        (D == 128 ? 2 * (q8 >> 1) + (k8 >> 2) : lane >> 2);
+        const int u = D == 128 ? (k8 & 3) + 4 * ((q8 & 1) ^ (k8 >> 2)) : lane & 3;
+        const int dst_row = (u / 4) * kHalfBytes + row * 128;
+        const int dst0 = dst_row + 16 * (((u % 4) * 2) ^ (row & 7));
+        const int dst1 = dst_row + 16 * (((u % 4) * 2 + 1) ^ (row & 7));
+        static_assert(kRows % 8 == 0, "the swizzle of a lane's row stays");
+        uint32_t st = 0, round = 0, v_st = 0, v_round = 0;
+#pragma unroll 1
+        while (ok && next_run(a, w, g)) {
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j) {
+                if (!(ok = wait_for(&bar.raw_full[st], round & 1, abort))) break;
+                if (v_round > 0 &&
+                    !(ok = wait_for(&bar.value_empty[v_st], (v_round - 1) & 1, abort)))
+                    break;
+                const uint8_t *src = raws + st * Sh::kRawBytes + row * D + 16 * u;
+                uint8_t *dst = values + v_st * Sh::kTileBytes;
+#pragma unroll 4
+                for (int i = 0; i < kSteps; ++i) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(src + i * (kRows * D));
+                    uint4 lo, hi;
+                    codes_to<BF16>(x.x, lo.x, lo.y);
+                    codes_to<BF16>(x.y, lo.z, lo.w);
+                    codes_to<BF16>(x.z, hi.x, hi.y);
+                    codes_to<BF16>(x.w, hi.z, hi.w);
+                    *reinterpret_cast<uint4 *>(dst + dst0 + i * (kRows * 128)) = lo;
+                    *reinterpret_cast<uint4 *>(dst + dst1 + i * (kRows * 128)) = hi;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&bar.value_full[v_st]);
+                    mbar_arrive(&bar.raw_empty[st]);
+                }
+                if (++st == static_cast<uint32_t>(kRaws)) {
+                    st = 0;
+                    ++round;
+                }
+                if (++v_st == Sh::kValues) {
+                    v_st = 0;
+                    ++v_round;
+                }
+            }
+        }
+        if (!ok) fail();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ softmax ---
+        const uint32_t lanes = tmem + (warp << 21);
+        const int key = tid;
+        uint32_t n = 0, votes = 0, st = 0;
+        int piece = 0;  // runs of this CTA so far
+        int x = x0;
+        // All four warps reach it; then each sees what the others wrote before.
+        auto meet = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.vote);
+            const bool r = wait_for(&bar.vote, votes & 1, abort);
+            ++votes;
+            return r;
+        };
+#pragma unroll 1
+        for (; ok && next_run(a, w, g); ++piece) {
+            const int rows = g.s.n * a.G;
+            const int p0 = g.s.first;  // the first token's position
+            // keys that every row sees
+            const int all_lo = a.window > 0 ? max(p0 + g.s.n - a.window, 0) : 0;
+            const int all_hi = max(p0 + 1, 0);
+            float l[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) l[r] = 0.0f;
+            if (tid < NR) m_s[tid] = -INFINITY;
+            float unit = 1.0f;  // int8: value scales are taken times it
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                if (!(ok = wait_for(&bar.s_full[b], (n >> 1) & 1, abort))) break;
+                tmem_fence_after();
+                const int t = j * kTile + key;
+                const uint32_t bad = dead_groups[n & 15] >> (key / 16) & 1;
+                const bool live = t >= g.lo && t < g.hi && !bad;
+                float ks = a.scale_log2, vs = 1.0f;
+                if constexpr (I8) {
+                    const float *sc =
+                        reinterpret_cast<const float *>(keys + st * Sh::kKeyBytes + kTile * D);
+                    ks = live ? sc[key] * a.scale_log2 : 0.0f;
+                    vs = live ? sc[kTile + key] : 0.0f;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.key_empty[st]);
+                    if (++st == Sh::kKeys) st = 0;
+                }
+                const bool edge = j * kTile < all_lo || (j + 1) * kTile > all_hi || bad;
+                // this key's logits, those of rows that do not see it at -infinity
+                float s[NR];
+                auto logits = [&] {
+#pragma unroll
+                    for (int i = 0; i < NR; i += 16) tmem_ld16(lanes + b * NR + i, s + i);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < NR; i += 16) pin16(s + i);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) s[r] *= ks;
+                    if (edge) {
+                        int tok = 0, in = 0;
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            const int p = p0 + tok;
+                            if (!live || t > p || (a.window > 0 && t <= p - a.window))
+                                s[r] = -INFINITY;
+                            if (++in == a.G) {
+                                in = 0;
+                                ++tok;
+                            }
+                        }
+                    }
+                };
+                logits();
+                // P's buffer: the product of two tiles ago is done
+                if (n >= 2 && !(ok = wait_for(&bar.o_done[b], ((n >> 1) - 1) & 1, abort))) break;
+                bool fix = j == g.j0;
+#pragma unroll 1
+                for (;;) {
+                    if (fix) {
+                        // each row's maximum, over the warp's keys, then over all
+                        float mine = -INFINITY;
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            const uint32_t k = __reduce_max_sync(0xffffffffu, float_to_key(s[r]));
+                            if (lane == r) mine = __uint_as_float(k);
+                        }
+                        if (lane < NR) red[warp][lane] = mine;
+                        if constexpr (I8) {
+                            const uint32_t v = __float_as_uint(vs);
+                            const uint32_t top =
+                                __reduce_max_sync(0xffffffffu, v < 0x7f800000u ? v : 0u);
+                            if (lane == 0) top_scale[warp] = __uint_as_float(top);
+                        }
+                        // O as it stands is complete
+                        if (j > g.j0 &&
+                            !(ok = wait_for(&bar.o_done[b ^ 1], ((n - 1) >> 1) & 1, abort)))
+                            break;
+                        if (!(ok = meet())) break;
+                        if constexpr (I8) {
+                            // a power of two near the largest value scale
+                            const float top = fmaxf(fmaxf(top_scale[0], top_scale[1]),
+                                                    fmaxf(top_scale[2], top_scale[3]));
+                            const int e = min(max((__float_as_int(top) >> 23 & 255) - 126, -100), 100);
+                            const float fresh = __int_as_float((127 - e) << 23);
+                            if (j == g.j0 || fresh < unit) unit = fresh;  // same in all threads
+                        }
+                        if (tid < NR) {
+                            uint32_t k = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                k = max(k, __float_as_uint(red[i][tid]));
+                            const float top = key_to_float(k);
+                            const float m = m_s[tid], mn = fmaxf(m, top);
+                            f_s[tid] = m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
+                            m_s[tid] = mn;
+                            if (tid == 0) {
+                                unit_s[1] = j == g.j0 ? 1.0f : unit / unit_s[0];
+                                unit_s[0] = unit;
+                            }
+                        }
+                        if (!(ok = meet())) break;
+                        const float fu = I8 ? unit_s[1] : 1.0f;
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) l[r] *= f_s[r];
+                        if (j > g.j0) {
+#pragma unroll 1
+                            for (int i = 0; i < NR; i += 16) {
+                                float o[16];
+                                tmem_ld16(lanes + kOColumn + i, o);
+                                tmem_wait_ld();
+                                pin16(o);
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) o[r] *= f_s[i + r] * fu;
+                                tmem_st16(lanes + kOColumn + i, reinterpret_cast<uint32_t *>(o));
+                            }
+                            tmem_wait_st();
+                            tmem_fence_before();
+                        }
+                    }
+                    const float v = I8 ? vs * unit : 1.0f;
+                    float top = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const float m = m_s[r];
+                        s[r] = exp2_approx(s[r] - (m == -INFINITY ? 0.0f : m));
+                        top = fmaxf(top, s[r]);
+                    }
+                    if (fix) break;  // no weight passes 1
+                    if (__any_sync(0xffffffffu, top > kRedo || (I8 && v > 4.0f)) && lane == 0)
+                        flag[votes & 1] = votes + 1;
+                    const uint32_t mine = votes;
+                    if (!(ok = meet())) break;
+                    if (*(volatile int *)&flag[mine & 1] != static_cast<int>(mine + 1)) break;
+                    fix = true;
+                    logits();
+                }
+                if (!ok) break;
+                // the weights, and P^T: row r's 128 keys in two swizzled halves
+                const float v = I8 ? vs * unit : 1.0f;
+                uint8_t *p = p_smem + b * Sh::kPBytes + (key / 64) * (NR * 128) + (key % 8) * 2;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    l[r] += s[r];
+                    const float x = I8 ? s[r] * v : s[r];
+                    *reinterpret_cast<uint16_t *>(p + r * 128 + (((key % 64) / 8) ^ (r & 7)) * 16) =
+                        static_cast<uint16_t>(pack2<BF16>(x, 0.0f));
+                }
+                fence_proxy_async();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[b]);
+            }
+            if (!ok) break;
+            // ---- the run's sums
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+            }
+            float mine = 0.0f;
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if (lane == r) mine = l[r];
+            if (lane < NR) sums[warp][lane] = mine;
+            if (!(ok = wait_for(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort))) break;
+            tmem_fence_after();
+            if (!(ok = meet())) break;
+            float sum = 0.0f, m = -INFINITY;  // of row `lane`
+            if (lane < NR) {
+                sum = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
+                m = m_s[lane];
+            }
+            float o[NR];
+#pragma unroll
+            for (int i = 0; i < NR; i += 16) tmem_ld16(lanes + kOColumn + i, o + i);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < NR; i += 16) pin16(o + i);
+            const bool channel = key < D;
+            const bool whole = g.off == 0 && g.j1 - g.j0 == g.tiles;
+            const float out_unit = I8 ? 1.0f / unit : 1.0f;  // a power of two
+            uint16_t *out = a.out + static_cast<int64_t>(g.s.s0) * a.out_stride +
+                            static_cast<int64_t>(g.head) * a.G * D + key;
+            const float inv = sum > 0.0f || sum != sum ? out_unit / sum : 0.0f;
+            const uint32_t slot = 2 * blockIdx.x + (piece == 0 ? 0 : 1);
+            auto write = [&](int r, float x) {  // channel `key` of row r
+                const int tok = r / a.G;
+                out[tok * a.out_stride + (r - tok * a.G) * D] =
+                    static_cast<uint16_t>(pack2<BF16>(x, 0.0f));
+            };
+            if (whole) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const float f = __shfl_sync(0xffffffffu, inv, r);
+                    if (channel && r < rows) write(r, f != 0.0f ? o[r] * f : 0.0f);
+                }
+            } else {
+                if (warp == 0 && lane < rows) a.ml[slot * NR + lane] = make_float2(m, sum);
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    if (channel && r < rows) a.acc[(slot * NR + r) * D + key] = o[r] * out_unit;
+                // the last of the item's CTAs to arrive joins them
+                const int begin = x - g.off, end = begin + g.tiles;
+                const int c0 = cta_of(begin), c1 = cta_of(end - 1);
+                __threadfence();
+                if (!(ok = meet())) break;
+                if (tid == 0) {
+                    const unsigned was = atomic_add_acq_rel_gpu(&a.arrived[c0], 1u);
+                    last_piece = was == static_cast<unsigned>(c1 - c0);
+                    if (last_piece) a.arrived[c0] = 0;
+                }
+                if (!(ok = meet())) break;
+                if (last_piece) {
+                    __threadfence();
+                    // CTA c0's piece is its last run, the others' their first
+                    const uint32_t first_slot = 2 * c0 + (cut(c0) < begin ? 1 : 0);
+#pragma unroll 1
+                    for (int r = 0; r < rows; ++r) {
+                        float top = -INFINITY;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c)
+                            top = fmaxf(top, __ldcg(&a.ml[(c == c0 ? first_slot : 2 * c) * NR + r]).x);
+                        float x = 0.0f, den = 0.0f;
+#pragma unroll 4
+                        for (int c = c0; c <= c1; ++c) {
+                            const uint32_t at = (c == c0 ? first_slot : 2 * c) * NR + r;
+                            const float2 ml = __ldcg(&a.ml[at]);
+                            const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
+                            den = fmaf(f, ml.y, den);
+                            if (channel && f != 0.0f) x = fmaf(f, __ldcg(&a.acc[at * D + key]), x);
+                        }
+                        if (channel) write(r, den > 0.0f || den != den ? x / den : 0.0f);
+                    }
+                }
+            }
+            x += g.j1 - g.j0;
+        }
+        if (!ok) fail();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 6) {
+        tmem_fence_after();
+        tmem_free(tmem, Sh::kColumns);
+    }
+}
+
+struct DecodePlan {
+    int ctas;
+    size_t ml, acc, total;
+};
+
+DecodePlan plan_of(int rows, int D) {
+    DecodePlan w;
+    w.ctas = device_sm_count();
+    const size_t nr = rows <= 16 ? 16 : 32;
+    w.ml = paged_counter_bytes();
+    w.acc = w.ml + (w.ctas * 2 * nr * sizeof(float2) + 255) / 256 * 256;
+    w.total = w.acc + (w.ctas * 2 * nr * D * sizeof(float) + 255) / 256 * 256;
+    return w;
+}
+
+template <bool BF16, int D, int NR, bool I8>
+cudaError_t launch_shape(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
+    using Sh = DecodeShape<D, NR, I8>;
+    DecodeArgs a = {};
+    CUtensorMap q_map, k_map, v_map;
+    constexpr CUtensorMapSwizzle k_swizzle = I8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                           : CU_TENSOR_MAP_SWIZZLE_128B;
+    constexpr CUtensorMapSwizzle v_swizzle =
+        I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
+    if (!fill_launch(p, p.max_new, k_swizzle, v_swizzle, a, q_map, k_map, v_map))
+        return cudaErrorInvalidValue;
+    const DecodePlan w = plan_of(p.max_new * p.G, D);
+    a.min_tiles = 2;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    a.arrived = reinterpret_cast<uint32_t *>(base);
+    a.ml = reinterpret_cast<float2 *>(base + w.ml);
+    a.acc = reinterpret_cast<float *>(base + w.acc);
+    auto *kernel = decode_paged_kernel<BF16, D, NR, I8>;
+    cudaError_t e =
+        prepare_kernel(reinterpret_cast<const void *>(kernel), Sh::kThreads, Sh::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(kernel, dim3(w.ctas), dim3(Sh::kThreads), Sh::kSmem, st, true, a, q_map, k_map,
+                     v_map);
+}
+
+template <bool BF16, bool I8>
+cudaError_t launch_type(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
+    const bool narrow = p.max_new * p.G <= 16;
+    if (p.c.head_dim == 64)
+        return narrow ? launch_shape<BF16, 64, 16, I8>(p, ws, st)
+                      : launch_shape<BF16, 64, 32, I8>(p, ws, st);
+    return narrow ? launch_shape<BF16, 128, 16, I8>(p, ws, st)
+                  : launch_shape<BF16, 128, 32, I8>(p, ws, st);
+}
+
+}  // namespace
+
+size_t paged_counter_bytes() {
+    return (device_sm_count() * sizeof(uint32_t) + 255) / 256 * 256;
+}
+
+size_t paged_decode_ws(int rows, int D) { return plan_of(rows, D).total; }
+
+cudaError_t launch_paged_decode(const PagedAttnArgs &a, void *ws, cudaStream_t st) {
+    if (a.c.dtype == KVD_INT8)
+        return a.bf16 ? launch_type<true, true>(a, ws, st) : launch_type<false, true>(a, ws, st);
+    return a.bf16 ? launch_type<true, false>(a, ws, st) : launch_type<false, false>(a, ws, st);
+}
+
+}  // namespace kvd

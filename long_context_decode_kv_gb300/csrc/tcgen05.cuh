@@ -79,10 +79,11 @@ __device__ __forceinline__ uint32_t warp_uniform(uint32_t v) {
     return __shfl_sync(0xffffffffu, v, 0);
 }
 
-// Instruction descriptor: f32 accumulator, A and B both f16 or both bf16,
-// m x n, B K-major or MN-major (A K-major or in tensor memory).
-constexpr uint32_t mma_idesc(bool bf16, int m, int n, bool b_mn) {
-    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (b_mn ? 1u << 16 : 0u) |
+// Instruction descriptor: f32 accumulator, A and B both f16 or both bf16, m x n,
+// either K-major or MN-major (A in tensor memory: K-major).
+constexpr uint32_t mma_idesc(bool bf16, int m, int n, bool b_mn, bool a_mn = false) {
+    return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) |
+           (b_mn ? 1u << 16 : 0u) |
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
@@ -150,6 +151,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r) {
         "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
         "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r) {
+    tmem_st16(addr, r);
+    tmem_st16(addr + 16, r + 16);
 }
 
 // Tiled TMA loads global -> shared.  x counts elements and x times the element
