@@ -14,11 +14,13 @@
 // arrive, from f32 partials.
 //
 // Roles: warps 0-3 softmax (thread = key); warps 4 and 5 load key and value tiles
-// by TMA, a ring each; warp 6 issues the products.  int8: warps 8-11 turn key
-// codes into f16 or bf16 whole numbers in tensor memory, where the product takes
-// its first operand from, and warps 12-15 value codes in shared memory.  Keys that
-// went through shared memory once more (64 KB of the tile's 200) would cost it
-// more time than HBM takes for the tile.
+// by TMA, a ring each; warps 6 and 7 issue the two products.  int8: warps 8-11
+// turn key codes into f16 or bf16 whole numbers in tensor memory, where the
+// product takes its first operand from, and warps 12-15 value codes in shared
+// memory.  Keys that went through shared memory once more (64 KB of the tile's
+// 200) would cost it more time than HBM takes for the tile.  The scales are read
+// by the warps that turn the keys: as copies of a page's 16 to 128 numbers they
+// would keep the loading warp longer than the codes do.
 //
 // The weights' reference m follows a row's maximum loosely: a weight that passes
 // 2^13 (rarely any; f16 holds 2^16) has the four warps find the maximum and
@@ -29,6 +31,19 @@ namespace kvd {
 namespace {
 
 constexpr float kRedo = 8192.0f;  // above it a weight asks for a new reference
+
+// Barriers of the 128 softmax threads; the second tells whether any said yes.
+__device__ __forceinline__ void meet_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool any_of_128(bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(mine))
+        : "memory");
+    return r != 0;
+}
 
 struct DecodeArgs : AttnArgs {
     uint32_t *arrived;  // [CTAs], zero between calls: pieces of the item that CTA c's last
@@ -91,8 +106,8 @@ struct DecodeShape {
     static constexpr int kQHalf = NR * 128;            // 64 channels of the rows
     static constexpr int kQBytes = kQHalf * (D / 64);
     static constexpr int kPBytes = NR * 256;           // weights of a tile
-    // keys: as the product takes them, or (int8) codes and the rows' scales
-    static constexpr int kKeyBytes = I8 ? kTile * (D + 8) : kTileBytes;
+    // keys: as the product takes them, or (int8) codes
+    static constexpr int kKeyBytes = I8 ? kTile * D : kTileBytes;
     static constexpr int kKeys = D == 128 ? (I8 ? 4 : 3) : 6;
     static constexpr int kRawBytes = kTile * D;        // int8: value codes
     static constexpr int kRaws = !I8 ? 0 : D == 128 ? 4 : 6;
@@ -105,7 +120,7 @@ struct DecodeShape {
 
 struct DecodeBars {
     uint64_t q_full, q_empty, key_full[6], key_empty[6], raw_full[6], raw_empty[6], value_full[6],
-        value_empty[6], turned_full[2], turned_empty[2], s_full[2], p_full[2], o_done[2], vote,
+        value_empty[6], turned_full[2], turned_empty[2], s_full[2], p_full[2], o_done[2],
         done;
 };
 
@@ -122,9 +137,11 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
     extern __shared__ uint8_t raw_smem[];
     __shared__ DecodeBars bar;
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag, flag[2], last_piece;
+    __shared__ int abort_flag, last_piece;
     __shared__ uint32_t dead_groups[16];  // per key tile: its 16-key groups on bad pages
-    __shared__ __align__(16) float m_s[NR], f_s[NR];  // references, and the factor to a new one
+    __shared__ int tile_rows[16][8];      // int8, per key tile: its boxes' cache rows
+    __shared__ float2 scales[I8 ? 4 : 1][kTile];  // and its keys' scales of keys and values
+    __shared__ __align__(16) float m_s[NR], base_s[NR], f_s[NR];  // references, less or 0, to a new one
     __shared__ float red[4][NR], sums[4][NR], top_scale[4];
     __shared__ float unit_s[2];  // int8: O in units of unit_s[1]; value scales times unit_s[0]
 
@@ -142,8 +159,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
         mbar_init(&bar.q_empty, 1);
         for (int i = 0; i < 6; ++i) {
             mbar_init(&bar.key_full[i], 1);
-            // freed by the product, or (int8) by who reads codes and who reads scales
-            mbar_init(&bar.key_empty[i], I8 ? 8 : 1);
+            mbar_init(&bar.key_empty[i], I8 ? 4 : 1);  // by the product, or who reads codes
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], 4);
             mbar_init(&bar.value_full[i], I8 ? 4 : 1);
@@ -155,10 +171,8 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 4);
             mbar_init(&bar.o_done[i], 1);
-            flag[i] = 0;
         }
-        mbar_init(&bar.vote, 4);
-        mbar_init(&bar.done, 1);
+        mbar_init(&bar.done, 2);
         fence_barrier_init();
         abort_flag = 0;
     }
@@ -288,28 +302,20 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                 const bool bad = row < 0;
                 if (bad) row = a.dead_row;
                 if (round > 0 && !(ok = wait_for(&empty[st], (round - 1) & 1, abort))) break;
-                int bytes = I8 ? kTile * D : Sh::kTileBytes;
-                const bool scales = I8 && is_k && lane < boxes && row != a.dead_row;
                 if (is_k) {
                     const int k = a.box / 16;
                     const uint32_t groups = __reduce_or_sync(
                         0xffffffffu, bad ? ((1u << k) - 1) << (lane % boxes * k) : 0u);
                     if (lane == 0) dead_groups[n & 15] = groups;
-                    if (I8) bytes += __popc(__ballot_sync(0xffffffffu, scales)) * a.box * 8;
+                    if (I8 && lane < boxes) tile_rows[n & 15][lane] = row;
+                    __syncwarp();
                 }
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], bytes);
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], I8 ? kTile * D : Sh::kTileBytes);
                 __syncwarp();
                 uint8_t *dst = ring + st * place_bytes;
                 if (lane < boxes) {
                     if constexpr (I8) {
                         tma_load_2d(dst + lane * a.box * D, map, 0, row, &full[st], policy);
-                        if (scales) {
-                            float *sc = reinterpret_cast<float *>(dst + kTile * D) + lane * a.box;
-                            tma_load_1d(sc, static_cast<const float *>(a.c.k_scale) + row,
-                                        a.box * 4, &full[st], policy);
-                            tma_load_1d(sc + kTile, static_cast<const float *>(a.c.v_scale) + row,
-                                        a.box * 4, &full[st], policy);
-                        }
                     } else {
 #pragma unroll
                         for (int h = 0; h < kHalves; ++h)
@@ -334,102 +340,111 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             }
         }
     } else if (warp == 6) {
-        // --------------------------------------------------------- products ---
+        // ------------------------------------------------- products S^T = K Q^T ---
         constexpr uint32_t kIdS = mma_idesc(BF16, kTile, NR, false);
-        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, NR, false, true);
-        const uint32_t key_addr = smem_addr(keys), value_addr = smem_addr(values);
+        const uint32_t key_addr = smem_addr(keys);
         const uint32_t tmem_u = warp_uniform(tmem);
         const uint32_t q = warp_uniform(desc_low(smem_addr(q_smem), 16));
-        uint32_t n = 0;                         // tiles whose O is issued
-        uint32_t k_st = 0, k_round = 0, v_st = 0, v_round = 0, q_phase = 0;
+        uint32_t n = 0, st = 0, round = 0, q_phase = 0;
 #pragma unroll 1
         while (ok && next_run(a, w, g)) {
             if (!(ok = wait_for(&bar.q_full, q_phase, abort))) break;
             q_phase ^= 1;
-            // step j: O of tile j, and S of tile j + 2
 #pragma unroll 1
-            for (int j = g.j0 - 2; ok && j < g.j1; ++j) {
-                const bool has_o = j >= g.j0, has_s = j + 2 < g.j1;
-                const uint32_t b = (n + (has_o ? 0 : j + 2 - g.j0)) & 1;  // buffers of j and j + 2
-                if (has_o) {
-                    if (!(ok = wait_for(&bar.value_full[v_st], v_round & 1, abort))) break;
-                    const int from = max(g.lo - j * kTile, 0), to = min(g.hi - j * kTile, kTile);
-                    if (!I8 && (from > 0 || to < kTile)) {
-                        // value rows that no token sees may hold NaN: clear them
-                        uint8_t *vs = values + v_st * Sh::kTileBytes;
-                        const int c = (from + (kTile - max(to, 0))) * 8 * kHalves;
-#pragma unroll 1
-                        for (int i = lane; i < c; i += 32) {
-                            int r = i / (8 * kHalves);
-                            if (r >= from) r += max(to, 0) - from;
-                            *reinterpret_cast<uint4 *>(vs + (i / 8) % kHalves * kHalfBytes +
-                                                       r * 128 + i % 8 * 16) =
-                                make_uint4(0, 0, 0, 0);
-                        }
-                        fence_proxy_async();
-                        __syncwarp();
-                    }
-                    if (!(ok = wait_for(&bar.p_full[b], (n >> 1) & 1, abort))) break;
-                    tmem_fence_after();
-                    const uint32_t v = warp_uniform(
-                        desc_low(value_addr + v_st * Sh::kTileBytes, D == 128 ? kHalfBytes : 0));
-                    const uint32_t p = warp_uniform(desc_low(smem_addr(p_smem) + b * Sh::kPBytes, 16));
-                    const uint32_t add = warp_uniform(j > g.j0);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int i = 0; i < kTile / 16; ++i)
-                            mma_ss(tmem_u + kOColumn, smem_desc(v + i * (2048 / 16)),
-                                   smem_desc(p + ((i / 4) * (NR * 128) + (i % 4) * 32) / 16), kIdO,
-                                   i > 0 ? 1 : add);
-                        mma_commit(&bar.value_empty[v_st]);
-                        mma_commit(&bar.o_done[b]);
-                    }
-                    __syncwarp();
-                    ++n;
-                    if (++v_st == Sh::kValues) {
-                        v_st = 0;
-                        ++v_round;
-                    }
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                uint32_t k_at = 0, code = 0;
+                if constexpr (I8) {
+                    if (!(ok = wait_for(&bar.turned_full[b], (n >> 1) & 1, abort))) break;
+                    code = warp_uniform(tmem_u + kCodeColumn + b * (D / 2));
+                } else {
+                    if (!(ok = wait_for(&bar.key_full[st], round & 1, abort))) break;
+                    k_at = warp_uniform(desc_low(key_addr + st * Sh::kKeyBytes, 16));
                 }
-                if (has_s) {
-                    uint32_t a_at, code = 0;
-                    if constexpr (I8) {
-                        // the codes' buffers alternate as S does
-                        const uint32_t c = n + (has_o ? 1 : j + 2 - g.j0);  // tile number
-                        if (!(ok = wait_for(&bar.turned_full[b], (c >> 1) & 1, abort))) break;
-                        tmem_fence_after();
-                        a_at = 0;
-                        code = warp_uniform(tmem_u + kCodeColumn + b * (D / 2));
-                    } else {
-                        if (!(ok = wait_for(&bar.key_full[k_st], k_round & 1, abort))) break;
-                        a_at = warp_uniform(desc_low(key_addr + k_st * Sh::kKeyBytes, 16));
-                    }
-                    const uint32_t s_at = warp_uniform(tmem_u + b * NR);
-                    if (elect_one()) {
+                // the logits of two tiles ago have been read, and their weights: what
+                // the softmax needs to know to overwrite P comes with S
+                if (n >= 2 && !(ok = wait_for(&bar.o_done[b], ((n >> 1) - 1) & 1, abort))) break;
+                tmem_fence_after();
+                const uint32_t s_at = warp_uniform(tmem_u + b * NR);
+                if (elect_one()) {
 #pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t in = (i % 4) * 32;
-                            const uint64_t qd = smem_desc(q + ((i / 4) * Sh::kQHalf + in) / 16);
-                            if constexpr (I8)
-                                mma_ts(s_at, code + i * 8, qd, kIdS, i > 0);
-                            else
-                                mma_ss(s_at, smem_desc(a_at + ((i / 4) * kHalfBytes + in) / 16), qd,
-                                       kIdS, i > 0);
-                        }
-                        mma_commit(&bar.s_full[b]);
-                        mma_commit(I8 ? &bar.turned_empty[b] : &bar.key_empty[k_st]);
-                        if (j + 3 == g.j1) mma_commit(&bar.q_empty);
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t in = (i % 4) * 32;
+                        const uint64_t qd = smem_desc(q + ((i / 4) * Sh::kQHalf + in) / 16);
+                        if constexpr (I8)
+                            mma_ts(s_at, code + i * 8, qd, kIdS, i > 0);
+                        else
+                            mma_ss(s_at, smem_desc(k_at + ((i / 4) * kHalfBytes + in) / 16), qd,
+                                   kIdS, i > 0);
                     }
-                    __syncwarp();
-                    if (++k_st == Sh::kKeys) {
-                        k_st = 0;
-                        ++k_round;
-                    }
+                    mma_commit(&bar.s_full[b]);
+                    mma_commit(I8 ? &bar.turned_empty[b] : &bar.key_empty[st]);
+                    if (j + 1 == g.j1) mma_commit(&bar.q_empty);
+                }
+                __syncwarp();
+                if (++st == Sh::kKeys) {
+                    st = 0;
+                    ++round;
                 }
             }
         }
         if (!ok) fail();
         // every product and every barrier arrival is done before the CTA goes
+        if (elect_one()) mma_commit(&bar.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&bar.done, 0, &none)) fail();
+    } else if (warp == 7) {
+        // ---------------------------------------------- products O^T += V^T P^T ---
+        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, NR, false, true);
+        const uint32_t value_addr = smem_addr(values);
+        const uint32_t tmem_u = warp_uniform(tmem);
+        uint32_t n = 0, st = 0, round = 0;
+#pragma unroll 1
+        while (ok && next_run(a, w, g)) {
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                if (!(ok = wait_for(&bar.value_full[st], round & 1, abort))) break;
+                const int from = max(g.lo - j * kTile, 0), to = min(g.hi - j * kTile, kTile);
+                if (!I8 && (from > 0 || to < kTile)) {
+                    // value rows that no token sees may hold NaN: clear them
+                    uint8_t *vs = values + st * Sh::kTileBytes;
+                    const int c = (from + (kTile - max(to, 0))) * 8 * kHalves;
+#pragma unroll 1
+                    for (int i = lane; i < c; i += 32) {
+                        int r = i / (8 * kHalves);
+                        if (r >= from) r += max(to, 0) - from;
+                        *reinterpret_cast<uint4 *>(vs + (i / 8) % kHalves * kHalfBytes + r * 128 +
+                                                   i % 8 * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                if (!(ok = wait_for(&bar.p_full[b], (n >> 1) & 1, abort))) break;
+                tmem_fence_after();
+                // at D = 64 lanes 64 to 127 repeat the others
+                const uint32_t v = warp_uniform(
+                    desc_low(value_addr + st * Sh::kTileBytes, D == 128 ? kHalfBytes : 0));
+                const uint32_t p = warp_uniform(desc_low(smem_addr(p_smem) + b * Sh::kPBytes, 16));
+                const uint32_t add = warp_uniform(j > g.j0);
+                if (elect_one()) {
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i)
+                        mma_ss(tmem_u + kOColumn, smem_desc(v + i * (2048 / 16)),
+                               smem_desc(p + ((i / 4) * (NR * 128) + (i % 4) * 32) / 16), kIdO,
+                               i > 0 ? 1 : add);
+                    mma_commit(&bar.value_empty[st]);
+                    mma_commit(&bar.o_done[b]);
+                }
+                __syncwarp();
+                if (++st == Sh::kValues) {
+                    st = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok) fail();
         if (elect_one()) mma_commit(&bar.done);
         __syncwarp();
         volatile int none = 0;
@@ -445,6 +460,15 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j) {
                 if (!(ok = wait_for(&bar.key_full[st], round & 1, abort))) break;
+                // this key's scales, on their way while its codes are turned
+                const int cache_row = tile_rows[n & 15][row / a.box];
+                const int tok = j * kTile + row;
+                const bool live = cache_row != a.dead_row && tok >= g.lo && tok < g.hi;
+                float2 sc = make_float2(0.0f, 0.0f);
+                if (live) {
+                    sc.x = static_cast<const float *>(a.c.k_scale)[cache_row + row % a.box];
+                    sc.y = static_cast<const float *>(a.c.v_scale)[cache_row + row % a.box];
+                }
                 if (n >= 2 && !(ok = wait_for(&bar.turned_empty[n & 1], ((n >> 1) - 1) & 1, abort)))
                     break;
                 tmem_fence_after();
@@ -463,6 +487,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     }
                     tmem_st32(lanes + (n & 1) * (D / 2) + c * 8, o);
                 }
+                scales[n & 3][row] = make_float2(sc.x * a.scale_log2, sc.y);
                 tmem_wait_st();
                 tmem_fence_before();
                 __syncwarp();
@@ -538,19 +563,17 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
         // ------------------------------------------------------------ softmax ---
         const uint32_t lanes = tmem + (warp << 21);
         const int key = tid;
-        uint32_t n = 0, votes = 0, st = 0;
+        uint32_t n = 0;
         int piece = 0;  // runs of this CTA so far
         int x = x0;
-        // All four warps reach it; then each sees what the others wrote before.
-        auto meet = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.vote);
-            const bool r = wait_for(&bar.vote, votes & 1, abort);
-            ++votes;
-            return r;
+        // These warps meet at barriers of the hardware, which have no limit: so none
+        // leaves its loops before the others, and a wait that ran out only makes the
+        // waits behind it pass.
+        auto wait = [&](uint64_t *b, uint32_t parity) {
+            if (ok) ok = wait_for(b, parity, abort);
         };
 #pragma unroll 1
-        for (; ok && next_run(a, w, g); ++piece) {
+        for (; next_run(a, w, g); ++piece) {
             const int rows = g.s.n * a.G;
             const int p0 = g.s.first;  // the first token's position
             // keys that every row sees
@@ -559,77 +582,65 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-            if (tid < NR) m_s[tid] = -INFINITY;
             float unit = 1.0f;  // int8: value scales are taken times it
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
                 const uint32_t b = n & 1;
-                if (!(ok = wait_for(&bar.s_full[b], (n >> 1) & 1, abort))) break;
+                wait(&bar.s_full[b], (n >> 1) & 1);
                 tmem_fence_after();
                 const int t = j * kTile + key;
                 const uint32_t bad = dead_groups[n & 15] >> (key / 16) & 1;
-                const bool live = t >= g.lo && t < g.hi && !bad;
                 float ks = a.scale_log2, vs = 1.0f;
                 if constexpr (I8) {
-                    const float *sc =
-                        reinterpret_cast<const float *>(keys + st * Sh::kKeyBytes + kTile * D);
-                    ks = live ? sc[key] * a.scale_log2 : 0.0f;
-                    vs = live ? sc[kTile + key] : 0.0f;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.key_empty[st]);
-                    if (++st == Sh::kKeys) st = 0;
+                    const float2 sc = scales[n & 3][key];
+                    ks = sc.x;
+                    vs = sc.y;
                 }
-                const bool edge = j * kTile < all_lo || (j + 1) * kTile > all_hi || bad;
-                // this key's logits, those of rows that do not see it at -infinity
-                float s[NR];
-                auto logits = [&] {
+                // the rows that see this key
+                uint32_t seen = 0xffffffffu;
+                if (j * kTile < all_lo || (j + 1) * kTile > all_hi || bad) {
+                    seen = 0;
+                    if (t >= g.lo && t < g.hi && !bad) {
+                        // of the tokens from t on, and with a window to t + window - 1
+                        const int first = max(t - p0, 0);
+                        int last = g.s.n - 1;
+                        if (a.window > 0) last = min(last, t + a.window - 1 - p0);
+                        if (first <= last) {
+                            const int r0 = first * a.G, r1 = (last + 1) * a.G;  // r1 <= 32
+                            seen = (r1 >= 32 ? 0xffffffffu : (1u << r1) - 1) & ~((1u << r0) - 1);
+                        }
+                    }
+                }
+                bool fix = j == g.j0;
+                float p[NR];
+                float v;
+#pragma unroll 1
+                for (;;) {
+                    float s[NR];
 #pragma unroll
                     for (int i = 0; i < NR; i += 16) tmem_ld16(lanes + b * NR + i, s + i);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < NR; i += 16) pin16(s + i);
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) s[r] *= ks;
-                    if (edge) {
-                        int tok = 0, in = 0;
-#pragma unroll
-                        for (int r = 0; r < NR; ++r) {
-                            const int p = p0 + tok;
-                            if (!live || t > p || (a.window > 0 && t <= p - a.window))
-                                s[r] = -INFINITY;
-                            if (++in == a.G) {
-                                in = 0;
-                                ++tok;
-                            }
-                        }
-                    }
-                };
-                logits();
-                // P's buffer: the product of two tiles ago is done
-                if (n >= 2 && !(ok = wait_for(&bar.o_done[b], ((n >> 1) - 1) & 1, abort))) break;
-                bool fix = j == g.j0;
-#pragma unroll 1
-                for (;;) {
                     if (fix) {
                         // each row's maximum, over the warp's keys, then over all
                         float mine = -INFINITY;
 #pragma unroll
                         for (int r = 0; r < NR; ++r) {
-                            const uint32_t k = __reduce_max_sync(0xffffffffu, float_to_key(s[r]));
+                            const uint32_t k = __reduce_max_sync(
+                                0xffffffffu, float_to_key(seen >> r & 1 ? s[r] * ks : -INFINITY));
                             if (lane == r) mine = __uint_as_float(k);
                         }
                         if (lane < NR) red[warp][lane] = mine;
                         if constexpr (I8) {
-                            const uint32_t v = __float_as_uint(vs);
+                            const uint32_t u = __float_as_uint(vs);
                             const uint32_t top =
-                                __reduce_max_sync(0xffffffffu, v < 0x7f800000u ? v : 0u);
+                                __reduce_max_sync(0xffffffffu, u < 0x7f800000u ? u : 0u);
                             if (lane == 0) top_scale[warp] = __uint_as_float(top);
                         }
                         // O as it stands is complete
-                        if (j > g.j0 &&
-                            !(ok = wait_for(&bar.o_done[b ^ 1], ((n - 1) >> 1) & 1, abort)))
-                            break;
-                        if (!(ok = meet())) break;
+                        if (j > g.j0) wait(&bar.o_done[b ^ 1], ((n - 1) >> 1) & 1);
+                        meet_128();
                         if constexpr (I8) {
                             // a power of two near the largest value scale
                             const float top = fmaxf(fmaxf(top_scale[0], top_scale[1]),
@@ -641,22 +652,24 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                         if (tid < NR) {
                             uint32_t k = 0;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                k = max(k, __float_as_uint(red[i][tid]));
+                            for (int i = 0; i < 4; ++i) k = max(k, __float_as_uint(red[i][tid]));
                             const float top = key_to_float(k);
-                            const float m = m_s[tid], mn = fmaxf(m, top);
+                            const float m = j == g.j0 ? -INFINITY : m_s[tid];
+                            const float mn = fmaxf(m, top);
                             f_s[tid] = m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                             m_s[tid] = mn;
+                            base_s[tid] = mn == -INFINITY ? 0.0f : -mn;
                             if (tid == 0) {
                                 unit_s[1] = j == g.j0 ? 1.0f : unit / unit_s[0];
                                 unit_s[0] = unit;
                             }
                         }
-                        if (!(ok = meet())) break;
+                        meet_128();
                         const float fu = I8 ? unit_s[1] : 1.0f;
 #pragma unroll
                         for (int r = 0; r < NR; ++r) l[r] *= f_s[r];
                         if (j > g.j0) {
+                            tmem_fence_after();
 #pragma unroll 1
                             for (int i = 0; i < NR; i += 16) {
                                 float o[16];
@@ -671,32 +684,39 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             tmem_fence_before();
                         }
                     }
-                    const float v = I8 ? vs * unit : 1.0f;
+                    v = I8 ? vs * unit : 1.0f;
+                    const float2 k2 = make_float2(ks, ks);
                     float top = 0.0f;
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const float m = m_s[r];
-                        s[r] = exp2_approx(s[r] - (m == -INFINITY ? 0.0f : m));
-                        top = fmaxf(top, s[r]);
+                    for (int r = 0; r < NR; r += 4) {
+                        const float4 base = *reinterpret_cast<const float4 *>(base_s + r);
+                        const float2 u0 = __ffma2_rn(make_float2(s[r], s[r + 1]), k2,
+                                                     make_float2(base.x, base.y));
+                        const float2 u1 = __ffma2_rn(make_float2(s[r + 2], s[r + 3]), k2,
+                                                     make_float2(base.z, base.w));
+                        p[r] = exp2_approx(u0.x);
+                        p[r + 1] = exp2_approx(u0.y);
+                        p[r + 2] = exp2_approx(u1.x);
+                        p[r + 3] = exp2_approx(u1.y);
                     }
+                    if (seen != 0xffffffffu)
+#pragma unroll
+                        for (int r = 0; r < NR; ++r)
+                            if (!(seen >> r & 1)) p[r] = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < NR; r += 2) top = fmax3(top, p[r], p[r + 1]);
                     if (fix) break;  // no weight passes 1
-                    if (__any_sync(0xffffffffu, top > kRedo || (I8 && v > 4.0f)) && lane == 0)
-                        flag[votes & 1] = votes + 1;
-                    const uint32_t mine = votes;
-                    if (!(ok = meet())) break;
-                    if (*(volatile int *)&flag[mine & 1] != static_cast<int>(mine + 1)) break;
+                    if (!any_of_128(top > kRedo || (I8 && v > 4.0f))) break;
                     fix = true;
-                    logits();
                 }
-                if (!ok) break;
                 // the weights, and P^T: row r's 128 keys in two swizzled halves
-                const float v = I8 ? vs * unit : 1.0f;
-                uint8_t *p = p_smem + b * Sh::kPBytes + (key / 64) * (NR * 128) + (key % 8) * 2;
+                uint8_t *dst = p_smem + b * Sh::kPBytes + (key / 64) * (NR * 128) + (key % 8) * 2;
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
-                    l[r] += s[r];
-                    const float x = I8 ? s[r] * v : s[r];
-                    *reinterpret_cast<uint16_t *>(p + r * 128 + (((key % 64) / 8) ^ (r & 7)) * 16) =
+                    l[r] += p[r];
+                    const float x = I8 ? p[r] * v : p[r];
+                    *reinterpret_cast<uint16_t *>(dst + r * 128 +
+                                                  (((key % 64) / 8) ^ (r & 7)) * 16) =
                         static_cast<uint16_t>(pack2<BF16>(x, 0.0f));
                 }
                 fence_proxy_async();
@@ -704,7 +724,6 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_full[b]);
             }
-            if (!ok) break;
             // ---- the run's sums
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
@@ -716,9 +735,9 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             for (int r = 0; r < NR; ++r)
                 if (lane == r) mine = l[r];
             if (lane < NR) sums[warp][lane] = mine;
-            if (!(ok = wait_for(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort))) break;
+            wait(&bar.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
             tmem_fence_after();
-            if (!(ok = meet())) break;
+            meet_128();
             float sum = 0.0f, m = -INFINITY;  // of row `lane`
             if (lane < NR) {
                 sum = (sums[0][lane] + sums[1][lane]) + (sums[2][lane] + sums[3][lane]);
@@ -757,13 +776,13 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                 const int begin = x - g.off, end = begin + g.tiles;
                 const int c0 = cta_of(begin), c1 = cta_of(end - 1);
                 __threadfence();
-                if (!(ok = meet())) break;
+                meet_128();
                 if (tid == 0) {
                     const unsigned was = atomic_add_acq_rel_gpu(&a.arrived[c0], 1u);
                     last_piece = was == static_cast<unsigned>(c1 - c0);
                     if (last_piece) a.arrived[c0] = 0;
                 }
-                if (!(ok = meet())) break;
+                meet_128();
                 if (last_piece) {
                     __threadfence();
                     // CTA c0's piece is its last run, the others' their first
