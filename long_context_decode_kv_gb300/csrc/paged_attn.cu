@@ -26,6 +26,8 @@
 // of O rare.
 // P is rounded to the input type (the tensor core's operand): a relative error
 // of half a step in each weight, which sums and statistics in f32 do not add to.
+#include <type_traits>
+
 #include "paged_attn_dev.cuh"
 
 namespace kvd {
@@ -159,6 +161,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
     using Sh = Shape<D, MODE, I8>;
     constexpr bool PAIR = MODE == kPair;
+    // int8: weights and value codes are f16 whatever the queries are (three more
+    // bits, and the codes take fewer instructions)
+    constexpr bool kPBf16 = BF16 && !I8;
     constexpr int kThreads = threads_of(I8);
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
@@ -515,7 +520,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             // stream's softmax beside the other's products.  Otherwise one warp
             // serves the streams' key tiles in turn.
             constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kTile, false);
-            constexpr uint32_t kIdO = mma_idesc(BF16, kTile, D, true);
+            constexpr uint32_t kIdO = mma_idesc(kPBf16, kTile, D, true);
             const int who = warp - kIssuer;  // kPair: the stream
             const uint32_t ring_addr = smem_addr(ring);
             const uint32_t q =
@@ -701,17 +706,24 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 uint8_t *dst = ring + st * Sh::kTileBytes;
                 // rolled: the roles' hot lines have to stay in the instruction cache
                 // together (unrolled 8 times a tile took 1.4 times as long)
+                auto codes = [&](auto bf16_tag) {
+                    constexpr bool kBf16 = decltype(bf16_tag)::value;
 #pragma unroll 4
-                for (int i = 0; i < kSteps; ++i) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(src + i * (kStepRows * D));
-                    uint4 lo, hi;
-                    codes_to<BF16>(w.x, lo.x, lo.y);
-                    codes_to<BF16>(w.y, lo.z, lo.w);
-                    codes_to<BF16>(w.z, hi.x, hi.y);
-                    codes_to<BF16>(w.w, hi.z, hi.w);
-                    *reinterpret_cast<uint4 *>(dst + dst0 + i * (kStepRows * 128)) = lo;
-                    *reinterpret_cast<uint4 *>(dst + dst1 + i * (kStepRows * 128)) = hi;
-                }
+                    for (int i = 0; i < kSteps; ++i) {
+                        const uint4 w = *reinterpret_cast<const uint4 *>(src + i * (kStepRows * D));
+                        uint4 lo, hi;
+                        codes_to<kBf16>(w.x, lo.x, lo.y);
+                        codes_to<kBf16>(w.y, lo.z, lo.w);
+                        codes_to<kBf16>(w.z, hi.x, hi.y);
+                        codes_to<kBf16>(w.w, hi.z, hi.w);
+                        *reinterpret_cast<uint4 *>(dst + dst0 + i * (kStepRows * 128)) = lo;
+                        *reinterpret_cast<uint4 *>(dst + dst1 + i * (kStepRows * 128)) = hi;
+                    }
+                };
+                if (BF16 && is_k)
+                    codes(std::true_type());
+                else
+                    codes(std::false_type());
                 fence_proxy_async();
                 __syncwarp();
                 if (lane == 0) {
@@ -899,7 +911,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                     if (I8)
                                         x = __fmul2_rn(x, c % 2 == 0 ? make_float2(v4.x, v4.y)
                                                                      : make_float2(v4.z, v4.w));
-                                    p[8 * h + c] = pack2<BF16>(x.x, x.y);
+                                    p[8 * h + c] = pack2<kPBf16>(x.x, x.y);
                                 }
                             }
                             tmem_st16(s_addr + c0 / 2, p);

@@ -133,6 +133,9 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
     constexpr int kRaws = I8 ? Sh::kRaws : 1;
+    // int8: weights and value codes are f16 whatever the queries are (three more
+    // bits, and the codes take fewer instructions)
+    constexpr bool kPBf16 = BF16 && !I8;
 
     extern __shared__ uint8_t raw_smem[];
     __shared__ DecodeBars bar;
@@ -396,7 +399,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
         if (!mbar_wait(&bar.done, 0, &none)) fail();
     } else if (warp == 7) {
         // ---------------------------------------------- products O^T += V^T P^T ---
-        constexpr uint32_t kIdO = mma_idesc(BF16, kTile, NR, false, true);
+        constexpr uint32_t kIdO = mma_idesc(kPBf16, kTile, NR, false, true);
         const uint32_t value_addr = smem_addr(values);
         const uint32_t tmem_u = warp_uniform(tmem);
         uint32_t n = 0, st = 0, round = 0;
@@ -535,10 +538,10 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                 for (int i = 0; i < kSteps; ++i) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(src + i * (kRows * D));
                     uint4 lo, hi;
-                    codes_to<BF16>(x.x, lo.x, lo.y);
-                    codes_to<BF16>(x.y, lo.z, lo.w);
-                    codes_to<BF16>(x.z, hi.x, hi.y);
-                    codes_to<BF16>(x.w, hi.z, hi.w);
+                    codes_to<false>(x.x, lo.x, lo.y);
+                    codes_to<false>(x.y, lo.z, lo.w);
+                    codes_to<false>(x.z, hi.x, hi.y);
+                    codes_to<false>(x.w, hi.z, hi.w);
                     *reinterpret_cast<uint4 *>(dst + dst0 + i * (kRows * 128)) = lo;
                     *reinterpret_cast<uint4 *>(dst + dst1 + i * (kRows * 128)) = hi;
                 }
@@ -717,7 +720,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     const float x = I8 ? p[r] * v : p[r];
                     *reinterpret_cast<uint16_t *>(dst + r * 128 +
                                                   (((key % 64) / 8) ^ (r & 7)) * 16) =
-                        static_cast<uint16_t>(pack2<BF16>(x, 0.0f));
+                        static_cast<uint16_t>(pack2<kPBf16>(x, 0.0f));
                 }
                 fence_proxy_async();
                 tmem_fence_before();
