@@ -42,8 +42,7 @@ enum Mode { kPair, kOne };  // how a call's rows lie on the tiles (see above)
 constexpr int threads_of(bool i8) { return i8 ? 512 : 384; }
 constexpr int softmax_regs(bool i8) { return i8 ? 184 : 208; }
 constexpr int other_regs(bool i8) { return i8 ? 72 : 88; }
-// Warps that turn int8 codes: 12 and 13 the key tiles, 14 and 15 the value tiles.
-constexpr int kTeam = 12, kTeamWarps = 2;
+constexpr int kTeam = 12, kTeamWarps = 4;  // warps that turn int8 codes
 // A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
 // weights add up to more than kRaise raises m for the next one, and one above
 // kRedo is computed again (f16 holds weights up to 65,504).
@@ -635,7 +634,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             if (!mbar_wait(&bar.done, 0, &none)) fail();
         }
         if (I8 && warp >= kTeam) {
-            const int team = (warp - kTeam) / kTeamWarps, place = (warp - kTeam) % kTeamWarps;
+            const int place = warp - kTeam;
             // --------------------------------------------- int8 to f16 or bf16 ---
             // Codes are whole numbers up to 127, exact in either type; the scales
             // go to the softmax, so the products lose nothing.
@@ -740,7 +739,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 #pragma unroll 1
                 while (ok && vj < j1) {  // the order of the loads
                     const bool is_k = kj < min(j1, vj + kAhead);
-                    if (is_k == (team == 0)) ok = turn(is_k, kj, kj == j0);
+                    ok = turn(is_k, kj, kj == j0);
                     ++n;
                     keys += is_k;
                     ++(is_k ? kj : vj);
