@@ -35,6 +35,7 @@ namespace {
 
 // A tile of rows has kTile of them too.
 constexpr int kProducer = 8, kIssuer = 9;  // warps; the issuer of stream 1: 10
+constexpr int kValueProducer = 11;         // f16 and bf16 caches: value tiles
 enum Mode { kPair, kOne };  // how a call's rows lie on the tiles (see above)
 // Registers a thread: 168 at launch (64,512 for 384 threads), or 128 (65,536 for
 // 512), moved to the softmax warps, which hold a row's 128 logits:
@@ -126,6 +127,8 @@ __device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, S
     return true;
 }
 
+constexpr int kFewSeqs = 48;  // sequences whose row tiles are counted a warp each
+
 // ------------------------------------------------------------ the kernel ---
 template <int D, Mode MODE, bool I8>
 struct Shape {
@@ -178,6 +181,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     __shared__ int value_exp[8];            // int8: per key tile, see Scales
     __shared__ __align__(16) float ones[I8 ? kTile : 1];
     __shared__ long scan_total[kThreads / 32];
+    __shared__ long seq_tiles[kFewSeqs];
+    __shared__ long found_rest;
+    __shared__ int found_seq;
     __shared__ Walk start;
 
     uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
@@ -202,7 +208,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             mbar_init(&bar.turn[i], 1);
         }
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&bar.kv_full[i], I8 ? kTeamWarps : 1);
+            mbar_init(&bar.kv_full[i], I8 ? kTeamWarps : 2);
             mbar_init(&bar.kv_empty[i], PAIR ? 2 : 1);  // the streams that use a tile
         }
         for (int i = 0; i < Sh::kRaw; ++i) {
@@ -249,7 +255,24 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         return sum;
     };
     long before = 0;
-    long cost = cost_of(tid, blockIdx.x == 0);
+    long cost;
+    if (a.c.batch <= kFewSeqs) {
+        // few sequences may be long: a warp counts one's tiles, a lane a row tile
+#pragma unroll 1
+        for (int b = warp; b < a.c.batch; b += kThreads / 32) {
+            const Seq s = seq_of(a, b, blockIdx.x == 0);
+            long n = 0;
+#pragma unroll 1
+            for (int t = lane; t * width < s.n; t += 32) n += item_of(a, s, t, width).tiles;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+            if (lane == 0) seq_tiles[b] = n;
+        }
+        __syncthreads();
+        cost = tid < a.c.batch ? seq_tiles[tid] * a.c.n_kv_heads : 0;
+    } else {
+        cost = cost_of(tid, blockIdx.x == 0);
+    }
     long total = scan(cost, before);
     const bool one_pass = a.c.batch <= kThreads;
 #pragma unroll 1
@@ -274,26 +297,41 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 base += sum;
             }
             if (before <= x0 && x0 < before + cost) {
-                Walk w;
-                w.b = b0 + tid;
-                w.s = seq_of(a, w.b, false);
-                const long per_head = cost / a.c.n_kv_heads;
-                long r = x0 - before;
-                w.head = static_cast<int>(r / per_head);
-                r -= w.head * per_head;
-                w.tile = 0;
-#pragma unroll 1
-                for (;;) {
-                    const int n = item_of(a, w.s, w.tile, width).tiles;
-                    if (r < n) break;
-                    r -= n;
-                    ++w.tile;
-                }
-                w.off = static_cast<int>(r);
-                w.left = x1 - x0;
-                w.k = 0;
-                start = w;
+                found_seq = b0 + tid;
+                found_rest = x0 - before;
+                seq_tiles[0] = cost / a.c.n_kv_heads;  // of one head
             }
+        }
+        __syncthreads();
+        if (warp == 0) {  // the row tile, 32 at a time
+            Walk w;
+            w.b = found_seq;
+            w.s = seq_of(a, w.b, false);
+            const long per_head = seq_tiles[0];
+            w.head = static_cast<int>(found_rest / per_head);
+            long r = found_rest - w.head * per_head;
+#pragma unroll 1
+            for (int t0 = 0;; t0 += 32) {
+                const int t = t0 + lane;
+                const int n = t * width < w.s.n ? item_of(a, w.s, t, width).tiles : 0;
+                int upto = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += u;
+                }
+                const uint32_t in = __ballot_sync(0xffffffffu, r < upto);
+                if (in || t0 * width >= w.s.n) {
+                    const int l = in ? __ffs(in) - 1 : 0;
+                    w.tile = t0 + l;
+                    w.off = static_cast<int>(r) - __shfl_sync(0xffffffffu, upto - n, l);
+                    break;
+                }
+                r -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+            w.left = x1 - x0;
+            w.k = 0;
+            if (lane == 0) start = w;
         }
     }
     tmem_fence_before();
@@ -351,18 +389,20 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 
     if (warp >= kProducer) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(other_regs(I8)));
-        if (warp == kProducer) {
+        if (warp == kProducer || (!I8 && warp == kValueProducer)) {
         // ------------------------------------------------------- loads ---
+        const bool first_warp = warp == kProducer;  // keys and all else
         const uint64_t policy = PAIR ? l2_policy_evict_last() : l2_policy_evict_first();
         const int boxes = kTile / a.box;
         const int ahead_tiles = 32 / boxes;  // whose rows one read of the page table gives
         const int ps = a.c.page_size;
+        constexpr uint32_t kRawPlaces = I8 ? Sh::kRaw : 1;
         uint32_t st = 0, keys = 0;  // the next place (int8: of the raw ring), key tiles loaded
         uint32_t it = 0;            // int8: tiles loaded
-        // Bits of the ring's places: whether what lies there is freed by its own
-        // arrival (a key tile behind a value tile is freed by that one's), and
-        // the parity of the next arrival.
-        uint32_t own = 0, phase = 0;
+        // Bits of the ring's places: whether one was used before, and the parity of
+        // its next release.  Releases come in the order of the tiles, so a warp that
+        // waits for every second one never falls a whole turn behind.
+        uint32_t used = 0, phase = 0;
         uint32_t filled = 0, fills = 0;  // places whose full barrier was used; its next parity
         uint32_t q_phase = 0;
         bool ok = true;
@@ -371,12 +411,12 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         while (ok && next_segment(a, width, w, g)) {
             int j0, j1;
             span_of(g, j0, j1);
-            if (g.k > 0) {
+            if (first_warp && g.k > 0) {
                 ok = wait_for(&bar.q_empty, q_phase, abort);
                 q_phase ^= 1;
                 if (!ok) break;
             }
-            if (lane == 0 && j1 > j0) {
+            if (first_warp && lane == 0 && j1 > j0) {
                 const int rows = a.q_tokens * a.G;
 #pragma unroll 1
                 for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
@@ -402,7 +442,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             };
             // int8: the tile's codes as they lie, and with keys both rows' scales
             auto load_raw = [&](int row, const CUtensorMap *map, bool keys_too) -> bool {
-                if (it >= Sh::kRaw) {
+                if (it >= kRawPlaces) {
                     if (!wait_for(&bar.raw_empty[st], phase >> st & 1, abort)) return false;
                     phase ^= 1u << st;
                 }
@@ -424,7 +464,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 a.box * 4, &bar.raw_full[st], policy);
                 }
                 ++it;
-                st = st + 1 == (I8 ? Sh::kRaw : 1) ? 0 : st + 1;
+                st = st + 1 == kRawPlaces ? 0 : st + 1;
                 return true;
             };
             // The tiles in the order of the products: kAhead key tiles, then value
@@ -453,7 +493,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     const int n = a.box / 16;
                     const uint32_t groups = __reduce_or_sync(
                         0xffffffffu, bad ? ((1u << n) - 1) << (lane % boxes * n) : 0u);
-                    if (lane == 0) dead_groups[keys & 7] = groups;
+                    if (lane == 0 && first_warp) dead_groups[keys & 7] = groups;
                     ++keys;
                     ++kj;
                 } else {
@@ -463,29 +503,33 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 if constexpr (I8) {
                     ok = load_raw(row, map, is_k);
                 } else {
-                    // The next place of the ring, free.  A value tile, and the key
-                    // tile that follows it in the same step of the products, complete
-                    // on the value tile's barrier; the first key tiles on their own.
-                    if (own >> st & 1) {
-                        if (!(ok = wait_for(&bar.kv_empty[st], phase >> st & 1, abort))) break;
-                        phase ^= 1u << st;
-                    }
-                    own = (own & ~(1u << st)) | (!is_k || pre ? 1u << st : 0u);
+                    // The next place of the ring.  A value tile, and the key tile that
+                    // follows it in the same step of the products, complete on the value
+                    // tile's barrier; the first key tiles on their own.  A barrier counts
+                    // two arrivals: of both tiles' warps, or of one warp twice.
+                    const bool again = used >> st & 1;
+                    const uint32_t parity = phase >> st & 1;
+                    if (again) phase ^= 1u << st;
+                    used |= 1u << st;
                     if (!is_k || pre) {
                         full = &bar.kv_full[st];
                         filled |= 1u << st;
                         fills ^= 1u << st;
-                        if (lane == 0)
-                            mbar_arrive_expect_tx(full,
-                                                  (!is_k && kj < j1 ? 2 : 1) * Sh::kTileBytes);
-                        __syncwarp();
                     }
-                    if (lane < boxes)
+                    if (is_k == first_warp) {
+                        if (again && !(ok = wait_for(&bar.kv_empty[st], parity, abort))) break;
+                        if (lane == 0) {
+                            mbar_arrive_expect_tx(full, Sh::kTileBytes);
+                            if (is_k ? pre : kj == j1) mbar_arrive(full);
+                        }
+                        __syncwarp();
+                        if (lane < boxes)
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h)
-                            tma_load_2d(ring + st * Sh::kTileBytes + h * kHalfBytes +
-                                            lane * a.box * 128,
-                                        map, h * 64, row, full, policy);
+                            for (int h = 0; h < kHalves; ++h)
+                                tma_load_2d(ring + st * Sh::kTileBytes + h * kHalfBytes +
+                                                lane * a.box * 128,
+                                            map, h * 64, row, full, policy);
+                    }
                     st = st + 1 == kStages ? 0 : st + 1;
                 }
             }
@@ -499,7 +543,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             }
         }
         if (!ok) fail();
-        if (lane == 0) {
+        if (lane == 0 && first_warp) {
             a.merge[2 * blockIdx.x] = rec0;
             a.merge[2 * blockIdx.x + 1] = rec1;
         }
@@ -585,7 +629,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         }
                         next_place();
                     }
-                    const bool own_k = has_s && (I8 || !has_o);  // a barrier and release of its own
+                    const bool own_k = has_s && (I8 || !has_o);  // a barrier of its own
                     if (own_k && !(ok = wait_tile())) break;
                     const uint32_t k = warp_uniform(desc_low(ring_addr + st * Sh::kTileBytes, 16));
                     const uint32_t add = warp_uniform(j >= mine + kStep);
@@ -619,7 +663,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         if (PAIR) mbar_arrive(&bar.turn[t ^ 1]);
                         // the tiles are used up, and with the last S the queries
                         if (has_o) mma_commit(&bar.kv_empty[v_st]);
-                        if (own_k) mma_commit(&bar.kv_empty[st]);
+                        if (has_s) mma_commit(&bar.kv_empty[st]);
                         if (do_s && ahead + 1 == end) mma_commit(&bar.q_empty);
                     }
                     __syncwarp();
@@ -754,6 +798,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         const uint32_t lanes = tmem + ((warp & 3) << 21);  // this warp's 32 lanes
         const uint32_t s_addr = lanes + t * 128, o_addr = lanes + 256 + t * 128;
         uint32_t s_phase = 0, o_phase = 0, join_phase = 0, keys = 0;
+        const int tok = row / a.G, head_at = (row - tok * a.G) * D;  // of this row
         bool ok = true;
 #pragma unroll 1
         while (ok && next_segment(a, width, w, g)) {
@@ -762,7 +807,6 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             const Part part = part_of(g, t);
             const int rows = part.cnt * a.G;
             const bool warp_live = (warp & 3) * 32 < rows;
-            const int tok = row / a.G;
             const int pos = part.p0 + tok;
             // keys [lo, hi) of this row
             const int hi = row < rows ? max(pos + 1, 0) : 0x7fffffff;
@@ -981,7 +1025,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
             }
             const bool live = row < rows;
-            if (whole) {
+            if (whole && (PAIR || t == 0)) {
                 const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
                 mine = some ? mine * inv : 0.0f;
                 other *= inv;
@@ -991,64 +1035,50 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             if (live)
                 dst += static_cast<int64_t>(g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0) + tok) *
                            a.out_stride +
-                       static_cast<int64_t>(g.head * a.G + row % a.G) * D;
+                       static_cast<int64_t>(g.head) * a.G * D + head_at;
             float4 *part_dst = reinterpret_cast<float4 *>(a.acc) +
                                ((slot * (a.ws_rows / 32) + prow / 32) * (D / 4)) * 32 + lane;
+            // 16 channels at a time, in short code: it runs once a segment, from
+            // beyond the instruction cache
 #pragma unroll 1
-            for (int h = 0; h < kHalves; ++h) {
-                if (!PAIR && h > 0) {
+            for (int i = 0; i < D / 16; ++i) {
+                if (!PAIR && i > 0 && i % 4 == 0) {  // the join buffer holds 64
                     ok = t == 1 ? wait_for(&bar.join_empty, join_phase ^ 1, abort)
                                 : wait_for(&bar.join_full, join_phase, abort);
                     if (!ok) break;
                 }
-#pragma unroll 1
-                for (int i = 2 * h; i < 2 * h + 2; ++i) {
-                    float o[32];
-                    if (warp_live && some) {
-                        tmem_ld32(o_addr + 32 * i, o);
-                        tmem_wait_ld();
-                        pin32(o);
-                    } else {
+                float o[16];
+                if (some) {
+                    tmem_ld16(o_addr + 16 * i, o);
+                    tmem_wait_ld();
+                    pin16(o);
+                }
+                float *at = join + i % 4 * 16 * kTile + row;
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = 0.0f;
-                    }
+                for (int c = 0; c < 16; ++c) {
+                    o[c] = some && (PAIR || mine != 0.0f) ? o[c] * mine : 0.0f;
                     if constexpr (!PAIR) {
-                        if (t == 1) {
-                            if (warp_live)
-#pragma unroll
-                                for (int c = 0; c < 32; ++c)
-                                    join[((i & 1) * 32 + c) * kTile + row] =
-                                        I8 ? o[c] * unit : o[c];
-                            continue;
-                        }
-                        if (warp_live)
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float u = join[((i & 1) * 32 + c) * kTile + row];
-                                o[c] = (mine != 0.0f ? o[c] * mine : 0.0f) +
-                                       (other != 0.0f ? u * other : 0.0f);
-                            }
-                    } else if (whole || I8) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] *= mine;
+                        if (t == 1) at[c * kTile] = o[c];
+                        else if (other != 0.0f) o[c] = fmaf(at[c * kTile], other, o[c]);
                     }
-                    if (live && whole) {
+                }
+                if (live && (PAIR || t == 0)) {
+                    if (whole) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
-                            *reinterpret_cast<uint4 *>(dst + 32 * i + c) =
+                        for (int c = 0; c < 16; c += 8)
+                            *reinterpret_cast<uint4 *>(dst + 16 * i + c) =
                                 make_uint4(pack2<BF16>(o[c], o[c + 1]), pack2<BF16>(o[c + 2], o[c + 3]),
                                            pack2<BF16>(o[c + 4], o[c + 5]),
                                            pack2<BF16>(o[c + 6], o[c + 7]));
-                    } else if (live) {
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            part_dst[(8 * i + c / 4) * 32] =
+                        for (int c = 0; c < 16; c += 4)
+                            part_dst[(4 * i + c / 4) * 32] =
                                 make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                     }
-                    __syncwarp();
                 }
-                if constexpr (!PAIR) {
-                    __syncwarp();
+                __syncwarp();
+                if (!PAIR && i % 4 == 3) {
                     if (lane == 0) mbar_arrive(t == 1 ? &bar.join_full : &bar.join_empty);
                     join_phase ^= 1;
                 }
