@@ -24,7 +24,8 @@
 //
 // The weights' reference m follows a row's maximum loosely: a weight that passes
 // 2^13 (rarely any; f16 holds 2^16) has the four warps find the maximum and
-// compute the tile again, as the first tile of an item does.
+// compute the tile again, as the first tile of an item does, and each one until all
+// rows have seen a key (a window or a bad page may hide the first tiles from some).
 #include "paged_attn_dev.cuh"
 
 namespace kvd {
@@ -586,6 +587,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.0f;
             float unit = 1.0f;  // int8: value scales are taken times it
+            bool open = true;   // a row has seen no key yet, and so has no reference
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
                 const uint32_t b = n & 1;
@@ -614,7 +616,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                         }
                     }
                 }
-                bool fix = j == g.j0;
+                bool fix = open;
                 float p[NR];
                 float v;
 #pragma unroll 1
@@ -652,6 +654,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             const float fresh = __int_as_float((127 - e) << 23);
                             if (j == g.j0 || fresh < unit) unit = fresh;  // same in all threads
                         }
+                        bool none = false;
                         if (tid < NR) {
                             uint32_t k = 0;
 #pragma unroll
@@ -661,13 +664,14 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             const float mn = fmaxf(m, top);
                             f_s[tid] = m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                             m_s[tid] = mn;
+                            none = tid < rows && mn == -INFINITY;
                             base_s[tid] = mn == -INFINITY ? 0.0f : -mn;
                             if (tid == 0) {
                                 unit_s[1] = j == g.j0 ? 1.0f : unit / unit_s[0];
                                 unit_s[0] = unit;
                             }
                         }
-                        meet_128();
+                        open = any_of_128(none);
                         const float fu = I8 ? unit_s[1] : 1.0f;
 #pragma unroll
                         for (int r = 0; r < NR; ++r) l[r] *= f_s[r];

@@ -323,6 +323,23 @@ def test_growing_logits_and_tiny_values(dtype):
         _check_attn(c, q, [1, 1])
 
 
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.BF16, kvd.INT8])
+@pytest.mark.parametrize("new,L,G,window", [(20, 140, 1, 8), (7, 1030, 4, 5), (30, 1300, 1, 100), (60, 170, 2, 8)])
+def test_rows_whose_first_keys_come_in_a_later_tile(dtype, new, L, G, window):
+    """A window hides the first tile from the last tokens, and their logits are far below zero."""
+    D = 128
+    x = X.get(dtype, torch.float16)
+    c = _cache(dtype, [L], 1, D, 64, 21)
+    k = torch.randn(c.k.shape, generator=_gen(22), device=DEV) * 0.3 + 2.0
+    if dtype == kvd.INT8:
+        c.k_scale.copy_(k.abs().amax(-1) / 127)
+        c.k.copy_((k / c.k_scale[..., None]).round())
+    else:
+        c.k.copy_(k)
+    q = (torch.randn(new, G, D, generator=_gen(23), device=DEV) * 0.3 - 2.0).to(x)
+    _check_attn(c, q, [new], window)
+
+
 def test_strided_queries_and_outputs():
     c = _cache(kvd.BF16, [90, 33], 2, 128, 32, 14)
     wide = torch.randn(12, 14, 128, device=DEV).bfloat16()
