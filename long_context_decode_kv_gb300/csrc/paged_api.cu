@@ -261,7 +261,7 @@ kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int3
     a.G = G;
     a.n_tokens = n_tokens;
     a.max_new = max_new;
-    a.window = window;
+    a.window = window < cache->len ? window : 0;  // positions plus it stay in 31 bits
     a.starts = starts;
     a.scale_log2 = softmax_scale * kLog2e;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);

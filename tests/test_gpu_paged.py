@@ -340,6 +340,16 @@ def test_rows_whose_first_keys_come_in_a_later_tile(dtype, new, L, G, window):
     _check_attn(c, q, [new], window)
 
 
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
+@pytest.mark.parametrize("new", [1, 30, 300])
+def test_a_window_longer_than_any_sequence(dtype, new):
+    c = _cache(dtype, [1000, 700], 2, 128, 64, 24)
+    q = _q(2 * new, 2, 128, torch.float16, 25)
+    plain = _attend(c, q, [new, new])
+    for window in (1000, 1001, 2 ** 30, 2 ** 31 - 1):
+        assert torch.equal(_attend(c, q, [new, new], window), plain)
+
+
 def test_strided_queries_and_outputs():
     c = _cache(kvd.BF16, [90, 33], 2, 128, 32, 14)
     wide = torch.randn(12, 14, 128, device=DEV).bfloat16()
