@@ -99,7 +99,11 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     bool store_kv = false;
     if constexpr (PAGED) {
         const int b = sequence_of(a.starts, a.cache.batch, t, lane);
-        const int s0 = a.starts[b], s1 = a.starts[b + 1], end = a.starts[a.cache.batch];
+        // starts in their range, as the attention takes them
+        const int r0 = a.starts[b], r1 = a.starts[b + 1], end = a.starts[a.cache.batch];
+        const int s0 = max(r0, 0), s1 = min(r1, a.n_tokens);
+        if ((s0 != r0 || s1 != r1) && lane == 0)
+            report_status(a.cache.dev_status, KVD_ERR_INVALID);
         if (t < s0 || t >= s1) {
             // behind the last sequence, or starts that are not in order
             if (t < end && lane == 0) report_status(a.cache.dev_status, KVD_ERR_INVALID);
@@ -304,8 +308,8 @@ cudaError_t launch(const RopeArgs &a, cudaStream_t st) {
     // Warps a token: one, or as many as give every SM 16 warps
     const int most = (a.q.n_heads + kRows - 1) / kRows + (a.k.n_heads + kRows - 1) / kRows +
                      (a.v.n_heads + kRows - 1) / kRows;
-    int parts = (16 * device_sm_count() + a.n_tokens - 1) / a.n_tokens;
-    if (parts > most) parts = most;
+    const int64_t want = (16ll * device_sm_count() + a.n_tokens - 1) / a.n_tokens;
+    const int parts = want < most ? static_cast<int>(want) : most;
     const int64_t units = static_cast<int64_t>(a.n_tokens) * parts;
     constexpr int kWarps = kThreads / 32;
     return launch_ex(rope_kernel<IN, LPR, VPL, U, PAGED>,

@@ -167,6 +167,25 @@ def test_append_checks_what_the_device_holds():
     assert c.device_status() == 1
 
 
+def test_starts_outside_the_tokens_are_moved_into_them():
+    """A first start below 0 and a last one above n_tokens: reported, and both calls take the same rows."""
+    c = _cache(kvd.F16, [20, 20, 20], 2, 64, 16, 5)
+    k = _q(12, 2, 64, torch.float16, 6)
+    before = c.k.clone()
+    starts = torch.tensor([-2, 4, 8, 15], dtype=torch.int32, device=DEV)
+    kvd.paged_append(c, k, k, starts)
+    assert c.device_status() == 1
+    for b in range(3):
+        page = int(c.page_table[b, 1])                          # positions 16 .. 19
+        assert torch.equal(c.k[page, :, :4].transpose(0, 1), k[4 * b:4 * b + 4])
+    assert int((c.k != before).any(-1).any(1).sum()) == 12
+    out = torch.full_like(k, math.nan)
+    kvd.paged_attn(c, k, starts, 4, 0.125, out, kvd.make_paged_workspace(c, 2, 12, 4))
+    assert c.device_status() == 1
+    want, tol = R.attn_ref(c, k, [0, 4, 8, 12], [20, 20, 20], 0.125)
+    R.assert_within(out, want, tol)
+
+
 def test_append_a_large_batch_finds_every_token():
     B = 1500
     lens = [1 + b % 37 for b in range(B)]
