@@ -369,6 +369,41 @@ def test_a_window_longer_than_any_sequence(dtype, new):
         assert torch.equal(_attend(c, q, [new, new], window), plain)
 
 
+@pytest.mark.parametrize("dtype,x", [(kvd.F16, torch.float16), (kvd.BF16, torch.bfloat16),
+                                     (kvd.INT8, torch.float16), (kvd.INT8, torch.bfloat16)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G,new", [(4, [9, 30, 1, 0]), (16, [3, 8, 8, 1]), (1, [33, 128, 2, 100])])
+@pytest.mark.parametrize("window", [0, 70])
+def test_33_to_128_rows(dtype, x, D, G, new, window):
+    lens = [5000, 300, 77, 129]
+    c = _cache(dtype, lens, 2, D, 48, D + G + window)
+    _check_attn(c, _q(sum(new), 2 * G, D, x, G, scale=1.5), new, window)
+
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
+def test_one_workspace_for_calls_of_every_length(dtype):
+    """Made for the longest, used by chunks and single tokens in turn, and by two graphs of them."""
+    H, D = 8, 128
+    c = _cache(dtype, [4000, 900], 2, D, 64, 26)
+    ws = kvd.make_paged_workspace(c, H, 600, 300)
+    sizes = [300, 1, 20, 8, 300, 2, 1]
+    q = {n: _q(2 * n, H, D, torch.float16, n) for n in sizes}
+    want = {n: _attend(c, q[n], [n, n]) for n in sizes}
+    for n in sizes:
+        assert torch.equal(_attend(c, q[n], [n, n], ws=ws), want[n])
+    graphs, outs = {}, {n: torch.full_like(q[n], math.nan) for n in (300, 1)}
+    starts = {n: _starts([n, n]) for n in (300, 1)}
+    for n in (300, 1):
+        graphs[n] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[n]):
+            kvd.paged_attn(c, q[n], starts[n], n, D ** -0.5, outs[n], ws)
+    for n in (300, 1, 1, 300, 1):
+        outs[n].fill_(math.nan)
+        graphs[n].replay()
+        assert torch.equal(outs[n], want[n])
+    assert c.device_status() == 0
+
+
 def test_strided_queries_and_outputs():
     c = _cache(kvd.BF16, [90, 33], 2, 128, 32, 14)
     wide = torch.randn(12, 14, 128, device=DEV).bfloat16()

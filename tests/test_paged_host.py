@@ -188,3 +188,15 @@ def test_binding_checks_shapes_before_the_library():
         kvd._heads(torch.zeros(3, 8, 64, dtype=torch.float64))
     s = kvd._heads(torch.zeros(3, 12, 64, dtype=torch.bfloat16)[:, 4:8])
     assert (s.stride, s.dtype, s.n_heads) == (768, 1, 4)
+
+
+def test_caches_too_long_to_count():
+    """Lengths above 2^30 and more than 2^31 - 1 key tiles are refused, by every call."""
+    L = kvd.lib()
+    for kw in (dict(ps=1 << 16, cols=1 << 15, pages=4, length=(1 << 30) + 1),
+               dict(ps=1 << 16, cols=1 << 15, pages=4, B=1 << 12, length=1 << 30)):
+        c, k = C.byref(_c(**kw)), _h()
+        assert L.kvd_paged_append(c, k, k, 4, FAKE, None, None, None, None, None, 1e-6, None) == UNSUPPORTED
+        assert L.kvd_paged_attn(c, _h(n=32), 4, FAKE, 4, 0.1, 0, _h(FAKE + (1 << 30), n=32), FAKE, 1 << 40,
+                                None) == UNSUPPORTED
+        assert L.kvd_paged_workspace_bytes(c, 32, 4, 4) == 0
