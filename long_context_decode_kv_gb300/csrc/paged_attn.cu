@@ -129,6 +129,19 @@ __device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, S
 
 constexpr int kFewSeqs = 48;  // sequences whose row tiles are counted a warp each
 
+// 32 bytes; wide: on a 32-byte boundary, in one store (the lanes' rows lie apart, so
+// a store takes the L1 as many cycles as it has lanes, whatever it brings).
+__device__ __forceinline__ void store32(void *p, const uint32_t (&w)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                     "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
 // ------------------------------------------------------------ the kernel ---
 template <int D, Mode MODE, bool I8>
 struct Shape {
@@ -1038,6 +1051,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                        static_cast<int64_t>(g.head) * a.G * D + head_at;
             float4 *part_dst = reinterpret_cast<float4 *>(a.acc) +
                                ((slot * (a.ws_rows / 32) + prow / 32) * (D / 4)) * 32 + lane;
+            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
             // 16 channels at a time, in short code: it runs once a segment, from
             // beyond the instruction cache
 #pragma unroll 1
@@ -1055,21 +1069,27 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 float *at = join + i % 4 * 16 * kTile + row;
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
+                for (int c = 0; c < 16; ++c)
                     o[c] = some && (PAIR || mine != 0.0f) ? o[c] * mine : 0.0f;
-                    if constexpr (!PAIR) {
-                        if (t == 1) at[c * kTile] = o[c];
-                        else if (other != 0.0f) o[c] = fmaf(at[c * kTile], other, o[c]);
+                if constexpr (!PAIR) {
+                    if (t == 1) {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) at[c * kTile] = o[c];
+                    } else {
+                        float u[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) u[c] = at[c * kTile];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            if (other != 0.0f) o[c] = fmaf(u[c], other, o[c]);
                     }
                 }
                 if (live && (PAIR || t == 0)) {
                     if (whole) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int c = 0; c < 16; c += 8)
-                            *reinterpret_cast<uint4 *>(dst + 16 * i + c) =
-                                make_uint4(pack2<BF16>(o[c], o[c + 1]), pack2<BF16>(o[c + 2], o[c + 3]),
-                                           pack2<BF16>(o[c + 4], o[c + 5]),
-                                           pack2<BF16>(o[c + 6], o[c + 7]));
+                        for (int c = 0; c < 8; ++c) w[c] = pack2<BF16>(o[2 * c], o[2 * c + 1]);
+                        store32(dst + 16 * i, w, wide);
                     } else {
 #pragma unroll
                         for (int c = 0; c < 16; c += 4)

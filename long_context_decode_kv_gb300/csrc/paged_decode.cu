@@ -852,7 +852,7 @@ cudaError_t launch_shape(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
     if (!fill_launch(p, p.max_new, k_swizzle, v_swizzle, a, q_map, k_map, v_map))
         return cudaErrorInvalidValue;
     const DecodePlan w = plan_of(p.max_new * p.G, D);
-    a.min_tiles = 2;
+    a.min_tiles = 4;
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.arrived = reinterpret_cast<uint32_t *>(base);
     a.ml = reinterpret_cast<float2 *>(base + w.ml);
