@@ -1134,27 +1134,25 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Dev 
         const int tok = prow / kTile * a.q_tokens + r / a.G;
         if (r >= a.q_tokens * a.G || tok >= rec.w) continue;
         float m = -INFINITY;
+#pragma unroll 8
         for (int i = 0; i < rec.x; ++i)
             m = fmaxf(m, a.ml[(i == 0 ? first : next + 2 * i) * a.ws_rows + prow].x);
         float o[8] = {};
         float l = 0.0f;
+#pragma unroll 4
         for (int i = 0; i < rec.x; ++i) {
             const size_t slot = i == 0 ? first : next + 2 * i;
             const float2 ml = a.ml[slot * a.ws_rows + prow];
-            if (ml.x == -INFINITY) continue;
-            const float f = exp2_approx(ml.x - m);
-            l += f * ml.y;
+            const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
             const float4 *p = reinterpret_cast<const float4 *>(a.acc) +
                               ((slot * blocks + prow / 32) * (D / 4) + 2 * c8) * 32 + lane;
             const float4 u0 = p[0], u1 = p[32];
-            o[0] = fmaf(f, u0.x, o[0]);
-            o[1] = fmaf(f, u0.y, o[1]);
-            o[2] = fmaf(f, u0.z, o[2]);
-            o[3] = fmaf(f, u0.w, o[3]);
-            o[4] = fmaf(f, u1.x, o[4]);
-            o[5] = fmaf(f, u1.y, o[5]);
-            o[6] = fmaf(f, u1.z, o[6]);
-            o[7] = fmaf(f, u1.w, o[7]);
+            const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+            if (f != 0.0f) {
+                l = fmaf(f, ml.y, l);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) o[c] = fmaf(f, u[c], o[c]);
+            }
         }
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
         *reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(rec.z + tok) * a.out_stride +
@@ -1208,7 +1206,7 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
     e = launch_ex(kernel, dim3(w.ctas), dim3(threads), smem, st, true, a, q_map, k_map,
                   v_map);
     if (e != cudaSuccess) return e;
-    return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, MODE == kPair ? 4 : 1), dim3(256), 0, st, true, a);
+    return launch_ex(merge_kernel<BF16, D>, dim3(w.ctas, MODE == kPair ? 16 : 4), dim3(256), 0, st, true, a);
 }
 
 template <bool BF16, int D, bool I8>
