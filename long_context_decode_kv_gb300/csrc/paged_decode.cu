@@ -31,6 +31,7 @@
 namespace kvd {
 namespace {
 
+constexpr int kMaxCtas = 256;     // one an SM
 constexpr float kRedo = 8192.0f;  // above it a weight asks for a new reference
 
 // Barriers of the 128 softmax threads; the second tells whether any said yes.
@@ -781,7 +782,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     if (channel && r < rows) a.acc[(slot * NR + r) * D + key] = o[r] * out_unit;
                 // the last of the item's CTAs to arrive joins them
                 const int begin = x - g.off, end = begin + g.tiles;
-                const int c0 = cta_of(begin), c1 = cta_of(end - 1);
+                const int c0 = max(cta_of(begin), 0), c1 = min(cta_of(end - 1), ctas - 1);
                 __threadfence();
                 meet_128();
                 if (tid == 0) {
@@ -794,23 +795,69 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     __threadfence();
                     // CTA c0's piece is its last run, the others' their first
                     const uint32_t first_slot = 2 * c0 + (cut(c0) < begin ? 1 : 0);
+                    auto slot_of = [&](int c) { return c == c0 ? first_slot : 2u * c; };
+                    // The pieces' factors, a warp a row and a lane a piece, for half of the
+                    // rows at a time where P was (read already: the run's last product is
+                    // done); then the sums, a thread a channel with 32 reads under way.
+                    constexpr int kRowsAt = 2 * Sh::kPBytes / (kMaxCtas * 4);
+                    float *factors = reinterpret_cast<float *>(p_smem);
 #pragma unroll 1
-                    for (int r = 0; r < rows; ++r) {
-                        float top = -INFINITY;
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c)
-                            top = fmaxf(top, __ldcg(&a.ml[(c == c0 ? first_slot : 2 * c) * NR + r]).x);
-                        float x = 0.0f, den = 0.0f;
-#pragma unroll 4
-                        for (int c = c0; c <= c1; ++c) {
-                            const uint32_t at = (c == c0 ? first_slot : 2 * c) * NR + r;
-                            const float2 ml = __ldcg(&a.ml[at]);
-                            const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
-                            den = fmaf(f, ml.y, den);
-                            if (channel && f != 0.0f) x = fmaf(f, __ldcg(&a.acc[at * D + key]), x);
+                    for (int r0 = 0; r0 < rows; r0 += kRowsAt) {
+                        const int r1 = min(r0 + kRowsAt, rows);
+                        if (r0 > 0) meet_128();
+#pragma unroll 1
+                        for (int r = r0 + warp; r < r1; r += 4) {
+                            float top = -INFINITY, den = 0.0f;
+                            for (int c = c0 + lane; c <= c1; c += 32)
+                                top = fmaxf(top, __ldcg(&a.ml[slot_of(c) * NR + r]).x);
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1)
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                            for (int c = c0 + lane; c <= c1; c += 32) {
+                                const float2 ml = __ldcg(&a.ml[slot_of(c) * NR + r]);
+                                const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
+                                den = fmaf(f, ml.y, den);
+                                factors[(r - r0) * kMaxCtas + c - c0] = f;
+                            }
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1)
+                                den += __shfl_xor_sync(0xffffffffu, den, o);
+                            if (lane == 0) sums[0][r] = den > 0.0f || den != den ? 1.0f / den : 0.0f;
                         }
-                        if (channel) write(r, den > 0.0f || den != den ? x / den : 0.0f);
+                        meet_128();
+                        if (channel)
+#pragma unroll 1
+                            for (int r = r0; r < r1; r += 4) {
+                                float o[4] = {};
+#pragma unroll 1
+                                for (int c = c0; c <= c1; c += 8) {
+                                    float u[4][8];
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        if (r + q < r1)
+#pragma unroll
+                                            for (int i = 0; i < 8; ++i)
+                                                if (c + i <= c1)
+                                                    u[q][i] = __ldcg(
+                                                        &a.acc[(slot_of(c + i) * NR + r + q) * D + key]);
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q)
+                                        if (r + q < r1)
+#pragma unroll
+                                            for (int i = 0; i < 8; ++i)
+                                                if (c + i <= c1) {
+                                                    const float f = factors[(r + q - r0) * kMaxCtas +
+                                                                            c + i - c0];
+                                                    if (f != 0.0f) o[q] = fmaf(f, u[q][i], o[q]);
+                                                }
+                                }
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (r + q < r1) write(r + q, o[q] * sums[0][r + q]);
+                            }
                     }
+                    meet_128();           // the next tile's P goes there
+                    fence_proxy_async();
                 }
             }
             x += g.j1 - g.j0;
@@ -832,7 +879,7 @@ struct DecodePlan {
 
 DecodePlan plan_of(int rows, int D) {
     DecodePlan w;
-    w.ctas = device_sm_count();
+    w.ctas = device_sm_count() < kMaxCtas ? device_sm_count() : kMaxCtas;
     const size_t nr = rows <= 16 ? 16 : 32;
     w.ml = paged_counter_bytes();
     w.acc = w.ml + (w.ctas * 2 * nr * sizeof(float2) + 255) / 256 * 256;
