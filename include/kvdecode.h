@@ -26,7 +26,7 @@
  *    that returns anything but KVD_OK has enqueued nothing (the one
  *    exception, KVD_ERR_CUDA from a failed launch, is documented there).
  *  - Device pointers must be 16-byte aligned.  Layouts are dense row-major
- *    with the shapes given; no strides.
+ *    with the shapes given; no strides (kvd_heads, below, has one a token).
  *  - Faults found on the device (a bounded wait that ran out) are written to
  *    the cache's optional `dev_status` word (0 = fine); the kernels never
  *    trap.  Read the word after the stream has finished.
@@ -525,7 +525,10 @@ KVD_API kvd_status kvd_qk_norm_rope(const kvd_heads *q, const kvd_heads *q_out,
  * An f16 or int8 kvd_cache is such a cache with one page a sequence: page_size =
  * max_seq, n_pages = batch, page_table[b][0] = b.
  * Rows at or beyond a sequence's length may hold anything, NaN too.
- * The int32s on the device are checked there: a page outside [0, n_pages), a
+ * The calls below refuse (UNSUPPORTED) len above 2^30, and more than 2^31 - 1 key
+ * tiles (batch * n_kv_heads * (len / 128 + 1)) or rows of the pool (n_pages *
+ * n_kv_heads * page_size).
+ * The int32s on the device must not change while a call runs, and are checked there: a page outside [0, n_pages), a
  * length outside [0, len], or starts that fall or leave [0, n_tokens] write
  * KVD_ERR_INVALID to dev_status.  Such a page is neither read nor written (its
  * keys are left out), and a length or a start is moved into its range.  So does
@@ -565,7 +568,8 @@ typedef struct kvd_paged_cache {
 /* No bounds are kept: the selection works on kvd_cache.                     */
 /* Two sequences must not share a page that this call writes.                */
 /* n_tokens == 0 is a no-op.                                                  */
-/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, rot_dim); CUDA.         */
+/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, rot_dim, the cache's     */
+/* counts); CUDA.                                                              */
 /* ---------------------------------------------------------------------- */
 KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_heads *k,
                                     const kvd_heads *v, int32_t n_tokens, const int32_t *starts,
@@ -586,15 +590,15 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*   A non-finite value row spoils the outputs of its own sequence's tokens   */
 /*   in this call, those before it included.                                   */
 /*   q, out: [n_tokens, n_heads, head_dim] of one type: the cache's, or f16 or */
-/*   bf16 over an int8 cache.  softmax_scale > 0.                               */
+/*   bf16 over an int8 cache.  out must not overlap q.  softmax_scale > 0.      */
 /*   max_new: at least the largest n_b (it sizes the grid; the tokens of a     */
 /*   larger n_b are left out, and INVALID is reported to dev_status).          */
 /*   workspace: kvd_paged_workspace_bytes, zero-filled before its first use;   */
 /*   every call that completes leaves its counters at zero again.  Calls that  */
 /*   may overlap on the GPU need a workspace each.                              */
 /* n_tokens == 0 is a no-op.                                                    */
-/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, more than 16 query heads  */
-/* a KV head); WORKSPACE; CUDA.                                                  */
+/* Errors: INVALID; UNSUPPORTED (head_dim, page_size, the cache's counts, more   */
+/* than 16 query heads a KV head); WORKSPACE; CUDA.                              */
 /* ---------------------------------------------------------------------- */
 KVD_API kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q,
                                   int32_t n_tokens, const int32_t *starts, int32_t max_new,

@@ -1,5 +1,5 @@
 // paged.h -- launchers of the norm/rotation, paged append and paged attention
-// kernels (rope.cu, paged_attn.cu) for their C-ABI front end (paged_api.cu).
+// kernels (rope.cu, paged_attn.cu, paged_decode.cu) for their C-ABI front end (paged_api.cu).
 // Arguments are already validated by the caller.
 #pragma once
 
@@ -55,6 +55,9 @@ size_t paged_counter_bytes();
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st);
 size_t paged_attn_ws(const kvd_paged_cache &c, int H, int max_new);
 // At most kDecodeRows rows (new tokens times query heads of a KV head) a sequence.
+// Against the kernel for row tiles: one token over 512 tokens 9.3 us and 23.5, 32 rows
+// over 8 int8 sequences of 131,072 478 us and 767, over f16 ones 687 us and 631 (there
+// the wider tile would be 8 % ahead; over few tokens it is far behind).
 constexpr int kDecodeRows = 32;
 cudaError_t launch_paged_decode(const PagedAttnArgs &a, void *ws, cudaStream_t st);
 size_t paged_decode_ws(int rows, int D);

@@ -2,30 +2,48 @@
 //
 //   out = sum_t softmax(scale q . k_t)_t v_t,   p - window < t <= p
 //
-// One CTA per SM, persistent.  An item is one sequence's run of new tokens and
-// one KV head: the rows are the tokens' query heads of that KV head, up to 128
-// a tensor-core tile, over the key tiles of 128 tokens that any row sees.  All
-// items' key tiles form one line, cut into equal lengths for the CTAs: a long
-// decode spreads over all SMs, a causal chunk's short and long rows balance,
-// and an item that a cut divides is joined from f32 partials by merge_kernel.
+// For sequences with more than kDecodeRows rows (new tokens times query heads of a
+// KV head); fewer go to paged_decode.cu.
 //
-// A CTA runs two softmax streams so that one's exponentials hide behind the
-// other's products.  PAIR (sequences with more rows than a tile): two row tiles
-// over the same keys, each key tile loaded once for 256 rows.  Otherwise (decode
-// and short chunks): one row tile, its key tiles taken in turn by the streams,
-// which are joined at the item's end.
+// One CTA per SM, persistent.  An item is one sequence's run of new tokens and one
+// KV head: the rows are the tokens' query heads of that KV head, 128 a tensor-core
+// tile, over the key tiles of 128 tokens that any row sees.  All items' key tiles
+// form one line, cut into equal lengths for the CTAs: a causal chunk's short and
+// long rows balance, few rows over a long cache spread over all SMs, and an item
+// that a cut divides is joined from f32 partials by merge_kernel (16 warps' blocks
+// an item of 256 rows: one block alone took 13 to 30 us for 19 pieces).
+//
+// A CTA runs two softmax streams so that one's exponentials hide behind the other's
+// products.  kPair (calls with more rows than a tile): two row tiles over the same
+// keys, each key tile loaded once for 256 rows.  kOne (33 to 128 rows): one row
+// tile, its key tiles taken in turn by the streams, which are joined at the item's
+// end.
 //
 // Roles: warps 0-3 and 4-7 the streams' softmax, one row a thread (the row's
-// logits sit in one tensor-memory lane, so no shuffles); warp 8 loads by TMA
-// (pages land as they lie, 16 to 128 rows a box); warp 9 issues the products
+// logits sit in one tensor-memory lane, so no shuffles).  Warp 8 loads queries and
+// keys by TMA, warp 11 values (pages land as they lie, 16 to 128 rows a box; one
+// warp for both fell behind the products at pages of 16).  Warp 9, and in kPair
+// warp 10 for the second stream, issue the products
 //   S = Q K^T   shared x shared      O += P V   P from tensor memory
-// S of one tile is overwritten in place by P, so two streams' S and O fill the
-// 512 columns.  The reference m of a row's weights 2^(logit - m) follows its
-// maximum loosely, within a factor that f16 and f32 hold with the same relative
-// error; that spares the search for each tile's maximum and makes the rescaling
-// of O rare.
-// P is rounded to the input type (the tensor core's operand): a relative error
-// of half a step in each weight, which sums and statistics in f32 do not add to.
+// S of one tile is overwritten in place by P, so two streams' S and O fill the 512
+// columns.  int8: warp 8 loads keys and values as codes, warps 12-15 turn them into
+// f16 or bf16.
+//
+// The reference m of a row's weights 2^(logit - m) follows its maximum loosely,
+// within a factor that f16 and f32 hold with the same relative error; that spares
+// the search for each tile's maximum and makes the rescaling of O rare.
+// P is rounded to the input type (the tensor core's operand): a relative error of
+// half a step in each weight, which sums and statistics in f32 do not add to.
+//
+// What bounds it.  128 channels in f16: the power limit; 2048 tokens over 32,768
+// take 760 us = 1.40 PFLOP/s back to back (0.83 of what a plain matrix product
+// sustains), 670 us from a cool start.  64 channels: the two softmax warps a
+// scheduler has, not its products: 2 x 4001 tokens 105 us = 0.62 PFLOP/s.  int8:
+// the codes' way through shared memory beside the softmax: 250 tokens over 130,250
+// 548 us = 0.97 PFLOP/s.  Few key tiles an SM: the set-up (2.5 us), an item's first
+// loads and its last rows: 24 ragged sequences in a window 129 us = 0.77 PFLOP/s.
+// The roles' code together is near the instruction cache's size, so each stays
+// rolled and in one place: unrolling a role has cost others more than it gained.
 #include <type_traits>
 
 #include "paged_attn_dev.cuh"
@@ -716,7 +734,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             constexpr int kStepRows = kWarpRows * kTeamWarps;  // a multiple of 8
             static_assert(kStepRows % 8 == 0, "the swizzle of a lane's row stays");
             const int ct = place * 32 + lane;
-            uint32_t n = 0, keys = 0;  // tiles and key tiles so far, the other team's too
+            uint32_t n = 0, keys = 0;  // tiles and key tiles so far
             int exp_now = 0;
             bool ok = true;
             // The scales of key tile j for the softmax.
@@ -1191,6 +1209,9 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
         I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     if (!fill_launch(p, a.q_tokens, kv_swizzle, kv_swizzle, a, q_map, k_map, v_map))
         return cudaErrorInvalidValue;
+    // At 2 and at 4 key tiles a CTA at least 64 tokens over 2000 took 22.5 and 26.9 us,
+    // over none 18.0 and 29.3 (an item's fixed cost, 9 us, then comes several times in a
+    // row), over 448 16.6 and 16.3.
     a.min_tiles = 2;
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.merge = reinterpret_cast<int4 *>(base + w.merge);

@@ -18,6 +18,10 @@
 // product with the position, modulo 2^64, is the angle's fraction of a turn with
 // an error below position * 2^-64; its upper 32 bits go to sincospi.  In f32 the
 // product alone is off by 2^-24 of itself: 0.06 radians at position 1,000,000.
+//
+// Measured: 8192 tokens of 32 + 8 heads, bf16, normed and rotated 32.4 us (5.2 TB/s,
+// 0.76 of what a copy reaches); 8190 tokens of 32 + 8 + 8 appended to pages 44 us
+// (4.5 TB/s).  A few tokens take a launch and its host call, 8.7 us.
 #include <type_traits>
 
 #include "common.cuh"
@@ -305,7 +309,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
 template <typename IN, int LPR, int VPL, int U, bool PAGED>
 cudaError_t launch(const RopeArgs &a, cudaStream_t st) {
     constexpr int kRows = 32 / LPR;
-    // Warps a token: one, or as many as give every SM 16 warps
+    // Warps a token: one, or as many as give every SM 16 warps (a few tokens' heads
+    // would otherwise follow one another in one warp)
     const int most = (a.q.n_heads + kRows - 1) / kRows + (a.k.n_heads + kRows - 1) / kRows +
                      (a.v.n_heads + kRows - 1) / kRows;
     const int64_t want = (16ll * device_sm_count() + a.n_tokens - 1) / a.n_tokens;
