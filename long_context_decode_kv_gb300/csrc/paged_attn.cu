@@ -8,7 +8,7 @@
 // One CTA per SM, persistent.  An item is one sequence's run of new tokens and one
 // KV head: the rows are the tokens' query heads of that KV head, 128 a tensor-core
 // tile, over the key tiles of 128 tokens that any row sees.  All items' key tiles
-// form one line, cut into equal lengths for the CTAs: a causal chunk's short and
+// form one line, cut into equal costs for the CTAs: a causal chunk's short and
 // long rows balance, few rows over a long cache spread over all SMs, and an item
 // that a cut divides is joined from f32 partials by merge_kernel (16 warps' blocks
 // an item of 256 rows: one block alone took 13 to 30 us for 19 pieces).
@@ -38,10 +38,10 @@
 // What bounds it.  128 channels in f16: the power limit; 2048 tokens over 32,768
 // take 760 us = 1.40 PFLOP/s back to back (0.83 of what a plain matrix product
 // sustains), 670 us from a cool start.  64 channels: the two softmax warps a
-// scheduler has, not its products: 2 x 4001 tokens 105 us = 0.62 PFLOP/s.  int8:
+// scheduler has, not its products: 2 x 4001 tokens 92 us = 0.71 PFLOP/s.  int8:
 // the codes' way through shared memory beside the softmax: 250 tokens over 130,250
-// 548 us = 0.97 PFLOP/s.  Few key tiles an SM: the set-up (2.5 us), an item's first
-// loads and its last rows: 24 ragged sequences in a window 129 us = 0.77 PFLOP/s.
+// 541 us = 0.98 PFLOP/s.  Few key tiles an SM: the set-up (2.5 us), an item's first
+// loads and its last rows: 24 ragged sequences in a window 120 us = 0.83 PFLOP/s.
 // The roles' code together is near the instruction cache's size, so each stays
 // rolled and in one place: unrolling a role has cost others more than it gained.
 #include <type_traits>
@@ -94,10 +94,19 @@ __device__ __forceinline__ Item item_of(const Dev &a, const Seq &s, int tile, in
     return it;
 }
 
-// A CTA's walk along the line of items' key tiles, the same in every role.
+// What an item takes beside its key tiles (its queries' way in, the first products
+// and its rows' way out), in key tiles: the line is cut by tiles and these together,
+// an item's first kItemCost units standing for it.  Cut by tiles alone the CTAs with
+// many short items were the last by far (SMs busy 0.76 of the time); at 0, 1, 2, 3, 4
+// and 6 units 2 x 4001 tokens at 64 channels took 105, 97, 92, 92.5, 94 and 96 us, 24
+// ragged sequences 129, 122, 120, 120, 120 and 123.
+constexpr int kItemCost = 3;
+
+// A CTA's walk along the line of items, the same in every role.
 struct Walk {
-    int b, head, tile, off;
-    long left;
+    int b, head, tile;
+    int off;    // units of the item that lie before
+    long left;  // units
     int k;  // segments taken
     Seq s;
 };
@@ -112,15 +121,18 @@ struct Segment {
 __device__ __forceinline__ bool next_segment(const Dev &a, int width, Walk &w, Segment &g) {
     if (w.left <= 0) return false;
     g.it = item_of(a, w.s, w.tile, width);
-    const int take = static_cast<int>(min(static_cast<long>(g.it.tiles - w.off), w.left));
+    const int units = g.it.tiles + kItemCost;
+    const int take = static_cast<int>(min(static_cast<long>(units - w.off), w.left));
+    // the item's tiles are another CTA's: it begins with its first tile
+    if (w.off + take <= kItemCost) return false;
     g.b = w.b;
     g.s0 = w.s.s0;
     g.first_pos = w.s.first;
     g.head = w.head;
-    g.j0 = g.it.j0 + w.off;
-    g.j1 = g.j0 + take;
-    g.starts = w.off == 0;
-    g.ends = w.off + take == g.it.tiles;
+    g.j0 = g.it.j0 + max(w.off - kItemCost, 0);
+    g.j1 = g.it.j0 + w.off + take - kItemCost;
+    g.starts = w.off <= kItemCost;
+    g.ends = w.off + take == units;
     g.k = w.k++;
     w.left -= take;
     w.off = 0;
@@ -258,13 +270,13 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     pdl_wait();
     pdl_launch_dependents();
 
-    // ---- this CTA's piece of the line of key tiles
+    // ---- this CTA's piece of the line of items
     auto cost_of = [&](int b, bool report) -> long {
         if (b >= a.c.batch) return 0;
         const Seq s = seq_of(a, b, report);
         long n = 0;
 #pragma unroll 1
-        for (int t = 0; t * width < s.n; ++t) n += item_of(a, s, t, width).tiles;
+        for (int t = 0; t * width < s.n; ++t) n += item_of(a, s, t, width).tiles + kItemCost;
         return n * a.c.n_kv_heads;
     };
     auto scan = [&](long cost, long &before) -> long {  // exclusive prefix, and the sum
@@ -294,7 +306,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             const Seq s = seq_of(a, b, blockIdx.x == 0);
             long n = 0;
 #pragma unroll 1
-            for (int t = lane; t * width < s.n; t += 32) n += item_of(a, s, t, width).tiles;
+            for (int t = lane; t * width < s.n; t += 32)
+                n += item_of(a, s, t, width).tiles + kItemCost;
 #pragma unroll
             for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
             if (lane == 0) seq_tiles[b] = n;
@@ -344,7 +357,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
 #pragma unroll 1
             for (int t0 = 0;; t0 += 32) {
                 const int t = t0 + lane;
-                const int n = t * width < w.s.n ? item_of(a, w.s, t, width).tiles : 0;
+                const int n = t * width < w.s.n ? item_of(a, w.s, t, width).tiles + kItemCost : 0;
                 int upto = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -566,7 +579,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             }
             if (g.starts && !g.ends) {
                 // the item goes on in the next CTAs: leave word for merge_kernel
-                const long rest = g.it.tiles - (g.j1 - g.it.j0);
+                const long rest = g.it.j0 + g.it.tiles - g.j1;  // tiles, and units
                 int pieces = 1;
                 while (cut(blockIdx.x + pieces + 1) - x1 < rest) ++pieces;
                 rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
@@ -1209,10 +1222,7 @@ cudaError_t launch_shape(const PagedAttnArgs &p, const WsPlan &w, void *ws, cuda
         I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B;
     if (!fill_launch(p, a.q_tokens, kv_swizzle, kv_swizzle, a, q_map, k_map, v_map))
         return cudaErrorInvalidValue;
-    // At 2 and at 4 key tiles a CTA at least 64 tokens over 2000 took 22.5 and 26.9 us,
-    // over none 18.0 and 29.3 (an item's fixed cost, 9 us, then comes several times in a
-    // row), over 448 16.6 and 16.3.
-    a.min_tiles = 2;
+    a.min_tiles = kItemCost + 1;  // an item's first CTA takes a tile
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.merge = reinterpret_cast<int4 *>(base + w.merge);
     a.ml = reinterpret_cast<float2 *>(base + w.ml);

@@ -26,7 +26,7 @@ struct AttnArgs {  // of a launch
     float scale_log2;
     int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
     int dead_row;       // a cache row outside the pool
-    int min_tiles;      // least key tiles a CTA takes
+    int min_tiles;      // least key tiles a CTA takes (row tiles: with what an item costs)
 };
 
 // mbar_wait for the waits between the roles, in few instructions: the roles' hot
