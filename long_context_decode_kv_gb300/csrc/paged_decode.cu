@@ -27,7 +27,7 @@
 // compute the tile again, as the first tile of an item does, and each one until all
 // rows have seen a key (a window or a bad page may hide the first tiles from some).
 //
-// Measured: 8 sequences of 131,072 tokens, 32 heads over 8: 359 us int8 (6.2 TB/s,
+// Measured: 8 sequences of 131,072 tokens, 32 heads over 8: 361 us int8 (6.1 TB/s,
 // 0.91 of what a copy reaches), 610 us f16 (7.0 TB/s).  A decode step on 4 int8
 // sequences of 32,000 takes 65 us (0.62): a CTA's 20 tiles then stand beside the
 // set-up, the first bytes and the join.  One token over 512: 8.3 us, of which a
@@ -320,6 +320,18 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     if (lane == 0) dead_groups[n & 15] = groups;
                     if (I8 && lane < boxes) tile_rows[n & 15][lane] = row;
                     __syncwarp();
+                    if constexpr (I8) {
+                        // The scales, which the turning warps read later, on their way to
+                        // the L2: 16 tokens a lane, keys' and values'.  (8 sequences of
+                        // 131,072 tokens, several caches in turn: 402 us without, 362.)
+                        const int group = lane & 7;
+                        const int box_row = __shfl_sync(0xffffffffu, row, group / k);
+                        const float *sc = static_cast<const float *>(lane < 8 ? a.c.k_scale
+                                                                              : a.c.v_scale);
+                        if (lane < 16 && box_row != a.dead_row)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                                sc + box_row + group % k * 16));
+                    }
                 }
                 if (lane == 0) mbar_arrive_expect_tx(&full[st], I8 ? kTile * D : Sh::kTileBytes);
                 __syncwarp();
