@@ -594,8 +594,9 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*   max_new: at least the largest n_b (it sizes the grid; the tokens of a     */
 /*   larger n_b are left out, and INVALID is reported to dev_status).          */
 /*   workspace: kvd_paged_workspace_bytes, zero-filled before its first use;   */
-/*   every call that completes leaves its counters at zero again.  Calls that  */
-/*   may overlap on the GPU need a workspace each.                              */
+/*   every call that completes leaves its counters at zero again (after a       */
+/*   KVD_ERR_TIMEOUT in dev_status, zero it).  Calls that may overlap on the    */
+/*   GPU need a workspace each.                                                  */
 /* n_tokens == 0 is a no-op.                                                    */
 /* Errors: INVALID; UNSUPPORTED (head_dim, page_size, the cache's counts, more   */
 /* than 16 query heads a KV head); WORKSPACE; CUDA.                              */

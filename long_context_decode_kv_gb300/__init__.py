@@ -621,7 +621,8 @@ def paged_workspace_bytes(cache: PagedKVCache, n_heads: int, n_tokens: int, max_
 def make_paged_workspace(cache: PagedKVCache, n_heads: int, n_tokens: int,
                          max_new: int) -> torch.Tensor:
     """A zero-filled workspace for paged_attn calls of up to n_tokens new tokens, up to
-    max_new a sequence."""
+    max_new a sequence.  Calls that may overlap on the GPU need one each; after a wait
+    that ran out (KVD_ERR_TIMEOUT in the device status) it has to be zeroed."""
     n = paged_workspace_bytes(cache, n_heads, n_tokens, max_new)
     if n == 0:
         raise KvdError("kvd_paged_workspace_bytes", 1)

@@ -381,6 +381,16 @@ def test_33_to_128_rows(dtype, x, D, G, new, window):
 
 
 @pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
+@pytest.mark.parametrize("B,every,longest", [(1500, 3, 2), (700, 50, 40), (400, 7, 20), (45, 4, 90)])
+def test_large_batches(dtype, B, every, longest):
+    """More sequences than a block has threads, most of one token, some with none, a few with more."""
+    lens = [1 + b * 37 % 301 for b in range(B)]
+    new = [min(longest if b % every == 0 else b % every % 2, lens[b]) for b in range(B)]
+    c = _cache(dtype, lens, 1, 64, 32, B)
+    _check_attn(c, _q(sum(new), 4, 64, torch.float16, B), new, max_new=longest)
+
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
 def test_one_workspace_for_calls_of_every_length(dtype):
     """Made for the longest, used by chunks and single tokens in turn, and by two graphs of them."""
     H, D = 8, 128
