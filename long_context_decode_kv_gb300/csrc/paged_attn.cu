@@ -1179,8 +1179,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Dev 
                               ((slot * blocks + prow / 32) * (D / 4) + 2 * c8) * 32 + lane;
             const float4 u0 = p[0], u1 = p[32];
             const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+            l = fmaf(f, ml.y, l);  // a sum that is NaN stays one where f is 0
             if (f != 0.0f) {
-                l = fmaf(f, ml.y, l);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) o[c] = fmaf(f, u[c], o[c]);
             }
