@@ -855,8 +855,9 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             // keys [lo, hi) of this row
             const int hi = row < rows ? max(pos + 1, 0) : 0x7fffffff;
             const int lo = row < rows && a.window > 0 ? max(pos - a.window + 1, 0) : 0;
-            float m = row < rows ? -INFINITY : 0.0f;
-            // rows that are none keep a scale of their own
+            // Rows that are none (another sequence's queries stand there, or what the memory
+            // held): weights of 0 or NaN, and so no say in the votes
+            float m = row < rows ? -INFINITY : INFINITY;
             float l = 0.0f, last = 0.0f;
             const int first = PAIR ? part.j0 : j0 + t;
             int exp_now = 0;  // int8: O is in units of 2^exp_now

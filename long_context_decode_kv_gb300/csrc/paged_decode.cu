@@ -684,7 +684,11 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             f_s[tid] = m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                             m_s[tid] = mn;
                             none = tid < rows && mn == -INFINITY;
-                            base_s[tid] = mn == -INFINITY ? 0.0f : -mn;
+                            // rows that are none (another sequence's queries may stand
+                            // there): no weights, and no say in the votes
+                            base_s[tid] = tid >= rows      ? -INFINITY
+                                          : mn == -INFINITY ? 0.0f
+                                                            : -mn;
                             if (tid == 0) {
                                 unit_s[1] = j == g.j0 ? 1.0f : unit / unit_s[0];
                                 unit_s[0] = unit;

@@ -36,3 +36,33 @@ def test_a_query_that_is_not_finite_gives_a_nan_row(dtype, new, L):
     assert bool(torch.isnan(out[bad]).all())
     R.assert_within(out[~bad], want[~bad], tol[~bad])
     assert c.device_status() == 0
+
+
+# --------------------------------------------------------------- neighbours ---
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.BF16, kvd.INT8])
+@pytest.mark.parametrize("G,new", [(4, [1, 8]), (7, [2, 4]), (4, [9, 30]), (7, [5, 18]), (4, [20, 200]),
+                                   (3, [50, 300]), (7, [25, 90])])
+def test_a_sequence_does_not_depend_on_its_neighbour(dtype, G, new):
+    """The tile's rows behind a sequence's last are the next one's queries, or none's."""
+    c = _cache(dtype, [2000, 2300], 2, 128, 64, G)
+    q = _q(sum(new), 2 * G, 128, _x(dtype), G)
+    n = new[0]
+    first = _attend(c, q, new)[:n]
+    for other in (300.0, 0.0, math.nan):
+        p = q.clone()
+        p[n:] *= other
+        assert torch.equal(_attend(c, p, new)[:n], first)
+
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.BF16, kvd.INT8])
+@pytest.mark.parametrize("G,new", [(7, 4), (4, 20), (3, 11), (7, 200), (6, 300)])
+def test_a_call_does_not_depend_on_the_one_before(dtype, G, new):
+    """Rows of a tile that hold no query, after calls whose queries filled them with large values."""
+    c = _cache(dtype, [3000], 2, 128, 64, G + new)
+    q = _q(new, 2 * G, 128, _x(dtype), new)
+    first = _attend(c, q, [new])
+    for scale in (1e3, math.nan):
+        for g, n in ((G, new), (8, 16), (8, 200), (16, 2)):
+            _attend(c, torch.full((n, 2 * g, 128), scale, dtype=q.dtype, device=DEV), [n])
+        assert torch.equal(_attend(c, q, [new]), first)
