@@ -30,10 +30,11 @@
 // f16 or bf16.
 //
 // The reference m of a row's weights 2^(logit - m) follows its maximum loosely,
-// within a factor that f16 and f32 hold with the same relative error; that spares
-// the search for each tile's maximum and makes the rescaling of O rare.
-// P is rounded to the input type (the tensor core's operand): a relative error of
-// half a step in each weight, which sums and statistics in f32 do not add to.
+// from below: that spares the search for each tile's maximum, makes the rescaling of
+// O rare, and leaves small weights the range of f16 (lift_of).
+// P is rounded to the tensor core's operand type, bf16 for bf16 caches and f16 for f16
+// and int8 ones: half a step of each weight, and in f16 at least 2^-31 (int8: 2^-29)
+// of the row's largest.  Sums and statistics in f32 do not add to that.
 //
 // What bounds it.  128 channels in f16: the power limit; 2048 tokens over 32,768
 // take 760 us = 1.40 PFLOP/s back to back (0.83 of what a plain matrix product
@@ -62,10 +63,14 @@ constexpr int threads_of(bool i8) { return i8 ? 512 : 384; }
 constexpr int softmax_regs(bool i8) { return i8 ? 184 : 208; }
 constexpr int other_regs(bool i8) { return i8 ? 72 : 88; }
 constexpr int kTeam = 12, kTeamWarps = 4;  // warps that turn int8 codes
-// A row's weights are 2^(logit - m) with an m near its maximum: a tile whose
-// weights add up to more than kRaise raises m for the next one, and one above
-// kRedo is computed again (f16 holds weights up to 65,504).
-constexpr float kRaise = 256.0f, kRedo = 8192.0f;
+// A row's weights are 2^(logit - m).  m is set `lift` places below the row's maximum:
+// f16 holds numbers from 2^-24 (with all their bits from 2^-14) to 2^16, and a row
+// whose largest weight is an early key's (a sink's, say) has millions of small ones.  A
+// tile whose weights add up to more than kRaise (twice 128 weights of 2^lift) raises m
+// for the next one, and one above kRedo is computed again.  What has to fit is then
+// kRedo, and for int8 kRedo times a value scale below 2 (value_exp).  With lift 0 one
+// key with 0.99 of 131,072 keys' weight cost the others up to 0.3 % of theirs.
+constexpr float lift_of(bool i8) { return i8 ? 5.0f : 6.0f; }
 
 struct Dev : AttnArgs {
     int q_tokens;       // tokens of a row tile: 128 / G (kPair), or max_new
@@ -209,6 +214,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     // int8: weights and value codes are f16 whatever the queries are (three more
     // bits, and the codes take fewer instructions)
     constexpr bool kPBf16 = BF16 && !I8;
+    constexpr float kLift = lift_of(I8);
+    constexpr float kRaise = I8 ? 8192.0f : 16384.0f, kRedo = 2.0f * kRaise;  // 2^(lift + 8)
     constexpr int kThreads = threads_of(I8);
     constexpr int kHalves = D / 64;
     constexpr int kHalfBytes = kTile * 128;
@@ -768,8 +775,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
                 const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 100);
-                // kept while the scales stay below 4: weights up to kRedo fit f16
-                if (first || e > exp_now + 2) exp_now = e;
+                // kept while the scales stay below 2: weights up to kRedo fit f16
+                if (first || e > exp_now + 1) exp_now = e;
                 const float unit = __int_as_float((127 - exp_now) << 23);
                 float *to = scales + keys % Sh::kScales * (2 * kTile);
 #pragma unroll
@@ -939,8 +946,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                                 }
                             }
                             const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]) *
-                                              (I8 ? 1.0f : a.scale_log2);
-                            const float mn = fmaxf(last > kRaise ? m + __log2f(last) - 7.0f : m, top);
+                                                  (I8 ? 1.0f : a.scale_log2) -
+                                              kLift;
+                            const float mn = fmaxf(
+                                last > kRaise ? m + __log2f(last) - (kLift + 7.0f) : m, top);
                             const float f = m == -INFINITY || mn == -INFINITY
                                                 ? 1.0f
                                                 : exp2_approx(m - mn);
@@ -1025,7 +1034,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         }
                         sum[0] = __fadd2_rn(sum[0], sum[1]);
                         last = sum[0].x + sum[0].y;
-                        // after a fix no weight passes 1
+                        // after a fix no weight passes 2^lift
                         if (fix || !__any_sync(0xffffffffu, last > kRedo)) break;
                         fix = true;
                         last = 0.0f;

@@ -22,10 +22,11 @@
 // by the warps that turn the keys: as copies of a page's 16 to 128 numbers they
 // would keep the loading warp longer than the codes do.
 //
-// The weights' reference m follows a row's maximum loosely: a weight that passes
-// 2^13 (rarely any; f16 holds 2^16) has the four warps find the maximum and
-// compute the tile again, as the first tile of an item does, and each one until all
-// rows have seen a key (a window or a bad page may hide the first tiles from some).
+// The weights' reference m follows a row's maximum loosely, from kLift places below it
+// (f16's range, see paged_attn.cu): a weight that passes kRedo (rarely any) has the
+// four warps find the maximum and compute the tile again, as the first tile of an item
+// does, and each one until all rows have seen a key (a window or a bad page may hide
+// the first tiles from some).
 //
 // Measured: 8 sequences of 131,072 tokens, 32 heads over 8: 361 us int8 (6.1 TB/s,
 // 0.91 of what a copy reaches), 610 us f16 (7.0 TB/s).  A decode step on 4 int8
@@ -38,7 +39,7 @@ namespace kvd {
 namespace {
 
 constexpr int kMaxCtas = 256;     // one an SM
-constexpr float kRedo = 8192.0f;  // above it a weight asks for a new reference
+constexpr float kLift = 6.0f;     // a new reference: so far below the row's maximum
 
 // Barriers of the 128 softmax threads; the second tells whether any said yes.
 __device__ __forceinline__ void meet_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -144,6 +145,8 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
     // int8: weights and value codes are f16 whatever the queries are (three more
     // bits, and the codes take fewer instructions)
     constexpr bool kPBf16 = BF16 && !I8;
+    // above it a weight asks for a new reference (int8: weights are stored times up to 4)
+    constexpr float kRedo = I8 ? 8192.0f : 32768.0f;
 
     extern __shared__ uint8_t raw_smem[];
     __shared__ DecodeBars bar;
@@ -680,7 +683,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             for (int i = 0; i < 4; ++i) k = max(k, __float_as_uint(red[i][tid]));
                             const float top = key_to_float(k);
                             const float m = j == g.j0 ? -INFINITY : m_s[tid];
-                            const float mn = fmaxf(m, top);
+                            const float mn = fmaxf(m, top - kLift);
                             f_s[tid] = m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                             m_s[tid] = mn;
                             none = tid < rows && mn == -INFINITY;
@@ -735,7 +738,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             if (!(seen >> r & 1)) p[r] = 0.0f;
 #pragma unroll
                     for (int r = 0; r < NR; r += 2) top = fmax3(top, p[r], p[r + 1]);
-                    if (fix) break;  // no weight passes 1
+                    if (fix) break;  // no weight passes 2^kLift
                     if (!any_of_128(top > kRedo || (I8 && v > 4.0f))) break;
                     fix = true;
                 }

@@ -66,3 +66,94 @@ def test_a_call_does_not_depend_on_the_one_before(dtype, G, new):
         for g, n in ((G, new), (8, 16), (8, 200), (16, 2)):
             _attend(c, torch.full((n, 2 * g, 128), scale, dtype=q.dtype, device=DEV), [n])
         assert torch.equal(_attend(c, q, [new]), first)
+
+
+# ------------------------------------------------ weights of very different size ---
+
+U16 = 2.0 ** -11            # f16: half a step of a weight, relative; 2^-25 below 2^-14
+# Binary places above 1 that a row's largest weight takes, so that small ones keep as many more
+# (int8: of the product with the value's scale, which may be half of the unit it is counted in).
+REACH = {kvd.F16: 6, kvd.INT8: 4}
+
+
+def _set_rows(c, b, name, values, scale=None):
+    """Tokens [0, n) of sequence b, every KV head: values [n, D] (int8: codes, with scales [n])."""
+    n = values.shape[0]
+    p = torch.arange(n, device=DEV)
+    page, off = c.page_table[b, p // c.page_size].long(), p % c.page_size
+    c.t[name][page, :, off] = values[:, None].to(c.t[name].dtype)
+    if scale is not None:
+        c.t[name + "_scale"][page, :, off] = scale[:, None].float()
+
+
+def _few_channels(c, b, L, z, v, v_scale):
+    """A cache whose logits are z[t] (through channel 0 of a query of ones) and whose values are v[t]."""
+    k = torch.zeros(L, c.head_dim, device=DEV)
+    if c.dtype == kvd.INT8:
+        k[:, 0] = torch.where(z == 0, 0.0, 127.0 * z.sign())
+        _set_rows(c, b, "k", k, torch.where(z == 0, 1.0, z.abs() / 127).float())
+        _set_rows(c, b, "v", v, v_scale)
+    else:
+        k[:, 0] = z
+        _set_rows(c, b, "k", k)
+        _set_rows(c, b, "v", v * v_scale[:, None])
+
+
+@pytest.mark.parametrize("dtype,x", [(kvd.F16, torch.float16), (kvd.INT8, torch.float16),
+                                     (kvd.INT8, torch.bfloat16)])
+@pytest.mark.parametrize("new,L", SHAPES)
+@pytest.mark.parametrize("at", [0, 40, 390])
+@pytest.mark.parametrize("below", [22.4, 25.6])
+def test_one_key_holds_nearly_all_the_weight(dtype, x, new, L, at, below):
+    """The others are 2^-below of it each.  Its value is zero, so that theirs is what comes out.
+
+    A weight is off by half a step (2^-11 of it), or below f16's normal numbers by 2^-25 of
+    their reference, which lies REACH places below the row's largest weight; by its logit (2^-22
+    of it, and the exponential's 2^-22); the sums and the output add their own."""
+    if L <= at:
+        pytest.skip("the key lies behind the sequence")
+    D = 128
+    c = _cache(dtype, [L], 2, D, 64, L)
+    z = torch.zeros(L, device=DEV)
+    z[at] = 16.0
+    v = torch.full((L, D), 127.0, device=DEV)
+    v[at] = 0.0
+    _few_channels(c, 0, L, z, v, torch.full((L,), 8.0, device=DEV))
+    q = torch.zeros(new, 8, D, dtype=x, device=DEV)
+    q[..., 0] = 1.0
+    scale = below * math.log(2) / 16
+    out = _attend(c, q, [new], scale=scale).double()
+    p = torch.arange(L - new, L, device=DEV).double()
+    rest = torch.where(p >= at, p, p + 1)                  # keys beside it that a token sees
+    w = torch.where(p >= at, 2.0 ** -below, 1.0)
+    want = 1016 * rest * w / (rest * w + (p >= at))
+    off = torch.where(p >= at, 2.0 ** (-25 - REACH[dtype]) / w, 0.0)
+    err = want * (off.clamp_min(U16) + below * 2.0 ** -22 + (rest / 8 + 64) * 2.0 ** -23) * 1.01
+    tol = R.rounding(want, err, x)
+    R.assert_within(out, want[:, None, None].expand_as(out), tol[:, None, None].expand_as(out))
+    assert c.device_status() == 0
+
+
+def test_an_attention_sink_over_a_long_cache():
+    """131,072 keys, the first with 0.9 or 0.99 of the weight: what is left of the others' weights."""
+    D, L = 128, 131072
+    c = _cache(kvd.F16, [L], 1, D, 64, 9)
+    q = torch.zeros(1, 4, D, dtype=torch.float16, device=DEV)
+    q[..., 0] = 1.0
+    g = torch.Generator(device=DEV).manual_seed(10)
+    for share in (0.9, 0.99):
+        z = torch.randn(L, generator=g, device=DEV).half().float()
+        z[0] = 0.0
+        z[0] = float((z[1:].double().exp().sum() * share / (1 - share)).log())
+        z = z.half().float()
+        v = (torch.randn(L, D, generator=g, device=DEV) + 0.3).half().float()
+        _few_channels(c, 0, L, z, v, torch.ones(L, device=DEV))
+        out = _attend(c, q, [1], scale=1.0)[0].double()
+        w = torch.softmax(z.double(), 0)
+        want = w @ v.double()
+        # each weight's rounding taken as independent of the others': six deviations of their sum
+        step = torch.maximum(w * U16, 2.0 ** -25 / 2 ** REACH[kvd.F16] * w.max())
+        err = 6 * (step.square() @ v.double().square()).sqrt() / 3 ** 0.5
+        # logits, exponentials, and the running sums of 16 keys a step in the longest piece
+        err = err + (w @ v.double().abs()) * (32 * 2.0 ** -22 + (L / 152 / 8 + 512) * 2.0 ** -23)
+        R.assert_within(out, want.expand(4, D), R.rounding(want, err, torch.float16).expand(4, D))
