@@ -755,7 +755,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             static_assert(kStepRows % 8 == 0, "the swizzle of a lane's row stays");
             const int ct = place * 32 + lane;
             uint32_t n = 0, keys = 0;  // tiles and key tiles so far
-            int exp_now = 0;
+            ScaleUnit unit = {};
             bool ok = true;
             // The scales of key tile j for the softmax.
             auto turn_scales = [&](const float *sc, int j, bool first) {
@@ -774,19 +774,17 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                     if (v < 0x7f800000u && !(edge && dead(i * 32 + lane))) top = max(top, v);
                 }
                 top = __reduce_max_sync(0xffffffffu, top);
-                const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 100);
-                // kept while the scales stay below 2: weights up to kRedo fit f16
-                if (first || e > exp_now + 1) exp_now = e;
-                const float unit = __int_as_float((127 - exp_now) << 23);
+                unit.take(top, first, 1);  // scales below 2: weights up to kRedo fit f16
+                const float inv = __int_as_float((127 - unit.exp) << 23);
                 float *to = scales + keys % Sh::kScales * (2 * kTile);
 #pragma unroll
                 for (int at = ct; at < kTile; at += kTeamThreads) {
-                    float ks = sc[at] * a.scale_log2, vs = sc[kTile + at] * unit;
+                    float ks = sc[at] * a.scale_log2, vs = sc[kTile + at] * inv;
                     if (edge && dead(at)) ks = vs = 0.0f;
                     to[at] = ks;
                     to[kTile + at] = vs;
                 }
-                if (ct == 0) value_exp[keys % Sh::kScales] = exp_now;
+                if (ct == 0) value_exp[keys % Sh::kScales] = unit.exp;
             };
             // Tile n.
             auto turn = [&](bool is_k, int j, bool first) -> bool {
@@ -957,7 +955,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                             last = 0.0f;
                             l *= f;
                             if (j > first) {
-                                // by at most 2^-200 in one step: 0 where it matters
+                                // up by at most 2^60 (ScaleUnit), down to 0 where it matters
                                 const float fo =
                                     I8 ? f * exp2_approx(static_cast<float>(exp_now - new_exp)) : f;
 #pragma unroll 1

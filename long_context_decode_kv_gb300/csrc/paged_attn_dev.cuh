@@ -64,6 +64,29 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs &a, int b, bool report) {
     return s;
 }
 
+// int8: weights are stored times their values' scales, in units of 2^exp, and O is
+// counted in the same units.  The exponent follows the tiles' largest scales in both
+// directions (O is scaled where it changes), so that a tile with one far larger scale
+// takes f16's range from its own keys alone and not from all that follow it.
+struct ScaleUnit {
+    int exp, peak;  // the peak of the run of tiles so far
+    // The bits of a tile's largest finite scale (0: none but zeros).  `room`: how many
+    // places scales may pass the unit.  It falls where they are more than 5 below (the
+    // weights' lift stands against those 5; a change costs a pass over O, so scales that
+    // merely vary should cause none), and to at most 60 below the peak, from where O in
+    // smaller units could overflow f32.
+    __device__ __forceinline__ void take(uint32_t top, bool first, int room) {
+        const int e = min(max(static_cast<int>(top >> 23) - 126, -100), 100);
+        if (first)
+            exp = peak = e;
+        else if (e > exp + room)
+            exp = e;
+        else if (e < exp - 5 && top != 0)
+            exp = max(e, peak - 60);
+        peak = max(peak, exp);
+    }
+};
+
 // Four int8 codes as two words of f16 or bf16, exactly.  f16: code + 128 in the
 // low bits of 1024 + x, less 1152.  bf16: 128 + (code's low 7 bits), less 128 or,
 // for a negative code, 256.

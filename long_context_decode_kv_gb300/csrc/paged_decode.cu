@@ -156,8 +156,8 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
     __shared__ int tile_rows[16][8];      // int8, per key tile: its boxes' cache rows
     __shared__ float2 scales[I8 ? 4 : 1][kTile];  // and its keys' scales of keys and values
     __shared__ __align__(16) float m_s[NR], base_s[NR], f_s[NR];  // references, less or 0, to a new one
-    __shared__ float red[4][NR], sums[4][NR], top_scale[4];
-    __shared__ float unit_s[2];  // int8: O in units of unit_s[1]; value scales times unit_s[0]
+    __shared__ float red[4][NR], sums[4][NR];
+    __shared__ uint32_t top_scale[4];  // int8: bits of the warps' largest value scales
 
     uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     uint8_t *q_smem = smem;
@@ -608,7 +608,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             float l[NR];
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.0f;
-            float unit = 1.0f;  // int8: value scales are taken times it
+            ScaleUnit unit = {};  // int8
             bool open = true;   // a row has seen no key yet, and so has no reference
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
@@ -663,19 +663,16 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             const uint32_t u = __float_as_uint(vs);
                             const uint32_t top =
                                 __reduce_max_sync(0xffffffffu, u < 0x7f800000u ? u : 0u);
-                            if (lane == 0) top_scale[warp] = __uint_as_float(top);
+                            if (lane == 0) top_scale[warp] = top;
                         }
                         // O as it stands is complete
                         if (j > g.j0) wait(&bar.o_done[b ^ 1], ((n - 1) >> 1) & 1);
                         meet_128();
-                        if constexpr (I8) {
-                            // a power of two near the largest value scale
-                            const float top = fmaxf(fmaxf(top_scale[0], top_scale[1]),
-                                                    fmaxf(top_scale[2], top_scale[3]));
-                            const int e = min(max((__float_as_int(top) >> 23 & 255) - 126, -100), 100);
-                            const float fresh = __int_as_float((127 - e) << 23);
-                            if (j == g.j0 || fresh < unit) unit = fresh;  // same in all threads
-                        }
+                        const int old_exp = unit.exp;
+                        if constexpr (I8)  // (the 2: weights times up to 4 fit f16)
+                            unit.take(max(max(top_scale[0], top_scale[1]),
+                                          max(top_scale[2], top_scale[3])),
+                                      j == g.j0, 2);
                         bool none = false;
                         if (tid < NR) {
                             uint32_t k = 0;
@@ -692,13 +689,11 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             base_s[tid] = tid >= rows      ? -INFINITY
                                           : mn == -INFINITY ? 0.0f
                                                             : -mn;
-                            if (tid == 0) {
-                                unit_s[1] = j == g.j0 ? 1.0f : unit / unit_s[0];
-                                unit_s[0] = unit;
-                            }
                         }
                         open = any_of_128(none);
-                        const float fu = I8 ? unit_s[1] : 1.0f;
+                        // up by at most 2^60 (ScaleUnit), down to 0 where it matters
+                        const float fu =
+                            I8 ? exp2_approx(static_cast<float>(old_exp - unit.exp)) : 1.0f;
 #pragma unroll
                         for (int r = 0; r < NR; ++r) l[r] *= f_s[r];
                         if (j > g.j0) {
@@ -717,7 +712,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                             tmem_fence_before();
                         }
                     }
-                    v = I8 ? vs * unit : 1.0f;
+                    v = I8 ? vs * __int_as_float((127 - unit.exp) << 23) : 1.0f;
                     const float2 k2 = make_float2(ks, ks);
                     float top = 0.0f;
 #pragma unroll
@@ -739,7 +734,11 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
 #pragma unroll
                     for (int r = 0; r < NR; r += 2) top = fmax3(top, p[r], p[r + 1]);
                     if (fix) break;  // no weight passes 2^kLift
-                    if (!any_of_128(top > kRedo || (I8 && v > 4.0f))) break;
+                    // int8: a new unit too, where a scale does not fit, or a warp's are
+                    // so small that the unit may have to fall
+                    const bool low = I8 && !__any_sync(0xffffffffu, v >= 0x1p-6f) &&
+                                     __any_sync(0xffffffffu, v > 0.0f);
+                    if (!any_of_128(top > kRedo || (I8 && v > 4.0f) || low)) break;
                     fix = true;
                 }
                 // the weights, and P^T: row r's 128 keys in two swizzled halves
@@ -784,7 +783,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             for (int i = 0; i < NR; i += 16) pin16(o + i);
             const bool channel = key < D;
             const bool whole = g.off == 0 && g.j1 - g.j0 == g.tiles;
-            const float out_unit = I8 ? 1.0f / unit : 1.0f;  // a power of two
+            const float out_unit = I8 ? __int_as_float((127 + unit.exp) << 23) : 1.0f;
             uint16_t *out = a.out + static_cast<int64_t>(g.s.s0) * a.out_stride +
                             static_cast<int64_t>(g.head) * a.G * D + key;
             const float inv = sum > 0.0f || sum != sum ? out_unit / sum : 0.0f;

@@ -157,3 +157,41 @@ def test_an_attention_sink_over_a_long_cache():
         # logits, exponentials, and the running sums of 16 keys a step in the longest piece
         err = err + (w @ v.double().abs()) * (32 * 2.0 ** -22 + (L / 152 / 8 + 512) * 2.0 ** -23)
         R.assert_within(out, want.expand(4, D), R.rounding(want, err, torch.float16).expand(4, D))
+
+
+@pytest.mark.parametrize("x", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("new,L", [s for s in SHAPES if s[1] >= 300])
+@pytest.mark.parametrize("at", [0, 200])
+@pytest.mark.parametrize("places", [12, 24])
+def test_one_large_value_scale_on_a_key_without_weight(x, new, L, at, places):
+    """Its scale is 2^places of the others', and its weight 2^-100: only the keys of its own tile
+    may lose what f16 cannot hold beside it.
+
+    A product of weight and scale is off by half a step, or by 2^-25 in units of at most 64 times
+    the tile's largest scale (the unit is the power of two above that, or up to 2^5 of it before
+    it falls)."""
+    D = 128
+    c = _cache(kvd.INT8, [L], 2, D, 64, L)
+    g = torch.Generator(device=DEV).manual_seed(L + at)
+    z = torch.zeros(L, device=DEV)
+    z[at] = -100.0
+    v = torch.randint(64, 128, (L, D), generator=g, device=DEV).float()
+    vs = torch.rand(L, generator=g, device=DEV) * 0.5 + 0.5
+    vs[at] *= 2.0 ** places
+    _few_channels(c, 0, L, z, v, vs)
+    q = torch.zeros(new, 8, D, dtype=x, device=DEV)
+    q[..., 0] = 1.0
+    out = _attend(c, q, [new], scale=math.log(2)).double()
+    p = torch.arange(L - new, L, device=DEV)
+    t = torch.arange(L, device=DEV)
+    w = ((t <= p[:, None]) & (t != at)).double()
+    l = w.sum(-1, keepdim=True)
+    top = torch.stack([s.max() for s in vs.split(128)]).repeat_interleave(128)[:L].double()
+    val = v.double() * vs.double()[:, None]
+    want = w @ val / l
+    step = torch.maximum(U16 * vs.double(), 2.0 ** (-25 - REACH[kvd.INT8]) * 64 * top)
+    err = w @ (v.double() * step[:, None]) / l
+    err = err + want * ((l / 8 + 64) * 2.0 ** -23) * 1.01
+    want, tol = (a[:, None].expand_as(out) for a in (want, R.rounding(want, err, x)))
+    R.assert_within(out, want, tol)
+    assert c.device_status() == 0
