@@ -235,6 +235,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     __shared__ long found_rest;
     __shared__ int found_seq;
     __shared__ Walk start;
+    __shared__ uint4 loads[2];  // the loading warps' last: places and parities, of queries too
 
     uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
     uint8_t *q_smem = smem;
@@ -455,6 +456,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
         // waits for every second one never falls a whole turn behind.
         uint32_t used = 0, phase = 0;
         uint32_t filled = 0, fills = 0;  // places whose full barrier was used; its next parity
+        uint32_t q_filled = 0, q_fills = 0;  // and q_full's
         uint32_t q_phase = 0;
         bool ok = true;
         int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
@@ -473,6 +475,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 for (int t = 0; t < (PAIR ? 2 : 1); ++t) {
                     const Part p = part_of(g, t);
                     if (p.j0 == p.j1) continue;
+                    q_filled |= 1u << t;
+                    q_fills ^= 1u << t;
                     mbar_arrive_expect_tx(&bar.q_full[t], rows * 128 * kHalves);
 #pragma unroll 1
                     for (int h = 0; h < kHalves; ++h)
@@ -568,7 +572,10 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                         fills ^= 1u << st;
                     }
                     if (is_k == first_warp) {
-                        if (again && !(ok = wait_for(&bar.kv_empty[st], parity, abort))) break;
+                        if (again && !(ok = wait_for(&bar.kv_empty[st], parity, abort))) {
+                            fills ^= 1u << (full - bar.kv_full);  // not loaded
+                            break;
+                        }
                         if (lane == 0) {
                             mbar_arrive_expect_tx(full, Sh::kTileBytes);
                             if (is_k ? pre : kj == j1) mbar_arrive(full);
@@ -598,13 +605,7 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
             a.merge[2 * blockIdx.x] = rec0;
             a.merge[2 * blockIdx.x + 1] = rec1;
         }
-        if (*abort) {
-            // nothing may land in shared memory after the CTA has gone
-            volatile int none = 0;
-            uint64_t *full = I8 ? bar.raw_full : bar.kv_full;
-            for (uint32_t st = 0; st < 8; ++st)
-                if (filled >> st & 1) mbar_wait(&full[st], ~(fills >> st) & 1, &none);
-        }
+        if (lane == 0) loads[first_warp] = make_uint4(filled, fills, q_filled, q_fills);
         } else if (warp == kIssuer || (PAIR && warp == kIssuer + 1)) {
             // ------------------------------------------------ products ---
             // An issued product waits until the tensor pipe has room, so a warp that
@@ -1147,6 +1148,19 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
     }
     tmem_fence_before();
     __syncthreads();
+    if (*abort && (warp == kProducer || (!I8 && warp == kValueProducer))) {
+        // nothing may land in shared memory after the CTA has gone
+        const uint4 of = loads[warp == kProducer];
+        volatile int none = 0;
+        uint64_t *full = I8 ? bar.raw_full : bar.kv_full;
+        // a wait that runs out is for the other warp's part of a barrier; by then all
+        // has had the time to land
+        bool landed = true;
+        for (uint32_t st = 0; landed && st < 8; ++st)
+            if (of.x >> st & 1) landed = mbar_wait(&full[st], ~(of.y >> st) & 1, &none);
+        for (uint32_t t = 0; landed && t < 2; ++t)
+            if (of.z >> t & 1) landed = mbar_wait(&bar.q_full[t], ~(of.w >> t) & 1, &none);
+    }
     if (warp == kIssuer) {
         tmem_fence_after();
         tmem_free(tmem, 512);

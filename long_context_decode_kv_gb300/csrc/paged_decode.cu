@@ -279,14 +279,12 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
         uint64_t *full = is_k ? bar.key_full : I8 ? bar.raw_full : bar.value_full;
         uint64_t *empty = is_k ? bar.key_empty : I8 ? bar.raw_empty : bar.value_empty;
         const CUtensorMap *map = is_k ? &k_map : &v_map;
-        uint32_t n = 0, st = 0, round = 0, q_phase = 0;
+        uint32_t n = 0, st = 0, round = 0, queries = 0;  // queries: loads of them so far
 #pragma unroll 1
-        for (bool first = true; ok && next_run(a, w, g); first = false) {
+        while (ok && next_run(a, w, g)) {
             if (is_k) {
-                if (!first) {
-                    if (!(ok = wait_for(&bar.q_empty, q_phase, abort))) break;
-                    q_phase ^= 1;
-                }
+                if (queries > 0 && !(ok = wait_for(&bar.q_empty, (queries - 1) & 1, abort))) break;
+                ++queries;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bar.q_full, a.max_new * a.G * 128 * kHalves);
                     for (int h = 0; h < kHalves; ++h)
@@ -357,14 +355,19 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
             }
         }
         if (!ok) fail();
+        tmem_fence_before();
+        __syncthreads();  // all roles are done, and know whether a wait ran out
         if (*abort) {
             // nothing may land in shared memory after the CTA has gone
             volatile int none = 0;
-            for (int i = 0; i < places; ++i) {
+            bool landed = true;  // after one wait that runs out all has had the time to land
+            for (int i = 0; landed && i < places; ++i) {
                 const uint32_t fills = round + (static_cast<uint32_t>(i) < st ? 1 : 0);
-                if (fills > 0) mbar_wait(&full[i], (fills - 1) & 1, &none);
+                if (fills > 0) landed = mbar_wait(&full[i], (fills - 1) & 1, &none);
             }
+            if (landed && queries > 0) mbar_wait(&bar.q_full, (queries - 1) & 1, &none);
         }
+        return;
     } else if (warp == 6) {
         // ------------------------------------------------- products S^T = K Q^T ---
         constexpr uint32_t kIdS = mma_idesc(BF16, kTile, NR, false);
