@@ -633,11 +633,12 @@ KVD_API kvd_status kvd_debug_scores(const kvd_cache *cache, const float *q, int3
                             float *ub, void *stream);
 
 /* ---------------------------------------------------------------------- */
-/* Test export of the bounded-wait path: one kernel waits on an mbarrier    */
-/* phase that nothing completes, gives up after limit_us microseconds of    */
-/* wall time (the decode and selection kernels give up after 2 s), and      */
-/* writes KVD_ERR_TIMEOUT to *dev_status (a device int32) unless it holds a */
-/* code already.  The kernel then returns normally: the context stays       */
+/* Test export of the bounded-wait paths: one kernel waits on an mbarrier   */
+/* phase that nothing completes, in each of the forms that kernels wait in, */
+/* gives up after limit_us microseconds of wall time in each (the kernels   */
+/* themselves after 2 s), and writes KVD_ERR_TIMEOUT to *dev_status (a      */
+/* device int32) unless it holds a code already; KVD_ERR_CUDA if one did    */
+/* not give up.  The kernel then returns normally: the context stays        */
 /* usable.  Errors: INVALID (dev_status NULL or misaligned, limit_us 0 or   */
 /* above 1,000,000), CUDA.                                                  */
 /* ---------------------------------------------------------------------- */

@@ -31,16 +31,16 @@ struct AttnArgs {  // of a launch
 
 // mbar_wait for the waits between the roles, in few instructions: the roles' hot
 // lines have to fit the instruction cache together, and a wait mostly ends in its
-// first try.  Warps call it whole, and all lanes get the same answer.
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort) {
+// first try.  Warps call it whole, and all lanes get the same answer.  limit_ns < 2^32.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *abort,
+                                         uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
     uint32_t n = 0, t0 = 0;
 #pragma unroll 1
     while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) {
         if ((++n & 63u) == 0) {
             const uint32_t t = static_cast<uint32_t>(global_timer_ns());
             if (n == 64) t0 = t;
-            if (__any_sync(0xffffffffu, *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs)))
-                return false;
+            if (__any_sync(0xffffffffu, *abort || t - t0 > limit_ns)) return false;
         }
     }
     return true;

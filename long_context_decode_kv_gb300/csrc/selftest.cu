@@ -1,10 +1,13 @@
-// selftest.cu -- the bounded-wait path of the kernels, run on its own: a
-// kernel waits on an mbarrier phase that nothing completes, gives up after the
-// given time, and records KVD_ERR_TIMEOUT in the status word, as every decode
-// and selection wait does when its data never arrives.  The test export of
-// kvd_debug_wait_timeout; no fault, trap or endless loop is involved.
+// selftest.cu -- the bounded-wait paths of the kernels, run on their own: a
+// kernel waits on an mbarrier phase that nothing completes, first as the decode
+// and selection kernels do (mbar_wait_limit), then as the kernels over pages do
+// (wait_for: with the limit, and with an abort flag that is set).  Each gives
+// up, and KVD_ERR_TIMEOUT goes to the status word, as it does when data never
+// arrive; a wait that did not give up records KVD_ERR_CUDA instead.  The test
+// export of kvd_debug_wait_timeout; no fault, trap or endless loop is involved.
 #include "common.cuh"
 #include "internal.h"
+#include "paged_attn_dev.cuh"
 
 namespace kvd {
 namespace {
@@ -18,8 +21,13 @@ __global__ void __launch_bounds__(32) wait_probe_kernel(int32_t *status, uint64_
         fence_barrier_init();
     }
     __syncthreads();
-    const bool ok = mbar_wait_limit(&bar, 0, &never, limit_ns);
-    if (!ok && threadIdx.x == 0) report_status(status, KVD_ERR_TIMEOUT);
+    bool ok = mbar_wait_limit(&bar, 0, &never, limit_ns);
+    __syncwarp();
+    ok |= wait_for(&bar, 0, &never, static_cast<uint32_t>(limit_ns));
+    if (threadIdx.x == 0) never = 1;
+    __syncwarp();
+    ok |= wait_for(&bar, 0, &never);  // ends at once
+    if (threadIdx.x == 0) report_status(status, ok ? KVD_ERR_CUDA : KVD_ERR_TIMEOUT);
 }
 
 }  // namespace
