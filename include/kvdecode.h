@@ -558,8 +558,9 @@ typedef struct kvd_paged_cache {
 /* the rotation of kvd_qk_norm_rope on the way.                              */
 /*   starts: device int32 [batch + 1]: sequence b's new tokens are rows      */
 /*   [starts[b], starts[b + 1]) of k, v and q, and stand at positions        */
-/*   seq_lens[b] - n_b .. seq_lens[b] - 1.  Rows at or behind starts[batch]  */
-/*   (a padded batch) count for nothing, and their q_out is not written.     */
+/*   seq_lens[b] - n_b .. seq_lens[b] - 1.  Rows before starts[0] and at or  */
+/*   behind starts[batch] (a padded batch) count for nothing, and their       */
+/*   q_out is not written.                                                    */
 /*   k, v: [n_tokens, n_kv_heads, head_dim] of one type.  Keys are normed    */
 /*   (k_weight) and rotated (rope) in f32; then keys and values are rounded  */
 /*   to the cache's type, or quantized as by kvd_kv_append.  Only the rows   */
@@ -586,7 +587,8 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*     out = sum_t softmax(softmax_scale * q . k_t)_t v_t  over the cached    */
 /*     tokens t <= p, and p - window < t when window > 0                      */
 /*   (int8: k_t = scale_t * code_t, and q stays as it is).  A token that sees */
-/*   no key gets a zero row.  Rows at or behind starts[batch] are not written. */
+/*   no key gets a zero row.  Rows of no sequence (before starts[0], at or     */
+/*   behind starts[batch]) are not written.                                    */
 /*   A non-finite value row spoils the outputs of its own sequence's tokens   */
 /*   in this call, those before it included.                                   */
 /*   q, out: [n_tokens, n_heads, head_dim] of one type: the cache's, or f16 or */

@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         if ((s0 != r0 || s1 != r1) && lane == 0)
             report_status(a.cache.dev_status, KVD_ERR_INVALID);
         if (t < s0 || t >= s1) {
-            // behind the last sequence, or starts that are not in order
-            if (t < end && lane == 0) report_status(a.cache.dev_status, KVD_ERR_INVALID);
+            // before the first sequence, behind the last, or starts that are not in order
+            if (t >= a.starts[0] && t < end && lane == 0)
+                report_status(a.cache.dev_status, KVD_ERR_INVALID);
             return;
         }
         pos = static_cast<long>(checked_len(a.cache, b)) - (s1 - t);

@@ -195,3 +195,28 @@ def test_one_large_value_scale_on_a_key_without_weight(x, new, L, at, places):
     want, tol = (a[:, None].expand_as(out) for a in (want, R.rounding(want, err, x)))
     R.assert_within(out, want, tol)
     assert c.device_status() == 0
+
+
+# ------------------------------------------------------------- rows of no sequence ---
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
+@pytest.mark.parametrize("first,new", [(3, [2, 4]), (1, [1, 1, 1]), (70, [90, 0, 5]), (200, [1])])
+def test_rows_before_the_first_sequence_count_for_nothing(dtype, first, new):
+    """starts[0] above 0: a part of a larger batch's rows, and nothing to report."""
+    H, Hkv, D, T = 8, 2, 64, first + sum(new) + 2
+    lens = [n + 30 * b for b, n in enumerate(new)]
+    c = _cache(dtype, lens, Hkv, D, 16, first)
+    before = {n: c.t[n].clone() for n in ("k", "v")}
+    starts = _starts(new) + first
+    x = _q(T, H + 2 * Hkv, D, torch.float16, first)
+    q_out, out = (torch.full((T, H, D), 7.0, dtype=x.dtype, device=DEV) for _ in range(2))
+    kvd.paged_append(c, x[:, H:H + Hkv], x[:, H + Hkv:], starts, q=x[:, :H], q_out=q_out)
+    kvd.paged_attn(c, q_out, starts, max(new), 0.125, out, kvd.make_paged_workspace(c, H, T, max(new)))
+    assert c.device_status() == 0
+    rows = slice(first, first + sum(new))
+    assert torch.equal(q_out[rows], x[rows, :H])
+    want, tol = R.attn_ref(c, q_out, starts.tolist(), lens, 0.125)
+    R.assert_within(out[rows], want[rows], tol[rows])
+    for o in (q_out, out):
+        assert torch.all(o[:first] == 7.0) and torch.all(o[first + sum(new):] == 7.0)
+    assert int((c.k != before["k"]).any(-1).any(1).sum()) <= sum(new)
