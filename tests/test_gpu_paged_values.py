@@ -220,3 +220,22 @@ def test_rows_before_the_first_sequence_count_for_nothing(dtype, first, new):
     for o in (q_out, out):
         assert torch.all(o[:first] == 7.0) and torch.all(o[first + sum(new):] == 7.0)
     assert int((c.k != before["k"]).any(-1).any(1).sum()) <= sum(new)
+
+
+# --------------------------------------------------------------- long among many ---
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.INT8])
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("B,chunks", [(49, {0: 1100}), (50, {49: 1500, 20: 600}), (700, {3: 900, 31: 1025, 650: 1300})])
+def test_long_chunks_among_many_sequences(dtype, window, B, chunks):
+    """More sequences than are counted a warp each, some with more row tiles than a lane counts alone."""
+    lens = [1 + b * 29 % 200 for b in range(B)]
+    new = [b % 2 for b in range(B)]
+    for b, n in chunks.items():
+        lens[b], new[b] = n + 77, n
+    c = _cache(dtype, lens, 1, 64, 32, B)
+    q = _q(sum(new), 8, 64, torch.float16, B)
+    out = _attend(c, q, new, window)
+    want, tol = R.attn_ref(c, q, _starts(new).tolist(), lens, 0.125, window)
+    R.assert_within(out, want, tol)
+    assert c.device_status() == 0
