@@ -485,7 +485,8 @@ typedef struct kvd_rope {
  * factor >= 1 (ignored by NONE); orig_len, low < high: YARN (1 and 32 turns
  * where both are 0) and BANDS (1 and 4).  Host only.
  * Errors: INVALID (NULL, rot_dim not a positive multiple of 16 up to 1024,
- * base <= 1 or not finite, factor < 1, orig_len < 1, low < 0, low >= high). */
+ * base <= 1 or not finite, factor < 1, orig_len < 1, low < 0, low >= high,
+ * and with YARN, which takes its logarithm, low == 0 beside a high that is not). */
 KVD_API kvd_status kvd_rope_freqs(int32_t rot_dim, double base, int32_t scaling, double factor,
                                   double orig_len, double low, double high, uint64_t *freqs,
                                   float *mscale);
@@ -586,15 +587,22 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*   h / (n_heads / n_kv_heads), with p = seq_lens[b] - n_b + i:              */
 /*     out = sum_t softmax(softmax_scale * q . k_t)_t v_t  over the cached    */
 /*     tokens t <= p, and p - window < t when window > 0                      */
-/*   (int8: k_t = scale_t * code_t, and q stays as it is).  A token that sees */
-/*   no key gets a zero row.  Rows of no sequence (before starts[0], at or     */
-/*   behind starts[batch]) are not written.                                    */
+/*   (int8: k_t = scale_t * code_t, and q stays as it is).  Logits, maxima,   */
+/*   weights and their sum are f32.  For the product with the values weights   */
+/*   are rounded: over bf16 to 2^-9 of each; over f16 to 2^-11 of each, but    */
+/*   not below 2^-31 of the row's largest; over int8, times the value's scale, */
+/*   to 2^-11 of each, but not below 2^-24 of the row's largest weight times   */
+/*   the largest value scale among the 128 keys around (or 2^-60 of the        */
+/*   largest of all, where that is more).                                      */
+/*   A token that sees no key gets a zero row.  Rows of no sequence (before    */
+/*   starts[0], at or behind starts[batch]) are not written.                   */
 /*   A non-finite value row spoils the outputs of its own sequence's tokens   */
 /*   in this call, those before it included.                                   */
 /*   q, out: [n_tokens, n_heads, head_dim] of one type: the cache's, or f16 or */
 /*   bf16 over an int8 cache.  out must not overlap q.  softmax_scale > 0.      */
 /*   max_new: at least the largest n_b (it sizes the grid; the tokens of a     */
-/*   larger n_b are left out, and INVALID is reported to dev_status).          */
+/*   larger n_b are left out, and INVALID is reported to dev_status).  With    */
+/*   max_new == 0 no sequence has new tokens: a no-op, starts are not read.     */
 /*   workspace: kvd_paged_workspace_bytes, zero-filled before its first use;   */
 /*   every call that completes leaves its counters at zero again (after a       */
 /*   KVD_ERR_TIMEOUT in dev_status, zero it).  Calls that may overlap on the    */
@@ -609,8 +617,9 @@ KVD_API kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads 
                                   void *workspace, size_t workspace_bytes, void *stream);
 
 /* Workspace bytes of kvd_paged_attn for n_heads query heads, up to n_tokens new
- * tokens with up to max_new in one sequence, and any len the page table can hold.
- * Asked with the device current that will run the call.  0 on invalid arguments. */
+ * tokens with up to max_new in one sequence, and any len the page table can hold
+ * (the kernels as they are need the same for any n_tokens >= 1).  Asked with the
+ * device current that will run the call.  0 on invalid arguments. */
 KVD_API size_t kvd_paged_workspace_bytes(const kvd_paged_cache *cache, int32_t n_heads,
                                          int32_t n_tokens, int32_t max_new);
 

@@ -44,7 +44,7 @@ struct PagedAttnArgs {
     void *out;
     int64_t q_stride, out_stride;
     bool bf16;  // q and out: bf16, else f16
-    int H, G, n_tokens, max_new, window;
+    int G, n_tokens, max_new, window;
     const int32_t *starts;
     float scale_log2;  // softmax_scale * log2(e)
 };
@@ -55,9 +55,10 @@ size_t paged_counter_bytes();
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, void *ws, cudaStream_t st);
 size_t paged_attn_ws(const kvd_paged_cache &c, int H, int max_new);
 // At most kDecodeRows rows (new tokens times query heads of a KV head) a sequence.
-// Against the kernel for row tiles: one token over 512 tokens 9.3 us and 23.5, 32 rows
-// over 8 int8 sequences of 131,072 478 us and 767, over f16 ones 687 us and 631 (there
-// the wider tile would be 8 % ahead; over few tokens it is far behind).
+// Against the kernel for row tiles: one token over 512 f16 tokens 8.2 us and 17.9, 32
+// rows over 8 int8 sequences of 131,072 605 us and 776.  The limit is not the best for
+// f16: 32 rows over 8 sequences take 654 us and 617, 16 rows over one sequence of 32,764
+// 56 and 40, and 32 over 32,768 85 and 41.
 constexpr int kDecodeRows = 32;
 cudaError_t launch_paged_decode(const PagedAttnArgs &a, void *ws, cudaStream_t st);
 size_t paged_decode_ws(int rows, int D);

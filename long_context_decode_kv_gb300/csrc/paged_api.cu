@@ -257,7 +257,6 @@ kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int3
     a.q_stride = q->stride;
     a.out_stride = out->stride;
     a.bf16 = q->dtype == KVD_X_BF16;
-    a.H = q->n_heads;
     a.G = G;
     a.n_tokens = n_tokens;
     a.max_new = max_new;

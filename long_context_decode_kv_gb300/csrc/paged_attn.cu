@@ -37,12 +37,12 @@
 // of the row's largest.  Sums and statistics in f32 do not add to that.
 //
 // What bounds it.  128 channels in f16: the power limit; 2048 tokens over 32,768
-// take 760 us = 1.40 PFLOP/s back to back (0.83 of what a plain matrix product
-// sustains), 670 us from a cool start.  64 channels: the two softmax warps a
-// scheduler has, not its products: 2 x 4001 tokens 92 us = 0.71 PFLOP/s.  int8:
+// take 755 to 805 us back to back, by the GPU = 1.32 to 1.41 PFLOP/s (0.78 to 0.83 of
+// what a plain matrix product sustains).  64 channels: the two softmax warps a
+// scheduler has, not its products: 2 x 4001 tokens 94 us = 0.70 PFLOP/s.  int8:
 // the codes' way through shared memory beside the softmax: 250 tokens over 130,250
-// 541 us = 0.98 PFLOP/s.  Few key tiles an SM: the set-up (2.5 us), an item's first
-// loads and its last rows: 24 ragged sequences in a window 120 us = 0.83 PFLOP/s.
+// 544 us = 0.98 PFLOP/s.  Few key tiles an SM: the set-up (2.5 us), an item's first
+// loads and its last rows: 24 ragged sequences in a window 122 us = 0.81 PFLOP/s.
 // The roles' code together is near the instruction cache's size, so each stays
 // rolled and in one place: unrolling a role has cost others more than it gained.
 #include <type_traits>
@@ -103,8 +103,8 @@ __device__ __forceinline__ Item item_of(const Dev &a, const Seq &s, int tile, in
 // and its rows' way out), in key tiles: the line is cut by tiles and these together,
 // an item's first kItemCost units standing for it.  Cut by tiles alone the CTAs with
 // many short items were the last by far (SMs busy 0.76 of the time); at 0, 1, 2, 3, 4
-// and 6 units 2 x 4001 tokens at 64 channels took 105, 97, 92, 92.5, 94 and 96 us, 24
-// ragged sequences 129, 122, 120, 120, 120 and 123.
+// and 6 units 2 x 4001 tokens at 64 channels took 109, 97, 93, 94, 95.5 and 97 us, 24
+// ragged sequences 131, 123, 121, 121, 121 and 124.
 constexpr int kItemCost = 3;
 
 // A CTA's walk along the line of items, the same in every role.

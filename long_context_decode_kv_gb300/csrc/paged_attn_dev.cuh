@@ -21,7 +21,7 @@ struct AttnArgs {  // of a launch
     kvd_paged_cache c;
     uint16_t *out;
     int64_t out_stride;
-    int H, G, n_tokens, max_new, window;
+    int G, n_tokens, max_new, window;
     const int32_t *starts;
     float scale_log2;
     int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
@@ -156,7 +156,6 @@ inline bool fill_launch(const PagedAttnArgs &p, int q_tokens, CUtensorMapSwizzle
     a.c = c;
     a.out = static_cast<uint16_t *>(p.out);
     a.out_stride = p.out_stride;
-    a.H = p.H;
     a.G = p.G;
     a.n_tokens = p.n_tokens;
     a.max_new = p.max_new;

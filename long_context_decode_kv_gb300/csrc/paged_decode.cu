@@ -9,9 +9,9 @@
 // scales (int8) are then two numbers of its own, its exponentials as many as there
 // are rows, and the sums over keys stay apart until the end.
 //
-// One CTA per SM, persistent, the items (sequence, KV head) cut evenly as in
-// paged_attn.cu; an item that a cut divides is joined by the last of its CTAs to
-// arrive, from f32 partials.
+// One CTA per SM, persistent; the line of all items' (sequence, KV head) key tiles is
+// cut into equal pieces; an item that a cut divides is joined by the last of its CTAs
+// to arrive, from f32 partials.
 //
 // Roles: warps 0-3 softmax (thread = key); warps 4 and 5 load key and value tiles
 // by TMA, a ring each; warps 6 and 7 issue the two products.  int8: warps 8-11
@@ -28,11 +28,12 @@
 // does, and each one until all rows have seen a key (a window or a bad page may hide
 // the first tiles from some).
 //
-// Measured: 8 sequences of 131,072 tokens, 32 heads over 8: 361 us int8 (6.1 TB/s,
-// 0.91 of what a copy reaches), 610 us f16 (7.0 TB/s).  A decode step on 4 int8
-// sequences of 32,000 takes 65 us (0.62): a CTA's 20 tiles then stand beside the
-// set-up, the first bytes and the join.  One token over 512: 8.3 us, of which a
-// launch and its host call are 5.
+// Measured: 8 sequences of 131,072 tokens, 32 heads over 8: 364 us int8 (6.1 TB/s,
+// 0.89 of what a copy reaches; 460 with bf16 queries, whose key codes take 8
+// instructions for four where f16's take 5), 613 us f16 (7.0 TB/s).  A decode step on
+// 4 int8 sequences of 32,000, with its append, takes 68 us (0.58): a CTA's 20 tiles
+// then stand beside the set-up, the first bytes and the join.  One token over 512: 8.3
+// us, of which a launch and its host call are 5.
 #include "paged_attn_dev.cuh"
 
 namespace kvd {
@@ -926,9 +927,9 @@ cudaError_t launch_shape(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
     if (!fill_launch(p, p.max_new, k_swizzle, v_swizzle, a, q_map, k_map, v_map))
         return cudaErrorInvalidValue;
     const DecodePlan w = plan_of(p.max_new * p.G, D);
-    // Shorter pieces cost more in joining than they save: at 2, 4 and 6 tiles a CTA at
-    // least one token over 512, 1024, 4096 and 8192 tokens took 9.4, 10.1, 11.6 and 15.3
-    // us, 8.4, 11.0, 11.8 and 12.8, and 16.5, 15.4, 15.0 and 16.2.
+    // Shorter pieces cost more in joining than they mostly save: at 2, 4 and 6 tiles a
+    // CTA at least one token over 512, 1024, 4096 and 8192 tokens took 9.8, 10.4, 12.0
+    // and 15.6 us, 8.2, 11.3, 12.3 and 13.2, and 16.7, 15.5, 15.3 and 16.5.
     a.min_tiles = 4;
     uint8_t *base = static_cast<uint8_t *>(ws);
     a.arrived = reinterpret_cast<uint32_t *>(base);
@@ -945,7 +946,7 @@ cudaError_t launch_shape(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
 template <bool BF16, bool I8>
 cudaError_t launch_type(const PagedAttnArgs &p, void *ws, cudaStream_t st) {
     // 16 rows take half the logits and weights of 32: one token of 4 heads over an int8
-    // cache (4 sequences of 32,000) 65 us against 76, f16 over 512 tokens 9.3 against 10.4
+    // cache (4 sequences of 32,000) 67 us against 97, f16 over 512 tokens 8.2 against 10.3
     const bool narrow = p.max_new * p.G <= 16;
     if (p.c.head_dim == 64)
         return narrow ? launch_shape<BF16, 64, 16, I8>(p, ws, st)

@@ -4,8 +4,8 @@
 //   y = R(p) (x * w / sqrt(mean(x^2) + eps))
 //   R(p) turns channel pair i of the first rot_dim channels by p * f_i.
 //
-// Bound by HBM: each element is read once and written once.  What has to be kept
-// down is the work on each: a lane holds the two channel groups that turn into
+// Each element is read once and written once, and the least it can take is HBM's time
+// for that.  What has to be kept down is the work on each: a lane holds the two channel groups that turn into
 // each other (4 channels of the lower and 4 of the upper half; 8 neighbours when
 // pairs are interleaved), so no lane needs another's values but for the sum of
 // the norm, and two channels share an instruction (FFMA2).  A warp serves one
@@ -19,9 +19,10 @@
 // an error below position * 2^-64; its upper 32 bits go to sincospi.  In f32 the
 // product alone is off by 2^-24 of itself: 0.06 radians at position 1,000,000.
 //
-// Measured: 8192 tokens of 32 + 8 heads, bf16, normed and rotated 32.4 us (5.2 TB/s,
-// 0.76 of what a copy reaches); 8190 tokens of 32 + 8 + 8 appended to pages 44 us
-// (4.5 TB/s).  A few tokens take a launch and its host call, 8.7 us.
+// Measured: 8192 tokens of 32 + 8 heads, bf16, normed and rotated 32.6 us (5.2 TB/s,
+// 0.76 of what a copy reaches); 8190 tokens of 32 + 8 + 8 appended to pages 45 us
+// (4.5 TB/s), to int8 pages 58.  APPENDBOUND
+// A few tokens take a launch and its host call, 8.7 us.
 #include <type_traits>
 
 #include "common.cuh"
