@@ -19,10 +19,12 @@
 // an error below position * 2^-64; its upper 32 bits go to sincospi.  In f32 the
 // product alone is off by 2^-24 of itself: 0.06 radians at position 1,000,000.
 //
-// Measured: 8192 tokens of 32 + 8 heads, bf16, normed and rotated 32.6 us (5.2 TB/s,
-// 0.76 of what a copy reaches); 8190 tokens of 32 + 8 + 8 appended to pages 45 us
-// (4.5 TB/s), to int8 pages 58.  APPENDBOUND
-// A few tokens take a launch and its host call, 8.7 us.
+// Measured: 8192 tokens of 32 + 8 heads, bf16, normed and rotated 32.8 us (5.1 TB/s,
+// 0.75 of what a copy reaches); 8190 tokens of 32 + 8 + 8 appended to pages 45 us
+// (4.4 TB/s), to int8 pages 58.  Neither HBM (45 and 42 % of its cycles in a single cold
+// launch) nor the issue slots (56 and 48 %) hold these alone: an SM has 26 and 20 warps
+// at a time, and each waits on the reads and the fixed latencies of its own chain.  A
+// few tokens take a launch and its host call, 8.7 us.
 #include <type_traits>
 
 #include "common.cuh"
