@@ -589,7 +589,7 @@ KVD_API kvd_status kvd_paged_append(const kvd_paged_cache *cache, const kvd_head
 /*     tokens t <= p, and p - window < t when window > 0                      */
 /*   (int8: k_t = scale_t * code_t, and q stays as it is).  Logits, maxima,   */
 /*   weights and their sum are f32.  For the product with the values weights   */
-/*   are rounded: over bf16 to 2^-9 of each; over f16 to 2^-11 of each, but    */
+/*   are rounded: over bf16 to 2^-8 of each; over f16 to 2^-11 of each, but    */
 /*   not below 2^-31 of the row's largest; over int8, times the value's scale, */
 /*   to 2^-11 of each, but not below 2^-24 of the row's largest weight times   */
 /*   the largest value scale among the 128 keys around (or 2^-60 of the        */
