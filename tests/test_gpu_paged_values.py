@@ -239,3 +239,44 @@ def test_long_chunks_among_many_sequences(dtype, window, B, chunks):
     want, tol = R.attn_ref(c, q, _starts(new).tolist(), lens, 0.125, window)
     R.assert_within(out, want, tol)
     assert c.device_status() == 0
+
+
+# ----------------------------------------------------------- scales of all sizes ---
+
+@pytest.mark.parametrize("x", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("new,L", SHAPES)
+@pytest.mark.parametrize("places", [1, 3, 8])
+@pytest.mark.parametrize("window", [0, 150])
+def test_value_scales_of_all_sizes(x, new, L, places, window):
+    """Scales spread over several times 2^places, a tenth of them zero, within the header's bound:
+    weight times scale to 2^-11, and to 2^-24 of the row's largest weight times the largest scale
+    of the 128 keys around; logits and sums as in attn_ref."""
+    D, H, Hkv = 64, 8, 2
+    c = _cache(kvd.INT8, [L], Hkv, D, 16, L + places)
+    g = torch.Generator(device=DEV).manual_seed(L + places)
+    e = (torch.randn(c.v_scale.shape, generator=g, device=DEV) * places).clamp(-30, 30)
+    c.v_scale.copy_(torch.exp2(e - e.max() + 8))      # values stay in f16's range
+    c.v_scale[torch.rand(e.shape, generator=g, device=DEV) < 0.1] = 0.0
+    q = _q(new, H, D, x, new)
+    out = _attend(c, q, [new], window).double()
+    p = torch.arange(L - new, L, device=DEV)[:, None]
+    t = torch.arange(L, device=DEV)
+    seen = (t <= p) & ((t > p - window) | (window == 0))
+    first = max(0, L - new - window + 1) if window else 0  # before it no row sees a key
+    for h in range(H):
+        k, v, ks, vs = (R.rows_of(c.t[n], c.page_table[0], L, h // (H // Hkv)).double()
+                        for n in ("k", "v", "k_scale", "v_scale"))
+        k = k * ks[:, None]
+        qq = q[:, h].double() * D ** -0.5
+        z = torch.where(seen, qq @ k.T, -math.inf)
+        w = torch.softmax(z, -1)
+        near = torch.where(t < first, 0.0, vs)
+        near = torch.stack([s.max() for s in near.split(128)]).repeat_interleave(128)[:L]
+        step = torch.maximum(U16 * w * vs, 2.0 ** -24 * seen * w.amax(-1, keepdim=True) * near)
+        mag = torch.where(seen, qq.abs() @ k.abs().T, 0.0).amax(-1, keepdim=True)
+        n = seen.sum(-1, keepdim=True).double()
+        rest = 2 * D * 2.0 ** -23 * mag + (n / 8 + 64) * 2.0 ** -23
+        want = w @ (v * vs[:, None])
+        err = (step @ v.abs() + (w @ (v.abs() * vs[:, None])) * rest) * 1.01
+        R.assert_within(out[:, h], want, R.rounding(want, err, x), f"head {h}")
+    assert c.device_status() == 0
