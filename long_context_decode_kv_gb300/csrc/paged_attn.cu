@@ -33,8 +33,9 @@
 // from below: that spares the search for each tile's maximum, makes the rescaling of
 // O rare, and leaves small weights the range of f16 (lift_of).
 // P is rounded to the tensor core's operand type, bf16 for bf16 caches and f16 for f16
-// and int8 ones: half a step of each weight, and in f16 at least 2^-31 (int8: 2^-29)
-// of the row's largest.  Sums and statistics in f32 do not add to that.
+// and int8 ones: half a step of each weight, and in f16 at least 2^-31 of the row's
+// largest (int8: 2^-30 of it times ScaleUnit's unit).  Sums and statistics in f32 do not
+// add to that.
 //
 // What bounds it.  128 channels in f16: the power limit; 2048 tokens over 32,768
 // take 755 to 805 us back to back, by the GPU = 1.32 to 1.41 PFLOP/s (0.78 to 0.83 of
