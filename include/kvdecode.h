@@ -2,7 +2,7 @@
  * kvdecode.h -- C ABI of libkvdecode.so: single-token decode attention over a
  * long KV cache that reads only part of it (Quest-style block selection), and
  * what a server needs around it (positions and norms, a cache in pages, chunks
- * of new tokens), for NVIDIA GB300 (sm_103a), one GPU.
+ * of new tokens, latent rows, eviction), for NVIDIA GB300 (sm_103a), one GPU.
  *
  * Sources, by page title and section:
  *  [QUEST]  "Sparse Attention -- Quest-style block-selector for long-context
@@ -47,7 +47,7 @@
 extern "C" {
 #endif
 
-#define KVD_ABI_VERSION 4
+#define KVD_ABI_VERSION 5
 
 /* Exported symbols (the library is built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -622,6 +622,187 @@ KVD_API kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads 
  * device current that will run the call.  0 on invalid arguments. */
 KVD_API size_t kvd_paged_workspace_bytes(const kvd_paged_cache *cache, int32_t n_heads,
                                          int32_t n_tokens, int32_t max_new);
+
+/* ---------------------------------------------------------------------- */
+/* kvd_paged_attn that also gives each row's softmax statistic, for */
+/* kvd_paged_mass or to join attention over several caches: */
+/*   lse[t, h] = ln sum_s exp(softmax_scale * q . k_s)   over the keys the */
+/*   row sees, -infinity where it sees none; device f32 [n_tokens, n_heads]. */
+/*   Rows of no sequence are not written.  out is kvd_paged_attn's, bit for */
+/*   bit. */
+/* Errors: as kvd_paged_attn; INVALID also for lse NULL or misaligned. */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_paged_attn_lse(const kvd_paged_cache *cache, const kvd_heads *q,
+                                      int32_t n_tokens, const int32_t *starts, int32_t max_new,
+                                      float softmax_scale, int32_t window, const kvd_heads *out,
+                                      float *lse, void *workspace, size_t workspace_bytes,
+                                      void *stream);
+
+/* ====================================================================== */
+/* Smaller caches: rows that all heads share (latent attention), and fewer */
+/* rows (eviction by accumulated weight).  They have no counterpart on the */
+/* pages. */
+/* ====================================================================== */
+
+/*
+ * A cache of latent rows in pages: one row a token, shared by all query heads.
+ * Its first `rank` channels are the token's latent vector, normed, which is the
+ * value and the larger part of the key; the other rope_dim are the key's rotated
+ * part.  A model with per-head projections W_k (latent to key) and W_v (latent to
+ * value) asks for it with q W_k in place of q, and applies W_v to the output
+ * (the absorbed form).
+ *   rows        [n_pages, page_size, rank + rope_dim]  f16 or bf16
+ * Pages, lengths, limits and what is checked on the device: as kvd_paged_cache with
+ * one KV head.
+ */
+typedef struct kvd_latent_cache {
+    int32_t dtype;        /* KVD_F16 or KVD_BF16 */
+    int32_t batch;        /* sequences >= 1 */
+    int32_t rank;         /* 128, 256, 384 or 512 */
+    int32_t rope_dim;     /* 16, 32, 48 or 64 */
+    int32_t n_pages;      /* pages of the pool */
+    int32_t page_size;    /* tokens, a multiple of 16 */
+    int32_t max_pages;    /* columns of page_table */
+    int32_t len;          /* at least the largest of seq_lens, <= max_pages * page_size */
+    void *rows;
+    const int32_t *page_table;
+    const int32_t *seq_lens;
+    int32_t *dev_status;  /* may be NULL */
+} kvd_latent_cache;
+
+/* Parts of heads: kvd_heads whose heads lie head_stride elements apart, so that
+ * some channels of each head can be passed as they lie.  x is 16-byte aligned, both
+ * strides times the element size are multiples of 16, head_stride >= the part's
+ * channels, and stride >= (n_heads - 1) * head_stride + the part's channels. */
+typedef struct kvd_head_parts {
+    void *x;
+    int64_t stride;
+    int64_t head_stride;
+    int32_t dtype;        /* kvd_x_dtype */
+    int32_t n_heads;
+} kvd_head_parts;
+
+/* ---------------------------------------------------------------------- */
+/* Append new tokens of a ragged batch to their latent pages. */
+/*   row = (c * c_weight / sqrt(mean(c^2) + eps), R(p) k_pe), each rounded */
+/*   once to the cache's type; without c_weight no norm, without rope no */
+/*   rotation (rot_dim <= rope_dim). */
+/*   c, k_pe: [n_tokens, 1, rank] and [n_tokens, 1, rope_dim] of one type. */
+/*   starts, positions and padding rows as for kvd_paged_append. */
+/*   q, q_out (both NULL, or both given): the queries' rotated parts */
+/*   [n_tokens, n_heads, rope_dim], turned as the keys' are; q_out may be q */
+/*   itself (same address, strides and type) and must not overlap it otherwise. */
+/* n_tokens == 0 is a no-op. */
+/* Errors: INVALID; UNSUPPORTED (rank, rope_dim, page_size, rot_dim, the cache's */
+/* counts); CUDA. */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_latent_append(const kvd_latent_cache *cache, const kvd_heads *c,
+                                     const kvd_heads *k_pe, int32_t n_tokens,
+                                     const int32_t *starts, const kvd_rope *rope,
+                                     const float *c_weight, const kvd_head_parts *q,
+                                     const kvd_head_parts *q_out, float eps, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Attention of a ragged batch's new tokens over their latent pages. */
+/*   For token i of sequence b's n_b and query head h, p = seq_lens[b] - n_b + i: */
+/*     z_t = softmax_scale * q . row_t  (all rank + rope_dim channels) */
+/*     out = sum_t softmax(z)_t row_t[:rank]    over the cached tokens t <= p, */
+/*     and p - window < t when window > 0; lse = ln sum_t exp(z_t). */
+/*   Logits, maxima, weights and their sum are f32.  For the product with the */
+/*   rows weights are rounded: over bf16 to 2^-8 of each; over f16 to 2^-11 of */
+/*   each, but not below 2^-31 of the row's largest. */
+/*   A token that sees no key gets a zero row and an lse of -infinity.  Rows of no */
+/*   sequence are not written.  A non-finite row of the cache spoils the outputs */
+/*   of its own sequence's tokens in this call, those before it included. */
+/*   q: [n_tokens, n_heads, rank + rope_dim], out: [n_tokens, n_heads, rank], of the */
+/*   cache's type; out must not overlap q.  n_heads <= 1024.  softmax_scale > 0. */
+/*   lse: device f32 [n_tokens, n_heads], or NULL. */
+/*   starts, max_new, window, workspace (kvd_latent_workspace_bytes): as for */
+/*   kvd_paged_attn; this workspace needs no zeros. */
+/* n_tokens == 0 or max_new == 0 is a no-op. */
+/* Errors: INVALID; UNSUPPORTED (rank, rope_dim, page_size, the cache's counts, more */
+/* than 2^31 - 1 row tiles times key tiles); WORKSPACE; CUDA. */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_latent_attn(const kvd_latent_cache *cache, const kvd_heads *q,
+                                   int32_t n_tokens, const int32_t *starts, int32_t max_new,
+                                   float softmax_scale, int32_t window, const kvd_heads *out,
+                                   float *lse, void *workspace, size_t workspace_bytes,
+                                   void *stream);
+
+/* Workspace bytes of kvd_latent_attn, as kvd_paged_workspace_bytes.  0 on invalid
+ * arguments. */
+KVD_API size_t kvd_latent_workspace_bytes(const kvd_latent_cache *cache, int32_t n_heads,
+                                          int32_t n_tokens, int32_t max_new);
+
+/* ---------------------------------------------------------------------- */
+/* Accumulated attention weight of each cached token, for an eviction. */
+/*   For sequence b, KV head g and cached token t < seq_lens[b]: */
+/*     out[b, g, t] = (t < seq_lens[b] - n_b ? decay * mass[b, g, t] : 0) */
+/*                    + sum over the new tokens that see t and g's query heads */
+/*                      of exp(softmax_scale * q . k_t - lse) */
+/*   that is, the weights of the attention call with the same q, starts, */
+/*   max_new, softmax_scale and window, whose lse it is; the new tokens begin at 0. */
+/*   What stands at or behind seq_lens[b], and a row whose lse is -infinity, count */
+/*   for nothing; the former is not written.  Keys on a bad page get no weight. */
+/*   A row whose lse is not finite otherwise spoils the weights that it adds to. */
+/*   Logits, weights and sums are f32, added in a fixed order: repeated calls give */
+/*   the same bits. */
+/*   q: [n_tokens, n_heads, head_dim] (latent: rank + rope_dim), the type that the */
+/*   attention call takes; lse: f32 [n_tokens, n_heads]. */
+/*   mass, out: f32 [batch, n_kv_heads, ..], mass_stride and out_stride elements */
+/*   from one (sequence, head) to the next, both >= len; out may be mass itself (same */
+/*   stride) and must not overlap it otherwise.  decay is finite and >= 0 (0: mass is */
+/*   not read, and may be NULL). */
+/*   n_tokens == 0 or max_new == 0: only the decay. */
+/* Errors: INVALID; UNSUPPORTED (as the attention calls); CUDA. */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_paged_mass(const kvd_paged_cache *cache, const kvd_heads *q, const float *lse,
+                                  int32_t n_tokens, const int32_t *starts, int32_t max_new,
+                                  float softmax_scale, int32_t window, const float *mass,
+                                  int64_t mass_stride, float decay, float *out, int64_t out_stride,
+                                  void *stream);
+KVD_API kvd_status kvd_latent_mass(const kvd_latent_cache *cache, const kvd_heads *q,
+                                   const float *lse, int32_t n_tokens, const int32_t *starts,
+                                   int32_t max_new, float softmax_scale, int32_t window,
+                                   const float *mass, int64_t mass_stride, float decay, float *out,
+                                   int64_t out_stride, void *stream);
+
+/* ---------------------------------------------------------------------- */
+/* Eviction: of each (sequence, KV head) the tokens that stay, in order, to */
+/* the pages of another table. */
+/*   A sequence of more than `keep` tokens keeps its first `sink`, its last */
+/*   `recent`, and of those between the ones with the largest mass, `keep` in */
+/*   all; equal masses (-0 is 0) go to the lower index, and NaN is below every */
+/*   number.  A shorter one keeps all. */
+/*   mass: f32 [batch, n_kv_heads, ..], mass_stride >= len elements apart. */
+/*   kept: device int32 [batch, n_kv_heads, keep]: the kept tokens' old indices, */
+/*   ascending, min(keep, seq_lens[b]) of them (the rest of a row is left as it was). */
+/*   Row r of the kept, codes and scales as they are, goes to token r of the */
+/*   sequence in page_table_out (device int32 [batch, max_pages_out], pages of the */
+/*   same pool).  mass_out (may be NULL), f32 [batch, n_kv_heads, ..] mass_out_stride */
+/*   >= keep elements apart, gets their masses; it must not overlap mass. */
+/*   seq_lens_out: device int32 [batch], min(keep, seq_lens[b]).  It must not be */
+/*   seq_lens itself. */
+/*   No page of page_table_out may be one that this call reads, or stand in it twice, */
+/*   among the entries that the kept rows need (wrong rows, no fault).  A caller goes */
+/*   on with the new table and lengths, and may then give the old pages back.  The keys */
+/*   keep the rotation of their old positions: later tokens' positions are no longer */
+/*   their places in the cache, so rotate them with kvd_qk_norm_rope and append without rope. */
+/*   Bad pages of either table are reported as INVALID to dev_status, and their rows are */
+/*   not moved. */
+/* Errors: INVALID (keep < 1, sink or recent < 0, sink + recent > keep, strides, too few */
+/* columns in page_table_out for min(keep, len)); UNSUPPORTED (as kvd_paged_append); CUDA. */
+/* ---------------------------------------------------------------------- */
+KVD_API kvd_status kvd_paged_evict(const kvd_paged_cache *cache, const float *mass,
+                                   int64_t mass_stride, int32_t keep, int32_t sink, int32_t recent,
+                                   const int32_t *page_table_out, int32_t max_pages_out,
+                                   int32_t *kept, int32_t *seq_lens_out, float *mass_out,
+                                   int64_t mass_out_stride, void *stream);
+KVD_API kvd_status kvd_latent_evict(const kvd_latent_cache *cache, const float *mass,
+                                    int64_t mass_stride, int32_t keep, int32_t sink, int32_t recent,
+                                    const int32_t *page_table_out, int32_t max_pages_out,
+                                    int32_t *kept, int32_t *seq_lens_out, float *mass_out,
+                                    int64_t mass_out_stride, void *stream);
 
 /* Static description of a status code.  Host only. */
 KVD_API const char *kvd_status_string(kvd_status status);

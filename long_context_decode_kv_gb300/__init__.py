@@ -10,7 +10,9 @@ Entry points (same names as the C ABI, without the ``kvd_`` prefix):
   kv_append, select_blocks, decode_attn, decode_attn_dense, decode_step,
   decode_step_host, workspace_bytes, selected_count, status_string,
   debug_qk_int8, debug_scores, decode_attn_static; and around the decode
-  rope_table (kvd_rope_freqs), qk_norm_rope, paged_append, paged_attn.
+  rope_table (kvd_rope_freqs), qk_norm_rope, paged_append, paged_attn; over
+  latent rows latent_append, latent_attn; and paged_mass, paged_evict (of
+  either cache).
 """
 from __future__ import annotations
 
@@ -43,7 +45,9 @@ EXPORTS = ("kvd_kv_append", "kvd_select_blocks", "kvd_decode_attn", "kvd_decode_
            "kvd_decode_attn_tail", "kvd_kv_append_f32", "kvd_select_blocks_per_head",
            "kvd_decode_attn_per_head", "kvd_debug_wait_timeout", "kvd_debug_stage_marks",
            "kvd_rope_freqs", "kvd_qk_norm_rope", "kvd_paged_append", "kvd_paged_attn",
-           "kvd_paged_workspace_bytes")
+           "kvd_paged_workspace_bytes", "kvd_paged_attn_lse", "kvd_latent_append",
+           "kvd_latent_attn", "kvd_latent_workspace_bytes", "kvd_paged_mass", "kvd_latent_mass",
+           "kvd_paged_evict", "kvd_latent_evict")
 
 
 class KvdError(RuntimeError):
@@ -70,6 +74,20 @@ class PagedCacheStruct(C.Structure):
                 ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p),
                 ("v_scale", C.c_void_p), ("page_table", C.c_void_p), ("seq_lens", C.c_void_p),
                 ("dev_status", C.c_void_p)]
+
+
+class LatentCacheStruct(C.Structure):
+    """Mirror of ``kvd_latent_cache``."""
+    _fields_ = [("dtype", C.c_int32), ("batch", C.c_int32), ("rank", C.c_int32),
+                ("rope_dim", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32),
+                ("max_pages", C.c_int32), ("len", C.c_int32), ("rows", C.c_void_p),
+                ("page_table", C.c_void_p), ("seq_lens", C.c_void_p), ("dev_status", C.c_void_p)]
+
+
+class PartsStruct(C.Structure):
+    """Mirror of ``kvd_head_parts``."""
+    _fields_ = [("x", C.c_void_p), ("stride", C.c_int64), ("head_stride", C.c_int64),
+                ("dtype", C.c_int32), ("n_heads", C.c_int32)]
 
 
 class HeadsStruct(C.Structure):
@@ -131,6 +149,19 @@ def lib():
         L.kvd_paged_attn.argtypes = [pc, hp, i32, p, i32, C.c_float, i32, hp, p, sz, p]
         L.kvd_paged_workspace_bytes.argtypes = [pc, i32, i32, i32]
         L.kvd_paged_workspace_bytes.restype = sz
+        lc, qp, f32, i64 = C.POINTER(LatentCacheStruct), C.POINTER(PartsStruct), C.c_float, \
+            C.c_int64
+        L.kvd_paged_attn_lse.argtypes = [pc, hp, i32, p, i32, f32, i32, hp, p, p, sz, p]
+        L.kvd_latent_append.argtypes = [lc, hp, hp, i32, p, rp, p, qp, qp, f32, p]
+        L.kvd_latent_attn.argtypes = [lc, hp, i32, p, i32, f32, i32, hp, p, p, sz, p]
+        L.kvd_latent_workspace_bytes.argtypes = [lc, i32, i32, i32]
+        L.kvd_latent_workspace_bytes.restype = sz
+        mass = [hp, p, i32, p, i32, f32, i32, p, i64, f32, p, i64, p]
+        L.kvd_paged_mass.argtypes = [pc] + mass
+        L.kvd_latent_mass.argtypes = [lc] + mass
+        evict = [p, i64, i32, i32, i32, p, i32, p, p, p, i64, p]
+        L.kvd_paged_evict.argtypes = [pc] + evict
+        L.kvd_latent_evict.argtypes = [lc] + evict
         _lib = L
     return _lib
 
@@ -650,19 +681,240 @@ def paged_append(cache: PagedKVCache, k: torch.Tensor, v: torch.Tensor, starts: 
           _weight(k_weight, D), _heads(q), _heads(q_out), _weight(q_weight, D), eps)
 
 
+def _lse(t: Optional[torch.Tensor], n: int, h: int):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or tuple(t.shape) != (n, h):
+        raise ValueError("lse is a float32 tensor [n_tokens, n_heads]")
+    return _ptr(t)
+
+
 def paged_attn(cache: PagedKVCache, q: torch.Tensor, starts: torch.Tensor, max_new: int,
                softmax_scale: float, out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
-               stream=None):
+               stream=None, lse: Optional[torch.Tensor] = None):
     """Causal attention of rows [starts[b], starts[b+1]) of q [T, H, D], sequence b's last
-    tokens, over its pages (with a window: the last `window` keys), into out [T, H, D]."""
-    T, _, D = q.shape
+    tokens, over its pages (with a window: the last `window` keys), into out [T, H, D].
+    lse (float32 [T, H]): receives the logarithm of each row's sum of exponentials."""
+    T, H, D = q.shape
     if out.shape != q.shape or D != cache.head_dim:
         raise ValueError("q and out are [n_tokens, n_heads, head_dim]")
     d = q.get_device()
-    _one_device(d, cache.t["k"], starts, out, workspace)
-    _call("kvd_paged_attn", d, stream, lib().kvd_paged_attn, cache.s, _heads(q), T,
+    _one_device(d, cache.t["k"], starts, out, workspace, lse)
+    args = (cache.s, _heads(q), T, _int32(starts, cache.batch + 1, "starts"), max_new,
+            softmax_scale, window, _heads(out))
+    ws = (_ptr(workspace), workspace.numel() * workspace.element_size())
+    if lse is None:
+        _call("kvd_paged_attn", d, stream, lib().kvd_paged_attn, *args, *ws)
+    else:
+        _call("kvd_paged_attn_lse", d, stream, lib().kvd_paged_attn_lse, *args, _lse(lse, T, H), *ws)
+
+
+# ------------------------------------------ latent rows, weights, eviction ---
+class LatentCache:
+    """A pool of pages of rows that all query heads share, and the C descriptor.
+
+    rows        [n_pages, page_size, rank + rope_dim] float16 or bfloat16: a token's normed
+                latent vector, then the rotated part of its key
+    page_table, seq_lens, status, len: as PagedKVCache
+    """
+
+    def __init__(self, dtype: int, batch: int, n_pages: int, page_size: int, max_pages: int,
+                 rank: int = 512, rope_dim: int = 64, device="cuda",
+                 tensors: Optional[dict] = None):
+        self.dtype, self.batch, self.n_pages = dtype, batch, n_pages
+        self.page_size, self.max_pages, self.rank, self.rope_dim = page_size, max_pages, rank, rope_dim
+        dev = torch.device(device)
+        t = dict(tensors) if tensors is not None else {}
+        kind = {F16: torch.float16, BF16: torch.bfloat16}.get(dtype)
+        if kind is None:
+            raise KvdError("LatentCache", 2)
+        want = {"rows": ((n_pages, page_size, rank + rope_dim), kind),
+                "page_table": ((batch, max_pages), torch.int32),
+                "seq_lens": ((batch,), torch.int32), "status": ((1,), torch.int32)}
+        for name, (shape, x) in want.items():
+            if name not in t:
+                t[name] = (torch.empty if name == "rows" else torch.zeros)(shape, dtype=x, device=dev)
+            elif tuple(t[name].shape) != shape or t[name].dtype != x:
+                raise ValueError(f"{name} is {x} of shape {shape}")
+        self.t = t
+        self.device = t["rows"].device
+        _one_device(t["rows"].get_device(), *t.values())
+        self.s = LatentCacheStruct(dtype, batch, rank, rope_dim, n_pages, page_size, max_pages, 0,
+                                   *(_ptr(t[n]) for n in ("rows", "page_table", "seq_lens", "status")))
+
+    @property
+    def len(self) -> int:
+        return self.s.len
+
+    @len.setter
+    def len(self, n: int):
+        self.s.len = int(n)
+
+    def __getattr__(self, name):
+        t = self.__dict__.get("t")
+        if t is not None and name in t:
+            return t[name]
+        raise AttributeError(name)
+
+    def ref(self):
+        return C.byref(self.s)
+
+    def device_status(self) -> int:
+        return int(self.t["status"].item())
+
+
+def _row(t: torch.Tensor, d: int, name: str):
+    """kvd_heads of rows [n_tokens, d], one head each."""
+    x = _X.get(t.dtype)
+    if x is None or t.dim() != 2 or t.shape[1] != d:
+        raise ValueError(f"{name} is [n_tokens, {d}] of float16, bfloat16 or float32")
+    if t.stride(1) != 1 and d != 1:
+        raise ValueError("the channels of a token must be dense")
+    return HeadsStruct(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else d, x, 1)
+
+
+def _parts(t: Optional[torch.Tensor]):
+    """kvd_head_parts of [n_tokens, n_heads, channels]; token and head strides are free."""
+    if t is None:
+        return None
+    x = _X.get(t.dtype)
+    if x is None or t.dim() != 3:
+        raise ValueError("head parts are [n_tokens, n_heads, channels] of float16, bfloat16 or float32")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if s2 != 1:
+        raise ValueError("the channels of a head must be dense")
+    s1 = s1 if h > 1 else d
+    return PartsStruct(t.data_ptr(), s0 if n > 1 else h * s1, s1, x, h)
+
+
+def latent_append(cache: LatentCache, c: torch.Tensor, k_pe: torch.Tensor, starts: torch.Tensor,
+                  rope: Optional[RopeTable] = None, c_weight: Optional[torch.Tensor] = None,
+                  eps: float = 1e-6, q_pe: Optional[torch.Tensor] = None,
+                  q_out: Optional[torch.Tensor] = None, stream=None):
+    """Rows [starts[b], starts[b+1]) of the latents c [T, rank] (normed with c_weight) and the
+    shared key parts k_pe [T, rope_dim] (rotated) to sequence b's last positions.  q_pe
+    [T, H, rope_dim], rotated too, goes to the last channels of q_out [T, H, rank + rope_dim],
+    whose others (the absorbed part) are not touched."""
+    T, R, P = c.shape[0], cache.rank, cache.rope_dim
+    if k_pe.dim() != 2 or k_pe.shape[0] != T:
+        raise ValueError("c and k_pe are [n_tokens, rank] and [n_tokens, rope_dim]")
+    to = None
+    if q_pe is not None:
+        if q_out is None or q_pe.dim() != 3 or tuple(q_pe.shape[::2]) != (T, P) or \
+                tuple(q_out.shape) != (T, q_pe.shape[1], R + P):
+            raise ValueError("q_pe is [n_tokens, n_heads, rope_dim], q_out [n_tokens, n_heads, "
+                             "rank + rope_dim]")
+        to = q_out[:, :, R:]
+    elif q_out is not None:
+        raise ValueError("q_pe and q_out are given together")
+    d = c.get_device()
+    _one_device(d, cache.t["rows"], k_pe, starts, c_weight, q_pe, q_out,
+                None if rope is None else rope.freqs)
+    _call("kvd_latent_append", d, stream, lib().kvd_latent_append, cache.s, _row(c, R, "c"),
+          _row(k_pe, P, "k_pe"), T, _int32(starts, cache.batch + 1, "starts"),
+          None if rope is None else rope.s, _weight(c_weight, R), _parts(q_pe), _parts(to), eps)
+
+
+def latent_workspace_bytes(cache: LatentCache, n_heads: int, n_tokens: int, max_new: int) -> int:
+    with torch.cuda.device(cache.device):
+        return int(lib().kvd_latent_workspace_bytes(cache.ref(), n_heads, n_tokens, max_new))
+
+
+def make_latent_workspace(cache: LatentCache, n_heads: int, n_tokens: int,
+                          max_new: int) -> torch.Tensor:
+    """A workspace for latent_attn calls of up to n_tokens new tokens, up to max_new a
+    sequence.  Calls that may overlap on the GPU need one each."""
+    n = latent_workspace_bytes(cache, n_heads, n_tokens, max_new)
+    if n == 0:
+        raise KvdError("kvd_latent_workspace_bytes", 1)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+
+def latent_attn(cache: LatentCache, q: torch.Tensor, starts: torch.Tensor, max_new: int,
+                softmax_scale: float, out: torch.Tensor, workspace: torch.Tensor, window: int = 0,
+                stream=None, lse: Optional[torch.Tensor] = None):
+    """Causal attention of rows [starts[b], starts[b+1]) of q [T, H, rank + rope_dim], sequence
+    b's last tokens, over its latent rows, whose first `rank` channels are the values, into
+    out [T, H, rank].  lse as for paged_attn."""
+    T, H, W = q.shape
+    if tuple(out.shape) != (T, H, cache.rank) or W != cache.rank + cache.rope_dim:
+        raise ValueError("q is [n_tokens, n_heads, rank + rope_dim], out [n_tokens, n_heads, rank]")
+    d = q.get_device()
+    _one_device(d, cache.t["rows"], starts, out, workspace, lse)
+    _call("kvd_latent_attn", d, stream, lib().kvd_latent_attn, cache.s, _heads(q), T,
           _int32(starts, cache.batch + 1, "starts"), max_new, softmax_scale, window, _heads(out),
-          _ptr(workspace), workspace.numel() * workspace.element_size())
+          _lse(lse, T, H), _ptr(workspace), workspace.numel() * workspace.element_size())
+
+
+def _kind(cache):
+    """("latent" or "paged", number of KV heads, channels of a key) of a cache in pages."""
+    if isinstance(cache, LatentCache):
+        return "latent", 1, cache.rank + cache.rope_dim
+    return "paged", cache.n_kv_heads, cache.head_dim
+
+
+def _mass(t: Optional[torch.Tensor], batch: int, heads: int, least: int, name: str):
+    """(pointer, stride) of weights [batch, heads, >= least]; rows dense and evenly apart."""
+    if t is None:
+        return None, 0
+    if t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != (batch, heads) or \
+            t.shape[2] < least:
+        raise ValueError(f"{name} is a float32 tensor [batch, n_kv_heads, at least {least}]")
+    s0, s1, s2 = t.stride()
+    if heads == 1:
+        s1 = s0 if batch > 1 else t.shape[2]
+    if (s2 != 1 and t.shape[2] > 1) or (batch > 1 and s0 != heads * s1):
+        raise ValueError(f"the rows of {name} must be dense and evenly apart")
+    return t.data_ptr(), s1
+
+
+def paged_mass(cache, q: torch.Tensor, lse: torch.Tensor, starts: torch.Tensor, max_new: int,
+               softmax_scale: float, mass: Optional[torch.Tensor], out: Optional[torch.Tensor] = None,
+               decay: float = 1.0, window: int = 0, stream=None):
+    """What an attention call's rows weighed each cached token with, added up a KV head:
+    out = decay * mass + the sum of weights, new tokens from 0; mass and out float32 [batch,
+    Hkv, >= cache.len] (out None: in place).  cache, q, starts, max_new, softmax_scale and
+    window are those of the paged_attn or latent_attn call that gave lse."""
+    kind, heads, D = _kind(cache)
+    T, H, W = q.shape
+    if W != D:
+        raise ValueError("q is [n_tokens, n_heads, channels of a key]")
+    out = mass if out is None else out
+    if out is None or (mass is None and decay != 0):
+        raise ValueError("without a mass the decay is 0 and out is given")
+    at, stride = _mass(mass, cache.batch, heads, cache.len, "mass")
+    to, to_stride = _mass(out, cache.batch, heads, cache.len, "out")
+    d = q.get_device()
+    _one_device(d, cache.t["page_table"], starts, lse, mass, out)
+    _call(f"kvd_{kind}_mass", d, stream, getattr(lib(), f"kvd_{kind}_mass"), cache.s, _heads(q),
+          _lse(lse, T, H), T, _int32(starts, cache.batch + 1, "starts"), max_new, softmax_scale,
+          window, at, stride, decay, to, to_stride)
+
+
+def paged_evict(cache, mass: torch.Tensor, keep: int, page_table_out: torch.Tensor,
+                kept: torch.Tensor, seq_lens_out: torch.Tensor,
+                mass_out: Optional[torch.Tensor] = None, sink: int = 0, recent: int = 0,
+                stream=None):
+    """Of each sequence and KV head the first `sink` tokens, the last `recent` and those of
+    most mass between, `keep` in all (all of a shorter sequence), in order to the pages of
+    page_table_out (int32 [batch, columns]; none that the cache's table needs).  kept (int32
+    [batch, Hkv, keep]) receives their old indices, seq_lens_out (int32 [batch]) the new
+    lengths, mass_out (float32 [batch, Hkv, >= keep]) their masses.  The caller goes on with
+    a cache over the new table and lengths; keys keep the rotation of their old positions."""
+    kind, heads, _ = _kind(cache)
+    if page_table_out.dtype != torch.int32 or page_table_out.dim() != 2 or \
+            page_table_out.shape[0] != cache.batch:
+        raise ValueError("page_table_out is an int32 tensor [batch, columns]")
+    if kept.dtype != torch.int32 or tuple(kept.shape) != (cache.batch, heads, keep):
+        raise ValueError("kept is an int32 tensor [batch, n_kv_heads, keep]")
+    at, stride = _mass(mass, cache.batch, heads, cache.len, "mass")
+    to, to_stride = _mass(mass_out, cache.batch, heads, keep, "mass_out")
+    d = mass.get_device()
+    _one_device(d, cache.t["page_table"], page_table_out, kept, seq_lens_out, mass_out)
+    _call(f"kvd_{kind}_evict", d, stream, getattr(lib(), f"kvd_{kind}_evict"), cache.s, at, stride,
+          keep, sink, recent, _ptr(page_table_out), page_table_out.shape[1], _ptr(kept),
+          _int32(seq_lens_out, cache.batch, "seq_lens_out"), to, to_stride)
 
 
 __all__ = ["F16", "INT8", "Q8_0", "Q4_0", "BF16", "BLOCK", "HEAD_DIM", "KVCache", "KvdError", "CacheStruct", "lib",
@@ -674,4 +926,6 @@ __all__ = ["F16", "INT8", "Q8_0", "Q4_0", "BF16", "BLOCK", "HEAD_DIM", "KVCache"
            "decode_step_host", "debug_qk_int8", "debug_scores", "debug_wait_timeout", "synth", "EXPORTS",
            "PagedCacheStruct", "HeadsStruct", "RopeStruct", "RopeTable", "rope_table",
            "qk_norm_rope", "PagedKVCache", "paged_workspace_bytes", "make_paged_workspace",
-           "paged_append", "paged_attn", "SCALINGS"]
+           "paged_append", "paged_attn", "SCALINGS", "LatentCacheStruct", "PartsStruct",
+           "LatentCache", "latent_append", "latent_workspace_bytes", "make_latent_workspace",
+           "latent_attn", "paged_mass", "paged_evict"]

@@ -1,0 +1,997 @@
+// latent_attn.cu -- attention of a ragged batch's new tokens over a paged cache of latent
+// rows, which all query heads share (kvd_latent_attn):
+//
+//   z_t = scale q . row_t (R + P channels),  out = sum_t softmax(z)_t row_t[:R],
+//   p - window < t <= p
+//
+// A row is key and value at once, so it comes into shared memory once and both products
+// read it there.  An output row has R = 512 channels in f32: 128 of them would fill the
+// tensor memory and leave none for the logits.  So the rows (tokens' query heads) stand
+// on the products' narrow side, up to 64 of them,
+//   S^T = K Q^T   64 keys x rows          O^T += V^T P^T   128 channels x rows, R / 128 times
+// with S twice and O in 2 * 64 + 4 * 64 columns, and key tiles are 64 tokens, of which
+// two fit beside the queries (72 KB each at 576 channels).  Measured, clocks a product
+// of 16: 64 x 64 32, 128 x 64 48 (shared memory's rate; 128 x 128 64): 1920 for 64 rows
+// and 64 keys of 576 channels, 1.35 PFLOP/s at most.
+//
+// One CTA per SM, persistent.  An item is a run of a sequence's new tokens and a group of
+// heads, together up to 64 rows, over the key tiles that any of them sees.  All items' key
+// tiles form one line, cut into equal costs for the CTAs; an item that a cut divides is
+// joined from f32 partials by join_kernel.
+//
+// Roles: warps 0-3 softmax, a thread 2 keys and a quarter of the rows (the layout of
+// 16 x 256-bit reads from tensor memory, of which 64-lane products fill 16 lanes a warp);
+// warp 4 loads by TMA, warp 5 issues S^T, warp 6 O^T.  A key tile's places are released
+// 128 channels at a time, as O^T is done with them.
+//
+// The reference m of a row's weights 2^(logit - m) follows its maximum loosely, from kLift
+// places below it, as in paged_decode.cu: no search for a tile's maximum unless a weight
+// passes kRedo.  P is rounded to the cache's type; sums and statistics are f32.
+#include <cstddef>
+
+#include "paged_attn_dev.cuh"
+
+namespace kvd {
+namespace {
+
+constexpr int kKeys = 64;              // keys a tile
+constexpr int kHalf = kKeys * 128;     // 64 channels of it
+constexpr int kPair = 2 * kHalf;       // 128 channels
+constexpr int kMaxRing = 8;            // tiles in shared memory
+constexpr int kMaxTops = 4;            // 128-channel parts of the latent vector
+constexpr int kThreads = 256;
+constexpr float kLift = 6.0f;          // a new reference: so far below the row's maximum
+constexpr float kRedo = 32768.0f;      // a weight above it asks for one
+constexpr int kFewSeqs = 48;           // sequences whose items are counted a warp each
+// What an item takes beside its key tiles (queries in, first products, rows out), in tiles.
+constexpr int kItemCost = 3;
+constexpr int kSmemTop = 232448;       // shared memory a CTA can have
+
+struct LatentDev : AttnArgs {
+    int tops;                   // R / 128
+    int rope_steps;             // 16-channel steps of the rotated part
+    int heads, groups, tokens;  // an item: heads (of so many groups), tokens
+    int ring;                   // tiles in shared memory
+    float *acc;                 // partial outputs [2 * CTAs][NR][R]
+    float2 *ml;                 // their references and sums [2 * CTAs][NR]
+    int4 *join;                 // [CTAs][2]: what join_kernel joins
+};
+
+// ---------------------------------------------------------------- items ---
+struct Item {
+    int i0, cnt;    // tokens of the sequence's new ones
+    int lo, hi;     // keys [lo, hi) that any of them sees
+    int j0, tiles;  // key tiles: one at least, so that rows that see nothing are written
+};
+__device__ __forceinline__ Item item_of(const LatentDev &a, const Seq &s, int tile) {
+    Item it;
+    it.i0 = tile * a.tokens;
+    it.cnt = min(a.tokens, s.n - it.i0);
+    const int p0 = s.first + it.i0;
+    it.hi = max(p0 + it.cnt, 0);
+    it.lo = a.window > 0 ? min(max(p0 - a.window + 1, 0), it.hi) : 0;
+    it.j0 = it.lo / kKeys;
+    it.tiles = max((it.hi + kKeys - 1) / kKeys - it.j0, 1);
+    return it;
+}
+
+// A CTA's walk along the line of items, the same in every role.  The line counts an item
+// as kItemCost units and then its tiles.
+struct Walk {
+    int b, tile, group;
+    int off;    // units of the item that lie before
+    int k;      // segments taken
+    long left;  // units
+    Seq s;
+};
+struct Segment {
+    Item it;
+    int b, s0, p0, group;
+    int j0, j1;         // key tiles
+    bool starts, ends;  // whether it holds its item's first and last tile
+    int k;
+};
+__device__ __forceinline__ bool next_segment(const LatentDev &a, Walk &w, Segment &g) {
+    if (w.left <= 0) return false;
+    g.it = item_of(a, w.s, w.tile);
+    const int units = g.it.tiles + kItemCost;
+    const int take = static_cast<int>(min(static_cast<long>(units - w.off), w.left));
+    // the item's tiles are another CTA's: it begins with its first tile
+    if (w.off + take <= kItemCost) return false;
+    g.b = w.b;
+    g.s0 = w.s.s0;
+    g.p0 = w.s.first + g.it.i0;
+    g.group = w.group;
+    g.j0 = g.it.j0 + max(w.off - kItemCost, 0);
+    g.j1 = g.it.j0 + w.off + take - kItemCost;
+    g.starts = w.off <= kItemCost;
+    g.ends = w.off + take == units;
+    g.k = w.k++;
+    w.left -= take;
+    w.off = 0;
+    if (w.left > 0 && ++w.group == a.groups) {
+        w.group = 0;
+        if ((w.tile + 1) * a.tokens < w.s.n) {
+            ++w.tile;
+        } else {
+            w.tile = 0;
+            do {
+                if (++w.b >= a.c.batch) {  // the line has no more items
+                    w.left = 0;
+                    break;
+                }
+                w.s = seq_of(a, w.b, false);
+            } while (w.s.n == 0);
+        }
+    }
+    return true;
+}
+
+// 16 lanes' columns [0, NR) of the calling warp's quarter: v[4 i + e] is lane l / 4 (e < 2) or
+// l / 4 + 8, column 8 i + 2 (l % 4) + e % 2.
+template <int NR>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&v)[NR / 2]) {
+    uint32_t *r = reinterpret_cast<uint32_t *>(v);
+#pragma unroll
+    for (int i = 0; i < NR / 2; i += 8)
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+            : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]),
+              "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+            : "r"(addr + 2 * i));
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < NR / 2; i += 8)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]),
+                          "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+
+// wait_for where each lane (of those that take part) has its own barrier.
+__device__ __forceinline__ bool wait_lanes(bool mine, uint64_t *bar, uint32_t parity,
+                                           volatile int *abort) {
+    uint32_t n = 0, t0 = 0;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity))) {
+        if ((++n & 63u) == 0) {
+            const uint32_t t = static_cast<uint32_t>(global_timer_ns());
+            if (n == 64) t0 = t;
+            if (__any_sync(0xffffffffu, *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs)))
+                return false;
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ void meet_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool any_of_128(bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(mine))
+        : "memory");
+    return r != 0;
+}
+
+// What stands behind the tiles in shared memory.
+struct Small {
+    uint64_t q_full, q_empty, full[kMaxRing][kMaxTops + 1], empty[kMaxRing][kMaxTops + 1],
+        s_full[2], p_full[2], o_done[2], done;
+    uint32_t tmem_slot;
+    int abort_flag, found_seq;
+    uint32_t dead_groups[16];  // per key tile: its 16-key groups on bad pages
+    alignas(16) float m[64];  // rows' references,
+    alignas(16) float base[64], f[64];  // less or 0, and the factor to a new one
+    union {
+        alignas(16) float red[4][64];
+        struct {
+            long seq_units[kFewSeqs], scan_total[kThreads / 32], found_rest;
+            Walk start;
+        };
+    };
+};
+static_assert(sizeof(Small) <= 3072, "two tiles of 576 channels and 64 rows leave no more");
+static_assert(offsetof(Small, base) % 8 == 0, "read by pairs");
+
+template <int NR>
+struct LatentShape {
+    static constexpr int kP = NR == 64 ? 1 : 2;  // buffers of weights, 64 keys of 128 bytes
+    static constexpr uint32_t kColumns = NR == 64 ? 512 : NR == 32 ? 256 : 128;
+};
+
+template <bool BF16, int NR>
+__global__ void __launch_bounds__(kThreads, 1)
+latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUtensorMap q_map,
+              const __grid_constant__ CUtensorMap k_map) {
+    using Sh = LatentShape<NR>;
+    constexpr int kQChunk = NR * 128;  // 64 channels of the rows
+    constexpr uint32_t kO = 2 * NR;    // columns of O
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const int parts = a.tops + 1;      // of a row: the rotated part, then 128 channels each
+    const int tile_bytes = a.tops * kPair + kHalf;
+    uint8_t *q_smem = smem;            // the rotated part's chunk first
+    uint8_t *p_smem = q_smem + (2 * a.tops + 1) * kQChunk;
+    uint8_t *ring = p_smem + Sh::kP * kHalf;
+    Small &sm = *reinterpret_cast<Small *>(ring + a.ring * tile_bytes);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (smem_addr(smem) & 1023) {      // (the launch asks for no other shared memory)
+        if (tid == 0) report_status(a.c.dev_status, KVD_ERR_CUDA);
+        return;
+    }
+    if (warp == 5) tmem_alloc(&sm.tmem_slot, Sh::kColumns);
+    if (tid == 0) {
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_empty, 1);
+        for (int i = 0; i < a.ring; ++i)
+            for (int p = 0; p < parts; ++p) {
+                mbar_init(&sm.full[i][p], 1);
+                mbar_init(&sm.empty[i][p], 1);
+            }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.s_full[i], 1);
+            mbar_init(&sm.p_full[i], 4);
+            mbar_init(&sm.o_done[i], 1);
+        }
+        mbar_init(&sm.done, 2);
+        fence_barrier_init();
+        sm.abort_flag = 0;
+        sm.start.left = 0;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // ---- this CTA's piece of the line of items
+    // of a group of heads of a sequence: a warp's lanes take a run of tokens each
+    auto units_of = [&](const Seq &s) -> long {
+        long n = 0;
+#pragma unroll 1
+        for (int t = lane; t * a.tokens < s.n; t += 32) n += item_of(a, s, t).tiles + kItemCost;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        return n;
+    };
+    constexpr int kAlone = 16;  // items that a lane counts by itself
+    auto cost_of = [&](int b, bool report) -> long {
+        Seq s = {};
+        if (b < a.c.batch) s = seq_of(a, b, report);
+        const bool many = s.n > kAlone * a.tokens;
+        long n = 0;
+#pragma unroll 1
+        for (int t = 0; !many && t * a.tokens < s.n; ++t) n += item_of(a, s, t).tiles + kItemCost;
+        uint32_t more = __ballot_sync(0xffffffffu, many);
+#pragma unroll 1
+        for (; more; more &= more - 1) {
+            const int l = __ffs(more) - 1;
+            const long u = units_of(seq_of(a, b - lane + l, false));
+            if (lane == l) n = u;
+        }
+        return n * a.groups;
+    };
+    auto scan = [&](long cost, long &before) -> long {  // exclusive prefix, and the sum
+        long v = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        if (lane == 31) sm.scan_total[warp] = v;
+        __syncthreads();
+        long sum = 0;
+        before = v - cost;
+        for (int i = 0; i < kThreads / 32; ++i) {
+            if (i < warp) before += sm.scan_total[i];
+            sum += sm.scan_total[i];
+        }
+        __syncthreads();
+        return sum;
+    };
+    long before = 0, cost;
+    if (a.c.batch <= kFewSeqs) {
+#pragma unroll 1
+        for (int b = warp; b < a.c.batch; b += kThreads / 32) {
+            const long n = units_of(seq_of(a, b, blockIdx.x == 0));
+            if (lane == 0) sm.seq_units[b] = n;
+        }
+        __syncthreads();
+        cost = tid < a.c.batch ? sm.seq_units[tid] * a.groups : 0;
+    } else {
+        cost = cost_of(tid, blockIdx.x == 0);
+    }
+    long total = scan(cost, before);
+    const bool one_pass = a.c.batch <= kThreads;
+#pragma unroll 1
+    for (int b0 = kThreads; b0 < a.c.batch; b0 += kThreads) {
+        long skip;
+        total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
+    }
+    const long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long>(a.min_tiles));
+    const long ctas = max(min(static_cast<long>(gridDim.x), (total + per - 1) / per), 1l);
+    const long share = total / ctas, spare = total % ctas;
+    auto cut = [&](long c) { return c * share + min(c, spare); };  // where CTA c begins
+    const long x0 = blockIdx.x < ctas ? cut(blockIdx.x) : total;
+    const long x1 = blockIdx.x < ctas ? cut(blockIdx.x + 1) : total;
+    if (x0 < x1) {
+        long base = 0;
+#pragma unroll 1
+        for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
+            if (!one_pass) {
+                cost = cost_of(b0 + tid, false);
+                const long sum = scan(cost, before);
+                before += base;
+                base += sum;
+            }
+            if (before <= x0 && x0 < before + cost) {
+                sm.found_seq = b0 + tid;
+                sm.found_rest = x0 - before;
+            }
+        }
+        __syncthreads();
+        if (warp == 0) {  // the run of tokens, 32 at a time; its groups follow one another
+            Walk w;
+            w.b = sm.found_seq;
+            w.s = seq_of(a, w.b, false);
+            long r = sm.found_rest;
+#pragma unroll 1
+            for (int t0 = 0;; t0 += 32) {
+                const int t = t0 + lane;
+                const int one = t * a.tokens < w.s.n ? item_of(a, w.s, t).tiles + kItemCost : 0;
+                const long n = static_cast<long>(one) * a.groups;
+                long upto = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long u = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += u;
+                }
+                const uint32_t in = __ballot_sync(0xffffffffu, r < upto);
+                if (in || t0 * a.tokens >= w.s.n) {
+                    const int l = in ? __ffs(in) - 1 : 0;
+                    const long rest = r - __shfl_sync(0xffffffffu, upto - n, l);
+                    const int unit = max(__shfl_sync(0xffffffffu, one, l), 1);
+                    w.tile = t0 + l;
+                    w.group = static_cast<int>(rest / unit);
+                    w.off = static_cast<int>(rest - static_cast<long>(w.group) * unit);
+                    break;
+                }
+                r -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+            w.left = x1 - x0;
+            w.k = 0;
+            if (lane == 0) sm.start = w;
+        }
+    }
+    __syncthreads();
+    const uint32_t tmem = sm.tmem_slot;
+    Walk w = sm.start;
+    Segment g;
+    volatile int *abort = &sm.abort_flag;
+    auto fail = [&] {
+        *abort = 1;
+        report_status(a.c.dev_status, KVD_ERR_TIMEOUT);
+    };
+    __syncthreads();  // `start` has been read: its memory is the softmax's
+    bool ok = true;
+
+    if (warp == 4) {
+        // ------------------------------------------------------------ loads ---
+        // rows that other items read too stay in the L2
+        const bool shared = a.groups > 1 || a.max_new > a.tokens;
+        const uint64_t policy = shared ? l2_policy_evict_last() : l2_policy_evict_first();
+        const int boxes = kKeys / a.box, ps = a.c.page_size;
+        const int per_read = 32 / boxes;  // tiles whose rows one read of the page table gives
+        uint32_t n = 0, mine = 0, queries = 0;  // tiles, this lane's loads of them, of queries
+        uint32_t st = 0, round = 0;
+        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
+#pragma unroll 1
+        while (ok && next_segment(a, w, g)) {
+            if (queries > 0 && !(ok = wait_for(&sm.q_empty, (queries - 1) & 1, abort))) break;
+            ++queries;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&sm.q_full, (2 * a.tops + 1) * a.heads * a.tokens * 128);
+            __syncwarp();
+            if (lane <= 2 * a.tops)
+                tma_load_4d(q_smem + lane * kQChunk, &q_map, lane == 0 ? a.tops * 128 : (lane - 1) * 64,
+                            g.group * a.heads, 0, g.s0 + g.it.i0, &sm.q_full);
+            // the cache rows of the boxes of tiles j, j + 1, .., a lane a box: dead_row
+            // where none is needed, -1 on a bad page
+            auto rows_of = [&](int j) -> int {
+                const int t0 = (j + lane / boxes) * kKeys + lane % boxes * a.box;
+                if (t0 >= g.j1 * kKeys || t0 >= g.it.hi || t0 + a.box <= g.it.lo) return a.dead_row;
+                const int col = t0 / ps;
+                const int page = checked_page(a.c, g.b, col);
+                return page < 0 ? -1 : page * ps + (t0 - col * ps);
+            };
+            int rows = 0, rows_next = rows_of(g.j0);
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j) {
+                const int in = (j - g.j0) % per_read;
+                if (in == 0) {
+                    rows = rows_next;
+                    rows_next = rows_of(j + per_read);
+                }
+                int row[4];
+                uint32_t bad = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    row[x] = __shfl_sync(0xffffffffu, rows, in * boxes + min(x, boxes - 1));
+                    if (row[x] < 0) {
+                        row[x] = a.dead_row;
+                        if (x < boxes) bad |= ((1u << (a.box / 16)) - 1) << (x * (a.box / 16));
+                    }
+                }
+                if (lane == 0) sm.dead_groups[n & 15] = bad;
+                __syncwarp();
+                // Lane 0 loads the rotated part, lane p the channels [128 (p - 1), 128 p), each
+                // as soon as its place is free.
+                uint64_t *full = &sm.full[st][min(lane, a.tops)];
+                uint64_t *empty = &sm.empty[st][min(lane, a.tops)];
+                uint8_t *dst = ring + st * tile_bytes + (lane == 0 ? a.tops * kPair : (lane - 1) * kPair);
+                bool todo = lane < parts;
+                uint32_t tries = 0, t0 = 0;
+#pragma unroll 1
+                while (__any_sync(0xffffffffu, todo)) {
+                    if (todo && (round == 0 || mbar_try_wait(empty, (round - 1) & 1))) {
+                        mbar_arrive_expect_tx(full, lane == 0 ? kHalf : kPair);
+                        const int x0 = lane == 0 ? a.tops * 128 : (lane - 1) * 128;
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            if (x < boxes) {
+                                tma_load_2d(dst + x * a.box * 128, &k_map, x0, row[x], full, policy);
+                                if (lane > 0)
+                                    tma_load_2d(dst + kHalf + x * a.box * 128, &k_map, x0 + 64, row[x],
+                                                full, policy);
+                            }
+                        todo = false;
+                        ++mine;
+                    }
+                    if ((++tries & 63u) == 0) {
+                        const uint32_t t = static_cast<uint32_t>(global_timer_ns());
+                        if (tries == 64) t0 = t;
+                        if (__any_sync(0xffffffffu,
+                                       *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs))) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                }
+                if (!ok) break;
+                ++n;
+                if (++st == static_cast<uint32_t>(a.ring)) {
+                    st = 0;
+                    ++round;
+                }
+            }
+            if (ok && g.starts && !g.ends) {
+                // the item goes on in the next CTAs: leave word for join_kernel
+                const long rest = g.it.j0 + g.it.tiles - g.j1;  // tiles, and units
+                int pieces = 1;
+                while (cut(blockIdx.x + pieces + 1) - x1 < rest) ++pieces;
+                rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
+                rec1 = make_int4(g.group, 0, 0, 0);
+            }
+        }
+        if (!ok) fail();
+        if (lane == 0) {
+            a.join[2 * blockIdx.x] = rec0;
+            a.join[2 * blockIdx.x + 1] = rec1;
+        }
+        tmem_fence_before();
+        __syncthreads();  // all roles are done, and know whether a wait ran out
+        if (*abort) {
+            // nothing may land in shared memory after the CTA has gone
+            volatile int none = 0;
+            bool landed = true;  // after one wait that runs out all has had the time to land
+            for (uint32_t i = 0; lane < parts && landed && i < static_cast<uint32_t>(a.ring); ++i) {
+                const uint32_t fills = (mine + a.ring - 1 - i) / a.ring;
+                if (fills > 0) landed = mbar_wait(&sm.full[i][lane], (fills - 1) & 1, &none);
+            }
+            __syncwarp();
+            if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, &none);
+        }
+        return;
+    } else if (warp == 5) {
+        // -------------------------------------------------- products S^T = K Q^T ---
+        constexpr uint32_t kIdS = mma_idesc(BF16, kKeys, NR, false);
+        const uint32_t ring_addr = smem_addr(ring);
+        const uint32_t q = warp_uniform(desc_low(smem_addr(q_smem), 16));
+        const uint32_t tmem_u = warp_uniform(tmem);
+        uint32_t n = 0, st = 0, round = 0, queries = 0;
+#pragma unroll 1
+        while (ok && next_segment(a, w, g)) {
+            if (!(ok = wait_for(&sm.q_full, queries & 1, abort))) break;
+            ++queries;
+#pragma unroll 1
+            for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                // the logits of two tiles ago have been read
+                if (n >= 2 && !(ok = wait_for(&sm.p_full[b], ((n >> 1) - 1) & 1, abort))) break;
+                tmem_fence_after();
+                const uint32_t s_at = warp_uniform(tmem_u + b * NR);
+                const uint32_t k = warp_uniform(desc_low(ring_addr + st * tile_bytes, 16));
+#pragma unroll 1
+                for (int p = 0; p < parts; ++p) {
+                    if (!(ok = wait_for(&sm.full[st][p], round & 1, abort))) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        if (p == 0) {
+                            const uint32_t k0 = k + a.tops * (kPair / 16);
+#pragma unroll 1
+                            for (int x = 0; x < a.rope_steps; ++x)
+                                mma_ss(s_at, smem_desc(k0 + 2 * x), smem_desc(q + 2 * x), kIdS, x > 0);
+                            mma_commit(&sm.empty[st][0]);
+                        } else {
+                            const uint32_t k0 = k + (p - 1) * (kPair / 16);
+                            const uint32_t q0 = q + (2 * p - 1) * (kQChunk / 16);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                mma_ss(s_at, smem_desc(k0 + x / 4 * (kHalf / 16) + x % 4 * 2),
+                                       smem_desc(q0 + x / 4 * (kQChunk / 16) + x % 4 * 2), kIdS, 1);
+                        }
+                        if (p == a.tops) {
+                            mma_commit(&sm.s_full[b]);
+                            if (j + 1 == g.j1) mma_commit(&sm.q_empty);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (++st == static_cast<uint32_t>(a.ring)) {
+                    st = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok) fail();
+        // every product and every barrier arrival is done before the CTA goes
+        if (elect_one()) mma_commit(&sm.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&sm.done, 0, &none)) fail();
+    } else if (warp == 6) {
+        // ---------------------------------------------- products O^T += V^T P^T ---
+        constexpr uint32_t kIdO = mma_idesc(BF16, 128, NR, true, true);
+        const uint32_t ring_addr = smem_addr(ring);
+        const uint32_t tmem_u = warp_uniform(tmem);
+        uint32_t n = 0, st = 0, round = 0;
+#pragma unroll 1
+        while (ok && next_segment(a, w, g)) {
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                if (!(ok = wait_for(&sm.p_full[b], (n >> 1) & 1, abort))) break;
+                // (they have landed: the logits come from them)
+                if (!(ok = wait_lanes(lane > 0 && lane < parts, &sm.full[st][min(lane, a.tops)],
+                                      round & 1, abort)))
+                    break;
+                tmem_fence_after();
+                const int from = max(g.it.lo - j * kKeys, 0), to = min(g.it.hi - j * kKeys, kKeys);
+                if (from > 0 || to < kKeys) {
+                    // rows that no token sees may hold NaN: clear them
+                    uint8_t *vs = ring + st * tile_bytes;
+                    const int per_row = 16 * a.tops;
+                    const int c = (from + (kKeys - max(to, 0))) * per_row;
+#pragma unroll 1
+                    for (int i = lane; i < c; i += 32) {
+                        int r = i / per_row;
+                        const int x = i - r * per_row;
+                        if (r >= from) r += max(to, 0) - from;
+                        *reinterpret_cast<uint4 *>(vs + x / 8 * kHalf + r * 128 + x % 8 * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+                const uint32_t v = warp_uniform(desc_low(ring_addr + st * tile_bytes, kHalf));
+                const uint32_t p = warp_uniform(
+                    desc_low(smem_addr(p_smem) + (Sh::kP == 2 ? b * kHalf : 0), kHalf));
+                const uint32_t add = warp_uniform(j > g.j0);
+                if (elect_one()) {
+#pragma unroll 1
+                    for (int m = 0; m < a.tops; ++m) {
+#pragma unroll
+                        for (int x = 0; x < kKeys / 16; ++x)
+                            mma_ss(tmem_u + kO + m * NR, smem_desc(v + m * (kPair / 16) + x * (2048 / 16)),
+                                   smem_desc(p + x * (2048 / 16)), kIdO, x > 0 ? 1 : add);
+                        mma_commit(&sm.empty[st][1 + m]);
+                    }
+                    mma_commit(&sm.o_done[b]);
+                }
+                __syncwarp();
+                if (++st == static_cast<uint32_t>(a.ring)) {
+                    st = 0;
+                    ++round;
+                }
+            }
+        }
+        if (!ok) fail();
+        if (elect_one()) mma_commit(&sm.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&sm.done, 0, &none)) fail();
+    } else if (warp < 4) {
+        // ------------------------------------------------------------ softmax ---
+        constexpr int kV = NR / 2;   // logits a thread: 4 for each 8 rows
+        const uint32_t lanes = tmem + (warp << 21);
+        const int key0 = warp * 16 + lane / 4, col0 = 2 * (lane & 3);
+        const int R = a.tops * 128;
+        uint32_t n = 0;
+        // These warps meet at barriers of the hardware, which have no limit: so none
+        // leaves its loops before the others, and a wait that ran out only makes the
+        // waits behind it pass.
+        auto wait = [&](uint64_t *b, uint32_t parity) {
+            if (ok) ok = wait_for(b, parity, abort);
+        };
+#pragma unroll 1
+        while (next_segment(a, w, g)) {
+            const int heads = min(a.heads, a.G - g.group * a.heads);
+            // keys that every row sees
+            const int all_lo = a.window > 0 ? max(g.p0 + g.it.cnt - a.window, 0) : 0;
+            const int all_hi = max(g.p0 + 1, 0);
+            auto live = [&](int r) { return r < g.it.cnt * a.heads && r % a.heads < heads; };
+            float l[kV / 2];
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) l[i] = 0.0f;
+            bool open = true;  // a row has seen no key yet, and so has no reference
+#pragma unroll 1
+            for (int j = g.j0; j < g.j1; ++j, ++n) {
+                const uint32_t b = n & 1;
+                wait(&sm.s_full[b], (n >> 1) & 1);
+                tmem_fence_after();
+                const uint32_t bad = sm.dead_groups[n & 15] >> warp & 1;
+                // the rows [r0, r1) that see each of the two keys
+                int r0[2] = {0, 0}, r1[2] = {NR, NR};
+                const bool edge = j * kKeys < all_lo || (j + 1) * kKeys > all_hi || bad;
+                if (edge) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int t = j * kKeys + key0 + 8 * e;
+                        r1[e] = 0;
+                        if (t >= g.it.lo && t < g.it.hi && !bad) {
+                            const int first = max(t - g.p0, 0);
+                            int last = g.it.cnt - 1;
+                            if (a.window > 0) last = min(last, t + a.window - 1 - g.p0);
+                            if (first <= last) {
+                                r0[e] = first * a.heads;
+                                r1[e] = (last + 1) * a.heads;
+                            }
+                        }
+                    }
+                }
+                bool fix = open;
+                float p[kV];
+#pragma unroll 1
+                for (;;) {
+                    float s[kV];
+                    tmem_ld_rows<NR>(lanes + b * NR, s);
+                    if (edge)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) {
+                            const int r = i / 4 * 8 + col0 + (i & 1), e = i >> 1 & 1;
+                            if (r < r0[e] || r >= r1[e]) s[i] = -INFINITY;
+                        }
+                    if (fix) {
+                        // each row's maximum, over the warp's keys, then over all
+#pragma unroll
+                        for (int i = 0; i < kV; i += 4)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float t = fmaxf(s[i + e], s[i + 2 + e]);
+#pragma unroll
+                                for (int o = 4; o < 32; o <<= 1)
+                                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
+                                if (lane < 4) sm.red[warp][i / 4 * 8 + col0 + e] = t;
+                            }
+                        // O as it stands is complete
+                        if (j > g.j0) wait(&sm.o_done[b ^ 1], ((n - 1) >> 1) & 1);
+                        meet_128();
+                        bool none = false;
+                        if (tid < NR) {
+                            const float top = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
+                                                    fmaxf(sm.red[2][tid], sm.red[3][tid]));
+                            const float m = j == g.j0 ? -INFINITY : sm.m[tid];
+                            const float mn = fmaxf(m, top * a.scale_log2 - kLift);
+                            sm.f[tid] =
+                                m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
+                            sm.m[tid] = mn;
+                            const bool some = live(tid);
+                            none = some && mn == -INFINITY;
+                            // rows that are none (another sequence's queries may stand
+                            // there): no weights, and no say in the votes
+                            sm.base[tid] = !some ? -INFINITY : mn == -INFINITY ? 0.0f : -mn;
+                        }
+                        open = any_of_128(none);
+#pragma unroll
+                        for (int i = 0; i < kV / 2; ++i) l[i] *= sm.f[i / 2 * 8 + col0 + (i & 1)];
+                        if (j > g.j0) {
+                            tmem_fence_after();
+#pragma unroll 1
+                            for (int i = 0; i < a.tops * NR; i += 16) {
+                                float o[16];
+                                tmem_ld16(lanes + kO + i, o);
+                                tmem_wait_ld();
+                                pin16(o);
+#pragma unroll
+                                for (int r = 0; r < 16; ++r) o[r] *= sm.f[i % NR + r];
+                                tmem_st16(lanes + kO + i, reinterpret_cast<uint32_t *>(o));
+                            }
+                            tmem_wait_st();
+                            tmem_fence_before();
+                        }
+                    }
+                    const float2 k2 = make_float2(a.scale_log2, a.scale_log2);
+                    float top = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kV; i += 4) {
+                        const float2 base =
+                            *reinterpret_cast<const float2 *>(&sm.base[i / 4 * 8 + col0]);
+#pragma unroll
+                        for (int e = 0; e < 4; e += 2) {
+                            const float2 u = __ffma2_rn(make_float2(s[i + e], s[i + e + 1]), k2, base);
+                            p[i + e] = exp2_approx(u.x);
+                            p[i + e + 1] = exp2_approx(u.y);
+                            top = fmax3(top, p[i + e], p[i + e + 1]);
+                        }
+                    }
+                    if (edge)  // (a row without a reference yet, or -infinity less infinity)
+#pragma unroll
+                        for (int i = 0; i < kV; ++i) {
+                            const int r = i / 4 * 8 + col0 + (i & 1), e = i >> 1 & 1;
+                            if (r < r0[e] || r >= r1[e]) p[i] = 0.0f;
+                        }
+                    if (fix) break;  // no weight passes 2^kLift
+                    if (!any_of_128(top > kRedo)) break;
+                    fix = true;
+                }
+                // P^T's buffer has been read
+                if (Sh::kP == 1) {
+                    if (n >= 1) wait(&sm.o_done[b ^ 1], ((n - 1) >> 1) & 1);
+                } else {
+                    if (n >= 2) wait(&sm.o_done[b], ((n >> 1) - 1) & 1);
+                }
+                // the weights, and P^T: a key's rows in 128 swizzled bytes
+                uint8_t *dst = p_smem + (Sh::kP == 2 ? b * kHalf : 0) + key0 * 128 + (lane & 3) * 4;
+#pragma unroll
+                for (int i = 0; i < kV; i += 4) {
+                    l[i / 2] += p[i] + p[i + 2];
+                    l[i / 2 + 1] += p[i + 1] + p[i + 3];
+                    const int at = ((i / 4) ^ (key0 & 7)) * 16;  // (key0 + 8 has the same low bits)
+                    *reinterpret_cast<uint32_t *>(dst + at) = pack2<BF16>(p[i], p[i + 1]);
+                    *reinterpret_cast<uint32_t *>(dst + 1024 + at) = pack2<BF16>(p[i + 2], p[i + 3]);
+                }
+                fence_proxy_async();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.p_full[b]);
+            }
+            // ---- the segment's sums
+            meet_128();  // the last references have been read
+#pragma unroll
+            for (int i = 0; i < kV / 2; ++i) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+                if (lane < 4) sm.red[warp][i / 2 * 8 + col0 + (i & 1)] = l[i];
+            }
+            wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
+            tmem_fence_after();
+            meet_128();
+            const bool whole = g.starts && g.ends;
+            const uint32_t slot = 2 * blockIdx.x + (g.k == 0 ? 0 : 1);
+            if (tid < NR) {
+                const float sum = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+                const float m = sm.m[tid];
+                sm.f[tid] = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+                if (live(tid)) {
+                    if (!whole) {
+                        a.ml[slot * NR + tid] = make_float2(m, sum);
+                    } else if (a.lse) {
+                        const int tok = tid / a.heads;
+                        a.lse[static_cast<int64_t>(g.s0 + g.it.i0 + tok) * a.G + g.group * a.heads +
+                              (tid - tok * a.heads)] = lse_of(m, sum);
+                    }
+                }
+            }
+            meet_128();
+            const int rows = g.it.cnt * a.heads;
+#pragma unroll 1
+            for (int m = 0; m < a.tops; ++m) {
+                const int channel = m * 128 + tid;
+#pragma unroll 1
+                for (int i = 0; i < NR && i < rows; i += 16) {
+                    float o[16];
+                    tmem_ld16(lanes + kO + m * NR + i, o);
+                    tmem_wait_ld();
+                    pin16(o);
+                    int tok = i / a.heads, head = i - tok * a.heads;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        if (i + r < rows && head < heads) {
+                            if (whole) {
+                                const float f = sm.f[i + r];
+                                a.out[static_cast<int64_t>(g.s0 + g.it.i0 + tok) * a.out_stride +
+                                      static_cast<int64_t>(g.group * a.heads + head) * R + channel] =
+                                    static_cast<uint16_t>(pack2<BF16>(f != 0.0f ? o[r] * f : 0.0f, 0.0f));
+                            } else {
+                                a.acc[(static_cast<size_t>(slot) * NR + i + r) * R + channel] = o[r];
+                            }
+                        }
+                        if (++head == a.heads) {
+                            head = 0;
+                            ++tok;
+                        }
+                    }
+                }
+            }
+            tmem_fence_before();
+            meet_128();  // the next segment's references go where these stood
+        }
+        if (!ok) fail();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tmem_fence_after();
+        tmem_free(tmem, Sh::kColumns);
+    }
+}
+
+// Joins the items that a cut between CTAs divided: CTA (c, y) serves rows y, y + gridDim.y, ..
+// of the item whose first piece is CTA c's last segment and goes on in the CTAs after it.
+//   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
+constexpr int kMaxCtas = 256;
+template <bool BF16, int NR>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ LatentDev a) {
+    __shared__ float factors[kMaxCtas + 1];
+    __shared__ float inverse;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 rec = a.join[2 * blockIdx.x];
+    if (rec.x == 0) return;
+    const int group = a.join[2 * blockIdx.x + 1].x;
+    const int tid = threadIdx.x, R = a.tops * 128;
+    const size_t first = 2 * blockIdx.x + rec.y, next = 2 * blockIdx.x;
+    auto slot_of = [&](int i) { return i == 0 ? first : next + 2 * i; };
+    const int heads = min(a.heads, a.G - group * a.heads);
+#pragma unroll 1
+    for (int r = blockIdx.y; r < rec.w * a.heads; r += gridDim.y) {
+        const int tok = r / a.heads, head = r - tok * a.heads;
+        if (head >= heads) continue;
+        __syncthreads();
+        if (tid < 32) {
+            float m = -INFINITY, l = 0.0f;
+            for (int i = tid; i < rec.x; i += 32) m = fmaxf(m, a.ml[slot_of(i) * NR + r].x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            for (int i = tid; i < rec.x; i += 32) {
+                const float2 ml = a.ml[slot_of(i) * NR + r];
+                const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
+                factors[i] = f;
+                l = fmaf(f, ml.y, l);  // a sum that is NaN stays one where f is 0
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            if (tid == 0) {
+                inverse = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+                if (a.lse)
+                    a.lse[static_cast<int64_t>(rec.z + tok) * a.G + group * a.heads + head] =
+                        lse_of(m, l);
+            }
+        }
+        __syncthreads();
+        if (tid * 4 < R) {
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+            for (int i = 0; i < rec.x; ++i) {
+                const float4 u =
+                    *reinterpret_cast<const float4 *>(a.acc + (slot_of(i) * NR + r) * R + tid * 4);
+                const float f = factors[i];
+                if (f != 0.0f) {
+                    o.x = fmaf(f, u.x, o.x);
+                    o.y = fmaf(f, u.y, o.y);
+                    o.z = fmaf(f, u.z, o.z);
+                    o.w = fmaf(f, u.w, o.w);
+                }
+            }
+            const float inv = inverse;
+            *reinterpret_cast<uint2 *>(a.out + static_cast<int64_t>(rec.z + tok) * a.out_stride +
+                                       static_cast<int64_t>(group * a.heads + head) * R + tid * 4) =
+                make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+        }
+    }
+}
+
+// ----------------------------------------------------------------- launch ---
+struct Plan {
+    int ctas, heads, groups, tokens, nr;
+    size_t ml, acc, total;
+};
+
+Plan plan_of(int H, int rank, int max_new) {
+    Plan w;
+    w.ctas = device_sm_count() < kMaxCtas ? device_sm_count() : kMaxCtas;
+    w.groups = (H + 63) / 64;
+    w.heads = (H + w.groups - 1) / w.groups;
+    w.tokens = 64 / w.heads < max_new ? 64 / w.heads : max_new;
+    const int rows = w.heads * w.tokens;
+    w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    w.ml = up(static_cast<size_t>(w.ctas) * 2 * sizeof(int4));
+    // (of any max_new: 64 rows)
+    w.acc = w.ml + up(static_cast<size_t>(w.ctas) * 2 * 64 * sizeof(float2));
+    w.total = w.acc + up(static_cast<size_t>(w.ctas) * 2 * w.nr * rank * sizeof(float));
+    return w;
+}
+
+template <bool BF16, int NR>
+cudaError_t launch_rows(const PagedAttnArgs &p, int rank, const Plan &w, void *ws, cudaStream_t st) {
+    using Sh = LatentShape<NR>;
+    const kvd_paged_cache &c = p.c;
+    LatentDev a = {};
+    a.c = c;
+    a.out = static_cast<uint16_t *>(p.out);
+    a.out_stride = p.out_stride;
+    a.G = p.G;
+    a.n_tokens = p.n_tokens;
+    a.max_new = p.max_new;
+    a.window = p.window;
+    a.starts = p.starts;
+    a.scale_log2 = p.scale_log2;
+    a.lse = p.lse;
+    a.box = 16;
+    while (a.box < kKeys && c.page_size % (2 * a.box) == 0) a.box *= 2;
+    const int64_t pool = static_cast<int64_t>(c.n_pages) * c.page_size;
+    a.dead_row = static_cast<int>(pool);
+    a.min_tiles = kItemCost + 2;  // an item's first CTA takes a tile
+    a.tops = rank / 128;
+    a.rope_steps = (c.head_dim - rank) / 16;
+    a.heads = w.heads;
+    a.groups = w.groups;
+    a.tokens = w.tokens;
+    const int fixed = (2 * a.tops + 1) * NR * 128 + Sh::kP * kHalf + static_cast<int>(sizeof(Small));
+    const int tile = a.tops * kPair + kHalf;
+    a.ring = (kSmemTop - fixed) / tile;
+    if (a.ring > kMaxRing) a.ring = kMaxRing;
+    const size_t smem = static_cast<size_t>(fixed) + static_cast<size_t>(a.ring) * tile;
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    a.join = reinterpret_cast<int4 *>(base);
+    a.ml = reinterpret_cast<float2 *>(base + w.ml);
+    a.acc = reinterpret_cast<float *>(base + w.acc);
+
+    CUtensorMap q_map, k_map;
+    const cuuint64_t W = static_cast<cuuint64_t>(c.head_dim);
+    const cuuint64_t qd[4] = {W, static_cast<cuuint64_t>(p.G), 1, static_cast<cuuint64_t>(p.n_tokens)};
+    const cuuint64_t qs[3] = {W * 2, W * 2 * p.G, static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(a.heads), 1, static_cast<cuuint32_t>(a.tokens)};
+    const cuuint64_t kd[2] = {W, static_cast<cuuint64_t>(pool)};
+    const cuuint64_t ks[1] = {W * 2};
+    const cuuint32_t kb[2] = {64, static_cast<cuuint32_t>(a.box)};
+    if (!make_map(&q_map, c.dtype, p.q, 4, qd, qs, qb) || !make_map(&k_map, c.dtype, c.k, 2, kd, ks, kb))
+        return cudaErrorInvalidValue;
+    auto *kernel = latent_kernel<BF16, NR>;
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), kThreads, smem);
+    if (e != cudaSuccess) return e;
+    e = launch_ex(kernel, dim3(w.ctas), dim3(kThreads), smem, st, true, a, q_map, k_map);
+    if (e != cudaSuccess) return e;
+    return launch_ex(join_kernel<BF16, NR>, dim3(w.ctas, NR / 2), dim3(128), 0, st, true, a);
+}
+
+template <bool BF16>
+cudaError_t launch_type(const PagedAttnArgs &p, int rank, void *ws, cudaStream_t st) {
+    const Plan w = plan_of(p.G, rank, p.max_new);
+    if (w.nr == 16) return launch_rows<BF16, 16>(p, rank, w, ws, st);
+    if (w.nr == 32) return launch_rows<BF16, 32>(p, rank, w, ws, st);
+    return launch_rows<BF16, 64>(p, rank, w, ws, st);
+}
+
+}  // namespace
+
+cudaError_t launch_latent_attn(const PagedAttnArgs &a, int rank, void *ws, cudaStream_t st) {
+    return a.bf16 ? launch_type<true>(a, rank, ws, st) : launch_type<false>(a, rank, ws, st);
+}
+
+size_t latent_attn_ws(int H, int rank, int max_new) { return plan_of(H, rank, max_new).total; }
+
+}  // namespace kvd

@@ -1,5 +1,7 @@
-// paged.h -- launchers of the norm/rotation, paged append and paged attention
-// kernels (rope.cu, paged_attn.cu, paged_decode.cu) for their C-ABI front end (paged_api.cu).
+// paged.h -- launchers of the kernels around a cache in pages for their C-ABI front ends:
+// norm/rotation, append and attention (rope.cu, paged_attn.cu, paged_decode.cu, for
+// paged_api.cu), latent rows (latent.cu, latent_attn.cu, for latent_api.cu), accumulated
+// weights and eviction (mass.cu, evict.cu, for evict_api.cu).
 // Arguments are already validated by the caller.
 #pragma once
 
@@ -47,6 +49,7 @@ struct PagedAttnArgs {
     int G, n_tokens, max_new, window;
     const int32_t *starts;
     float scale_log2;  // softmax_scale * log2(e)
+    float *lse;        // [n_tokens][heads] or NULL
 };
 
 // The workspace begins with paged_counter_bytes() of counters, zero between calls,
@@ -62,5 +65,58 @@ size_t paged_attn_ws(const kvd_paged_cache &c, int H, int max_new);
 constexpr int kDecodeRows = 32;
 cudaError_t launch_paged_decode(const PagedAttnArgs &a, void *ws, cudaStream_t st);
 size_t paged_decode_ws(int rows, int D);
+
+// Latent rows.  The cache is a kvd_paged_cache with one KV head of rank + rope_dim
+// channels, its rows in k, and no v.
+struct LatentAppendArgs {
+    RowsIn c, k_pe, q;  // q: zero heads where there are none
+    int64_t q_head;     // elements from one head of q to the next
+    RowsOut q_out;
+    int64_t q_out_head;
+    const float *c_weight;
+    float eps, inv_rank;
+    int rank, rope_dim, n_tokens;
+    kvd_rope rope;  // rot_dim 0: no rotation
+    const int32_t *starts;
+    kvd_paged_cache cache;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs &a, int x_dtype, cudaStream_t st);
+
+// Attention over them: G is the number of query heads, c.head_dim the row's channels.
+cudaError_t launch_latent_attn(const PagedAttnArgs &a, int rank, void *ws, cudaStream_t st);
+size_t latent_attn_ws(int H, int rank, int max_new);
+
+// Each cached token's weight, added up over the rows of its KV head.
+struct MassArgs {
+    PagedAttnArgs attn;  // out: unused; lse: read
+    const float *mass;
+    float *out;
+    int64_t mass_stride, out_stride;  // from one (sequence, head) to the next
+    float decay;
+};
+cudaError_t launch_mass(const MassArgs &a, cudaStream_t st);
+
+struct EvictArgs {
+    kvd_paged_cache c;  // v NULL: rows in k alone; k_scale and v_scale NULL: none
+    int row_bytes;      // of k, and of v
+    const float *mass;
+    int64_t mass_stride;
+    int keep, sink, recent;
+    const int32_t *to;  // page table of the rows that stay
+    int to_cols;
+    int32_t *kept, *lens_out;
+    float *mass_out;  // may be NULL
+    int64_t mass_out_stride;
+};
+cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st);
+
+// Argument checks that the front ends share (paged_api.cu).
+bool aligned(const void *p, size_t a);
+kvd_status check_rows(const kvd_heads *h, int head_dim);
+kvd_status check_rope(const kvd_rope *r, int head_dim, const float *qw, const float *kw, float eps);
+kvd_status check_paged(const kvd_paged_cache *c);
+kvd_status check_latent(const kvd_latent_cache *c);
+// The latent cache as the kernels take it.
+kvd_paged_cache latent_as_paged(const kvd_latent_cache &c);
 
 }  // namespace kvd

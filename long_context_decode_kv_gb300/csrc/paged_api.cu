@@ -7,12 +7,35 @@
 #include "paged.h"
 
 namespace kvd {
-namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-kvd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVD_OK : KVD_ERR_CUDA; }
+
+namespace {
 
 size_t x_size(int dtype) { return dtype == KVD_X_F32 ? 4 : 2; }
+
+// What every cache in pages has: the page table and the counts.
+kvd_status check_pages(const kvd_paged_cache *c) {
+    if (c->batch < 1 || c->n_kv_heads < 1 || c->n_pages < 1 || c->max_pages < 1)
+        return KVD_ERR_INVALID;
+    if (c->page_size < 1) return KVD_ERR_INVALID;
+    if (c->page_size % 16 != 0) return KVD_ERR_UNSUPPORTED;
+    if (c->len < 0 || c->len > static_cast<int64_t>(c->max_pages) * c->page_size)
+        return KVD_ERR_INVALID;
+    // tokens, key tiles and rows of the pool are counted in 31 bits
+    if (c->len > (1 << 30) ||
+        static_cast<__int128>(c->batch) * c->n_kv_heads * (c->len / 128 + 1) > 0x7fffffff)
+        return KVD_ERR_UNSUPPORTED;
+    if (static_cast<__int128>(c->n_pages) * c->n_kv_heads * c->page_size > 0x7fffffff)
+        return KVD_ERR_UNSUPPORTED;
+    if (!c->k || !aligned(c->k, 16)) return KVD_ERR_INVALID;
+    if (!c->page_table || !aligned(c->page_table, 4) || !c->seq_lens || !aligned(c->seq_lens, 4))
+        return KVD_ERR_INVALID;
+    if (c->dev_status && !aligned(c->dev_status, 4)) return KVD_ERR_INVALID;
+    return KVD_OK;
+}
+
+}  // namespace
 
 kvd_status check_rows(const kvd_heads *h, int head_dim) {
     if (!h || !h->x || !aligned(h->x, 16)) return KVD_ERR_INVALID;
@@ -39,6 +62,56 @@ kvd_status check_rope(const kvd_rope *r, int head_dim, const float *qw, const fl
     return KVD_OK;
 }
 
+kvd_status check_paged(const kvd_paged_cache *c) {
+    if (!c) return KVD_ERR_INVALID;
+    if (c->dtype == KVD_Q8_0 || c->dtype == KVD_Q4_0) return KVD_ERR_UNSUPPORTED;
+    if (c->dtype != KVD_F16 && c->dtype != KVD_BF16 && c->dtype != KVD_INT8)
+        return KVD_ERR_INVALID;
+    if (c->batch < 1 || c->n_kv_heads < 1 || c->n_pages < 1 || c->max_pages < 1)
+        return KVD_ERR_INVALID;
+    if (c->head_dim != 64 && c->head_dim != 128) return KVD_ERR_UNSUPPORTED;
+    const kvd_status s = check_pages(c);
+    if (s != KVD_OK) return s;
+    if (!c->v || !aligned(c->v, 16)) return KVD_ERR_INVALID;
+    if (c->dtype == KVD_INT8 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) ||
+                                 !aligned(c->v_scale, 16)))
+        return KVD_ERR_INVALID;
+    return KVD_OK;
+}
+
+kvd_paged_cache latent_as_paged(const kvd_latent_cache &c) {
+    kvd_paged_cache p = {};
+    p.dtype = c.dtype;
+    p.batch = c.batch;
+    p.n_kv_heads = 1;
+    p.head_dim = c.rank + c.rope_dim;
+    p.n_pages = c.n_pages;
+    p.page_size = c.page_size;
+    p.max_pages = c.max_pages;
+    p.len = c.len;
+    p.k = c.rows;
+    p.page_table = c.page_table;
+    p.seq_lens = c.seq_lens;
+    p.dev_status = c.dev_status;
+    return p;
+}
+
+kvd_status check_latent(const kvd_latent_cache *c) {
+    if (!c) return KVD_ERR_INVALID;
+    if (c->dtype == KVD_INT8 || c->dtype == KVD_Q8_0 || c->dtype == KVD_Q4_0)
+        return KVD_ERR_UNSUPPORTED;
+    if (c->dtype != KVD_F16 && c->dtype != KVD_BF16) return KVD_ERR_INVALID;
+    if (c->rank < 1 || c->rope_dim < 1) return KVD_ERR_INVALID;
+    if (c->rank % 128 != 0 || c->rank > 512 || c->rope_dim % 16 != 0 || c->rope_dim > 64)
+        return KVD_ERR_UNSUPPORTED;
+    const kvd_paged_cache p = latent_as_paged(*c);
+    return check_pages(&p);
+}
+
+namespace {
+
+kvd_status cuda_status(cudaError_t e) { return e == cudaSuccess ? KVD_OK : KVD_ERR_CUDA; }
+
 // Whether two row arrays are the same array, which may be worked on in place.
 bool same_rows(const kvd_heads *a, const kvd_heads *b) {
     return a->x == b->x && a->stride == b->stride && a->dtype == b->dtype;
@@ -53,34 +126,6 @@ kvd_status check_pair(const kvd_heads *in, const kvd_heads *out, int head_dim) {
     return KVD_OK;
 }
 
-kvd_status check_paged(const kvd_paged_cache *c) {
-    if (!c) return KVD_ERR_INVALID;
-    if (c->dtype == KVD_Q8_0 || c->dtype == KVD_Q4_0) return KVD_ERR_UNSUPPORTED;
-    if (c->dtype != KVD_F16 && c->dtype != KVD_BF16 && c->dtype != KVD_INT8)
-        return KVD_ERR_INVALID;
-    if (c->batch < 1 || c->n_kv_heads < 1 || c->n_pages < 1 || c->max_pages < 1)
-        return KVD_ERR_INVALID;
-    if (c->head_dim != 64 && c->head_dim != 128) return KVD_ERR_UNSUPPORTED;
-    if (c->page_size < 1) return KVD_ERR_INVALID;
-    if (c->page_size % 16 != 0) return KVD_ERR_UNSUPPORTED;
-    if (c->len < 0 || c->len > static_cast<int64_t>(c->max_pages) * c->page_size)
-        return KVD_ERR_INVALID;
-    // tokens, key tiles and rows of the pool are counted in 31 bits
-    if (c->len > (1 << 30) ||
-        static_cast<__int128>(c->batch) * c->n_kv_heads * (c->len / 128 + 1) > 0x7fffffff)
-        return KVD_ERR_UNSUPPORTED;
-    if (static_cast<__int128>(c->n_pages) * c->n_kv_heads * c->page_size > 0x7fffffff)
-        return KVD_ERR_UNSUPPORTED;
-    if (!c->k || !aligned(c->k, 16) || !c->v || !aligned(c->v, 16)) return KVD_ERR_INVALID;
-    if (c->dtype == KVD_INT8 && (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) ||
-                                 !aligned(c->v_scale, 16)))
-        return KVD_ERR_INVALID;
-    if (!c->page_table || !aligned(c->page_table, 4) || !c->seq_lens || !aligned(c->seq_lens, 4))
-        return KVD_ERR_INVALID;
-    if (c->dev_status && !aligned(c->dev_status, 4)) return KVD_ERR_INVALID;
-    return KVD_OK;
-}
-
 bool few_rows(int G, int max_new) { return static_cast<int64_t>(G) * max_new <= kDecodeRows; }
 
 size_t attn_ws(const kvd_paged_cache &c, int H, int max_new) {
@@ -91,6 +136,47 @@ size_t attn_ws(const kvd_paged_cache &c, int H, int max_new) {
 
 RowsIn rows_in(const kvd_heads *h) { return RowsIn{h->x, h->stride, h->n_heads}; }
 RowsOut rows_out(const kvd_heads *h) { return RowsOut{h->x, h->stride, h->dtype}; }
+
+kvd_status attn_call(const kvd_paged_cache *cache, const kvd_heads *q, int32_t n_tokens,
+                     const int32_t *starts, int32_t max_new, float softmax_scale, int32_t window,
+                     const kvd_heads *out, float *lse, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    kvd_status s = check_paged(cache);
+    if (s != KVD_OK) return s;
+    if (n_tokens < 0 || max_new < 0 || window < 0) return KVD_ERR_INVALID;
+    if (n_tokens == 0 || max_new == 0) return KVD_OK;
+    const int D = cache->head_dim;
+    if ((s = check_pair(q, out, D)) != KVD_OK) return s;
+    if (q->n_heads % cache->n_kv_heads != 0 || q->dtype != out->dtype || q->x == out->x)
+        return KVD_ERR_INVALID;
+    if (q->dtype != KVD_X_F16 && q->dtype != KVD_X_BF16) return KVD_ERR_INVALID;
+    if (cache->dtype != KVD_INT8 && (cache->dtype == KVD_BF16) != (q->dtype == KVD_X_BF16))
+        return KVD_ERR_INVALID;
+    if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return KVD_ERR_INVALID;
+    const int G = q->n_heads / cache->n_kv_heads;
+    if (G > 16) return KVD_ERR_UNSUPPORTED;
+    if (!starts || !aligned(starts, 4)) return KVD_ERR_INVALID;
+    if (!workspace || !aligned(workspace, 256) ||
+        workspace_bytes < attn_ws(*cache, q->n_heads, max_new))
+        return KVD_ERR_WORKSPACE;
+    PagedAttnArgs a = {};
+    a.c = *cache;
+    a.q = q->x;
+    a.out = out->x;
+    a.q_stride = q->stride;
+    a.out_stride = out->stride;
+    a.bf16 = q->dtype == KVD_X_BF16;
+    a.G = G;
+    a.n_tokens = n_tokens;
+    a.max_new = max_new;
+    a.window = window < cache->len ? window : 0;  // positions plus it stay in 31 bits
+    a.starts = starts;
+    a.scale_log2 = softmax_scale * kLog2e;
+    a.lse = lse;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(few_rows(G, max_new) ? launch_paged_decode(a, workspace, st)
+                                            : launch_paged_attn(a, workspace, st));
+}
 
 }  // namespace
 }  // namespace kvd
@@ -232,40 +318,17 @@ kvd_status kvd_paged_attn(const kvd_paged_cache *cache, const kvd_heads *q, int3
                           const int32_t *starts, int32_t max_new, float softmax_scale,
                           int32_t window, const kvd_heads *out, void *workspace,
                           size_t workspace_bytes, void *stream) {
-    kvd_status s = check_paged(cache);
-    if (s != KVD_OK) return s;
-    if (n_tokens < 0 || max_new < 0 || window < 0) return KVD_ERR_INVALID;
-    if (n_tokens == 0 || max_new == 0) return KVD_OK;
-    const int D = cache->head_dim;
-    if ((s = check_pair(q, out, D)) != KVD_OK) return s;
-    if (q->n_heads % cache->n_kv_heads != 0 || q->dtype != out->dtype || q->x == out->x)
-        return KVD_ERR_INVALID;
-    if (q->dtype != KVD_X_F16 && q->dtype != KVD_X_BF16) return KVD_ERR_INVALID;
-    if (cache->dtype != KVD_INT8 && (cache->dtype == KVD_BF16) != (q->dtype == KVD_X_BF16))
-        return KVD_ERR_INVALID;
-    if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return KVD_ERR_INVALID;
-    const int G = q->n_heads / cache->n_kv_heads;
-    if (G > 16) return KVD_ERR_UNSUPPORTED;
-    if (!starts || !aligned(starts, 4)) return KVD_ERR_INVALID;
-    if (!workspace || !aligned(workspace, 256) ||
-        workspace_bytes < attn_ws(*cache, q->n_heads, max_new))
-        return KVD_ERR_WORKSPACE;
-    PagedAttnArgs a = {};
-    a.c = *cache;
-    a.q = q->x;
-    a.out = out->x;
-    a.q_stride = q->stride;
-    a.out_stride = out->stride;
-    a.bf16 = q->dtype == KVD_X_BF16;
-    a.G = G;
-    a.n_tokens = n_tokens;
-    a.max_new = max_new;
-    a.window = window < cache->len ? window : 0;  // positions plus it stay in 31 bits
-    a.starts = starts;
-    a.scale_log2 = softmax_scale * kLog2e;
-    const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(few_rows(G, max_new) ? launch_paged_decode(a, workspace, st)
-                                            : launch_paged_attn(a, workspace, st));
+    return attn_call(cache, q, n_tokens, starts, max_new, softmax_scale, window, out, nullptr,
+                     workspace, workspace_bytes, stream);
+}
+
+kvd_status kvd_paged_attn_lse(const kvd_paged_cache *cache, const kvd_heads *q, int32_t n_tokens,
+                              const int32_t *starts, int32_t max_new, float softmax_scale,
+                              int32_t window, const kvd_heads *out, float *lse, void *workspace,
+                              size_t workspace_bytes, void *stream) {
+    if (!lse || !aligned(lse, 16)) return KVD_ERR_INVALID;
+    return attn_call(cache, q, n_tokens, starts, max_new, softmax_scale, window, out, lse,
+                     workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

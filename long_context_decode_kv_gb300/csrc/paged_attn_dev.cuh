@@ -27,7 +27,18 @@ struct AttnArgs {  // of a launch
     int box;            // cache rows a TMA box: the largest of 16..128 that divides a page
     int dead_row;       // a cache row outside the pool
     int min_tiles;      // least key tiles a CTA takes (row tiles: with what an item costs)
+    float *lse;         // [n_tokens][n_kv_heads * G] or NULL
 };
+
+// A row's statistic from the reference m (base 2) and the sum l of its weights 2^(logit - m).
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return l > 0.0f || l != l ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+}
+// Where it stands: row r (tokens' heads of one KV head) from token t0 on.
+__device__ __forceinline__ float *lse_at(const AttnArgs &a, int t0, int head, int r) {
+    const int tok = r / a.G;
+    return a.lse + static_cast<int64_t>(t0 + tok) * a.c.n_kv_heads * a.G + head * a.G + (r - tok * a.G);
+}
 
 // mbar_wait for the waits between the roles, in few instructions: the roles' hot
 // lines have to fit the instruction cache together, and a wait mostly ends in its
@@ -162,6 +173,7 @@ inline bool fill_launch(const PagedAttnArgs &p, int q_tokens, CUtensorMapSwizzle
     a.window = p.window;
     a.starts = p.starts;
     a.scale_log2 = p.scale_log2;
+    a.lse = p.lse;
     a.box = 16;
     while (a.box < kTile && c.page_size % (2 * a.box) == 0) a.box *= 2;
     const int64_t rows = static_cast<int64_t>(c.n_pages) * c.n_kv_heads * c.page_size;

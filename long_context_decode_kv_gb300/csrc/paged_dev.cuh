@@ -44,6 +44,37 @@ __device__ __forceinline__ int checked_page(const kvd_paged_cache &c, int b, int
     return -1;
 }
 
+// Where new token t goes: its position, and the page and the place in it.
+struct TokenPlace {
+    bool some;  // a sequence has it
+    long pos;
+    int page, in_page;  // page -1: nowhere (a bad page, or before position 0)
+};
+__device__ __forceinline__ TokenPlace place_of(const kvd_paged_cache &c, const int32_t *starts,
+                                               int n_tokens, int t, int lane) {
+    TokenPlace at = {false, 0, -1, 0};
+    const int b = sequence_of(starts, c.batch, t, lane);
+    // starts in their range, as the attention takes them
+    const int r0 = starts[b], r1 = starts[b + 1], end = starts[c.batch];
+    const int s0 = max(r0, 0), s1 = min(r1, n_tokens);
+    if ((s0 != r0 || s1 != r1) && lane == 0) report_status(c.dev_status, KVD_ERR_INVALID);
+    if (t < s0 || t >= s1) {
+        // before the first sequence, behind the last, or starts that are not in order
+        if (t >= starts[0] && t < end && lane == 0) report_status(c.dev_status, KVD_ERR_INVALID);
+        return at;
+    }
+    at.some = true;
+    at.pos = static_cast<long>(checked_len(c, b)) - (s1 - t);
+    if (at.pos >= 0) {
+        const int j = static_cast<int>(at.pos) / c.page_size;
+        at.page = checked_page(c, b, j);
+        at.in_page = static_cast<int>(at.pos) - j * c.page_size;
+    } else if (lane == 0) {
+        report_status(c.dev_status, KVD_ERR_INVALID);
+    }
+    return at;
+}
+
 // Two f32 as one word of f16 or bf16, each rounded to nearest even.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {

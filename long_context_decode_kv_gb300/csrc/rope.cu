@@ -31,52 +31,12 @@
 #include "internal.h"
 #include "paged.h"
 #include "paged_dev.cuh"
+#include "rope_dev.cuh"
 
 namespace kvd {
 namespace {
 
 constexpr int kThreads = 128;
-
-// 4 channels as loaded.
-template <typename T>
-struct Raw {
-    uint2 w;
-    __device__ __forceinline__ void load(const void *p) { w = *static_cast<const uint2 *>(p); }
-    __device__ __forceinline__ void get(float2 (&x)[2]) const {
-        constexpr bool kBf16 = !std::is_same<T, __half>::value;
-        x[0] = unpack2<kBf16>(w.x);
-        x[1] = unpack2<kBf16>(w.y);
-    }
-};
-template <>
-struct Raw<float> {
-    float4 w;
-    __device__ __forceinline__ void load(const void *p) { w = *static_cast<const float4 *>(p); }
-    __device__ __forceinline__ void get(float2 (&x)[2]) const {
-        x[0] = make_float2(w.x, w.y);
-        x[1] = make_float2(w.z, w.w);
-    }
-};
-
-// 4 channels to element `at` of an array of the given type.
-__device__ __forceinline__ void store4(void *p, int dtype, size_t at, const float2 (&x)[2]) {
-    if (dtype == KVD_X_F32)
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) =
-            make_float4(x[0].x, x[0].y, x[1].x, x[1].y);
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + at) =
-            dtype == KVD_X_BF16
-                ? make_uint2(pack2<true>(x[0].x, x[0].y), pack2<true>(x[1].x, x[1].y))
-                : make_uint2(pack2<false>(x[0].x, x[0].y), pack2<false>(x[1].x, x[1].y));
-}
-
-__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
-
-// The first channels of the two groups of 4 that chunk c of a row holds.
-__device__ __forceinline__ int2 groups_of(const kvd_rope &r, int c) {
-    if (!r.interleaved && c < r.rot_dim / 8) return make_int2(4 * c, r.rot_dim / 2 + 4 * c);
-    return make_int2(8 * c, 8 * c + 4);  // no pair apart: neighbours
-}
 
 // LPR lanes hold one row, lane l chunks l, l + LPR, .. (VPL of them).
 template <typename IN, int LPR, int VPL, int U, bool PAGED>
@@ -105,28 +65,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     size_t row0 = 0;  // cache row of KV head 0
     bool store_kv = false;
     if constexpr (PAGED) {
-        const int b = sequence_of(a.starts, a.cache.batch, t, lane);
-        // starts in their range, as the attention takes them
-        const int r0 = a.starts[b], r1 = a.starts[b + 1], end = a.starts[a.cache.batch];
-        const int s0 = max(r0, 0), s1 = min(r1, a.n_tokens);
-        if ((s0 != r0 || s1 != r1) && lane == 0)
-            report_status(a.cache.dev_status, KVD_ERR_INVALID);
-        if (t < s0 || t >= s1) {
-            // before the first sequence, behind the last, or starts that are not in order
-            if (t >= a.starts[0] && t < end && lane == 0)
-                report_status(a.cache.dev_status, KVD_ERR_INVALID);
-            return;
-        }
-        pos = static_cast<long>(checked_len(a.cache, b)) - (s1 - t);
-        if (pos >= 0) {
-            const int ps = a.cache.page_size;
-            const int j = static_cast<int>(pos) / ps;
-            const int page = checked_page(a.cache, b, j);
-            store_kv = page >= 0;
-            row0 = static_cast<size_t>(page) * a.cache.n_kv_heads * ps + (pos - j * ps);
-        } else if (lane == 0) {
-            report_status(a.cache.dev_status, KVD_ERR_INVALID);
-        }
+        const TokenPlace at = place_of(a.cache, a.starts, a.n_tokens, t, lane);
+        if (!at.some) return;
+        pos = at.pos;
+        store_kv = at.page >= 0;
+        if (store_kv)
+            row0 = static_cast<size_t>(at.page) * a.cache.n_kv_heads * a.cache.page_size + at.in_page;
     } else if (a.rope.rot_dim) {
         pos = a.positions[t];
     }
@@ -139,15 +83,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
         float c[4] = {1.0f, 1.0f, 1.0f, 1.0f}, s[4] = {};
         if (8 * (col + i * LPR) < a.rope.rot_dim) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint64_t frac =
-                    static_cast<uint64_t>(pos) * a.rope.freqs[4 * (col + i * LPR) + j];
-                // signed upper half: half turns in [-1, 1)
-                const float x = static_cast<float>(static_cast<int32_t>(frac >> 32)) * 0x1p-31f;
-                sincospif(x, &s[j], &c[j]);
-                c[j] *= a.rope.mscale;
-                s[j] *= a.rope.mscale;
-            }
+            for (int j = 0; j < 4; ++j)
+                angle_of(a.rope, pos, 4 * (col + i * LPR) + j, c[j], s[j]);
         }
         cs[i][0] = make_float2(c[0], c[1]);
         cs[i][1] = make_float2(c[2], c[3]);
