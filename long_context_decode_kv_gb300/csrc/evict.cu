@@ -7,8 +7,8 @@
 // tokens before it writes them.  The weights are read once, into shared memory, where a
 // slice fits it.
 //
-// move_kernel: a warp looks up 16 rows' places, a lane a row, and copies them 16 bytes a
-// lane with all its loads in flight.  The rows go to other pages than they come from
+// move_kernel: a warp looks up 32 rows' places, a lane a row, and copies them 16 bytes a
+// lane, 8 loads in flight.  The rows go to other pages than they come from
 // (which other sequences may share), so no order between the copies matters.
 #include <cooperative_groups.h>
 
@@ -33,17 +33,19 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kThreads)
-choose_kernel(const __grid_constant__ EvictArgs a, int blocks) {
-    extern __shared__ uint32_t cached[];
-    __shared__ uint32_t hist[2][kBins];
+choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
+    extern __shared__ uint32_t cached[];  // `room` keys
+    __shared__ uint32_t hist[kBins];
+    __shared__ __align__(16) uint32_t total[3][kBins];  // of the cluster, in its first block
     __shared__ int warp_sum[kWarps], warp_gt[kWarps], warp_eq[kWarps];
     __shared__ int found_bin, found_above;
-    __shared__ int total_gt, total_eq;
+    __shared__ int block_gt[kMaxCluster], block_eq[kMaxCluster];  // in each block
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(blockIdx.x) % blocks;
     const int row = static_cast<int>(blockIdx.x) / blocks;  // of a sequence and a head
     const int b = row / a.c.n_kv_heads;
+    for (int i = tid; i < kBins; i += kThreads) hist[i] = total[0][i] = total[1][i] = total[2][i] = 0;
     pdl_wait();
     pdl_launch_dependents();
     const int L = checked_len(a.c, b);
@@ -57,48 +59,54 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks) {
         if (mass_out) mass_out[at] = w;
     };
     const int lo = L <= a.keep ? L : a.sink, hi = L <= a.keep ? L : L - a.recent;
+    // this block's slice of those between, on its way
+    int need = n - lo - (L - hi);
+    const int slice = ((hi - lo + blocks - 1) / blocks + kThreads - 1) / kThreads * kThreads;
+    const int t0 = min(lo + rank * slice, hi), count = min(slice, hi - t0);
+    const bool fits = slice <= room;
+    if (need > 0 && fits)
+#pragma unroll 4
+        for (int i = tid; i < count; i += kThreads) cached[i] = weight_key(mass[t0 + i]);
     // those that stay whatever they weigh
     for (int t = rank * kThreads + tid; t < lo; t += blocks * kThreads) put(t, t, mass[t]);
     for (int t = hi + rank * kThreads + tid; t < L; t += blocks * kThreads)
         put(n - (L - t), t, mass[t]);
-    int need = n - lo - (L - hi);
     if (need <= 0) return;  // the same for the whole cluster
-
-    // this block's slice of the others
-    const int slice = ((hi - lo + blocks - 1) / blocks + kThreads - 1) / kThreads * kThreads;
-    const int t0 = min(lo + rank * slice, hi), count = min(slice, hi - t0);
-    const bool fits = slice <= kCached;
-    for (int i = tid; i < 2 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
-    if (fits)
-        for (int i = tid; i < count; i += kThreads) cached[i] = weight_key(mass[t0 + i]);
-    __syncthreads();
     auto key_of = [&](int i) { return fits ? cached[i] : weight_key(mass[t0 + i]); };
+    cluster.sync();  // the sums are clear, in the first block too
 
     uint32_t prefix = 0, mask = 0;  // the bits of the n-th largest found so far
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-        uint32_t *h = hist[pass & 1];
 #pragma unroll 4
         for (int i = tid; i < count; i += kThreads) {
             const uint32_t k = key_of(i);
-            if ((k & mask) == prefix) atomicAdd(&h[(k >> shift) & (bins - 1)], 1u);
+            if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+        }
+        __syncthreads();
+        uint32_t *sums = cluster.map_shared_rank(&total[pass][0], 0);
+#pragma unroll
+        for (int i = tid; i < kBins; i += kThreads) {
+            const uint32_t v = hist[i];
+            if (v) {
+                atomicAdd(&sums[i], v);
+                hist[i] = 0;
+            }
         }
         cluster.sync();
-        // the buffer of the pass before is free: its readers have come to this barrier
-        if (pass == 1)
-            for (int i = tid; i < kBins; i += kThreads) hist[0][i] = 0;
         // bins from the top, 4 a thread: where the sum passes `need`
         constexpr int kEach = kBins / kThreads;
-        int at[kEach], sum = 0;
-#pragma unroll
-        for (int j = 0; j < kEach; ++j) {
-            const int bin = bins - 1 - (tid * kEach + j);
-            at[j] = 0;
-            if (bin >= 0)
-                for (int r = 0; r < blocks; ++r)
-                    at[j] += static_cast<int>(*cluster.map_shared_rank(&h[bin], r));
-            sum += at[j];
+        static_assert(kEach == 4, "read as one vector");
+        const int bottom = bins - kEach * (tid + 1);
+        int at[kEach] = {}, sum = 0;
+        if (bottom >= 0) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(&sums[bottom]);
+            at[0] = v.w;
+            at[1] = v.z;
+            at[2] = v.y;
+            at[3] = v.x;
+            sum = at[0] + at[1] + at[2] + at[3];
         }
         int upto = sum;
 #pragma unroll
@@ -109,7 +117,9 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks) {
         if (lane == 31) warp_sum[warp] = upto;
         __syncthreads();
         int above = upto - sum;
-        for (int w = 0; w < warp; ++w) above += warp_sum[w];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            if (w < warp) above += warp_sum[w];
 #pragma unroll
         for (int j = 0; j < kEach; ++j) {
             if (above < need && above + at[j] >= need) {
@@ -139,28 +149,27 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks) {
         warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
+    if (tid < blocks) {  // the block's counts to every block
         int g = 0, e = 0;
         for (int w = 0; w < kWarps; ++w) {
             g += warp_gt[w];
             e += warp_eq[w];
         }
-        total_gt = g;
-        total_eq = e;
+        *cluster.map_shared_rank(&block_gt[rank], tid) = g;
+        *cluster.map_shared_rank(&block_eq[rank], tid) = e;
     }
-    cluster.sync();
+    cluster.sync();  // (after it no block's memory is another's business)
     gt = eq = 0;
     for (int r = 0; r < rank; ++r) {
-        gt += *cluster.map_shared_rank(&total_gt, r);
-        eq += *cluster.map_shared_rank(&total_eq, r);
+        gt += block_gt[r];
+        eq += block_eq[r];
     }
-    cluster.sync();  // no block goes while others read from it
     for (int w = 0; w < warp; ++w) {
         gt += warp_gt[w];
         eq += warp_eq[w];
     }
     const uint32_t below = (1u << lane) - 1;
-#pragma unroll 1
+#pragma unroll 2
     for (int i = i0; i < i1; i += 32) {
         const bool in = i + lane < i1;
         const uint32_t k = in ? key_of(i + lane) : 0u;
@@ -177,15 +186,16 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks) {
     }
 }
 
-constexpr int kMoveRows = 16;  // a warp's
+constexpr int kMoveRows = 32;  // a warp's
 constexpr int kMoveThreads = 128;
 
+// VECS: 16-byte parts of a row of k, and of v (0: any number, of k alone)
+template <int VECS>
 __global__ void __launch_bounds__(kMoveThreads)
 move_kernel(const __grid_constant__ EvictArgs a, int64_t units, int per_row) {
     const int lane = threadIdx.x & 31;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32);
-    const int vecs = a.row_bytes / 16;
     const int ps = a.c.page_size, Hkv = a.c.n_kv_heads;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * (kMoveThreads / 32);
     pdl_wait();
     pdl_launch_dependents();
     for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
@@ -195,54 +205,99 @@ move_kernel(const __grid_constant__ EvictArgs a, int64_t units, int per_row) {
         const int b = row / Hkv, g = row - b * Hkv;
         const int n = min(a.keep, min(max(a.c.seq_lens[b], 0), a.c.len));
         if (r0 >= n) continue;
-        const int rows = min(kMoveRows, n - r0);
-        int64_t src = -1, dst = -1;  // cache rows
-        if (lane < rows) {
-            const int t = a.kept[static_cast<size_t>(row) * a.keep + r0 + lane], r = r0 + lane;
-            const int from = checked_page(a.c, b, t / ps);
+        int src = -1, dst = -1;  // cache rows (the pool has fewer than 2^31)
+        if (r0 + lane < n) {
+            const int r = r0 + lane;
+            const int t = __ldcs(a.kept + static_cast<size_t>(row) * a.keep + r);
             const int to = a.to[static_cast<size_t>(b) * a.to_cols + r / ps];
+            const int from = checked_page(a.c, b, t / ps);
             if (to < 0 || to >= a.c.n_pages) {
                 report_status(a.c.dev_status, KVD_ERR_INVALID);
             } else if (from >= 0) {
-                src = (static_cast<int64_t>(from) * Hkv + g) * ps + t % ps;
-                dst = (static_cast<int64_t>(to) * Hkv + g) * ps + r % ps;
-                if (a.c.k_scale) {
-                    float *ks = static_cast<float *>(a.c.k_scale);
-                    float *vs = static_cast<float *>(a.c.v_scale);
-                    ks[dst] = ks[src];
-                    vs[dst] = vs[src];
-                }
+                src = (from * Hkv + g) * ps + t % ps;
+                dst = (to * Hkv + g) * ps + r % ps;
             }
         }
-        const int total = rows * vecs, step_r = 32 / vecs, step_v = 32 % vecs;
-        auto copy = [&](uint8_t *base) {
-            int r = lane / vecs, v = lane % vecs;
-            constexpr int U = 8;
-            for (int i0 = 0; i0 < total; i0 += 32 * U) {
-                uint4 x[U];
-                int64_t to[U];
+        float k_scale = 0.0f, v_scale = 0.0f;
+        if (a.c.k_scale && dst >= 0) {
+            k_scale = static_cast<float *>(a.c.k_scale)[src];
+            v_scale = static_cast<float *>(a.c.v_scale)[src];
+        }
+        uint4 *k = static_cast<uint4 *>(a.c.k), *v = static_cast<uint4 *>(a.c.v);
+        if constexpr (VECS > 0) {
+            // a step: 32 / VECS rows of k and v; U steps' reads are under way together
+            constexpr int kAt = 32 / VECS, U = VECS < 4 ? VECS : 4;
+            const int part = lane % VECS;
+#pragma unroll 1
+            for (int i = 0; i < VECS; i += U) {
+                uint4 x[U], y[U];
 #pragma unroll
                 for (int j = 0; j < U; ++j) {
-                    const int64_t s = __shfl_sync(0xffffffffu, src, r & 31);
-                    const int64_t d = __shfl_sync(0xffffffffu, dst, r & 31);
-                    to[j] = r < rows && d >= 0 ? d * a.row_bytes + 16 * v : -1;
-                    if (to[j] >= 0)
-                        x[j] = __ldcs(reinterpret_cast<const uint4 *>(base + s * a.row_bytes + 16 * v));
-                    r += step_r;
-                    v += step_v;
-                    if (v >= vecs) {
-                        v -= vecs;
-                        ++r;
+                    const int s = __shfl_sync(0xffffffffu, src, (i + j) * kAt + lane / VECS);
+                    if (s >= 0) {
+                        x[j] = __ldcs(k + static_cast<size_t>(s) * VECS + part);
+                        y[j] = __ldcs(v + static_cast<size_t>(s) * VECS + part);
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < U; ++j)
-                    if (to[j] >= 0) *reinterpret_cast<uint4 *>(base + to[j]) = x[j];
+                for (int j = 0; j < U; ++j) {
+                    const int d = __shfl_sync(0xffffffffu, dst, (i + j) * kAt + lane / VECS);
+                    if (d >= 0) {
+                        k[static_cast<size_t>(d) * VECS + part] = x[j];
+                        v[static_cast<size_t>(d) * VECS + part] = y[j];
+                    }
+                }
             }
-        };
-        copy(static_cast<uint8_t *>(a.c.k));
-        if (a.c.v) copy(static_cast<uint8_t *>(a.c.v));
+        } else {
+            const int vecs = a.row_bytes / 16, rows = min(kMoveRows, n - r0);
+            constexpr int U = 8;
+            const int total = rows * vecs, step_r = 32 / vecs, step_v = 32 % vecs;
+            int r = lane / vecs, part = lane % vecs;
+#pragma unroll 1
+            for (int i = 0; i < total; i += 32 * U) {
+                uint4 x[U];
+                const int was_r = r, was_part = part;
+                auto next = [&] {
+                    r += step_r;
+                    part += step_v;
+                    if (part >= vecs) {
+                        part -= vecs;
+                        ++r;
+                    }
+                };
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int s = __shfl_sync(0xffffffffu, src, r & 31);
+                    if (r < rows && s >= 0) x[j] = __ldcs(k + static_cast<size_t>(s) * vecs + part);
+                    next();
+                }
+                r = was_r;
+                part = was_part;
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int d = __shfl_sync(0xffffffffu, dst, r & 31);
+                    if (r < rows && d >= 0) k[static_cast<size_t>(d) * vecs + part] = x[j];
+                    next();
+                }
+            }
+        }
+        if (a.c.k_scale && dst >= 0) {
+            static_cast<float *>(a.c.k_scale)[dst] = k_scale;
+            static_cast<float *>(a.c.v_scale)[dst] = v_scale;
+        }
     }
+}
+
+template <int VECS>
+cudaError_t launch_move(const EvictArgs &a, int rows, cudaStream_t st) {
+    const int most = a.keep < a.c.len ? a.keep : a.c.len;
+    const int per_row = (most + kMoveRows - 1) / kMoveRows;
+    const int64_t units = static_cast<int64_t>(rows) * per_row;
+    const int64_t want = (units + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
+    const int64_t grid = want < (1 << 20) ? want : 1 << 20;
+    if (grid == 0) return cudaSuccess;
+    return launch_ex(move_kernel<VECS>, dim3(static_cast<unsigned>(grid)), dim3(kMoveThreads), 0, st,
+                     true, a, units, per_row);
 }
 
 }  // namespace
@@ -252,19 +307,19 @@ cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
     int blocks = 1;
     while (blocks < kMaxCluster && a.c.len > blocks * 2048) blocks *= 2;
     const int rows = a.c.batch * a.c.n_kv_heads;
-    const size_t smem = kCached * sizeof(uint32_t);
+    const int slice = ((a.c.len + blocks - 1) / blocks + kThreads - 1) / kThreads * kThreads;
+    const int room = slice < kCached ? slice : kCached;
+    const size_t smem = room * sizeof(uint32_t);
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(choose_kernel), kThreads, smem);
     if (e != cudaSuccess) return e;
-    e = launch_cluster(choose_kernel, dim3(rows * blocks), dim3(kThreads), blocks, smem, st, a, blocks);
+    e = launch_cluster(choose_kernel, dim3(rows * blocks), dim3(kThreads), blocks, smem, st, a, blocks,
+                       room);
     if (e != cudaSuccess) return e;
-    const int most = a.keep < a.c.len ? a.keep : a.c.len;
-    const int per_row = (most + kMoveRows - 1) / kMoveRows;
-    const int64_t units = static_cast<int64_t>(rows) * per_row;
-    const int64_t want = (units + kMoveThreads / 32 - 1) / (kMoveThreads / 32);
-    const int64_t grid = want < 64ll * device_sm_count() ? want : 64ll * device_sm_count();
-    if (grid == 0) return cudaSuccess;
-    return launch_ex(move_kernel, dim3(static_cast<unsigned>(grid)), dim3(kMoveThreads), 0, st, true,
-                     a, units, per_row);
+    const int vecs = a.c.v ? a.row_bytes / 16 : 0;
+    if (vecs == 4) return launch_move<4>(a, rows, st);
+    if (vecs == 8) return launch_move<8>(a, rows, st);
+    if (vecs == 16) return launch_move<16>(a, rows, st);
+    return launch_move<0>(a, rows, st);
 }
 
 }  // namespace kvd

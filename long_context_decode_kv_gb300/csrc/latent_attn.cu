@@ -9,7 +9,7 @@
 // tensor memory and leave none for the logits.  So the rows (tokens' query heads) stand
 // on the products' narrow side, up to 64 of them,
 //   S^T = K Q^T   64 keys x rows          O^T += V^T P^T   128 channels x rows, R / 128 times
-// with S twice and O in 2 * 64 + 4 * 64 columns, and key tiles are 64 tokens, of which
+// with S of four tiles and O in 4 * 64 + 4 * 64 columns, and key tiles are 64 tokens, of which
 // two fit beside the queries (72 KB each at 576 channels).  Measured, clocks a product
 // of 16: 64 x 64 32, 128 x 64 48 (shared memory's rate; 128 x 128 64): 1920 for 64 rows
 // and 64 keys of 576 channels, 1.35 PFLOP/s at most.
@@ -19,9 +19,11 @@
 // tiles form one line, cut into equal costs for the CTAs; an item that a cut divides is
 // joined from f32 partials by join_kernel.
 //
-// Roles: warps 0-3 softmax, a thread 2 keys and a quarter of the rows (the layout of
-// 16 x 256-bit reads from tensor memory, of which 64-lane products fill 16 lanes a warp);
-// warp 4 loads by TMA, warp 5 issues S^T, warp 6 O^T.  A key tile's places are released
+// Roles: warps 0-3 and 4-7 softmax of the rows' first and second half, a thread 2 keys and
+// an eighth of the rows (the layout of 16 x 256-bit reads from tensor memory, of which
+// 64-lane products fill 16 lanes a warp); warp 8 issues S^T, warp 9 O^T, warps 10-12 load by
+// TMA (a copy's issue takes a warp some 100 clocks, and pages of 16 tokens take 36 of them a
+// tile).  A key tile's places are released
 // 128 channels at a time, as O^T is done with them.
 //
 // The reference m of a row's weights 2^(logit - m) follows its maximum loosely, from kLift
@@ -39,7 +41,9 @@ constexpr int kHalf = kKeys * 128;     // 64 channels of it
 constexpr int kPair = 2 * kHalf;       // 128 channels
 constexpr int kMaxRing = 8;            // tiles in shared memory
 constexpr int kMaxTops = 4;            // 128-channel parts of the latent vector
-constexpr int kThreads = 256;
+constexpr int kLogits = 4;             // tiles' logits in tensor memory
+constexpr int kLoaders = 3;            // loading warps
+constexpr int kThreads = 32 * (10 + kLoaders);
 constexpr float kLift = 6.0f;          // a new reference: so far below the row's maximum
 constexpr float kRedo = 32768.0f;      // a weight above it asks for one
 constexpr int kFewSeqs = 48;           // sequences whose items are counted a warp each
@@ -127,23 +131,28 @@ __device__ __forceinline__ bool next_segment(const LatentDev &a, Walk &w, Segmen
     return true;
 }
 
-// 16 lanes' columns [0, NR) of the calling warp's quarter: v[4 i + e] is lane l / 4 (e < 2) or
+// 16 lanes' N columns of the calling warp's quarter: v[4 i + e] is lane l / 4 (e < 2) or
 // l / 4 + 8, column 8 i + 2 (l % 4) + e % 2.
-template <int NR>
-__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&v)[NR / 2]) {
+template <int N>
+__device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&v)[N / 2]) {
     uint32_t *r = reinterpret_cast<uint32_t *>(v);
+    if constexpr (N == 8) {
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(addr));
+    } else {
 #pragma unroll
-    for (int i = 0; i < NR / 2; i += 8)
-        asm volatile(
-            "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-            : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]),
-              "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-            : "r"(addr + 2 * i));
+        for (int i = 0; i < N / 2; i += 8)
+            asm volatile(
+                "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                : "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]),
+                  "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+                : "r"(addr + 2 * i));
+    }
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < NR / 2; i += 8)
-        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]),
-                          "+f"(v[i + 4]), "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+    for (int i = 0; i < N / 2; i += 4)
+        asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]));
 }
 
 // wait_for where each lane (of those that take part) has its own barrier.
@@ -162,12 +171,13 @@ __device__ __forceinline__ bool wait_lanes(bool mine, uint64_t *bar, uint32_t pa
     return true;
 }
 
-__device__ __forceinline__ void meet_128() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-__device__ __forceinline__ bool any_of_128(bool mine) {
+// Barriers of the 256 softmax threads; the second tells whether any said yes.
+__device__ __forceinline__ void meet() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ bool any_says(bool mine) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "bar.red.or.pred p, 1, 128, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "bar.red.or.pred p, 1, 256, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r)
         : "r"(static_cast<uint32_t>(mine))
         : "memory");
@@ -177,12 +187,16 @@ __device__ __forceinline__ bool any_of_128(bool mine) {
 // What stands behind the tiles in shared memory.
 struct Small {
     uint64_t q_full, q_empty, full[kMaxRing][kMaxTops + 1], empty[kMaxRing][kMaxTops + 1],
-        s_full[2], p_full[2], o_done[2], done;
+        s_full[kLogits], p_full[kLogits], o_done[2], done;
     uint32_t tmem_slot;
     int abort_flag, found_seq;
     uint32_t dead_groups[16];  // per key tile: its 16-key groups on bad pages
     alignas(16) float m[64];  // rows' references,
-    alignas(16) float base[64], f[64];  // less or 0, and the factor to a new one
+    union {
+        alignas(16) float base[64];     // less or 0,
+        int row_at[64];                 // (at a segment's end: token * 65536 + head, -1: none)
+    };
+    alignas(16) float f[64];            // and the factor to a new one
     union {
         alignas(16) float red[4][64];
         struct {
@@ -206,7 +220,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
               const __grid_constant__ CUtensorMap k_map) {
     using Sh = LatentShape<NR>;
     constexpr int kQChunk = NR * 128;  // 64 channels of the rows
-    constexpr uint32_t kO = 2 * NR;    // columns of O
+    constexpr uint32_t kO = kLogits * NR;  // columns of O
 
     extern __shared__ __align__(1024) uint8_t smem[];
     const int parts = a.tops + 1;      // of a row: the rotated part, then 128 channels each
@@ -221,7 +235,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         if (tid == 0) report_status(a.c.dev_status, KVD_ERR_CUDA);
         return;
     }
-    if (warp == 5) tmem_alloc(&sm.tmem_slot, Sh::kColumns);
+    if (warp == 8) tmem_alloc(&sm.tmem_slot, Sh::kColumns);
     if (tid == 0) {
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_empty, 1);
@@ -230,11 +244,11 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 mbar_init(&sm.full[i][p], 1);
                 mbar_init(&sm.empty[i][p], 1);
             }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kLogits; ++i) {
             mbar_init(&sm.s_full[i], 1);
-            mbar_init(&sm.p_full[i], 4);
-            mbar_init(&sm.o_done[i], 1);
+            mbar_init(&sm.p_full[i], 8);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.o_done[i], 1);
         mbar_init(&sm.done, 2);
         fence_barrier_init();
         sm.abort_flag = 0;
@@ -377,24 +391,34 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
     __syncthreads();  // `start` has been read: its memory is the softmax's
     bool ok = true;
 
-    if (warp == 4) {
+    if (warp >= 10) {
         // ------------------------------------------------------------ loads ---
         // rows that other items read too stay in the L2
         const bool shared = a.groups > 1 || a.max_new > a.tokens;
         const uint64_t policy = shared ? l2_policy_evict_last() : l2_policy_evict_first();
         const int boxes = kKeys / a.box, ps = a.c.page_size;
         const int per_read = 32 / boxes;  // tiles whose rows one read of the page table gives
+        // Lane l of warp w loads part w + kLoaders l of each tile: the rotated part (0), or the
+        // channels [128 (p - 1), 128 p)
+        const bool first_warp = warp == 10;     // and queries
+        const int part = warp - 10 + kLoaders * lane;
+        const bool loads = part < parts;
+        const int my_part = loads ? part : 0;
+        const int my_x = part == 0 ? a.tops * 128 : (part - 1) * 128;
+        const int my_at = part == 0 ? a.tops * kPair : (part - 1) * kPair;
         uint32_t n = 0, mine = 0, queries = 0;  // tiles, this lane's loads of them, of queries
         uint32_t st = 0, round = 0;
         int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
 #pragma unroll 1
         while (ok && next_segment(a, w, g)) {
-            if (queries > 0 && !(ok = wait_for(&sm.q_empty, (queries - 1) & 1, abort))) break;
-            ++queries;
-            if (lane == 0)
-                mbar_arrive_expect_tx(&sm.q_full, (2 * a.tops + 1) * a.heads * a.tokens * 128);
-            __syncwarp();
-            if (lane <= 2 * a.tops)
+            if (first_warp) {
+                if (queries > 0 && !(ok = wait_for(&sm.q_empty, (queries - 1) & 1, abort))) break;
+                ++queries;
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&sm.q_full, (2 * a.tops + 1) * a.heads * a.tokens * 128);
+                __syncwarp();
+            }
+            if (first_warp && lane <= 2 * a.tops)
                 tma_load_4d(q_smem + lane * kQChunk, &q_map, lane == 0 ? a.tops * 128 : (lane - 1) * 64,
                             g.group * a.heads, 0, g.s0 + g.it.i0, &sm.q_full);
             // the cache rows of the boxes of tiles j, j + 1, .., a lane a box: dead_row
@@ -424,27 +448,24 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                         if (x < boxes) bad |= ((1u << (a.box / 16)) - 1) << (x * (a.box / 16));
                     }
                 }
-                if (lane == 0) sm.dead_groups[n & 15] = bad;
+                if (first_warp && lane == 0) sm.dead_groups[n & 15] = bad;
                 __syncwarp();
-                // Lane 0 loads the rotated part, lane p the channels [128 (p - 1), 128 p), each
-                // as soon as its place is free.
-                uint64_t *full = &sm.full[st][min(lane, a.tops)];
-                uint64_t *empty = &sm.empty[st][min(lane, a.tops)];
-                uint8_t *dst = ring + st * tile_bytes + (lane == 0 ? a.tops * kPair : (lane - 1) * kPair);
-                bool todo = lane < parts;
+                // each part as soon as its place is free
+                uint64_t *full = &sm.full[st][my_part], *empty = &sm.empty[st][my_part];
+                uint8_t *dst = ring + st * tile_bytes + my_at;
+                bool todo = loads;
                 uint32_t tries = 0, t0 = 0;
 #pragma unroll 1
                 while (__any_sync(0xffffffffu, todo)) {
                     if (todo && (round == 0 || mbar_try_wait(empty, (round - 1) & 1))) {
-                        mbar_arrive_expect_tx(full, lane == 0 ? kHalf : kPair);
-                        const int x0 = lane == 0 ? a.tops * 128 : (lane - 1) * 128;
+                        mbar_arrive_expect_tx(full, part == 0 ? kHalf : kPair);
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
                             if (x < boxes) {
-                                tma_load_2d(dst + x * a.box * 128, &k_map, x0, row[x], full, policy);
-                                if (lane > 0)
-                                    tma_load_2d(dst + kHalf + x * a.box * 128, &k_map, x0 + 64, row[x],
-                                                full, policy);
+                                tma_load_2d(dst + x * a.box * 128, &k_map, my_x, row[x], full, policy);
+                                if (part > 0)
+                                    tma_load_2d(dst + kHalf + x * a.box * 128, &k_map, my_x + 64,
+                                                row[x], full, policy);
                             }
                         todo = false;
                         ++mine;
@@ -476,7 +497,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             }
         }
         if (!ok) fail();
-        if (lane == 0) {
+        if (first_warp && lane == 0) {
             a.join[2 * blockIdx.x] = rec0;
             a.join[2 * blockIdx.x + 1] = rec1;
         }
@@ -486,15 +507,15 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             // nothing may land in shared memory after the CTA has gone
             volatile int none = 0;
             bool landed = true;  // after one wait that runs out all has had the time to land
-            for (uint32_t i = 0; lane < parts && landed && i < static_cast<uint32_t>(a.ring); ++i) {
+            for (uint32_t i = 0; loads && landed && i < static_cast<uint32_t>(a.ring); ++i) {
                 const uint32_t fills = (mine + a.ring - 1 - i) / a.ring;
-                if (fills > 0) landed = mbar_wait(&sm.full[i][lane], (fills - 1) & 1, &none);
+                if (fills > 0) landed = mbar_wait(&sm.full[i][part], (fills - 1) & 1, &none);
             }
             __syncwarp();
             if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, &none);
         }
         return;
-    } else if (warp == 5) {
+    } else if (warp == 8) {
         // -------------------------------------------------- products S^T = K Q^T ---
         constexpr uint32_t kIdS = mma_idesc(BF16, kKeys, NR, false);
         const uint32_t ring_addr = smem_addr(ring);
@@ -507,34 +528,37 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             ++queries;
 #pragma unroll 1
             for (int j = g.j0; ok && j < g.j1; ++j, ++n) {
-                const uint32_t b = n & 1;
-                // the logits of two tiles ago have been read
-                if (n >= 2 && !(ok = wait_for(&sm.p_full[b], ((n >> 1) - 1) & 1, abort))) break;
+                const uint32_t b = n % kLogits;
+                // the logits that were there have been read
+                if (n >= kLogits && !(ok = wait_for(&sm.p_full[b], (n / kLogits - 1) & 1, abort)))
+                    break;
                 tmem_fence_after();
                 const uint32_t s_at = warp_uniform(tmem_u + b * NR);
                 const uint32_t k = warp_uniform(desc_low(ring_addr + st * tile_bytes, 16));
-#pragma unroll 1
-                for (int p = 0; p < parts; ++p) {
+                const uint32_t k_rope = warp_uniform(k + a.tops * (kPair / 16));
+#pragma unroll
+                for (int p = 0; p <= kMaxTops; ++p) {
+                    if (p > a.tops) break;
                     if (!(ok = wait_for(&sm.full[st][p], round & 1, abort))) break;
-                    tmem_fence_after();
                     if (elect_one()) {
                         if (p == 0) {
-                            const uint32_t k0 = k + a.tops * (kPair / 16);
-#pragma unroll 1
-                            for (int x = 0; x < a.rope_steps; ++x)
-                                mma_ss(s_at, smem_desc(k0 + 2 * x), smem_desc(q + 2 * x), kIdS, x > 0);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                if (x < a.rope_steps)
+                                    mma_ss(s_at, smem_desc(k_rope + 2 * x), smem_desc(q + 2 * x), kIdS,
+                                           x > 0);
                             mma_commit(&sm.empty[st][0]);
                         } else {
-                            const uint32_t k0 = k + (p - 1) * (kPair / 16);
-                            const uint32_t q0 = q + (2 * p - 1) * (kQChunk / 16);
 #pragma unroll
                             for (int x = 0; x < 8; ++x)
-                                mma_ss(s_at, smem_desc(k0 + x / 4 * (kHalf / 16) + x % 4 * 2),
-                                       smem_desc(q0 + x / 4 * (kQChunk / 16) + x % 4 * 2), kIdS, 1);
-                        }
-                        if (p == a.tops) {
-                            mma_commit(&sm.s_full[b]);
-                            if (j + 1 == g.j1) mma_commit(&sm.q_empty);
+                                mma_ss(s_at,
+                                       smem_desc(k + ((p - 1) * kPair + x / 4 * kHalf) / 16 + x % 4 * 2),
+                                       smem_desc(q + (2 * p - 1 + x / 4) * (kQChunk / 16) + x % 4 * 2),
+                                       kIdS, 1);
+                            if (p == a.tops) {
+                                mma_commit(&sm.s_full[b]);
+                                if (j + 1 == g.j1) mma_commit(&sm.q_empty);
+                            }
                         }
                     }
                     __syncwarp();
@@ -551,7 +575,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         __syncwarp();
         volatile int none = 0;
         if (!mbar_wait(&sm.done, 0, &none)) fail();
-    } else if (warp == 6) {
+    } else if (warp == 9) {
         // ---------------------------------------------- products O^T += V^T P^T ---
         constexpr uint32_t kIdO = mma_idesc(BF16, 128, NR, true, true);
         const uint32_t ring_addr = smem_addr(ring);
@@ -562,39 +586,23 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
                 const uint32_t b = n & 1;
-                if (!(ok = wait_for(&sm.p_full[b], (n >> 1) & 1, abort))) break;
+                if (!(ok = wait_for(&sm.p_full[n % kLogits], (n / kLogits) & 1, abort))) break;
                 // (they have landed: the logits come from them)
                 if (!(ok = wait_lanes(lane > 0 && lane < parts, &sm.full[st][min(lane, a.tops)],
                                       round & 1, abort)))
                     break;
                 tmem_fence_after();
-                const int from = max(g.it.lo - j * kKeys, 0), to = min(g.it.hi - j * kKeys, kKeys);
-                if (from > 0 || to < kKeys) {
-                    // rows that no token sees may hold NaN: clear them
-                    uint8_t *vs = ring + st * tile_bytes;
-                    const int per_row = 16 * a.tops;
-                    const int c = (from + (kKeys - max(to, 0))) * per_row;
-#pragma unroll 1
-                    for (int i = lane; i < c; i += 32) {
-                        int r = i / per_row;
-                        const int x = i - r * per_row;
-                        if (r >= from) r += max(to, 0) - from;
-                        *reinterpret_cast<uint4 *>(vs + x / 8 * kHalf + r * 128 + x % 8 * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
-                }
-                const uint32_t v = warp_uniform(desc_low(ring_addr + st * tile_bytes, kHalf));
                 const uint32_t p = warp_uniform(
                     desc_low(smem_addr(p_smem) + (Sh::kP == 2 ? b * kHalf : 0), kHalf));
                 const uint32_t add = warp_uniform(j > g.j0);
+                const uint32_t v = warp_uniform(desc_low(ring_addr + st * tile_bytes, kHalf));
                 if (elect_one()) {
-#pragma unroll 1
-                    for (int m = 0; m < a.tops; ++m) {
+#pragma unroll
+                    for (int m = 0; m < kMaxTops; ++m) {
+                        if (m >= a.tops) break;
 #pragma unroll
                         for (int x = 0; x < kKeys / 16; ++x)
-                            mma_ss(tmem_u + kO + m * NR, smem_desc(v + m * (kPair / 16) + x * (2048 / 16)),
+                            mma_ss(tmem_u + kO + m * NR, smem_desc(v + (m * kPair + x * 2048) / 16),
                                    smem_desc(p + x * (2048 / 16)), kIdO, x > 0 ? 1 : add);
                         mma_commit(&sm.empty[st][1 + m]);
                     }
@@ -612,13 +620,15 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         __syncwarp();
         volatile int none = 0;
         if (!mbar_wait(&sm.done, 0, &none)) fail();
-    } else if (warp < 4) {
+    } else {
         // ------------------------------------------------------------ softmax ---
-        constexpr int kV = NR / 2;   // logits a thread: 4 for each 8 rows
-        const uint32_t lanes = tmem + (warp << 21);
-        const int key0 = warp * 16 + lane / 4, col0 = 2 * (lane & 3);
+        constexpr int kV = NR / 4;   // logits a thread: 4 for each 8 of the half's rows
+        const int quarter = warp & 3, half = warp >> 2;
+        const uint32_t lanes = tmem + (quarter << 21);
+        const int key0 = quarter * 16 + lane / 4, col0 = half * (NR / 2) + 2 * (lane & 3);
         const int R = a.tops * 128;
-        uint32_t n = 0;
+        const int my_tok = tid / a.heads, my_head = tid - my_tok * a.heads;  // of row `tid`
+        uint32_t n = 0, st = 0;
         // These warps meet at barriers of the hardware, which have no limit: so none
         // leaves its loops before the others, and a wait that ran out only makes the
         // waits behind it pass.
@@ -631,7 +641,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             // keys that every row sees
             const int all_lo = a.window > 0 ? max(g.p0 + g.it.cnt - a.window, 0) : 0;
             const int all_hi = max(g.p0 + 1, 0);
-            auto live = [&](int r) { return r < g.it.cnt * a.heads && r % a.heads < heads; };
+            const bool live = my_tok < g.it.cnt && my_head < heads;
             float l[kV / 2];
 #pragma unroll
             for (int i = 0; i < kV / 2; ++i) l[i] = 0.0f;
@@ -639,9 +649,10 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
                 const uint32_t b = n & 1;
-                wait(&sm.s_full[b], (n >> 1) & 1);
+                const uint32_t s_at = lanes + n % kLogits * NR + half * (NR / 2);
+                wait(&sm.s_full[n % kLogits], (n / kLogits) & 1);
                 tmem_fence_after();
-                const uint32_t bad = sm.dead_groups[n & 15] >> warp & 1;
+                const uint32_t bad = sm.dead_groups[n & 15] >> quarter & 1;
                 // the rows [r0, r1) that see each of the two keys
                 int r0[2] = {0, 0}, r1[2] = {NR, NR};
                 const bool edge = j * kKeys < all_lo || (j + 1) * kKeys > all_hi || bad;
@@ -666,7 +677,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 #pragma unroll 1
                 for (;;) {
                     float s[kV];
-                    tmem_ld_rows<NR>(lanes + b * NR, s);
+                    tmem_ld_rows<NR / 2>(s_at, s);
                     if (edge)
 #pragma unroll
                         for (int i = 0; i < kV; ++i) {
@@ -683,11 +694,11 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 #pragma unroll
                                 for (int o = 4; o < 32; o <<= 1)
                                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, o));
-                                if (lane < 4) sm.red[warp][i / 4 * 8 + col0 + e] = t;
+                                if (lane < 4) sm.red[quarter][i / 4 * 8 + col0 + e] = t;
                             }
                         // O as it stands is complete
                         if (j > g.j0) wait(&sm.o_done[b ^ 1], ((n - 1) >> 1) & 1);
-                        meet_128();
+                        meet();
                         bool none = false;
                         if (tid < NR) {
                             const float top = fmaxf(fmaxf(sm.red[0][tid], sm.red[1][tid]),
@@ -697,19 +708,18 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                             sm.f[tid] =
                                 m == -INFINITY || mn == -INFINITY ? 1.0f : exp2_approx(m - mn);
                             sm.m[tid] = mn;
-                            const bool some = live(tid);
-                            none = some && mn == -INFINITY;
+                            none = live && mn == -INFINITY;
                             // rows that are none (another sequence's queries may stand
                             // there): no weights, and no say in the votes
-                            sm.base[tid] = !some ? -INFINITY : mn == -INFINITY ? 0.0f : -mn;
+                            sm.base[tid] = !live ? -INFINITY : mn == -INFINITY ? 0.0f : -mn;
                         }
-                        open = any_of_128(none);
+                        open = any_says(none);
 #pragma unroll
                         for (int i = 0; i < kV / 2; ++i) l[i] *= sm.f[i / 2 * 8 + col0 + (i & 1)];
                         if (j > g.j0) {
                             tmem_fence_after();
 #pragma unroll 1
-                            for (int i = 0; i < a.tops * NR; i += 16) {
+                            for (int i = 16 * half; i < a.tops * NR; i += 32) {
                                 float o[16];
                                 tmem_ld16(lanes + kO + i, o);
                                 tmem_wait_ld();
@@ -743,14 +753,22 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                             if (r < r0[e] || r >= r1[e]) p[i] = 0.0f;
                         }
                     if (fix) break;  // no weight passes 2^kLift
-                    if (!any_of_128(top > kRedo)) break;
+                    if (!any_says(top > kRedo)) break;
                     fix = true;
                 }
                 // P^T's buffer has been read
-                if (Sh::kP == 1) {
-                    if (n >= 1) wait(&sm.o_done[b ^ 1], ((n - 1) >> 1) & 1);
-                } else {
-                    if (n >= 2) wait(&sm.o_done[b], ((n >> 1) - 1) & 1);
+                if (n >= Sh::kP) wait(&sm.o_done[(n - Sh::kP) & 1], ((n - Sh::kP) >> 1) & 1);
+                const int from = g.it.lo - j * kKeys, to = g.it.hi - j * kKeys;
+                if (from > 0 || to < kKeys) {
+                    // rows that no token sees may hold NaN: clear them (they have landed, and
+                    // the logits are done)
+                    uint8_t *vs = ring + st * tile_bytes + (tid >> 3 & 1) * kHalf + (tid & 7) * 16;
+#pragma unroll 1
+                    for (int r = tid >> 4; r < kKeys; r += 16)
+                        if (r < from || r >= to)
+                            for (int x = 0; x < a.tops; ++x)
+                                *reinterpret_cast<uint4 *>(vs + x * kPair + r * 128) =
+                                    make_uint4(0, 0, 0, 0);
                 }
                 // the weights, and P^T: a key's rows in 128 swizzled bytes
                 uint8_t *dst = p_smem + (Sh::kP == 2 ? b * kHalf : 0) + key0 * 128 + (lane & 3) * 4;
@@ -758,149 +776,212 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 for (int i = 0; i < kV; i += 4) {
                     l[i / 2] += p[i] + p[i + 2];
                     l[i / 2 + 1] += p[i + 1] + p[i + 3];
-                    const int at = ((i / 4) ^ (key0 & 7)) * 16;  // (key0 + 8 has the same low bits)
+                    const int at = ((i / 4 + half * (NR / 16)) ^ (key0 & 7)) * 16;  // (key0 + 8 has the same low bits)
                     *reinterpret_cast<uint32_t *>(dst + at) = pack2<BF16>(p[i], p[i + 1]);
                     *reinterpret_cast<uint32_t *>(dst + 1024 + at) = pack2<BF16>(p[i + 2], p[i + 3]);
                 }
                 fence_proxy_async();
                 tmem_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&sm.p_full[b]);
+                if (lane == 0) mbar_arrive(&sm.p_full[n % kLogits]);
+                if (++st == static_cast<uint32_t>(a.ring)) st = 0;
             }
             // ---- the segment's sums
-            meet_128();  // the last references have been read
+            meet();  // the last references have been read
 #pragma unroll
             for (int i = 0; i < kV / 2; ++i) {
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
-                if (lane < 4) sm.red[warp][i / 2 * 8 + col0 + (i & 1)] = l[i];
+                if (lane < 4) sm.red[quarter][i / 2 * 8 + col0 + (i & 1)] = l[i];
             }
             wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
             tmem_fence_after();
-            meet_128();
+            meet();
             const bool whole = g.starts && g.ends;
             const uint32_t slot = 2 * blockIdx.x + (g.k == 0 ? 0 : 1);
             if (tid < NR) {
                 const float sum = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
                 const float m = sm.m[tid];
                 sm.f[tid] = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                if (live(tid)) {
-                    if (!whole) {
+                const int h = g.group * a.heads + my_head;
+                sm.row_at[tid] = live ? my_tok << 16 | h : -1;
+                if (live) {
+                    if (!whole)
                         a.ml[slot * NR + tid] = make_float2(m, sum);
-                    } else if (a.lse) {
-                        const int tok = tid / a.heads;
-                        a.lse[static_cast<int64_t>(g.s0 + g.it.i0 + tok) * a.G + g.group * a.heads +
-                              (tid - tok * a.heads)] = lse_of(m, sum);
-                    }
+                    else if (a.lse)
+                        a.lse[static_cast<int64_t>(g.s0 + g.it.i0 + my_tok) * a.G + h] = lse_of(m, sum);
                 }
             }
-            meet_128();
+            meet();
             const int rows = g.it.cnt * a.heads;
+            // A thread holds a channel of 16 rows at a time.
 #pragma unroll 1
-            for (int m = 0; m < a.tops; ++m) {
-                const int channel = m * 128 + tid;
-#pragma unroll 1
-                for (int i = 0; i < NR && i < rows; i += 16) {
-                    float o[16];
-                    tmem_ld16(lanes + kO + m * NR + i, o);
-                    tmem_wait_ld();
-                    pin16(o);
-                    int tok = i / a.heads, head = i - tok * a.heads;
+            for (int x = half; x < a.tops * (NR / 16); x += 2) {
+                const int m = x / (NR / 16), i = x % (NR / 16) * 16;
+                if (i >= rows) continue;
+                const int channel = m * 128 + quarter * 32 + lane;
+                float o[16];
+                tmem_ld16(lanes + kO + m * NR + i, o);
+                tmem_wait_ld();
+                pin16(o);
+                if (whole) {
+                    uint16_t *out = a.out + static_cast<int64_t>(g.s0 + g.it.i0) * a.out_stride +
+                                    (channel & ~1);
+                    // even lanes take two channels of the even rows, odd lanes of the odd ones
+                    const bool odd = lane & 1;
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        if (i + r < rows && head < heads) {
-                            if (whole) {
-                                const float f = sm.f[i + r];
-                                a.out[static_cast<int64_t>(g.s0 + g.it.i0 + tok) * a.out_stride +
-                                      static_cast<int64_t>(g.group * a.heads + head) * R + channel] =
-                                    static_cast<uint16_t>(pack2<BF16>(f != 0.0f ? o[r] * f : 0.0f, 0.0f));
-                            } else {
-                                a.acc[(static_cast<size_t>(slot) * NR + i + r) * R + channel] = o[r];
-                            }
-                        }
-                        if (++head == a.heads) {
-                            head = 0;
-                            ++tok;
-                        }
+                    for (int r = 0; r < 16; r += 2) {
+                        const float f0 = sm.f[i + r], f1 = sm.f[i + r + 1];
+                        const float o0 = f0 != 0.0f ? o[r] * f0 : 0.0f;
+                        const float o1 = f1 != 0.0f ? o[r + 1] * f1 : 0.0f;
+                        const float other = __shfl_xor_sync(0xffffffffu, odd ? o0 : o1, 1);
+                        const int to = sm.row_at[i + r + odd];
+                        if (to >= 0)
+                            *reinterpret_cast<uint32_t *>(out + (to >> 16) * a.out_stride +
+                                                          (to & 0xffff) * R) =
+                                odd ? pack2<BF16>(other, o1) : pack2<BF16>(o0, other);
                     }
+                } else {
+                    float *to = a.acc + (static_cast<int64_t>(slot) * NR + i) * R + channel;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r, to += R)
+                        if (i + r < rows) *to = o[r];
                 }
             }
             tmem_fence_before();
-            meet_128();  // the next segment's references go where these stood
+            meet();  // the next segment's references go where these stood
         }
         if (!ok) fail();
     }
     tmem_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == 8) {
         tmem_fence_after();
         tmem_free(tmem, Sh::kColumns);
     }
 }
 
-// Joins the items that a cut between CTAs divided: CTA (c, y) serves rows y, y + gridDim.y, ..
-// of the item whose first piece is CTA c's last segment and goes on in the CTAs after it.
+// Joins the items that a cut between CTAs divided: the rows of all such items stand in one
+// line (record c: the item whose first piece is CTA c's last segment and goes on in the
+// CTAs after it).
 //   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
+// A warp takes PARTS times 128 channels of a row, the reads of AT pieces under way together.
 constexpr int kMaxCtas = 256;
-template <bool BF16, int NR>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ LatentDev a) {
-    __shared__ float factors[kMaxCtas + 1];
-    __shared__ float inverse;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int4 rec = a.join[2 * blockIdx.x];
-    if (rec.x == 0) return;
-    const int group = a.join[2 * blockIdx.x + 1].x;
-    const int tid = threadIdx.x, R = a.tops * 128;
-    const size_t first = 2 * blockIdx.x + rec.y, next = 2 * blockIdx.x;
-    auto slot_of = [&](int i) { return i == 0 ? first : next + 2 * i; };
-    const int heads = min(a.heads, a.G - group * a.heads);
+constexpr int kJoinThreads = 128;
+template <bool BF16, int NR, int PARTS, int AT>
+__device__ __forceinline__ void join_rows(const LatentDev &a, const int *before, int w, int warps,
+                                          int lane) {
+    const int R = a.tops * 128, units = PARTS == 1 ? a.tops : 1;
 #pragma unroll 1
-    for (int r = blockIdx.y; r < rec.w * a.heads; r += gridDim.y) {
-        const int tok = r / a.heads, head = r - tok * a.heads;
-        if (head >= heads) continue;
-        __syncthreads();
-        if (tid < 32) {
-            float m = -INFINITY, l = 0.0f;
-            for (int i = tid; i < rec.x; i += 32) m = fmaxf(m, a.ml[slot_of(i) * NR + r].x);
+    for (; w < before[kMaxCtas] * units; w += warps) {
+        const int u = w / units, part = w - u * units;
+        int c = 0;  // the last record that begins at or before u
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            for (int i = tid; i < rec.x; i += 32) {
-                const float2 ml = a.ml[slot_of(i) * NR + r];
-                const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
-                factors[i] = f;
+        for (int step = kMaxCtas / 2; step > 0; step >>= 1)
+            if (before[c + step] <= u) c += step;
+        const int r = u - before[c];
+        const int4 rec = a.join[2 * c];
+        const int group = a.join[2 * c + 1].x;
+        const int tok = r / a.heads, h = group * a.heads + r - tok * a.heads;
+        if (h >= a.G) continue;
+        // piece i is at slot 2 c + 2 i, the first maybe one on
+        auto slot_of = [&](int i) { return static_cast<size_t>(2 * (c + i) + (i == 0 ? rec.y : 0)); };
+        float m = -INFINITY, l = 0.0f;
+        for (int i = lane; i < rec.x; i += 32) m = fmaxf(m, a.ml[slot_of(i) * NR + r].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float4 o[PARTS];
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) o[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float *acc = a.acc + static_cast<size_t>(r) * R + part * 128 + lane * 4;
+#pragma unroll 1
+        for (int i0 = 0; i0 < rec.x; i0 += 32) {
+            float f = 0.0f;  // of piece i0 + lane
+            if (i0 + lane < rec.x) {
+                const float2 ml = a.ml[slot_of(i0 + lane) * NR + r];
+                f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - m);
                 l = fmaf(f, ml.y, l);  // a sum that is NaN stays one where f is 0
             }
+            const int n = min(32, rec.x - i0);
+#pragma unroll 1
+            for (int i = 0; i < n; i += AT) {
+                float4 v[AT][PARTS];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            if (tid == 0) {
-                inverse = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-                if (a.lse)
-                    a.lse[static_cast<int64_t>(rec.z + tok) * a.G + group * a.heads + head] =
-                        lse_of(m, l);
-            }
-        }
-        __syncthreads();
-        if (tid * 4 < R) {
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-            for (int i = 0; i < rec.x; ++i) {
-                const float4 u =
-                    *reinterpret_cast<const float4 *>(a.acc + (slot_of(i) * NR + r) * R + tid * 4);
-                const float f = factors[i];
-                if (f != 0.0f) {
-                    o.x = fmaf(f, u.x, o.x);
-                    o.y = fmaf(f, u.y, o.y);
-                    o.z = fmaf(f, u.z, o.z);
-                    o.w = fmaf(f, u.w, o.w);
+                for (int x = 0; x < AT; ++x)
+#pragma unroll
+                    for (int p = 0; p < PARTS; ++p)
+                        if (i + x < n && (PARTS == 1 || p < a.tops))
+                            v[x][p] = *reinterpret_cast<const float4 *>(
+                                acc + slot_of(i0 + i + x) * NR * R + 128 * p);
+#pragma unroll
+                for (int x = 0; x < AT; ++x) {
+                    const float g = __shfl_sync(0xffffffffu, f, (i + x) & 31);
+                    if (i + x < n && g != 0.0f)
+#pragma unroll
+                        for (int p = 0; p < PARTS; ++p) {
+                            o[p].x = fmaf(g, v[x][p].x, o[p].x);
+                            o[p].y = fmaf(g, v[x][p].y, o[p].y);
+                            o[p].z = fmaf(g, v[x][p].z, o[p].z);
+                            o[p].w = fmaf(g, v[x][p].w, o[p].w);
+                        }
                 }
             }
-            const float inv = inverse;
-            *reinterpret_cast<uint2 *>(a.out + static_cast<int64_t>(rec.z + tok) * a.out_stride +
-                                       static_cast<int64_t>(group * a.heads + head) * R + tid * 4) =
-                make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
         }
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+        const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+        const int64_t token = rec.z + tok;
+        if (a.lse && lane == 0 && part == 0) a.lse[token * a.G + h] = lse_of(m, l);
+        uint16_t *out = a.out + token * a.out_stride + static_cast<int64_t>(h) * R + part * 128 + lane * 4;
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p)
+            if (PARTS == 1 || p < a.tops)
+                *reinterpret_cast<uint2 *>(out + 128 * p) =
+                    make_uint2(pack2<BF16>(o[p].x * inv, o[p].y * inv),
+                               pack2<BF16>(o[p].z * inv, o[p].w * inv));
     }
+}
+
+template <bool BF16, int NR>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ LatentDev a, int ctas) {
+    __shared__ int before[kMaxCtas + 1];  // rows of the records before
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (warp == 0) {
+        constexpr int kEach = kMaxCtas / 32;
+        int n[kEach], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int c = lane * kEach + i;
+            int4 rec = make_int4(0, 0, 0, 0);
+            if (c < ctas) rec = a.join[2 * c];
+            n[i] = rec.x ? rec.w * a.heads : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) sum += n[i];
+        int upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        upto -= sum;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            before[lane * kEach + i] = upto;
+            upto += n[i];
+        }
+        if (lane == 31) before[kMaxCtas] = upto;
+    }
+    __syncthreads();
+    // a warp a row, or where there are few rows 128 channels of one
+    const int warps = gridDim.x * (kJoinThreads / 32);
+    const int w = blockIdx.x * (kJoinThreads / 32) + warp;
+    if (before[kMaxCtas] * a.tops <= warps)
+        join_rows<BF16, NR, 1, 8>(a, before, w, warps, lane);
+    else
+        join_rows<BF16, NR, kMaxTops, 3>(a, before, w, warps, lane);
 }
 
 // ----------------------------------------------------------------- launch ---
@@ -975,7 +1056,7 @@ cudaError_t launch_rows(const PagedAttnArgs &p, int rank, const Plan &w, void *w
     if (e != cudaSuccess) return e;
     e = launch_ex(kernel, dim3(w.ctas), dim3(kThreads), smem, st, true, a, q_map, k_map);
     if (e != cudaSuccess) return e;
-    return launch_ex(join_kernel<BF16, NR>, dim3(w.ctas, NR / 2), dim3(128), 0, st, true, a);
+    return launch_ex(join_kernel<BF16, NR>, dim3(4 * w.ctas), dim3(kJoinThreads), 0, st, true, a, w.ctas);
 }
 
 template <bool BF16>
