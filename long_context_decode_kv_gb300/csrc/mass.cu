@@ -101,55 +101,8 @@ __device__ __forceinline__ RowTile row_tile(const MassDev &a, const Stretch &g, 
     return r;
 }
 
-struct MassBars {
-    uint64_t q_full, q_empty, full[kMaxPlaces], empty[kMaxPlaces], raw_full[4], raw_empty[4],
-        s_full[2], s_empty[2], done;
-};
-
-// I8: 0, or the channels of a row of codes (64 or 128)
-template <bool BF16, int I8>
-__global__ void __launch_bounds__(I8 ? 448 : 320, 1)
-mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorMap q_map,
-            const __grid_constant__ CUtensorMap k_map) {
-    extern __shared__ uint8_t raw_smem[];
-    __shared__ MassBars bar;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_flag;
-    __shared__ __align__(16) float lse[2][kMaxRows];  // of a row tile, base 2, for each team
-    uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
-    uint8_t *q_smem = smem;
-    uint8_t *ring = smem + a.chunks * a.rows * 128;
-    const int place_bytes = a.per * kChunkBytes;
-    uint8_t *raws = ring + a.places * place_bytes;
-
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if (warp == 9) tmem_alloc(&tmem_slot, 512);
-    if (tid == 0) {
-        mbar_init(&bar.q_full, 1);
-        mbar_init(&bar.q_empty, 1);
-        for (int i = 0; i < kMaxPlaces; ++i) {
-            mbar_init(&bar.full[i], I8 ? 4 : 1);
-            mbar_init(&bar.empty[i], 1);
-        }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 4);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.s_empty[i], 4);
-        }
-        mbar_init(&bar.done, 1);
-        fence_barrier_init();
-        abort_flag = 0;
-    }
-    tmem_fence_before();
-    __syncthreads();
-    tmem_fence_after();
-    pdl_wait();
-    pdl_launch_dependents();
-
-    // ---- this CTA's piece of the line, found by each warp
+// This CTA's piece of the line; each warp finds it.
+__device__ __forceinline__ Line start_of_line(const MassDev &a, bool first_warp, int lane) {
     auto cost_of = [&](int b, bool report) -> int {
         return b < a.c.batch ? tiles_of(mass_seq(a, b, report)) * a.c.n_kv_heads : 0;
     };
@@ -161,7 +114,7 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
         }
         return v;
     };
-    const bool report = blockIdx.x == 0 && warp == 0;
+    const bool report = blockIdx.x == 0 && first_warp;
     int cost = cost_of(lane, report);
     int upto = scan(cost);
     int total = __shfl_sync(0xffffffffu, upto, 31);
@@ -198,6 +151,101 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
             if (b0 + 32 >= a.c.batch) break;
         }
     }
+    return w;
+}
+
+// The sum over rows [r0, r1) of 2^(ks * logit + base) of this thread's key; the logits stand
+// in `rows` columns of its lane, base is -lse.
+__device__ __forceinline__ float weights_of(uint32_t s_at, const float *base, int rows, int r0, int r1,
+                                            float ks) {
+    float2 acc[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.0f, 0.0f);
+    const float2 k2 = make_float2(ks, ks);
+#pragma unroll 1
+    for (int c0 = 0; c0 < rows; c0 += 32) {
+        float s[32];
+        tmem_ld32(s_at + c0, s);
+        const bool whole = __all_sync(0xffffffffu, r0 <= c0 && r1 >= c0 + 32);
+        tmem_wait_ld();
+        pin32(s);
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+            const float4 l = *reinterpret_cast<const float4 *>(base + c0 + c);
+            float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), k2, make_float2(l.x, l.y));
+            float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), k2, make_float2(l.z, l.w));
+            s[c] = exp2_approx(x.x);
+            s[c + 1] = exp2_approx(x.y);
+            s[c + 2] = exp2_approx(y.x);
+            s[c + 3] = exp2_approx(y.y);
+        }
+        if (!whole)
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+                if (c0 + c < r0 || c0 + c >= r1) s[c] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 32; c += 2)
+            acc[c / 2 % 4] = __fadd2_rn(acc[c / 2 % 4], make_float2(s[c], s[c + 1]));
+    }
+#pragma unroll
+    for (int x = 1; x < 4; ++x) acc[0] = __fadd2_rn(acc[0], acc[x]);
+    return acc[0].x + acc[0].y;
+}
+
+// What a weight's exponent begins with, base 2; a row that sees no key has no weights.
+__device__ __forceinline__ float base_of(float lse) {
+    return lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+}
+
+struct MassBars {
+    uint64_t q_full, q_empty, full[kMaxPlaces], empty[kMaxPlaces], raw_full[4], raw_empty[4],
+        s_full[2], s_empty[2], done;
+};
+
+// I8: 0, or the channels of a row of codes (64 or 128)
+template <bool BF16, int I8>
+__global__ void __launch_bounds__(I8 ? 448 : 320, 1)
+mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorMap q_map,
+            const __grid_constant__ CUtensorMap k_map) {
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ MassBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float bases[2][kMaxRows];  // -lse of a row tile, for each team
+    uint8_t *smem = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    uint8_t *q_smem = smem;
+    uint8_t *ring = smem + a.chunks * a.rows * 128;
+    const int place_bytes = a.per * kChunkBytes;
+    uint8_t *raws = ring + a.places * place_bytes;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == 9) tmem_alloc(&tmem_slot, 512);
+    if (tid == 0) {
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_empty, 1);
+        for (int i = 0; i < kMaxPlaces; ++i) {
+            mbar_init(&bar.full[i], I8 ? 4 : 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.s_empty[i], 4);
+        }
+        mbar_init(&bar.done, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    Line w = start_of_line(a, warp == 0, lane);
     const uint32_t tmem = tmem_slot;
     volatile int *abort = &abort_flag;
     auto fail = [&] {
@@ -410,7 +458,7 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
         // --------------------------------------------------------------- sums ---
         const int team = warp >> 2, key = tid & 127;
         const uint32_t s_at = tmem + ((warp & 3) << 21) + team * kMaxRows;
-        float *my_lse = lse[team];
+        float *my_base = bases[team];
         uint32_t n = 0;
         // A team's warps meet at barriers of the hardware, which have no limit: so none
         // leaves its loops before the others, and a wait that ran out only makes the waits
@@ -436,15 +484,12 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
                     meet();  // the rows before have been read
                     for (int x = key; x < a.rows; x += 128) {
                         const int tok = x / a.heads, h = x - tok * a.heads;
-                        float l = INFINITY;  // no row there: no weight
-                        if (tok < r.cnt && h < r.heads) {
-                            l = a.lse[static_cast<int64_t>(g.s.s0 + r.i0 + tok) *
-                                          (a.c.n_kv_heads * a.G) +
-                                      g.head * a.G + r.h0 + h] *
-                                kLog2e;
-                            if (l == -INFINITY) l = INFINITY;
-                        }
-                        my_lse[x] = l;
+                        float l = -INFINITY;  // no row there: no weight
+                        if (tok < r.cnt && h < r.heads)
+                            l = base_of(a.lse[static_cast<int64_t>(g.s.s0 + r.i0 + tok) *
+                                                  (a.c.n_kv_heads * a.G) +
+                                              g.head * a.G + r.h0 + h]);
+                        my_base[x] = l;
                     }
                     meet();
                 }
@@ -483,52 +528,10 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
                         if (ok) ok = wait_for(&bar.s_full[team], n & 1, abort);
                         ++n;
                         tmem_fence_after();
-                        float2 acc[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x) acc[x] = make_float2(0.0f, 0.0f);
-                        const float2 k2 = make_float2(ks, ks);
-                        auto add = [&](const float *s, int c0) {
-                            const bool whole =
-                                __all_sync(0xffffffffu, r0 <= c0 && r1 >= c0 + 32);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 l = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
-                                float2 x = __ffma2_rn(make_float2(s[c], s[c + 1]), k2,
-                                                      make_float2(-l.x, -l.y));
-                                float2 y = __ffma2_rn(make_float2(s[c + 2], s[c + 3]), k2,
-                                                      make_float2(-l.z, -l.w));
-                                x = make_float2(exp2_approx(x.x), exp2_approx(x.y));
-                                y = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                                if (!whole) {
-                                    const int at = c0 + c;
-                                    if (at < r0 || at >= r1) x.x = 0.0f;
-                                    if (at + 1 < r0 || at + 1 >= r1) x.y = 0.0f;
-                                    if (at + 2 < r0 || at + 2 >= r1) y.x = 0.0f;
-                                    if (at + 3 < r0 || at + 3 >= r1) y.y = 0.0f;
-                                }
-                                acc[c / 4 % 2] = __fadd2_rn(acc[c / 4 % 2], x);
-                                acc[2 + c / 4 % 2] = __fadd2_rn(acc[2 + c / 4 % 2], y);
-                            }
-                        };
-                        float s0[32], s1[32];
-                        tmem_ld32(s_at, s0);
-#pragma unroll 1
-                        for (int c = 0; c < a.rows; c += 64) {
-                            tmem_wait_ld();
-                            pin32(s0);
-                            if (c + 32 < a.rows) tmem_ld32(s_at + c + 32, s1);
-                            add(s0, c);
-                            tmem_wait_ld();
-                            pin32(s1);
-                            if (c + 64 < a.rows) tmem_ld32(s_at + c + 64, s0);
-                            if (c + 32 < a.rows) add(s1, c + 32);
-                        }
+                        sum += weights_of(s_at, my_base, a.rows, r0, r1, ks);
                         tmem_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&bar.s_empty[team]);
-#pragma unroll
-                        for (int x = 1; x < 4; ++x) acc[0] = __fadd2_rn(acc[0], acc[x]);
-                        sum += acc[0].x + acc[0].y;
                     }
                     if (t < g.s.len) sums[t] = sum;
                 }
@@ -544,11 +547,365 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
     }
 }
 
-template <bool BF16, int I8>
-cudaError_t launch_type(const MassArgs &m, cudaStream_t st) {
+// ------------------------------------------------------- many rows a KV head ---
+// Up to kHeld key tiles stay in shared memory (turned once, where they are int8), and the
+// queries stream past them in tiles of 128 rows, so that a product of 128 x 128 costs 8 KB
+// of queries where streaming keys would cost 32.  Four warps take a tile of keys each, and
+// a thread keeps its key's sum in a register until all rows have passed.  (With two teams
+// of four warps for the four tiles, in turn, the two warps of a scheduler waited on their
+// own latencies most of the time.)
+constexpr int kHeld = 4;       // and teams of four warps
+constexpr int kSumWarps = 4 * kHeld;
+constexpr int rows_threads(bool i8) { return 32 * (kSumWarps + (i8 ? 6 : 2)); }
+constexpr int kRowsAt = 128;   // rows of a query tile
+constexpr int kQueryPlaces = 2;
+constexpr int kLseSlots = 8;   // query tiles' statistics
+
+struct RowsBars {
+    uint64_t q_full[kQueryPlaces], q_empty[kQueryPlaces], lse_full[kLseSlots], lse_empty[kLseSlots],
+        key_full[kHeld], key_raw[kHeld], keys_empty, s_full[kHeld], s_empty[kHeld], done;
+};
+
+template <bool BF16, int D, bool I8>
+__global__ void __launch_bounds__(rows_threads(I8), 1)
+mass_rows_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorMap q_map,
+                 const __grid_constant__ CUtensorMap k_map) {
+    constexpr int kChunks = D / 64;
+    constexpr int kTileBytes = kChunks * kChunkBytes;      // of 128 rows, keys or queries
+    constexpr int kRaw = I8 ? kTileBytes / 2 : 0;          // codes stand in a tile's second half
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ RowsBars bar;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_flag;
+    __shared__ __align__(16) float bases[kLseSlots][kRowsAt];  // -lse
+    uint8_t *keys = raw_smem + ((1024 - (smem_addr(raw_smem) & 1023)) & 1023);
+    uint8_t *queries = keys + kHeld * kTileBytes;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (warp == kSumWarps + 1) tmem_alloc(&tmem_slot, 512);
+    if (tid == 0) {
+        for (int i = 0; i < kQueryPlaces; ++i) {
+            mbar_init(&bar.q_full[i], 1);
+            mbar_init(&bar.q_empty[i], 1);
+        }
+        for (int i = 0; i < kLseSlots; ++i) {
+            mbar_init(&bar.lse_full[i], 1);
+            mbar_init(&bar.lse_empty[i], kSumWarps);
+        }
+        for (int i = 0; i < kHeld; ++i) {
+            mbar_init(&bar.key_full[i], I8 ? 4 : 1);
+            mbar_init(&bar.key_raw[i], 1);
+        }
+        mbar_init(&bar.keys_empty, 1);
+        for (int i = 0; i < kHeld; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.s_empty[i], 4);
+        }
+        mbar_init(&bar.done, 1);
+        fence_barrier_init();
+        abort_flag = 0;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    pdl_wait();
+    pdl_launch_dependents();
+    Line w = start_of_line(a, warp == 0, lane);
+    const uint32_t tmem = tmem_slot;
+    volatile int *abort = &abort_flag;
+    auto fail = [&] {
+        *abort = 1;
+        report_status(a.c.dev_status, KVD_ERR_TIMEOUT);
+    };
+    Stretch g;
+    bool ok = true;
+
+    if (warp == kSumWarps) {
+        // ------------------------------------------------------------ loads ---
+        const uint64_t policy = l2_policy_evict_first();
+        const int boxes = kTile / a.box, ps = a.c.page_size;
+        uint32_t chunk = 0, q = 0, asked = 0;  // chunks of key tiles, query tiles, loads of those
+        uint32_t loaded[kHeld] = {};         // times each place of keys was loaded
+#pragma unroll 1
+        while (ok && next_stretch(a, w, g)) {
+#pragma unroll 1
+            for (int j0 = g.j0; ok && g.row_tiles > 0 && j0 < g.j1; j0 += kHeld, ++chunk) {
+                Stretch h = g;
+                h.j0 = j0;
+                h.j1 = min(j0 + kHeld, g.j1);
+                if (chunk > 0 && !(ok = wait_for(&bar.keys_empty, (chunk - 1) & 1, abort))) break;
+                // the cache rows of the boxes, a lane a box
+                int row = a.dead_row;
+                const int t0 = j0 * kTile + lane * a.box;
+                if (t0 < h.j1 * kTile && t0 < g.s.len) {
+                    const int col = t0 / ps, page = checked_page(a.c, g.b, col);
+                    if (page >= 0)
+                        row = (page * a.c.n_kv_heads + g.head) * ps + (t0 - col * ps);
+                }
+                const int mine = lane / boxes;  // tile of the chunk, 4 x 8 boxes at most
+#pragma unroll
+                for (int t = 0; t < kHeld; ++t) {
+                    if (j0 + t >= h.j1) break;
+                    uint64_t *full = I8 ? &bar.key_raw[t] : &bar.key_full[t];
+                    if (lane == 0) mbar_arrive_expect_tx(full, I8 ? kTile * D : kTileBytes);
+                    ++loaded[t];
+                    __syncwarp();
+                    if (mine == t) {
+                        uint8_t *dst = keys + t * kTileBytes;
+                        const int at = lane % boxes * a.box;
+                        if constexpr (I8) {
+                            tma_load_2d(dst + kRaw + at * D, &k_map, 0, row, full, policy);
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < kChunks; ++c)
+                                tma_load_2d(dst + c * kChunkBytes + at * 128, &k_map, c * 64, row,
+                                            full, policy);
+                        }
+                    }
+                    __syncwarp();
+                }
+#pragma unroll 1
+                for (int i = 0; i < g.row_tiles; ++i) {
+                    const RowTile r = row_tile(a, h, i);
+                    if (r.ja == r.jb) continue;
+                    // the rows' statistics, on their way
+                    float l[kRowsAt / 32];
+#pragma unroll
+                    for (int x = 0; x < kRowsAt / 32; ++x) {
+                        const int at = x * 32 + lane, tok = at / a.heads;
+                        l[x] = -INFINITY;  // no row there: no weight
+                        if (tok < r.cnt)
+                            l[x] = a.lse[static_cast<int64_t>(g.s.s0 + r.i0 + tok) *
+                                             (a.c.n_kv_heads * a.G) +
+                                         g.head * a.G + at - tok * a.heads];
+                    }
+                    const uint32_t st = q % kQueryPlaces, round = q / kQueryPlaces;
+                    if (round > 0 && !(ok = wait_for(&bar.q_empty[st], (round - 1) & 1, abort))) break;
+                    ++asked;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.q_full[st], kChunks * a.heads * a.tokens * 128);
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c)
+                            tma_load_4d(queries + st * kTileBytes + c * kChunkBytes, &q_map, c * 64, 0,
+                                        g.head, g.s.s0 + r.i0, &bar.q_full[st]);
+                    }
+                    if (q >= kLseSlots &&
+                        !(ok = wait_for(&bar.lse_empty[q % kLseSlots], (q / kLseSlots - 1) & 1, abort)))
+                        break;
+#pragma unroll
+                    for (int x = 0; x < kRowsAt / 32; ++x)
+                        bases[q % kLseSlots][x * 32 + lane] = base_of(l[x]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.lse_full[q % kLseSlots]);
+                    ++q;
+                }
+            }
+        }
+        if (!ok) fail();
+        tmem_fence_before();
+        __syncthreads();  // all roles are done, and know whether a wait ran out
+        if (*abort) {
+            // nothing may land in shared memory after the CTA has gone
+            volatile int none = 0;
+            bool landed = true;  // after one wait that runs out all has had the time to land
+#pragma unroll
+            for (int t = 0; t < kHeld; ++t)
+                if (landed && loaded[t] > 0)
+                    landed = mbar_wait(I8 ? &bar.key_raw[t] : &bar.key_full[t], (loaded[t] - 1) & 1, &none);
+            for (uint32_t i = 0; landed && i < kQueryPlaces; ++i) {
+                const uint32_t fills = (asked + kQueryPlaces - 1 - i) / kQueryPlaces;
+                if (fills > 0) landed = mbar_wait(&bar.q_full[i], (fills - 1) & 1, &none);
+            }
+        }
+        return;
+    } else if (warp == kSumWarps + 1) {
+        // -------------------------------------------------- products S^T = K Q^T ---
+        constexpr uint32_t kIdS = mma_idesc(BF16, kTile, kRowsAt, false);
+        const uint32_t k_base = warp_uniform(desc_low(smem_addr(keys), 16));
+        const uint32_t q_base = warp_uniform(desc_low(smem_addr(queries), 16));
+        const uint32_t tmem_u = warp_uniform(tmem);
+        uint32_t q = 0, loaded[kHeld] = {}, used = 0;  // used: bits, of the tiles' logits
+#pragma unroll 1
+        while (ok && next_stretch(a, w, g)) {
+#pragma unroll 1
+            for (int j0 = g.j0; ok && g.row_tiles > 0 && j0 < g.j1; j0 += kHeld) {
+                Stretch h = g;
+                h.j0 = j0;
+                h.j1 = min(j0 + kHeld, g.j1);
+#pragma unroll
+                for (int t = 0; t < kHeld; ++t)
+                    if (ok && j0 + t < h.j1) ok = wait_for(&bar.key_full[t], loaded[t]++ & 1, abort);
+                if (!ok) break;
+#pragma unroll 1
+                for (int i = 0; ok && i < g.row_tiles; ++i) {
+                    const RowTile r = row_tile(a, h, i);
+                    if (r.ja == r.jb) continue;
+                    const uint32_t st = q % kQueryPlaces;
+                    if (!(ok = wait_for(&bar.q_full[st], (q / kQueryPlaces) & 1, abort))) break;
+                    ++q;
+                    const uint32_t qd = warp_uniform(q_base + st * (kTileBytes / 16));
+#pragma unroll 1
+                    for (int j = r.ja; j < r.jb; ++j) {
+                        const int t = j - j0;
+                        // (the first wait of a barrier's life ends at once)
+                        if (!(ok = wait_for(&bar.s_empty[t], ~(used >> t) & 1, abort))) break;
+                        used ^= 1u << t;
+                        tmem_fence_after();
+                        const uint32_t s_at = warp_uniform(tmem_u + t * kRowsAt);
+                        const uint32_t k = warp_uniform(k_base + t * (kTileBytes / 16));
+                        if (elect_one()) {
+#pragma unroll
+                            for (int x = 0; x < D / 16; ++x) {
+                                const uint32_t at = (x / 4 * kChunkBytes + x % 4 * 32) / 16;
+                                mma_ss(s_at, smem_desc(k + at), smem_desc(qd + at), kIdS, x > 0);
+                            }
+                            mma_commit(&bar.s_full[t]);
+                            if (j + 1 == r.jb) mma_commit(&bar.q_empty[st]);
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (elect_one()) mma_commit(&bar.keys_empty);
+                __syncwarp();
+            }
+        }
+        if (!ok) fail();
+        // every product and every barrier arrival is done before the CTA goes
+        if (elect_one()) mma_commit(&bar.done);
+        __syncwarp();
+        volatile int none = 0;
+        if (!mbar_wait(&bar.done, 0, &none)) fail();
+    } else if (I8 && warp > kSumWarps + 1) {
+        // ------------------------------------------------ int8 to f16 or bf16 ---
+        // In place: all four warps hold a tile's codes in registers before they write.
+        constexpr int kUnits = D / 16;
+        constexpr int kRows = 32 / kUnits * 4;  // rows of a step of the four warps
+        constexpr int kSteps = kTile / kRows;
+        const int q8 = lane >> 3, k8 = lane & 7;
+        const int row = (warp - kSumWarps - 2) * (32 / kUnits) +
+                        (D == 128 ? 2 * (q8 >> 1) + (k8 >> 2) : lane >> 2);
+        const int u = D == 128 ? (k8 & 3) + 4 * ((q8 & 1) ^ (k8 >> 2)) : lane & 3;
+        const int dst_row = (u / 4) * kChunkBytes + row * 128;
+        const int dst0 = dst_row + 16 * (((u % 4) * 2) ^ (row & 7));
+        const int dst1 = dst_row + 16 * (((u % 4) * 2 + 1) ^ (row & 7));
+        static_assert(kRows % 8 == 0, "the swizzle of a lane's row stays");
+        uint32_t loaded[kHeld] = {};
+#pragma unroll 1
+        while (next_stretch(a, w, g)) {
+#pragma unroll 1
+            for (int j0 = g.j0; g.row_tiles > 0 && j0 < g.j1; j0 += kHeld) {
+#pragma unroll
+                for (int t = 0; t < kHeld; ++t) {
+                    if (j0 + t >= g.j1) break;
+                    // (none of the four leaves before the others: they meet below)
+                    if (ok) ok = wait_for(&bar.key_raw[t], loaded[t] & 1, abort);
+                    ++loaded[t];
+                    uint8_t *tile = keys + t * kTileBytes;
+                    const uint8_t *src = tile + kRaw + row * D + 16 * u;
+                    uint4 v[kSteps];
+#pragma unroll
+                    for (int x = 0; x < kSteps; ++x)
+                        v[x] = *reinterpret_cast<const uint4 *>(src + x * (kRows * D));
+                    asm volatile("bar.sync 3, 128;" ::: "memory");
+#pragma unroll
+                    for (int x = 0; x < kSteps; ++x) {
+                        uint4 lo, hi;
+                        codes_to<BF16>(v[x].x, lo.x, lo.y);
+                        codes_to<BF16>(v[x].y, lo.z, lo.w);
+                        codes_to<BF16>(v[x].z, hi.x, hi.y);
+                        codes_to<BF16>(v[x].w, hi.z, hi.w);
+                        *reinterpret_cast<uint4 *>(tile + dst0 + x * (kRows * 128)) = lo;
+                        *reinterpret_cast<uint4 *>(tile + dst1 + x * (kRows * 128)) = hi;
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.key_full[t]);
+                }
+            }
+        }
+        if (!ok) fail();
+    } else if (warp < kSumWarps) {
+        // --------------------------------------------------------------- sums ---
+        const int team = warp >> 2, key = tid & 127;
+        const uint32_t s_at = tmem + ((warp & 3) << 21) + team * kRowsAt;
+        uint32_t n = 0, q = 0;  // this team's products, query tiles
+#pragma unroll 1
+        while (ok && next_stretch(a, w, g)) {
+            const size_t row = static_cast<size_t>(g.b) * a.c.n_kv_heads + g.head;
+            const int ps = a.c.page_size;
+#pragma unroll 1
+            for (int j0 = g.j0; ok && j0 < g.j1; j0 += kHeld) {
+                Stretch h = g;
+                h.j0 = j0;
+                h.j1 = min(j0 + kHeld, g.j1);
+                // this thread's key: what stands there, its scale, whether it counts
+                const int j = j0 + team, t = j * kTile + key;
+                const bool here = j < h.j1 && t < g.s.len;
+                float sum = 0.0f, ks = a.scale_log2;
+                bool some = false;
+                if (here) {
+                    const int page = a.c.page_table[static_cast<size_t>(g.b) * a.c.max_pages + t / ps];
+                    some = page >= 0 && page < a.c.n_pages;
+                    if (I8 && some)
+                        ks *= static_cast<const float *>(
+                            a.c.k_scale)[(static_cast<size_t>(page) * a.c.n_kv_heads + g.head) * ps +
+                                         t % ps];
+                    if (a.mass && t < g.s.first) sum = a.decay * a.mass[row * a.mass_stride + t];
+                }
+#pragma unroll 1
+                for (int i = 0; i < g.row_tiles; ++i) {
+                    const RowTile r = row_tile(a, h, i);
+                    if (r.ja == r.jb) continue;
+                    const uint32_t slot = q % kLseSlots;
+                    if (!(ok = wait_for(&bar.lse_full[slot], (q / kLseSlots) & 1, abort))) break;
+                    ++q;
+                    if (j >= r.ja && j < r.jb) {
+                        // the rows [r0, r1) that see this key
+                        int r0 = 0, r1 = 0;
+                        if (some && t >= r.lo && t < r.hi) {
+                            const int f = max(t - r.p0, 0);
+                            int l = r.cnt - 1;
+                            if (a.window > 0) l = min(l, t + a.window - 1 - r.p0);
+                            if (f <= l) {
+                                r0 = f * a.heads;
+                                r1 = (l + 1) * a.heads;
+                            }
+                        }
+                        if (!(ok = wait_for(&bar.s_full[team], n & 1, abort))) break;
+                        ++n;
+                        tmem_fence_after();
+                        sum += weights_of(s_at, bases[slot], kRowsAt, r0, r1, ks);
+                        tmem_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (j >= r.ja && j < r.jb) mbar_arrive(&bar.s_empty[team]);
+                        mbar_arrive(&bar.lse_empty[slot]);
+                    }
+                }
+                if (here) a.sums[row * a.sums_stride + t] = sum;
+            }
+        }
+        if (!ok) fail();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kSumWarps + 1) {
+        tmem_fence_after();
+        tmem_free(tmem, 512);
+    }
+}
+
+struct Maps {
+    CUtensorMap q, k;
+};
+
+// The arguments that both kernels take; row tiles of whole tokens of a group of heads, up to
+// `most` rows.
+bool fill(const MassArgs &m, int most, MassDev &a, Maps &maps) {
     const PagedAttnArgs &p = m.attn;
     const kvd_paged_cache &c = p.c;
-    MassDev a = {};
+    const bool i8 = c.dtype == KVD_INT8;
     a.c = c;
     a.G = p.G;
     a.n_tokens = p.n_tokens;
@@ -567,14 +924,34 @@ cudaError_t launch_type(const MassArgs &m, cudaStream_t st) {
     const int64_t pool = static_cast<int64_t>(c.n_pages) * c.n_kv_heads * c.page_size;
     a.dead_row = static_cast<int>(pool);
     a.chunks = (c.head_dim + 63) / 64;
-    // Row tiles: whole tokens of a group of heads
-    const int most = a.chunks <= 2 ? kMaxRows : 128;
     const int G = p.G > 0 ? p.G : 1;
     a.groups = (G + most - 1) / most;
     a.heads = (G + a.groups - 1) / a.groups;
     a.tokens = most / a.heads;
     if (a.tokens > p.max_new && p.max_new > 0) a.tokens = p.max_new;
     a.rows = (a.heads * a.tokens + 15) / 16 * 16;
+
+    const cuuint64_t W = static_cast<cuuint64_t>(c.head_dim);
+    const cuuint64_t kd[2] = {W, static_cast<cuuint64_t>(pool)};
+    const cuuint64_t ks[1] = {W * (i8 ? 1 : 2)};
+    const cuuint32_t kb[2] = {i8 ? static_cast<cuuint32_t>(W) : 64, static_cast<cuuint32_t>(a.box)};
+    if (!make_map(&maps.k, c.dtype, c.k, 2, kd, ks, kb,
+                  i8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
+        return false;
+    if (!p.starts) return true;
+    const cuuint64_t qd[4] = {W, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(c.n_kv_heads),
+                              static_cast<cuuint64_t>(p.n_tokens)};
+    const cuuint64_t qs[3] = {W * 2, W * 2 * G, static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(a.heads), 1,
+                              static_cast<cuuint32_t>(a.tokens)};
+    return make_map(&maps.q, p.bf16 ? KVD_BF16 : KVD_F16, p.q, 4, qd, qs, qb);
+}
+
+template <bool BF16, int I8>
+cudaError_t launch_type(const MassArgs &m, cudaStream_t st) {
+    MassDev a = {};
+    Maps maps = {};
+    if (!fill(m, m.attn.c.head_dim <= 128 ? kMaxRows : 128, a, maps)) return cudaErrorInvalidValue;
     a.per = a.chunks <= 2 ? a.chunks : 1;
     a.raws = I8 ? 4 : 0;
     const int q_bytes = a.chunks * a.rows * 128, place = a.per * kChunkBytes;
@@ -582,41 +959,47 @@ cudaError_t launch_type(const MassArgs &m, cudaStream_t st) {
     a.places = rest / place < kMaxPlaces ? rest / place : kMaxPlaces;
     if (I8 && a.places > 2) a.places = 2;
     const size_t smem = 1024 + q_bytes + static_cast<size_t>(a.places) * place + a.raws * kTile * I8;
-
-    CUtensorMap q_map = {}, k_map;
-    const cuuint64_t W = static_cast<cuuint64_t>(c.head_dim);
-    const cuuint64_t kd[2] = {W, static_cast<cuuint64_t>(pool)};
-    const cuuint64_t ks[1] = {W * (I8 ? 1 : 2)};
-    const cuuint32_t kb[2] = {I8 ? static_cast<cuuint32_t>(I8) : 64, static_cast<cuuint32_t>(a.box)};
-    if (!make_map(&k_map, c.dtype, c.k, 2, kd, ks, kb,
-                  I8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B))
-        return cudaErrorInvalidValue;
-    if (p.starts) {
-        const cuuint64_t qd[4] = {W, static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(c.n_kv_heads),
-                                  static_cast<cuuint64_t>(p.n_tokens)};
-        const cuuint64_t qs[3] = {W * 2, W * 2 * G, static_cast<cuuint64_t>(p.q_stride) * 2};
-        const cuuint32_t qb[4] = {64, static_cast<cuuint32_t>(a.heads), 1,
-                                  static_cast<cuuint32_t>(a.tokens)};
-        if (!make_map(&q_map, BF16 ? KVD_BF16 : KVD_F16, p.q, 4, qd, qs, qb))
-            return cudaErrorInvalidValue;
-    }
     auto *kernel = mass_kernel<BF16, I8>;
     constexpr int threads = I8 ? 448 : 320;
     cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads, smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(kernel, dim3(device_sm_count()), dim3(threads), smem, st, true, a, q_map, k_map);
+    return launch_ex(kernel, dim3(device_sm_count()), dim3(threads), smem, st, true, a, maps.q, maps.k);
+}
+
+template <bool BF16, int D, bool I8>
+cudaError_t launch_many(const MassArgs &m, cudaStream_t st) {
+    MassDev a = {};
+    Maps maps = {};
+    if (!fill(m, kRowsAt, a, maps)) return cudaErrorInvalidValue;
+    constexpr size_t smem = 1024 + (kHeld + kQueryPlaces) * static_cast<size_t>(D / 64 * kChunkBytes);
+    auto *kernel = mass_rows_kernel<BF16, D, I8>;
+    constexpr int threads = rows_threads(I8);
+    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(kernel), threads, smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(kernel, dim3(device_sm_count()), dim3(threads), smem, st, true, a, maps.q, maps.k);
+}
+
+template <bool BF16>
+cudaError_t launch_q(const MassArgs &m, cudaStream_t st) {
+    const kvd_paged_cache &c = m.attn.c;
+    // more rows than a tile that stays: the keys stay instead
+    const bool many = c.head_dim <= 128 && static_cast<int64_t>(m.attn.G) * m.attn.max_new > kMaxRows;
+    if (c.dtype == KVD_INT8) {
+        if (c.head_dim == 64)
+            return many ? launch_many<BF16, 64, true>(m, st) : launch_type<BF16, 64>(m, st);
+        return many ? launch_many<BF16, 128, true>(m, st) : launch_type<BF16, 128>(m, st);
+    }
+    if (!many) return launch_type<BF16, 0>(m, st);
+    return c.head_dim == 64 ? launch_many<BF16, 64, false>(m, st)
+                            : launch_many<BF16, 128, false>(m, st);
 }
 
 }  // namespace
 
 cudaError_t launch_mass(const MassArgs &a, cudaStream_t st) {
-    const kvd_paged_cache &c = a.attn.c;
-    if (c.dtype == KVD_INT8) {
-        if (c.head_dim == 64)
-            return a.attn.bf16 ? launch_type<true, 64>(a, st) : launch_type<false, 64>(a, st);
-        return a.attn.bf16 ? launch_type<true, 128>(a, st) : launch_type<false, 128>(a, st);
-    }
-    return c.dtype == KVD_BF16 ? launch_type<true, 0>(a, st) : launch_type<false, 0>(a, st);
+    // (without queries the type of the keys' products is any)
+    const bool bf16 = a.attn.c.dtype == KVD_BF16 || a.attn.bf16;
+    return bf16 ? launch_q<true>(a, st) : launch_q<false>(a, st);
 }
 
 }  // namespace kvd

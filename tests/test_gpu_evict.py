@@ -393,3 +393,13 @@ def test_mass_and_evict_in_a_graph_and_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(k2, kept) and torch.equal(m2[:, :, :400], mass[:, :, :400])
+
+
+@pytest.mark.parametrize("dtype", [kvd.F16, kvd.BF16, kvd.INT8])
+@pytest.mark.parametrize("H,Hkv,D,page,window", [(8, 2, 128, 16, 0), (14, 2, 64, 64, 200), (16, 1, 128, 128, 0),
+                                                 (3, 3, 64, 32, 0), (32, 2, 128, 64, 129)])
+def test_mass_of_many_rows(dtype, H, Hkv, D, page, window):
+    """More rows than stay in shared memory: chunks of key tiles, rows that see some of them."""
+    new, lens = [700, 1, 0, 400, 90], [2100, 900, 300, 400, 1500]
+    c = _paged(dtype, lens, Hkv, D, page, 4)
+    _check(c, _q(sum(new) + 2, H, D, X[dtype], 5), new, window=window)
