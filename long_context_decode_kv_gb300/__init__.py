@@ -763,29 +763,15 @@ class LatentCache:
         return int(self.t["status"].item())
 
 
-def _row(t: torch.Tensor, d: int, name: str):
-    """kvd_heads of rows [n_tokens, d], one head each."""
-    x = _X.get(t.dtype)
-    if x is None or t.dim() != 2 or t.shape[1] != d:
-        raise ValueError(f"{name} is [n_tokens, {d}] of float16, bfloat16 or float32")
-    if t.stride(1) != 1 and d != 1:
-        raise ValueError("the channels of a token must be dense")
-    return HeadsStruct(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else d, x, 1)
-
-
-def _parts(t: Optional[torch.Tensor]):
-    """kvd_head_parts of [n_tokens, n_heads, channels]; token and head strides are free."""
-    if t is None:
-        return None
-    x = _X.get(t.dtype)
-    if x is None or t.dim() != 3:
-        raise ValueError("head parts are [n_tokens, n_heads, channels] of float16, bfloat16 or float32")
+def _part_strides(t: torch.Tensor, name: str):
+    """Token and head strides of head parts [n_tokens, n_heads, channels], and the two counts."""
     n, h, d = t.shape
     s0, s1, s2 = t.stride()
     if s2 != 1:
-        raise ValueError("the channels of a head must be dense")
-    s1 = s1 if h > 1 else d
-    return PartsStruct(t.data_ptr(), s0 if n > 1 else h * s1, s1, x, h)
+        raise ValueError(f"the channels of a head of {name} must be dense")
+    if h == 1:
+        s1 = d
+    return n, h, (s0 if n > 1 else h * s1), s1
 
 
 def latent_append(cache: LatentCache, c: torch.Tensor, k_pe: torch.Tensor, starts: torch.Tensor,
@@ -796,24 +782,39 @@ def latent_append(cache: LatentCache, c: torch.Tensor, k_pe: torch.Tensor, start
     shared key parts k_pe [T, rope_dim] (rotated) to sequence b's last positions.  q_pe
     [T, H, rope_dim], rotated too, goes to the last channels of q_out [T, H, rank + rope_dim],
     whose others (the absorbed part) are not touched."""
-    T, R, P = c.shape[0], cache.rank, cache.rope_dim
-    if k_pe.dim() != 2 or k_pe.shape[0] != T:
-        raise ValueError("c and k_pe are [n_tokens, rank] and [n_tokens, rope_dim]")
-    to = None
+    T, R = c.shape
+    n, P = k_pe.shape
+    x = _X.get(c.dtype)
+    if R != cache.rank or P != cache.rope_dim or n != T or x is None or k_pe.dtype != c.dtype:
+        raise ValueError("c and k_pe are [n_tokens, rank] and [n_tokens, rope_dim] of one type: "
+                         "float16, bfloat16 or float32")
+    c0, c1 = c.stride()
+    k0, k1 = k_pe.stride()
+    if c1 != 1 or k1 != 1:
+        raise ValueError("the channels of a token must be dense")
+    q = to = None
     if q_pe is not None:
-        if q_out is None or q_pe.dim() != 3 or tuple(q_pe.shape[::2]) != (T, P) or \
-                tuple(q_out.shape) != (T, q_pe.shape[1], R + P):
+        if q_out is None or q_pe.dim() != 3 or q_out.dim() != 3:
+            raise ValueError("q_pe and q_out are given together, [n_tokens, n_heads, ..]")
+        n, h, q0, q1 = _part_strides(q_pe, "q_pe")
+        m, k, o0, o1 = _part_strides(q_out, "q_out")
+        y = _X.get(q_out.dtype)
+        if n != T or m != T or k != h or q_pe.shape[2] != P or q_out.shape[2] != R + P or \
+                q_pe.dtype != c.dtype or y is None:
             raise ValueError("q_pe is [n_tokens, n_heads, rope_dim], q_out [n_tokens, n_heads, "
                              "rank + rope_dim]")
-        to = q_out[:, :, R:]
+        q = PartsStruct(q_pe.data_ptr(), q0, q1, x, h)
+        to = PartsStruct(q_out.data_ptr() + R * (4 if y == 2 else 2), o0, o1, y, h)
     elif q_out is not None:
         raise ValueError("q_pe and q_out are given together")
     d = c.get_device()
     _one_device(d, cache.t["rows"], k_pe, starts, c_weight, q_pe, q_out,
                 None if rope is None else rope.freqs)
-    _call("kvd_latent_append", d, stream, lib().kvd_latent_append, cache.s, _row(c, R, "c"),
-          _row(k_pe, P, "k_pe"), T, _int32(starts, cache.batch + 1, "starts"),
-          None if rope is None else rope.s, _weight(c_weight, R), _parts(q_pe), _parts(to), eps)
+    _call("kvd_latent_append", d, stream, lib().kvd_latent_append, cache.s,
+          HeadsStruct(c.data_ptr(), c0 if T > 1 else R, x, 1),
+          HeadsStruct(k_pe.data_ptr(), k0 if T > 1 else P, x, 1), T,
+          _int32(starts, cache.batch + 1, "starts"), None if rope is None else rope.s,
+          _weight(c_weight, R), q, to, eps)
 
 
 def latent_workspace_bytes(cache: LatentCache, n_heads: int, n_tokens: int, max_new: int) -> int:
@@ -887,7 +888,8 @@ def paged_mass(cache, q: torch.Tensor, lse: torch.Tensor, starts: torch.Tensor, 
     to, to_stride = _mass(out, cache.batch, heads, cache.len, "out")
     d = q.get_device()
     _one_device(d, cache.t["page_table"], starts, lse, mass, out)
-    _call(f"kvd_{kind}_mass", d, stream, getattr(lib(), f"kvd_{kind}_mass"), cache.s, _heads(q),
+    name = "kvd_latent_mass" if kind == "latent" else "kvd_paged_mass"
+    _call(name, d, stream, getattr(lib(), name), cache.s, _heads(q),
           _lse(lse, T, H), T, _int32(starts, cache.batch + 1, "starts"), max_new, softmax_scale,
           window, at, stride, decay, to, to_stride)
 
@@ -912,7 +914,8 @@ def paged_evict(cache, mass: torch.Tensor, keep: int, page_table_out: torch.Tens
     to, to_stride = _mass(mass_out, cache.batch, heads, keep, "mass_out")
     d = mass.get_device()
     _one_device(d, cache.t["page_table"], page_table_out, kept, seq_lens_out, mass_out)
-    _call(f"kvd_{kind}_evict", d, stream, getattr(lib(), f"kvd_{kind}_evict"), cache.s, at, stride,
+    name = "kvd_latent_evict" if kind == "latent" else "kvd_paged_evict"
+    _call(name, d, stream, getattr(lib(), name), cache.s, at, stride,
           keep, sink, recent, _ptr(page_table_out), page_table_out.shape[1], _ptr(kept),
           _int32(seq_lens_out, cache.batch, "seq_lens_out"), to, to_stride)
 

@@ -65,7 +65,7 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
     const int t0 = min(lo + rank * slice, hi), count = min(slice, hi - t0);
     const bool fits = slice <= room;
     if (need > 0 && fits)
-#pragma unroll 4
+#pragma unroll 16
         for (int i = tid; i < count; i += kThreads) cached[i] = weight_key(mass[t0 + i]);
     // those that stay whatever they weigh
     for (int t = rank * kThreads + tid; t < lo; t += blocks * kThreads) put(t, t, mass[t]);
@@ -79,7 +79,7 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-#pragma unroll 4
+#pragma unroll 8
         for (int i = tid; i < count; i += kThreads) {
             const uint32_t k = key_of(i);
             if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
@@ -179,7 +179,9 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
         const int my_eq = eq + __popc(eqs & below);
         if (is_gt || (is_eq && my_eq < need)) {
             const int t = t0 + i + lane;
-            put(a.sink + gt + __popc(gts & below) + min(my_eq, need), t, mass[t]);
+            // (0: it was NaN)
+            put(a.sink + gt + __popc(gts & below) + min(my_eq, need), t,
+                k == 0 ? mass[t] : key_to_float(k));
         }
         gt += __popc(gts);
         eq += __popc(eqs);
@@ -303,15 +305,22 @@ cudaError_t launch_move(const EvictArgs &a, int rows, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictArgs &a, cudaStream_t st) {
-    // blocks a (sequence, head): up to 8, each with 2048 tokens at least
-    int blocks = 1;
-    while (blocks < kMaxCluster && a.c.len > blocks * 2048) blocks *= 2;
+    // Blocks a (sequence, head): as many as give each 1024 tokens and are all resident at
+    // once.
     const int rows = a.c.batch * a.c.n_kv_heads;
-    const int slice = ((a.c.len + blocks - 1) / blocks + kThreads - 1) / kThreads * kThreads;
-    const int room = slice < kCached ? slice : kCached;
-    const size_t smem = room * sizeof(uint32_t);
-    cudaError_t e = prepare_kernel(reinterpret_cast<const void *>(choose_kernel), kThreads, smem);
-    if (e != cudaSuccess) return e;
+    int blocks = kMaxCluster, room = 0, occ = 1;
+    size_t smem = 0;
+    cudaError_t e;
+    for (;; blocks /= 2) {
+        const int slice = ((a.c.len + blocks - 1) / blocks + kThreads - 1) / kThreads * kThreads;
+        room = slice < kCached ? slice : kCached;
+        smem = room * sizeof(uint32_t);
+        e = prepare_kernel(reinterpret_cast<const void *>(choose_kernel), kThreads, smem, &occ);
+        if (e != cudaSuccess) return e;
+        if (blocks == 1 || (a.c.len > 1024 * (blocks / 2) &&
+                            static_cast<int64_t>(rows) * blocks <= static_cast<int64_t>(occ) * device_sm_count()))
+            break;
+    }
     e = launch_cluster(choose_kernel, dim3(rows * blocks), dim3(kThreads), blocks, smem, st, a, blocks,
                        room);
     if (e != cudaSuccess) return e;
