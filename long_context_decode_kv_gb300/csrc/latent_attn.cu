@@ -14,10 +14,12 @@
 // of 16: 64 x 64 32, 128 x 64 48 (shared memory's rate; 128 x 128 64): 1920 for 64 rows
 // and 64 keys of 576 channels, 1.35 PFLOP/s at most.
 //
-// One CTA per SM, persistent.  An item is a run of a sequence's new tokens and a group of
-// heads, together up to 64 rows, over the key tiles that any of them sees.  All items' key
-// tiles form one line, cut into equal costs for the CTAs; an item that a cut divides is
-// joined from f32 partials by join_kernel.
+// One CTA per SM, persistent.  An item is a run of a sequence's new tokens, with its heads
+// up to 64 rows, over the key tiles that any of them sees.  All items' key tiles form one
+// line, cut into equal costs for the CTAs; an item that a cut divides is joined from f32
+// partials by join_kernel.  More than 64 heads are so many groups, and the CTAs teams of one
+// a group, which walk the same piece of the line at the same time: a key tile comes from
+// HBM once, and from the L2 for the others.
 //
 // Roles: warps 0-3 and 4-7 softmax of the rows' first and second half, a thread 2 keys and
 // an eighth of the rows (the layout of 16 x 256-bit reads from tensor memory, of which
@@ -79,10 +81,10 @@ __device__ __forceinline__ Item item_of(const LatentDev &a, const Seq &s, int ti
     return it;
 }
 
-// A CTA's walk along the line of items, the same in every role.  The line counts an item
-// as kItemCost units and then its tiles.
+// A CTA's walk along the line of items, the same in every role and in every CTA of a team.
+// The line counts an item as kItemCost units and then its tiles.
 struct Walk {
-    int b, tile, group;
+    int b, tile;
     int off;    // units of the item that lie before
     int k;      // segments taken
     long left;  // units
@@ -90,7 +92,7 @@ struct Walk {
 };
 struct Segment {
     Item it;
-    int b, s0, p0, group;
+    int b, s0, p0;
     int j0, j1;         // key tiles
     bool starts, ends;  // whether it holds its item's first and last tile
     int k;
@@ -105,7 +107,6 @@ __device__ __forceinline__ bool next_segment(const LatentDev &a, Walk &w, Segmen
     g.b = w.b;
     g.s0 = w.s.s0;
     g.p0 = w.s.first + g.it.i0;
-    g.group = w.group;
     g.j0 = g.it.j0 + max(w.off - kItemCost, 0);
     g.j1 = g.it.j0 + w.off + take - kItemCost;
     g.starts = w.off <= kItemCost;
@@ -113,8 +114,7 @@ __device__ __forceinline__ bool next_segment(const LatentDev &a, Walk &w, Segmen
     g.k = w.k++;
     w.left -= take;
     w.off = 0;
-    if (w.left > 0 && ++w.group == a.groups) {
-        w.group = 0;
+    if (w.left > 0) {
         if ((w.tile + 1) * a.tokens < w.s.n) {
             ++w.tile;
         } else {
@@ -261,7 +261,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
     pdl_launch_dependents();
 
     // ---- this CTA's piece of the line of items
-    // of a group of heads of a sequence: a warp's lanes take a run of tokens each
+    // of a sequence: a warp's lanes take a run of tokens each
     auto units_of = [&](const Seq &s) -> long {
         long n = 0;
 #pragma unroll 1
@@ -285,7 +285,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             const long u = units_of(seq_of(a, b - lane + l, false));
             if (lane == l) n = u;
         }
-        return n * a.groups;
+        return n;
     };
     auto scan = [&](long cost, long &before) -> long {  // exclusive prefix, and the sum
         long v = cost;
@@ -313,7 +313,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             if (lane == 0) sm.seq_units[b] = n;
         }
         __syncthreads();
-        cost = tid < a.c.batch ? sm.seq_units[tid] * a.groups : 0;
+        cost = tid < a.c.batch ? sm.seq_units[tid] : 0;
     } else {
         cost = cost_of(tid, blockIdx.x == 0);
     }
@@ -324,12 +324,14 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         long skip;
         total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
     }
-    const long per = max((total + gridDim.x - 1) / gridDim.x, static_cast<long>(a.min_tiles));
-    const long ctas = max(min(static_cast<long>(gridDim.x), (total + per - 1) / per), 1l);
-    const long share = total / ctas, spare = total % ctas;
-    auto cut = [&](long c) { return c * share + min(c, spare); };  // where CTA c begins
-    const long x0 = blockIdx.x < ctas ? cut(blockIdx.x) : total;
-    const long x1 = blockIdx.x < ctas ? cut(blockIdx.x + 1) : total;
+    const int group = blockIdx.x % a.groups, team = blockIdx.x / a.groups;
+    const long most = gridDim.x / a.groups;
+    const long per = max((total + most - 1) / most, static_cast<long>(a.min_tiles));
+    const long teams = max(min(most, (total + per - 1) / per), 1l);
+    const long share = total / teams, spare = total % teams;
+    auto cut = [&](long c) { return c * share + min(c, spare); };  // where team c begins
+    const long x0 = team < teams ? cut(team) : total;
+    const long x1 = team < teams ? cut(team + 1) : total;
     if (x0 < x1) {
         long base = 0;
 #pragma unroll 1
@@ -346,7 +348,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             }
         }
         __syncthreads();
-        if (warp == 0) {  // the run of tokens, 32 at a time; its groups follow one another
+        if (warp == 0) {  // the run of tokens, 32 at a time
             Walk w;
             w.b = sm.found_seq;
             w.s = seq_of(a, w.b, false);
@@ -354,8 +356,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 #pragma unroll 1
             for (int t0 = 0;; t0 += 32) {
                 const int t = t0 + lane;
-                const int one = t * a.tokens < w.s.n ? item_of(a, w.s, t).tiles + kItemCost : 0;
-                const long n = static_cast<long>(one) * a.groups;
+                const int n = t * a.tokens < w.s.n ? item_of(a, w.s, t).tiles + kItemCost : 0;
                 long upto = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -365,11 +366,8 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 const uint32_t in = __ballot_sync(0xffffffffu, r < upto);
                 if (in || t0 * a.tokens >= w.s.n) {
                     const int l = in ? __ffs(in) - 1 : 0;
-                    const long rest = r - __shfl_sync(0xffffffffu, upto - n, l);
-                    const int unit = max(__shfl_sync(0xffffffffu, one, l), 1);
                     w.tile = t0 + l;
-                    w.group = static_cast<int>(rest / unit);
-                    w.off = static_cast<int>(rest - static_cast<long>(w.group) * unit);
+                    w.off = static_cast<int>(r - __shfl_sync(0xffffffffu, upto - n, l));
                     break;
                 }
                 r -= __shfl_sync(0xffffffffu, upto, 31);
@@ -420,7 +418,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             }
             if (first_warp && lane <= 2 * a.tops)
                 tma_load_4d(q_smem + lane * kQChunk, &q_map, lane == 0 ? a.tops * 128 : (lane - 1) * 64,
-                            g.group * a.heads, 0, g.s0 + g.it.i0, &sm.q_full);
+                            group * a.heads, 0, g.s0 + g.it.i0, &sm.q_full);
             // the cache rows of the boxes of tiles j, j + 1, .., a lane a box: dead_row
             // where none is needed, -1 on a bad page
             auto rows_of = [&](int j) -> int {
@@ -488,12 +486,12 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 }
             }
             if (ok && g.starts && !g.ends) {
-                // the item goes on in the next CTAs: leave word for join_kernel
+                // the item goes on in the next teams: leave word for join_kernel
                 const long rest = g.it.j0 + g.it.tiles - g.j1;  // tiles, and units
                 int pieces = 1;
-                while (cut(blockIdx.x + pieces + 1) - x1 < rest) ++pieces;
+                while (cut(team + pieces + 1) - x1 < rest) ++pieces;
                 rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
-                rec1 = make_int4(g.group, 0, 0, 0);
+                rec1 = make_int4(group, 0, 0, 0);
             }
         }
         if (!ok) fail();
@@ -637,7 +635,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         };
 #pragma unroll 1
         while (next_segment(a, w, g)) {
-            const int heads = min(a.heads, a.G - g.group * a.heads);
+            const int heads = min(a.heads, a.G - group * a.heads);
             // keys that every row sees
             const int all_lo = a.window > 0 ? max(g.p0 + g.it.cnt - a.window, 0) : 0;
             const int all_hi = max(g.p0 + 1, 0);
@@ -803,7 +801,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 const float sum = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
                 const float m = sm.m[tid];
                 sm.f[tid] = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-                const int h = g.group * a.heads + my_head;
+                const int h = group * a.heads + my_head;
                 sm.row_at[tid] = live ? my_tok << 16 | h : -1;
                 if (live) {
                     if (!whole)
@@ -862,8 +860,8 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 }
 
 // Joins the items that a cut between CTAs divided: the rows of all such items stand in one
-// line (record c: the item whose first piece is CTA c's last segment and goes on in the
-// CTAs after it).
+// line (record c: the item whose first piece is CTA c's last segment and goes on in its
+// group's CTA of the teams after it).
 //   out = sum_i 2^(m_i - m) acc_i / sum_i 2^(m_i - m) l_i
 // A warp takes PARTS times 128 channels of a row, the reads of AT pieces under way together.
 constexpr int kMaxCtas = 256;
@@ -884,8 +882,10 @@ __device__ __forceinline__ void join_rows(const LatentDev &a, const int *before,
         const int group = a.join[2 * c + 1].x;
         const int tok = r / a.heads, h = group * a.heads + r - tok * a.heads;
         if (h >= a.G) continue;
-        // piece i is at slot 2 c + 2 i, the first maybe one on
-        auto slot_of = [&](int i) { return static_cast<size_t>(2 * (c + i) + (i == 0 ? rec.y : 0)); };
+        // piece i is CTA c + i * groups's first segment, the first piece maybe its second
+        auto slot_of = [&](int i) {
+            return static_cast<size_t>(2 * (c + i * a.groups) + (i == 0 ? rec.y : 0));
+        };
         float m = -INFINITY, l = 0.0f;
         for (int i = lane; i < rec.x; i += 32) m = fmaxf(m, a.ml[slot_of(i) * NR + r].x);
 #pragma unroll
