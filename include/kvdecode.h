@@ -720,8 +720,8 @@ KVD_API kvd_status kvd_latent_append(const kvd_latent_cache *cache, const kvd_he
 /*   starts, max_new, window, workspace (kvd_latent_workspace_bytes): as for */
 /*   kvd_paged_attn; this workspace needs no zeros. */
 /* n_tokens == 0 or max_new == 0 is a no-op. */
-/* Errors: INVALID; UNSUPPORTED (rank, rope_dim, page_size, the cache's counts, more */
-/* than 2^31 - 1 row tiles times key tiles); WORKSPACE; CUDA. */
+/* Errors: INVALID; UNSUPPORTED (rank, rope_dim, page_size, the cache's counts, n_heads); */
+/* WORKSPACE; CUDA. */
 /* ---------------------------------------------------------------------- */
 KVD_API kvd_status kvd_latent_attn(const kvd_latent_cache *cache, const kvd_heads *q,
                                    int32_t n_tokens, const int32_t *starts, int32_t max_new,

@@ -26,13 +26,6 @@ kvd_status check_parts(const kvd_head_parts *h, int channels) {
     return KVD_OK;
 }
 
-// Row tiles times key tiles, as the attention's line counts them, in 31 bits.
-bool too_long(const kvd_latent_cache *c, int n_heads, int n_tokens) {
-    return static_cast<__int128>(c->batch + static_cast<int64_t>(n_tokens)) *
-               ((n_heads + 63) / 64) * (c->len / 64 + 8) >
-           (static_cast<__int128>(1) << 62);
-}
-
 }  // namespace
 }  // namespace kvd
 
@@ -103,7 +96,7 @@ kvd_status kvd_latent_attn(const kvd_latent_cache *cache, const kvd_heads *q, in
     if (q->n_heads != out->n_heads || q->dtype != out->dtype || q->x == out->x)
         return KVD_ERR_INVALID;
     if (q->dtype != (cache->dtype == KVD_BF16 ? KVD_X_BF16 : KVD_X_F16)) return KVD_ERR_INVALID;
-    if (q->n_heads > kMaxHeads || too_long(cache, q->n_heads, n_tokens)) return KVD_ERR_UNSUPPORTED;
+    if (q->n_heads > kMaxHeads) return KVD_ERR_UNSUPPORTED;
     if (!std::isfinite(softmax_scale) || !(softmax_scale > 0.0f)) return KVD_ERR_INVALID;
     if (!starts || !aligned(starts, 4) || (lse && !aligned(lse, 16))) return KVD_ERR_INVALID;
     if (!workspace || !aligned(workspace, 256) ||

@@ -23,9 +23,11 @@
 //
 // Roles: warps 0-3 and 4-7 softmax of the rows' first and second half, a thread 2 keys and
 // an eighth of the rows (the layout of 16 x 256-bit reads from tensor memory, of which
-// 64-lane products fill 16 lanes a warp); warp 8 issues S^T, warp 9 O^T, warps 10-12 load by
-// TMA (a copy's issue takes a warp some 100 clocks, and pages of 16 tokens take 36 of them a
-// tile).  A key tile's places are released
+// 64-lane products fill 16 lanes a warp); warp 8 issues S^T, warp 9 O^T, warps 10 and 11
+// load by TMA (a copy's issue takes a warp some 100 clocks, and pages of 16 tokens take 36 of
+// them a tile; with one, two and three warps 24 ragged sequences took 111, 96 and 96 us, 4 x
+// 100,000 tokens 87, 86 and 90).  Asking the L2 for the tiles that follow made the calls
+// that HBM bounds slower: 94 us 2 tiles ahead, 101 us 6 ahead.  A key tile's places are released
 // 128 channels at a time, as O^T is done with them.
 //
 // The reference m of a row's weights 2^(logit - m) follows its maximum loosely, from kLift
@@ -44,7 +46,7 @@ constexpr int kPair = 2 * kHalf;       // 128 channels
 constexpr int kMaxRing = 8;            // tiles in shared memory
 constexpr int kMaxTops = 4;            // 128-channel parts of the latent vector
 constexpr int kLogits = 4;             // tiles' logits in tensor memory
-constexpr int kLoaders = 3;            // loading warps
+constexpr int kLoaders = 2;            // loading warps
 constexpr int kThreads = 32 * (10 + kLoaders);
 constexpr float kLift = 6.0f;          // a new reference: so far below the row's maximum
 constexpr float kRedo = 32768.0f;      // a weight above it asks for one
