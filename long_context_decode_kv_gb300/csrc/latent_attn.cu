@@ -151,7 +151,10 @@ __device__ __forceinline__ void tmem_ld_rows(uint32_t addr, float (&v)[N / 2]) {
                   "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
                 : "r"(addr + 2 * i));
     }
-    tmem_wait_ld();
+}
+// After tmem_wait_ld: no use of the loaded values moves above this point.
+template <int N>
+__device__ __forceinline__ void pin_rows(float (&v)[N / 2]) {
 #pragma unroll
     for (int i = 0; i < N / 2; i += 4)
         asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]));
@@ -648,11 +651,9 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
             bool open = true;  // a row has seen no key yet, and so has no reference
 #pragma unroll 1
             for (int j = g.j0; j < g.j1; ++j, ++n) {
-                const uint32_t b = n & 1;
                 const uint32_t s_at = lanes + n % kLogits * NR + half * (NR / 2);
                 wait(&sm.s_full[n % kLogits], (n / kLogits) & 1);
-                tmem_fence_after();
-                const uint32_t bad = sm.dead_groups[n & 15] >> quarter & 1;
+                const bool bad = sm.dead_groups[n & 15] >> quarter & 1;
                 // the rows [r0, r1) that see each of the two keys
                 int r0[2] = {0, 0}, r1[2] = {NR, NR};
                 const bool edge = j * kKeys < all_lo || (j + 1) * kKeys > all_hi || bad;
@@ -672,18 +673,23 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                         }
                     }
                 }
+                tmem_fence_after();
+                auto hidden = [&](int i) {
+                    const int r = i / 4 * 8 + col0 + (i & 1), e = i >> 1 & 1;
+                    return r < r0[e] || r >= r1[e];
+                };
                 bool fix = open;
                 float p[kV];
 #pragma unroll 1
                 for (;;) {
                     float s[kV];
                     tmem_ld_rows<NR / 2>(s_at, s);
+                    tmem_wait_ld();
+                    pin_rows<NR / 2>(s);
                     if (edge)
 #pragma unroll
-                        for (int i = 0; i < kV; ++i) {
-                            const int r = i / 4 * 8 + col0 + (i & 1), e = i >> 1 & 1;
-                            if (r < r0[e] || r >= r1[e]) s[i] = -INFINITY;
-                        }
+                        for (int i = 0; i < kV; ++i)
+                            if (hidden(i)) s[i] = -INFINITY;
                     if (fix) {
                         // each row's maximum, over the warp's keys, then over all
 #pragma unroll
@@ -697,7 +703,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                                 if (lane < 4) sm.red[quarter][i / 4 * 8 + col0 + e] = t;
                             }
                         // O as it stands is complete
-                        if (j > g.j0) wait(&sm.o_done[b ^ 1], ((n - 1) >> 1) & 1);
+                        if (j > g.j0) wait(&sm.o_done[(n - 1) & 1], ((n - 1) >> 1) & 1);
                         meet();
                         bool none = false;
                         if (tid < NR) {
@@ -740,18 +746,17 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                             *reinterpret_cast<const float2 *>(&sm.base[i / 4 * 8 + col0]);
 #pragma unroll
                         for (int e = 0; e < 4; e += 2) {
-                            const float2 u = __ffma2_rn(make_float2(s[i + e], s[i + e + 1]), k2, base);
-                            p[i + e] = exp2_approx(u.x);
-                            p[i + e + 1] = exp2_approx(u.y);
-                            top = fmax3(top, p[i + e], p[i + e + 1]);
+                            const float2 x = __ffma2_rn(make_float2(s[i + e], s[i + e + 1]), k2, base);
+                            p[i + e] = exp2_approx(x.x);
+                            p[i + e + 1] = exp2_approx(x.y);
                         }
                     }
                     if (edge)  // (a row without a reference yet, or -infinity less infinity)
 #pragma unroll
-                        for (int i = 0; i < kV; ++i) {
-                            const int r = i / 4 * 8 + col0 + (i & 1), e = i >> 1 & 1;
-                            if (r < r0[e] || r >= r1[e]) p[i] = 0.0f;
-                        }
+                        for (int i = 0; i < kV; ++i)
+                            if (hidden(i)) p[i] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kV; i += 2) top = fmax3(top, p[i], p[i + 1]);
                     if (fix) break;  // no weight passes 2^kLift
                     if (!any_says(top > kRedo)) break;
                     fix = true;
@@ -771,7 +776,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                                     make_uint4(0, 0, 0, 0);
                 }
                 // the weights, and P^T: a key's rows in 128 swizzled bytes
-                uint8_t *dst = p_smem + (Sh::kP == 2 ? b * kHalf : 0) + key0 * 128 + (lane & 3) * 4;
+                uint8_t *dst = p_smem + (Sh::kP == 2 ? (n & 1) * kHalf : 0) + key0 * 128 + (lane & 3) * 4;
 #pragma unroll
                 for (int i = 0; i < kV; i += 4) {
                     l[i / 2] += p[i] + p[i + 2];
