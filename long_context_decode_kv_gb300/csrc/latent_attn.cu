@@ -62,7 +62,7 @@ struct LatentDev : AttnArgs {
     int ring;                   // tiles in shared memory
     float *acc;                 // partial outputs [2 * CTAs][NR][R]
     float2 *ml;                 // their references and sums [2 * CTAs][NR]
-    int4 *join;                 // [CTAs][2]: what join_kernel joins
+    int4 *join;                 // [CTAs]: what join_kernel joins
 };
 
 // ---------------------------------------------------------------- items ---
@@ -310,88 +310,119 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         __syncthreads();
         return sum;
     };
-    long before = 0, cost;
-    if (a.c.batch <= kFewSeqs) {
+    // unit r of sequence b's: the run of tokens, 32 at a time
+    auto walk_from = [&](int b, long r) -> Walk {
+        Walk w;
+        w.b = b;
+        w.s = seq_of(a, b, false);
 #pragma unroll 1
-        for (int b = warp; b < a.c.batch; b += kThreads / 32) {
-            const long n = units_of(seq_of(a, b, blockIdx.x == 0));
-            if (lane == 0) sm.seq_units[b] = n;
+        for (int t0 = 0;; t0 += 32) {
+            const int t = t0 + lane;
+            const int n = t * a.tokens < w.s.n ? item_of(a, w.s, t).tiles + kItemCost : 0;
+            long upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long u = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const uint32_t in = __ballot_sync(0xffffffffu, r < upto);
+            if (in || t0 * a.tokens >= w.s.n) {
+                const int l = in ? __ffs(in) - 1 : 0;
+                w.tile = t0 + l;
+                w.off = static_cast<int>(r - __shfl_sync(0xffffffffu, upto - n, l));
+                break;
+            }
+            r -= __shfl_sync(0xffffffffu, upto, 31);
         }
-        __syncthreads();
-        cost = tid < a.c.batch ? sm.seq_units[tid] : 0;
-    } else {
-        cost = cost_of(tid, blockIdx.x == 0);
-    }
-    long total = scan(cost, before);
-    const bool one_pass = a.c.batch <= kThreads;
-#pragma unroll 1
-    for (int b0 = kThreads; b0 < a.c.batch; b0 += kThreads) {
-        long skip;
-        total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
-    }
+        w.k = 0;
+        return w;
+    };
     const int group = blockIdx.x % a.groups, team = blockIdx.x / a.groups;
     const long most = gridDim.x / a.groups;
-    const long per = max((total + most - 1) / most, static_cast<long>(a.min_tiles));
-    const long teams = max(min(most, (total + per - 1) / per), 1l);
-    const long share = total / teams, spare = total % teams;
+    long total = 0, share = 0, spare = 0, x0 = 0, x1 = 0;
     auto cut = [&](long c) { return c * share + min(c, spare); };  // where team c begins
-    const long x0 = team < teams ? cut(team) : total;
-    const long x1 = team < teams ? cut(team + 1) : total;
-    if (x0 < x1) {
-        long base = 0;
+    auto cut_line = [&] {  // this team's piece [x0, x1)
+        const long per = max((total + most - 1) / most, static_cast<long>(a.min_tiles));
+        const long teams = max(min(most, (total + per - 1) / per), 1l);
+        share = total / teams;
+        spare = total % teams;
+        x0 = team < teams ? cut(team) : total;
+        x1 = team < teams ? cut(team + 1) : total;
+    };
+    Walk w;
+    w.left = 0;
+    if (a.c.batch <= 32 && a.max_new <= kAlone * a.tokens) {
+        // short: each warp finds it by itself, a lane a sequence
+        const long cost = cost_of(lane, blockIdx.x == 0 && warp == 0);
+        long upto = cost;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long u = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += u;
+        }
+        total = __shfl_sync(0xffffffffu, upto, 31);
+        cut_line();
+        if (x0 < x1) {
+            const uint32_t in =
+                __ballot_sync(0xffffffffu, upto - cost <= x0 && x0 < upto);
+            const int l = __ffs(in) - 1;
+            w = walk_from(l, x0 - __shfl_sync(0xffffffffu, upto - cost, l));
+            w.left = x1 - x0;
+        }
+    } else {
+        long before = 0, cost;
+        if (a.c.batch <= kFewSeqs) {
 #pragma unroll 1
-        for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
-            if (!one_pass) {
-                cost = cost_of(b0 + tid, false);
-                const long sum = scan(cost, before);
-                before += base;
-                base += sum;
+            for (int b = warp; b < a.c.batch; b += kThreads / 32) {
+                const long n = units_of(seq_of(a, b, blockIdx.x == 0));
+                if (lane == 0) sm.seq_units[b] = n;
             }
-            if (before <= x0 && x0 < before + cost) {
-                sm.found_seq = b0 + tid;
-                sm.found_rest = x0 - before;
+            __syncthreads();
+            cost = tid < a.c.batch ? sm.seq_units[tid] : 0;
+        } else {
+            cost = cost_of(tid, blockIdx.x == 0);
+        }
+        total = scan(cost, before);
+        const bool one_pass = a.c.batch <= kThreads;
+#pragma unroll 1
+        for (int b0 = kThreads; b0 < a.c.batch; b0 += kThreads) {
+            long skip;
+            total += scan(cost_of(b0 + tid, blockIdx.x == 0), skip);
+        }
+        cut_line();
+        if (x0 < x1) {
+            long base = 0;
+#pragma unroll 1
+            for (int b0 = 0; b0 < a.c.batch; b0 += kThreads) {
+                if (!one_pass) {
+                    cost = cost_of(b0 + tid, false);
+                    const long sum = scan(cost, before);
+                    before += base;
+                    base += sum;
+                }
+                if (before <= x0 && x0 < before + cost) {
+                    sm.found_seq = b0 + tid;
+                    sm.found_rest = x0 - before;
+                }
+            }
+            __syncthreads();
+            if (warp == 0) {  // the run of tokens, 32 at a time
+                Walk w = walk_from(sm.found_seq, sm.found_rest);
+                w.left = x1 - x0;
+                if (lane == 0) sm.start = w;
             }
         }
         __syncthreads();
-        if (warp == 0) {  // the run of tokens, 32 at a time
-            Walk w;
-            w.b = sm.found_seq;
-            w.s = seq_of(a, w.b, false);
-            long r = sm.found_rest;
-#pragma unroll 1
-            for (int t0 = 0;; t0 += 32) {
-                const int t = t0 + lane;
-                const int n = t * a.tokens < w.s.n ? item_of(a, w.s, t).tiles + kItemCost : 0;
-                long upto = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const long u = __shfl_up_sync(0xffffffffu, upto, o);
-                    if (lane >= o) upto += u;
-                }
-                const uint32_t in = __ballot_sync(0xffffffffu, r < upto);
-                if (in || t0 * a.tokens >= w.s.n) {
-                    const int l = in ? __ffs(in) - 1 : 0;
-                    w.tile = t0 + l;
-                    w.off = static_cast<int>(r - __shfl_sync(0xffffffffu, upto - n, l));
-                    break;
-                }
-                r -= __shfl_sync(0xffffffffu, upto, 31);
-            }
-            w.left = x1 - x0;
-            w.k = 0;
-            if (lane == 0) sm.start = w;
-        }
+        w = sm.start;
+        __syncthreads();  // `start` has been read: its memory is the softmax's
     }
-    __syncthreads();
     const uint32_t tmem = sm.tmem_slot;
-    Walk w = sm.start;
     Segment g;
     volatile int *abort = &sm.abort_flag;
     auto fail = [&] {
         *abort = 1;
         report_status(a.c.dev_status, KVD_ERR_TIMEOUT);
     };
-    __syncthreads();  // `start` has been read: its memory is the softmax's
     bool ok = true;
 
     if (warp >= 10) {
@@ -411,7 +442,7 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
         const int my_at = part == 0 ? a.tops * kPair : (part - 1) * kPair;
         uint32_t n = 0, mine = 0, queries = 0;  // tiles, this lane's loads of them, of queries
         uint32_t st = 0, round = 0;
-        int4 rec0 = make_int4(0, 0, 0, 0), rec1 = make_int4(0, 0, 0, 0);
+        int4 rec = make_int4(0, 0, 0, 0);
 #pragma unroll 1
         while (ok && next_segment(a, w, g)) {
             if (first_warp) {
@@ -495,14 +526,12 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 const long rest = g.it.j0 + g.it.tiles - g.j1;  // tiles, and units
                 int pieces = 1;
                 while (cut(team + pieces + 1) - x1 < rest) ++pieces;
-                rec0 = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
-                rec1 = make_int4(group, 0, 0, 0);
+                rec = make_int4(pieces + 1, g.k == 0 ? 0 : 1, g.s0 + g.it.i0, g.it.cnt);
             }
         }
         if (!ok) fail();
         if (first_warp && lane == 0) {
-            a.join[2 * blockIdx.x] = rec0;
-            a.join[2 * blockIdx.x + 1] = rec1;
+            a.join[blockIdx.x] = rec;
         }
         tmem_fence_before();
         __syncthreads();  // all roles are done, and know whether a wait ran out
@@ -874,8 +903,8 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
 constexpr int kMaxCtas = 256;
 constexpr int kJoinThreads = 128;
 template <bool BF16, int NR, int PARTS, int AT>
-__device__ __forceinline__ void join_rows(const LatentDev &a, const int *before, int w, int warps,
-                                          int lane) {
+__device__ __forceinline__ void join_rows(const LatentDev &a, const int *before, const int4 *recs, int w,
+                                          int warps, int lane) {
     const int R = a.tops * 128, units = PARTS == 1 ? a.tops : 1;
 #pragma unroll 1
     for (; w < before[kMaxCtas] * units; w += warps) {
@@ -885,14 +914,25 @@ __device__ __forceinline__ void join_rows(const LatentDev &a, const int *before,
         for (int step = kMaxCtas / 2; step > 0; step >>= 1)
             if (before[c + step] <= u) c += step;
         const int r = u - before[c];
-        const int4 rec = a.join[2 * c];
-        const int group = a.join[2 * c + 1].x;
+        const int4 rec = recs[c];  // pieces, whether the first is its CTA's second segment, token, tokens
+        const int group = c % a.groups;
         const int tok = r / a.heads, h = group * a.heads + r - tok * a.heads;
         if (h >= a.G) continue;
         // piece i is CTA c + i * groups's first segment, the first piece maybe its second
         auto slot_of = [&](int i) {
             return static_cast<size_t>(2 * (c + i * a.groups) + (i == 0 ? rec.y : 0));
         };
+        const float *acc = a.acc + static_cast<size_t>(r) * R + part * 128 + lane * 4;
+        float4 v[AT][PARTS];
+        auto read = [&](int i0, int n) {  // pieces i0 .. i0 + n, AT at most
+#pragma unroll
+            for (int x = 0; x < AT; ++x)
+#pragma unroll
+                for (int p = 0; p < PARTS; ++p)
+                    if (x < n && (PARTS == 1 || p < a.tops))
+                        v[x][p] = *reinterpret_cast<const float4 *>(acc + slot_of(i0 + x) * NR * R + 128 * p);
+        };
+        read(0, rec.x);  // (beside the references)
         float m = -INFINITY, l = 0.0f;
         for (int i = lane; i < rec.x; i += 32) m = fmaxf(m, a.ml[slot_of(i) * NR + r].x);
 #pragma unroll
@@ -900,7 +940,6 @@ __device__ __forceinline__ void join_rows(const LatentDev &a, const int *before,
         float4 o[PARTS];
 #pragma unroll
         for (int p = 0; p < PARTS; ++p) o[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float *acc = a.acc + static_cast<size_t>(r) * R + part * 128 + lane * 4;
 #pragma unroll 1
         for (int i0 = 0; i0 < rec.x; i0 += 32) {
             float f = 0.0f;  // of piece i0 + lane
@@ -912,14 +951,7 @@ __device__ __forceinline__ void join_rows(const LatentDev &a, const int *before,
             const int n = min(32, rec.x - i0);
 #pragma unroll 1
             for (int i = 0; i < n; i += AT) {
-                float4 v[AT][PARTS];
-#pragma unroll
-                for (int x = 0; x < AT; ++x)
-#pragma unroll
-                    for (int p = 0; p < PARTS; ++p)
-                        if (i + x < n && (PARTS == 1 || p < a.tops))
-                            v[x][p] = *reinterpret_cast<const float4 *>(
-                                acc + slot_of(i0 + i + x) * NR * R + 128 * p);
+                if (i0 + i > 0) read(i0 + i, n - i);
 #pragma unroll
                 for (int x = 0; x < AT; ++x) {
                     const float g = __shfl_sync(0xffffffffu, f, (i + x) & 31);
@@ -952,6 +984,7 @@ __device__ __forceinline__ void join_rows(const LatentDev &a, const int *before,
 template <bool BF16, int NR>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ LatentDev a, int ctas) {
     __shared__ int before[kMaxCtas + 1];  // rows of the records before
+    __shared__ int4 recs[kMaxCtas];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_launch_dependents();
@@ -962,7 +995,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
         for (int i = 0; i < kEach; ++i) {
             const int c = lane * kEach + i;
             int4 rec = make_int4(0, 0, 0, 0);
-            if (c < ctas) rec = a.join[2 * c];
+            if (c < ctas) rec = a.join[c];
+            recs[c] = rec;
             n[i] = rec.x ? rec.w * a.heads : 0;
         }
 #pragma unroll
@@ -986,9 +1020,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     const int warps = gridDim.x * (kJoinThreads / 32);
     const int w = blockIdx.x * (kJoinThreads / 32) + warp;
     if (before[kMaxCtas] * a.tops <= warps)
-        join_rows<BF16, NR, 1, 8>(a, before, w, warps, lane);
+        join_rows<BF16, NR, 1, 8>(a, before, recs, w, warps, lane);
     else
-        join_rows<BF16, NR, kMaxTops, 3>(a, before, w, warps, lane);
+        join_rows<BF16, NR, kMaxTops, 3>(a, before, recs, w, warps, lane);
 }
 
 // ----------------------------------------------------------------- launch ---
@@ -1006,7 +1040,7 @@ Plan plan_of(int H, int rank, int max_new) {
     const int rows = w.heads * w.tokens;
     w.nr = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    w.ml = up(static_cast<size_t>(w.ctas) * 2 * sizeof(int4));
+    w.ml = up(static_cast<size_t>(w.ctas) * sizeof(int4));
     // (of any max_new: 64 rows)
     w.acc = w.ml + up(static_cast<size_t>(w.ctas) * 2 * 64 * sizeof(float2));
     w.total = w.acc + up(static_cast<size_t>(w.ctas) * 2 * w.nr * rank * sizeof(float));
