@@ -160,22 +160,6 @@ __device__ __forceinline__ void pin_rows(float (&v)[N / 2]) {
         asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]));
 }
 
-// wait_for where each lane (of those that take part) has its own barrier.
-__device__ __forceinline__ bool wait_lanes(bool mine, uint64_t *bar, uint32_t parity,
-                                           volatile int *abort) {
-    uint32_t n = 0, t0 = 0;
-#pragma unroll 1
-    while (!__all_sync(0xffffffffu, !mine || mbar_try_wait(bar, parity))) {
-        if ((++n & 63u) == 0) {
-            const uint32_t t = static_cast<uint32_t>(global_timer_ns());
-            if (n == 64) t0 = t;
-            if (__any_sync(0xffffffffu, *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs)))
-                return false;
-        }
-    }
-    return true;
-}
-
 // Barriers of the 256 softmax threads; the second tells whether any said yes.
 __device__ __forceinline__ void meet() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 __device__ __forceinline__ bool any_says(bool mine) {
@@ -484,36 +468,21 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 }
                 if (first_warp && lane == 0) sm.dead_groups[n & 15] = bad;
                 __syncwarp();
-                // each part as soon as its place is free
-                uint64_t *full = &sm.full[st][my_part], *empty = &sm.empty[st][my_part];
+                // each part as soon as its place is free (a fresh barrier's is)
+                uint64_t *full = &sm.full[st][my_part];
                 uint8_t *dst = ring + st * tile_bytes + my_at;
-                bool todo = loads;
-                uint32_t tries = 0, t0 = 0;
-#pragma unroll 1
-                while (__any_sync(0xffffffffu, todo)) {
-                    if (todo && (round == 0 || mbar_try_wait(empty, (round - 1) & 1))) {
-                        mbar_arrive_expect_tx(full, part == 0 ? kHalf : kPair);
+                ok = each_when(loads, &sm.empty[st][my_part], ~round & 1, abort, [&] {
+                    mbar_arrive_expect_tx(full, part == 0 ? kHalf : kPair);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (x < boxes) {
-                                tma_load_2d(dst + x * a.box * 128, &k_map, my_x, row[x], full, policy);
-                                if (part > 0)
-                                    tma_load_2d(dst + kHalf + x * a.box * 128, &k_map, my_x + 64,
-                                                row[x], full, policy);
-                            }
-                        todo = false;
-                        ++mine;
-                    }
-                    if ((++tries & 63u) == 0) {
-                        const uint32_t t = static_cast<uint32_t>(global_timer_ns());
-                        if (tries == 64) t0 = t;
-                        if (__any_sync(0xffffffffu,
-                                       *abort || t - t0 > static_cast<uint32_t>(kWaitLimitNs))) {
-                            ok = false;
-                            break;
+                    for (int x = 0; x < 4; ++x)
+                        if (x < boxes) {
+                            tma_load_2d(dst + x * a.box * 128, &k_map, my_x, row[x], full, policy);
+                            if (part > 0)
+                                tma_load_2d(dst + kHalf + x * a.box * 128, &k_map, my_x + 64, row[x],
+                                            full, policy);
                         }
-                    }
-                }
+                    ++mine;
+                });
                 if (!ok) break;
                 ++n;
                 if (++st == static_cast<uint32_t>(a.ring)) {
@@ -620,8 +589,8 @@ latent_kernel(const __grid_constant__ LatentDev a, const __grid_constant__ CUten
                 const uint32_t b = n & 1;
                 if (!(ok = wait_for(&sm.p_full[n % kLogits], (n / kLogits) & 1, abort))) break;
                 // (they have landed: the logits come from them)
-                if (!(ok = wait_lanes(lane > 0 && lane < parts, &sm.full[st][min(lane, a.tops)],
-                                      round & 1, abort)))
+                if (!(ok = each_when(lane > 0 && lane < parts, &sm.full[st][min(lane, a.tops)],
+                                     round & 1, abort, [] {})))
                     break;
                 tmem_fence_after();
                 const uint32_t p = warp_uniform(
@@ -1066,7 +1035,7 @@ cudaError_t launch_rows(const PagedAttnArgs &p, int rank, const Plan &w, void *w
     while (a.box < kKeys && c.page_size % (2 * a.box) == 0) a.box *= 2;
     const int64_t pool = static_cast<int64_t>(c.n_pages) * c.page_size;
     a.dead_row = static_cast<int>(pool);
-    a.min_tiles = kItemCost + 2;  // an item's first CTA takes a tile
+    a.min_tiles = kItemCost + 1;  // an item's first CTA takes a tile
     a.tops = rank / 128;
     a.rope_steps = (c.head_dim - rank) / 16;
     a.heads = w.heads;

@@ -57,6 +57,28 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
+// The wait of lanes with a barrier each: those that take part (`mine`) do f() as soon as
+// their own barrier's phase has completed, whichever comes first.
+template <typename F>
+__device__ __forceinline__ bool each_when(bool mine, uint64_t *bar, uint32_t parity,
+                                          volatile int *abort, F f,
+                                          uint32_t limit_ns = static_cast<uint32_t>(kWaitLimitNs)) {
+    uint32_t n = 0, t0 = 0;
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, mine)) {
+        if (mine && mbar_try_wait(bar, parity)) {
+            f();
+            mine = false;
+        }
+        if ((++n & 63u) == 0) {
+            const uint32_t t = static_cast<uint32_t>(global_timer_ns());
+            if (n == 64) t0 = t;
+            if (__any_sync(0xffffffffu, *abort || t - t0 > limit_ns)) return false;
+        }
+    }
+    return true;
+}
+
 // ------------------------------------------------------------ sequences ---
 struct Seq {
     int s0, n, len;  // first token, new tokens (at most max_new), length

@@ -403,3 +403,92 @@ def test_mass_of_many_rows(dtype, H, Hkv, D, page, window):
     new, lens = [700, 1, 0, 400, 90], [2100, 900, 300, 400, 1500]
     c = _paged(dtype, lens, Hkv, D, page, 4)
     _check(c, _q(sum(new) + 2, H, D, X[dtype], 5), new, window=window)
+
+
+def test_pools_above_32_bits():
+    """Key-value pages at the end of a pool of more than 2^32 bytes a side."""
+    page, D = 256, 128
+    n_pages = (1 << 32) // (page * 2 * D * 2) + 20
+    shape = (n_pages, 2, page, D)
+    k, v = (torch.empty(shape, dtype=torch.float16, device=DEV) for _ in range(2))
+    for i, x in enumerate((k, v)):
+        x[-16:].copy_(torch.randn(16, 2, page, D, generator=_gen(i), device=DEV))
+    table = (n_pages - 1 - torch.arange(12, device=DEV, dtype=torch.int32)).view(2, 6)
+    lens = [1500, 300]
+    c = kvd.PagedKVCache(kvd.F16, 2, n_pages, 2, page, 6, tensors={
+        "k": k, "v": v, "page_table": table, "seq_lens": torch.tensor(lens, dtype=torch.int32, device=DEV)})
+    c.len = 1500
+    _check(c, _q(2, 8, D, torch.float16, 4), [1, 1])
+    _check(c, _q(400, 8, D, torch.float16, 5), [300, 100])
+    mass = _masses(2, 2, 1500, 3)
+    to = (torch.arange(4, device=DEV, dtype=torch.int32) + n_pages - 16).view(2, 2)
+    kept = torch.empty(2, 2, 300, dtype=torch.int32, device=DEV)
+    new = torch.empty(2, dtype=torch.int32, device=DEV)
+    kvd.paged_evict(c, mass, 300, to, kept, new, sink=2, recent=8)
+    assert c.device_status() == 0
+    for x in (k, v):
+        for g in range(2):
+            rows = x[table[0].long(), g].flatten(0, 1)
+            assert torch.equal(x[to[0].long(), g].flatten(0, 1)[:300], rows[kept[0, g].long()])
+
+
+def test_evict_of_sequences_that_share_pages():
+    """Two sequences over the same first pages, and one table read twice by its heads: they keep what
+    their own weights say, and the shared pages stay as they were."""
+    lens = [200, 180]
+    c = _room(_paged, lens, 64, 16, kvd.BF16, lens, 2, 64, 16, 2)
+    c.page_table[1, :8] = c.page_table[0, :8]
+    _evict(c, _masses(2, 2, 200, 5), 64, 4, 16)
+
+
+def test_mass_of_a_nan_statistic_spoils_its_own_head_only():
+    c = _paged(kvd.F16, [300, 300], 2, 64, 16, 2)
+    q = _q(2, 8, 64, torch.float16, 3)
+    _, lse = _attend(c, q, [1, 1])
+    zero = torch.zeros(2, 2, 300, device=DEV)
+    want, out = zero.clone(), zero.clone()
+    kvd.paged_mass(c, q, lse, _starts([1, 1]), 1, 0.1, zero, out=want)
+    lse[1, 5] = math.nan
+    kvd.paged_mass(c, q, lse, _starts([1, 1]), 1, 0.1, zero, out=out)
+    assert out[1, 1].isnan().all()
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, 0], want[1, 0])
+
+
+def test_mass_of_an_empty_cache_and_of_lengths_out_of_range():
+    c = _paged(kvd.F16, [40, 50], 2, 64, 16, 2)
+    q = _q(2, 8, 64, torch.float16, 3)
+    _, lse = _attend(c, q, [1, 1])
+    mass = torch.ones(2, 2, 64, device=DEV)
+    c.seq_lens.zero_()
+    c.len = 0
+    kvd.paged_mass(c, q, lse, _starts([1, 1]), 1, 0.1, mass, decay=0.5)
+    assert torch.all(mass == 1.0)
+    c.t["status"].zero_()
+    c.seq_lens.copy_(torch.tensor([10 ** 6, -4]))
+    c.len = 50
+    kvd.paged_mass(c, q, lse, _starts([1, 1]), 1, 0.1, mass, decay=0.5)
+    assert c.device_status() == 1
+    assert torch.all(mass[1] == 1.0) and torch.all(mass[0, :, 50:] == 1.0) and torch.all(mass[0, :, :49] >= 0.5)
+    kept = torch.full((2, 2, 5), -9, dtype=torch.int32, device=DEV)
+    new = torch.full((2,), -9, dtype=torch.int32, device=DEV)
+    c.seq_lens.zero_()
+    c.len = 0
+    kvd.paged_evict(c, mass, 5, torch.zeros(2, 1, dtype=torch.int32, device=DEV), kept, new)
+    assert new.tolist() == [0, 0] and torch.all(kept == -9)
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_runs_longer_than_told(latent):
+    """More new tokens in a sequence than max_new: reported, and the first max_new are counted."""
+    if latent:
+        c, D, scale = _latent(kvd.BF16, [100, 400], 16, 2, 128, 32), 160, 0.1
+    else:
+        c, D, scale = _paged(kvd.BF16, [100, 400], 1, 64, 16, 2), 64, 0.1
+    q = _q(30, 4, D, torch.bfloat16, 3)
+    _, lse = _attend(c, q, [10, 20], 0, scale)
+    mass = torch.zeros(2, 1, 400, device=DEV)
+    kvd.paged_mass(c, q, lse, _starts([10, 20]), 12, scale, mass)
+    assert c.device_status() == 1
+    full = LR.attn(c, q, [0, 10, 30], [100, 400], scale, 0, 1.0, torch.zeros_like(mass))["mass"]
+    LR.assert_close(mass[0], (full[0][0], full[1][0]))
+    assert abs(float(mass[1].double().sum()) - 12 * 4) < 12 * 4 * 2 * D * 2.0 ** -23 * 64

@@ -346,3 +346,89 @@ def test_decode_steps_as_a_server_runs_them():
         want = LR.attn(c, q, [0, 1, 2], c.seq_lens.tolist(), 0.08)
         LR.assert_close(out, want["out"], f"step {step}")
     assert c.device_status() == 0
+
+
+def test_rows_before_the_first_sequence_and_runs_longer_than_told():
+    c = _cache(kvd.F16, [90, 300], 16, 2)
+    q = _q(40, 16, 576, torch.float16, 3)
+    starts = torch.tensor([3, 13, 33], dtype=torch.int32, device=DEV)
+    out = torch.full((40, 16, 512), 7.0, device=DEV, dtype=torch.float16)
+    lse = torch.full((40, 16), 7.0, device=DEV)
+    ws = kvd.make_latent_workspace(c, 16, 40, 20)
+    kvd.latent_attn(c, q, starts, 20, 0.07, out, ws, lse=lse)
+    assert c.device_status() == 0
+    want = LR.attn(c, q, starts.tolist(), [90, 300], 0.07)
+    LR.assert_close(out, want["out"])
+    LR.assert_close(lse, want["lse"])
+    rest = [0, 1, 2] + list(range(33, 40))
+    assert torch.all(out[rest] == 7.0) and torch.all(lse[rest] == 7.0)
+    out.fill_(7.0)
+    kvd.latent_attn(c, q, starts, 12, 0.07, out, ws)              # the second run has 20: 12 are served
+    assert c.device_status() == 1
+    LR.assert_close(out[:25], (want["out"][0][:25], want["out"][1][:25]))
+    assert torch.all(out[25:] == 7.0)
+
+
+def test_an_empty_cache():
+    c = _cache(kvd.BF16, [1, 1], 16, 2)
+    c.seq_lens.zero_()
+    c.len = 0
+    q = _q(2, 16, 576, torch.bfloat16, 3)
+    out, lse = _attend(c, q, [1, 1])
+    assert c.device_status() == 1                                # a token needs a length of one
+    assert torch.all(out == 0) and torch.all(lse == -math.inf)
+
+
+@pytest.mark.parametrize("H", [300, 1024])
+def test_many_heads(H):
+    c = _cache(kvd.BF16, [100, 700], 64, 2, 128, 16)
+    _check(c, _q(5, H, 144, torch.bfloat16, 3), [1, 4])
+
+
+def test_two_streams_at_once():
+    """Calls on two caches, each with its workspace, at the same time."""
+    caches = [_cache(kvd.F16, [9000, 500], 64, i) for i in (2, 3)]
+    qs = [_q(2, 64, 576, torch.float16, i) for i in (4, 5)]
+    want = [_attend(c, q, [1, 1]) for c, q in zip(caches, qs)]
+    ws = [kvd.make_latent_workspace(c, 64, 2, 1) for c in caches]
+    outs = [torch.empty_like(w[0]) for w in want]
+    starts = _starts([1, 1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, q, w, o, s in zip(caches, qs, ws, outs, streams):
+            kvd.latent_attn(c, q, starts, 1, 0.07, o, w, stream=s)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w[0])
+
+
+def test_offsets_above_32_bits():
+    """Pages at the end of a pool of more than 2^32 bytes (and 2^31 elements)."""
+    page, rank, P = 256, 512, 64
+    n_pages = (1 << 32) // (page * 576) + 40
+    rows = torch.empty(n_pages, page, rank + P, dtype=torch.bfloat16, device=DEV)
+    table = (n_pages - 1 - torch.arange(24, device=DEV, dtype=torch.int32)).view(2, 12)
+    lens = [2500, 300]
+    c = kvd.LatentCache(kvd.BF16, 2, n_pages, page, 12, tensors={
+        "rows": rows, "page_table": table, "seq_lens": torch.tensor(lens, dtype=torch.int32, device=DEV)})
+    c.len = 2500
+    rows[-24:].copy_(torch.randn(24, page, rank + P, generator=_gen(1), device=DEV))
+    lat, k = _q(2, 1, rank, torch.bfloat16, 2)[:, 0], _q(2, 1, P, torch.bfloat16, 3)[:, 0]
+    kvd.latent_append(c, lat, k, _starts([1, 1]))
+    for b, n in enumerate(lens):
+        assert torch.equal(rows[int(table[b, (n - 1) // page]), (n - 1) % page], torch.cat([lat[b], k[b]]))
+    q = _q(2, 16, 576, torch.bfloat16, 4)
+    _, lse = _check(c, q, [1, 1])
+    mass = torch.zeros(2, 1, 2500, device=DEV)
+    kvd.paged_mass(c, q, lse, _starts([1, 1]), 1, 0.07, mass)
+    want = LR.attn(c, q, [0, 1, 2], lens, 0.07, 0, 1.0, torch.zeros_like(mass))
+    LR.assert_close(mass, want["mass"])
+    to = (torch.arange(4, device=DEV, dtype=torch.int32) + n_pages - 30).view(2, 2)
+    kept = torch.empty(2, 1, 400, dtype=torch.int32, device=DEV)
+    new = torch.empty(2, dtype=torch.int32, device=DEV)
+    kvd.paged_evict(c, mass, 400, to, kept, new)
+    assert new.tolist() == [400, 300] and c.device_status() == 0
+    ids = kept[0, 0].long()
+    got = rows[to[0].long()].flatten(0, 1)[:400]
+    assert torch.equal(got, rows[table[0].long()].flatten(0, 1)[ids])
