@@ -1101,7 +1101,8 @@ attn_kernel(const __grid_constant__ Dev a, const __grid_constant__ CUtensorMap q
                 mine = some ? mine * inv : 0.0f;
                 other *= inv;
                 if (a.lse && live)
-                    *lse_at(a, g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0), g.head, row) = lse_of(m, l);
+                    *lse_at(a, g.s0 + g.it.i0 + (PAIR ? t * a.q_tokens : 0) + tok, g.head,
+                            row - tok * a.G) = lse_of(m, l);
             }
             if ((PAIR || t == 0) && live && !whole) a.ml[slot * a.ws_rows + prow] = make_float2(m, l);
             uint16_t *dst = a.out;
@@ -1228,7 +1229,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Dev 
             }
         }
         const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-        if (a.lse && c8 == 0) *lse_at(a, rec.z + prow / kTile * a.q_tokens, head, r) = lse_of(m, l);
+        if (a.lse && c8 == 0) *lse_at(a, rec.z + tok, head, r % a.G) = lse_of(m, l);
         *reinterpret_cast<uint4 *>(a.out + static_cast<int64_t>(rec.z + tok) * a.out_stride +
                                    static_cast<int64_t>(head * a.G + r % a.G) * D + 8 * c8) =
             make_uint4(pack2<BF16>(o[0] * inv, o[1] * inv), pack2<BF16>(o[2] * inv, o[3] * inv),

@@ -31,13 +31,14 @@ struct AttnArgs {  // of a launch
 };
 
 // A row's statistic from the reference m (base 2) and the sum l of its weights 2^(logit - m).
+// References stand below the row's maximum, so l is above 16 where it is not 0, and the
+// logarithm's 2 units of its last place are 2^-21 of the result's.
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return l > 0.0f || l != l ? (m + log2f(l)) * 0.69314718056f : -INFINITY;
+    return l > 0.0f || l != l ? (m + __log2f(l)) * 0.69314718056f : -INFINITY;
 }
-// Where it stands: row r (tokens' heads of one KV head) from token t0 on.
-__device__ __forceinline__ float *lse_at(const AttnArgs &a, int t0, int head, int r) {
-    const int tok = r / a.G;
-    return a.lse + static_cast<int64_t>(t0 + tok) * a.c.n_kv_heads * a.G + head * a.G + (r - tok * a.G);
+// Where it stands: token t, query head h of KV head `head`.
+__device__ __forceinline__ float *lse_at(const AttnArgs &a, int t, int head, int h) {
+    return a.lse + static_cast<int64_t>(t) * (a.c.n_kv_heads * a.G) + head * a.G + h;
 }
 
 // mbar_wait for the waits between the roles, in few instructions: the roles' hot

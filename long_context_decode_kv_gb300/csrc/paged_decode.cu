@@ -798,7 +798,8 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                     static_cast<uint16_t>(pack2<BF16>(x, 0.0f));
             };
             if (whole) {
-                if (a.lse && warp == 0 && lane < rows) *lse_at(a, g.s.s0, g.head, lane) = lse_of(m, sum);
+                if (a.lse && warp == 0 && lane < rows)
+                    *lse_at(a, g.s.s0 + lane / a.G, g.head, lane % a.G) = lse_of(m, sum);
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
                     const float f = __shfl_sync(0xffffffffu, inv, r);
@@ -853,7 +854,7 @@ decode_paged_kernel(const __grid_constant__ DecodeArgs a, const __grid_constant_
                                 den += __shfl_xor_sync(0xffffffffu, den, o);
                             if (lane == 0) {
                                 sums[0][r] = den > 0.0f || den != den ? 1.0f / den : 0.0f;
-                                if (a.lse) *lse_at(a, g.s.s0, g.head, r) = lse_of(top, den);
+                                if (a.lse) *lse_at(a, g.s.s0 + r / a.G, g.head, r % a.G) = lse_of(top, den);
                             }
                         }
                         meet_128();
