@@ -744,7 +744,7 @@ KVD_API size_t kvd_latent_workspace_bytes(const kvd_latent_cache *cache, int32_t
 /*   max_new, softmax_scale and window, whose lse it is; the new tokens begin at 0. */
 /*   What stands at or behind seq_lens[b], and a row whose lse is -infinity, count */
 /*   for nothing; the former is not written.  Keys on a bad page get no weight. */
-/*   A row whose lse is not finite otherwise spoils the weights that it adds to. */
+/*   A row whose lse is NaN spoils the weights that it adds to. */
 /*   Logits, weights and sums are f32, added in a fixed order: repeated calls give */
 /*   the same bits. */
 /*   q: [n_tokens, n_heads, head_dim] (latent: rank + rope_dim), the type that the */
@@ -756,9 +756,9 @@ KVD_API size_t kvd_latent_workspace_bytes(const kvd_latent_cache *cache, int32_t
 /*   n_tokens == 0 or max_new == 0: only the decay. */
 /* Errors: INVALID; UNSUPPORTED (as the attention calls); CUDA. */
 /* ---------------------------------------------------------------------- */
-KVD_API kvd_status kvd_paged_mass(const kvd_paged_cache *cache, const kvd_heads *q, const float *lse,
-                                  int32_t n_tokens, const int32_t *starts, int32_t max_new,
-                                  float softmax_scale, int32_t window, const float *mass,
+KVD_API kvd_status kvd_paged_mass(const kvd_paged_cache *cache, const kvd_heads *q,
+                                  const float *lse, int32_t n_tokens, const int32_t *starts,
+                                  int32_t max_new, float softmax_scale, int32_t window, const float *mass,
                                   int64_t mass_stride, float decay, float *out, int64_t out_stride,
                                   void *stream);
 KVD_API kvd_status kvd_latent_mass(const kvd_latent_cache *cache, const kvd_heads *q,

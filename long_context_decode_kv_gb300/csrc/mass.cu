@@ -261,7 +261,8 @@ mass_kernel(const __grid_constant__ MassDev a, const __grid_constant__ CUtensorM
 
     if (warp == 8) {
         // ------------------------------------------------------------ loads ---
-        const uint64_t policy = a.max_new > a.tokens ? l2_policy_evict_last() : l2_policy_evict_first();
+        const bool again = a.max_new > a.tokens || a.groups > 1;  // keys are read more than once
+        const uint64_t policy = again ? l2_policy_evict_last() : l2_policy_evict_first();
         const int boxes = kTile / a.box, ps = a.c.page_size;
         const int per_read = 32 / boxes;  // tiles whose rows one read of the page table gives
         uint32_t st = 0, round = 0, queries = 0;
