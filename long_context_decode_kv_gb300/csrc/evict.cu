@@ -2,20 +2,22 @@
 // (kvd_paged_evict, kvd_latent_evict): which ones stay, then their rows to other pages.
 //
 // choose_kernel, a cluster a (sequence, head): the n-th largest weight by its bits, 11, 11
-// and 10 at a time (a histogram of each block's slice in shared memory, summed over the
-// cluster through it), then the kept tokens in order, each warp counting its run of
-// tokens before it writes them.  The weights are read once, into shared memory, where a
-// slice fits it.
+// and 10 at a time until a bin's keys stay as one (a histogram of each block's slice in
+// shared memory, added up in the first block's), then the kept tokens in order, each warp
+// counting its run of tokens before it writes them.  The weights are read once, into shared
+// memory, where a slice fits it.
 //
-// Measured, 8 sequences of up to 65,536 int8 tokens and 8 heads cut to 16,384: choosing 30 us
-// (its time goes into the meetings of the cluster and the blocks between short passes; with
-// the keys read four at a time 36), moving 72 us (6.4 TB/s, 0.95 of what a copy reaches).  4096
-// tokens of 8 heads to 1024: 14.8 us.
+// Measured, 8 sequences of up to 65,536 int8 tokens and 8 heads cut to 16,384: 107 us, of
+// which moving takes 72 (6.4 TB/s, 0.95 of what a copy reaches) and choosing the rest, in
+// passes of 4 us with a meeting of the cluster each (with the keys read four at a time it
+// took 6 more).  4096 tokens of 8 heads to 1024: 13.6 us.
 //
 // move_kernel: a warp looks up 32 rows' places, a lane a row, and copies them 16 bytes a
 // lane, 8 loads in flight.  The rows go to other pages than they come from
 // (which other sequences may share), so no order between the copies matters.
 #include <cooperative_groups.h>
+
+#include <utility>
 
 #include "common.cuh"
 #include "internal.h"
@@ -43,7 +45,7 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
     __shared__ uint32_t hist[kBins];
     __shared__ __align__(16) uint32_t total[3][kBins];  // of the cluster, in its first block
     __shared__ int warp_sum[kWarps], warp_gt[kWarps], warp_eq[kWarps];
-    __shared__ int found_bin, found_above;
+    __shared__ int found_bin, found_above, found_count;
     __shared__ int block_gt[kMaxCluster], block_eq[kMaxCluster];  // in each block
     cg::cluster_group cluster = cg::this_cluster();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -51,6 +53,7 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
     const int row = static_cast<int>(blockIdx.x) / blocks;  // of a sequence and a head
     const int b = row / a.c.n_kv_heads;
     for (int i = tid; i < kBins; i += kThreads) hist[i] = total[0][i] = total[1][i] = total[2][i] = 0;
+    auto cleared = cluster.barrier_arrive();
     pdl_wait();
     pdl_launch_dependents();
     const int L = checked_len(a.c, b);
@@ -76,9 +79,10 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
     for (int t = rank * kThreads + tid; t < lo; t += blocks * kThreads) put(t, t, mass[t]);
     for (int t = hi + rank * kThreads + tid; t < L; t += blocks * kThreads)
         put(n - (L - t), t, mass[t]);
-    if (need <= 0) return;  // the same for the whole cluster
+    cluster.barrier_wait(std::move(cleared));  // the sums are clear, in the first block too
+    if (need <= 0) return;                     // the same for the whole cluster
     auto key_of = [&](int i) { return fits ? cached[i] : weight_key(mass[t0 + i]); };
-    cluster.sync();  // the sums are clear, in the first block too
+    if (fits) __syncthreads();
 
     uint32_t prefix = 0, mask = 0;  // the bits of the n-th largest found so far
 #pragma unroll 1
@@ -130,6 +134,7 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
             if (above < need && above + at[j] >= need) {
                 found_bin = bins - 1 - (tid * kEach + j);
                 found_above = above;
+                found_count = at[j];
             }
             above += at[j];
         }
@@ -137,6 +142,12 @@ choose_kernel(const __grid_constant__ EvictArgs a, int blocks, int room) {
         need -= found_above;
         prefix |= static_cast<uint32_t>(found_bin) << shift;
         mask |= static_cast<uint32_t>(bins - 1) << shift;
+        if (found_count == need && prefix > 0) {
+            // all with these bits stay: those above the largest key below them
+            --prefix;
+            need = 0;
+            break;
+        }
     }
     // Kept: keys above prefix, and the first `need` of those equal to it.
     const int run = slice / kWarps, i0 = warp * run, i1 = min(i0 + run, count);
