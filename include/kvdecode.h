@@ -629,7 +629,7 @@ KVD_API size_t kvd_paged_workspace_bytes(const kvd_paged_cache *cache, int32_t n
 /*   lse[t, h] = ln sum_s exp(softmax_scale * q . k_s)   over the keys the */
 /*   row sees, -infinity where it sees none; device f32 [n_tokens, n_heads]. */
 /*   Rows of no sequence are not written.  out is kvd_paged_attn's, bit for */
-/*   bit. */
+/*   bit.  n_tokens == 0 or max_new == 0 is a no-op, whatever lse is. */
 /* Errors: as kvd_paged_attn; INVALID also for lse NULL or misaligned. */
 /* ---------------------------------------------------------------------- */
 KVD_API kvd_status kvd_paged_attn_lse(const kvd_paged_cache *cache, const kvd_heads *q,

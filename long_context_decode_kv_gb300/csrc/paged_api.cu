@@ -326,7 +326,8 @@ kvd_status kvd_paged_attn_lse(const kvd_paged_cache *cache, const kvd_heads *q, 
                               const int32_t *starts, int32_t max_new, float softmax_scale,
                               int32_t window, const kvd_heads *out, float *lse, void *workspace,
                               size_t workspace_bytes, void *stream) {
-    if (!lse || !aligned(lse, 16)) return KVD_ERR_INVALID;
+    // (without rows the call is a no-op, and an empty lse may be NULL)
+    if (n_tokens != 0 && max_new != 0 && (!lse || !aligned(lse, 16))) return KVD_ERR_INVALID;
     return attn_call(cache, q, n_tokens, starts, max_new, softmax_scale, window, out, lse,
                      workspace, workspace_bytes, stream);
 }

@@ -492,3 +492,21 @@ def test_runs_longer_than_told(latent):
     full = LR.attn(c, q, [0, 10, 30], [100, 400], scale, 0, 1.0, torch.zeros_like(mass))["mass"]
     LR.assert_close(mass[0], (full[0][0], full[1][0]))
     assert abs(float(mass[1].double().sum()) - 12 * 4) < 12 * 4 * 2 * D * 2.0 ** -23 * 64
+
+
+@pytest.mark.parametrize("latent", [False, True])
+def test_a_batch_without_new_tokens(latent):
+    """Steps whose batch is empty: attention with statistics is a no-op, the weights only decay."""
+    c, D = (_latent(kvd.BF16, [100, 40], 16, 2, 128, 32), 160) if latent else \
+        (_paged(kvd.BF16, [100, 40], 2, 64, 16, 2), 64)
+    heads, V = LR.heads_of(c), 128 if latent else 64
+    q = torch.empty(0, 8, D, dtype=torch.bfloat16, device=DEV)
+    out, lse = torch.empty(0, 8, V, dtype=torch.bfloat16, device=DEV), torch.empty(0, 8, device=DEV)
+    make, attend = (kvd.make_latent_workspace, kvd.latent_attn) if latent else (kvd.make_paged_workspace, kvd.paged_attn)
+    ws = make(c, 8, 1, 1)
+    for max_new in (0, 1):
+        attend(c, q, _starts([0, 0]), max_new, 0.1, out, ws, lse=lse)
+        mass = torch.ones(2, heads, 100, device=DEV)
+        kvd.paged_mass(c, q, lse, _starts([0, 0]), max_new, 0.1, mass, decay=0.5)
+        assert torch.all(mass[0] == 0.5) and torch.all(mass[1, :, :40] == 0.5) and torch.all(mass[1, :, 40:] == 1.0)
+    assert c.device_status() == 0

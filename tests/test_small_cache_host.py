@@ -134,6 +134,18 @@ def test_paged_lse_refusals():
     assert f(C.byref(_c()), _h(n=32), 4, FAKE, 4, 0.1, 0, _h(FAR, n=32), FAKE, None, 0, None) == WORKSPACE
 
 
+def test_a_call_without_rows_is_a_no_op_with_statistics_too():
+    """An empty tensor's pointer is NULL: without rows no call asks for q, out, lse or a workspace."""
+    f, lse = kvd.lib().kvd_paged_attn, kvd.lib().kvd_paged_attn_lse
+    for n, new in ((0, 4), (4, 0), (0, 0)):
+        assert f(C.byref(_c()), None, n, None, new, 0.1, 0, None, None, 0, None) == OK
+        assert lse(C.byref(_c()), None, n, None, new, 0.1, 0, None, None, None, 0, None) == OK
+        assert kvd.lib().kvd_latent_attn(C.byref(_l()), None, n, None, new, 0.1, 0, None, None, None, 0, None) == OK
+    for n, new in ((0, -1), (-1, 0)):
+        assert lse(C.byref(_c()), None, n, None, new, 0.1, 0, None, None, None, 0, None) == INVALID
+    assert lse(C.byref(_c(B=0)), None, 0, None, 0, 0.1, 0, None, None, None, 0, None) == INVALID
+
+
 def test_mass_refusals():
     for c in (_l(), _c()):
         assert _mass(c, n=-1) == INVALID and _mass(c, new=-1) == INVALID and _mass(c, window=-1) == INVALID
