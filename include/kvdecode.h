@@ -785,9 +785,15 @@ KVD_API kvd_status kvd_latent_mass(const kvd_latent_cache *cache, const kvd_head
 /*   seq_lens itself. */
 /*   No page of page_table_out may be one that this call reads, or stand in it twice, */
 /*   among the entries that the kept rows need (wrong rows, no fault).  A caller goes */
-/*   on with the new table and lengths, and may then give the old pages back.  The keys */
-/*   keep the rotation of their old positions: later tokens' positions are no longer */
-/*   their places in the cache, so rotate them with kvd_qk_norm_rope and append without rope. */
+/*   on with the new table and lengths, and may then give the old pages back. */
+/*   The keys keep the rotation of their old positions: later tokens' positions are no */
+/*   longer their places in the cache.  So norm and rotate them with kvd_qk_norm_rope, at */
+/*   positions that the caller counts, and append without rope and key or query weights. */
+/*   Latent: k_pe so (one head), and the queries' rotated parts as n_tokens * n_heads rows */
+/*   of one head each, their heads' stride as the rows' and each token's position once a */
+/*   head (tokens have to lie n_heads such strides apart); c and c_weight as always. */
+/*   A window of the attention and mass calls counts places in the cache, not positions: */
+/*   after an eviction it is the last `window` tokens that stayed. */
 /*   Bad pages of either table are reported as INVALID to dev_status, and their rows are */
 /*   not moved. */
 /* Errors: INVALID (keep < 1, sink or recent < 0, sink + recent > keep, strides, too few */

@@ -510,3 +510,67 @@ def test_a_batch_without_new_tokens(latent):
         kvd.paged_mass(c, q, lse, _starts([0, 0]), max_new, 0.1, mass, decay=0.5)
         assert torch.all(mass[0] == 0.5) and torch.all(mass[1, :, :40] == 0.5) and torch.all(mass[1, :, 40:] == 1.0)
     assert c.device_status() == 0
+
+
+@pytest.mark.parametrize("kind", ["paged", "latent", "latent, dense queries"])
+def test_rotated_tokens_behind_an_eviction(kind):
+    """After an eviction a token's position is not its place: qk_norm_rope rotates by the position and the
+    append takes rows as they are.  The latent cache's parts of heads go through it as rows of one head."""
+    lens, keep, page, H, T, P = [300, 120], 96, 16, 6, 2, 32
+    latent = kind != "paged"
+    if latent:
+        c = _room(_latent, lens, keep + 16, page, kvd.BF16, lens, page, 2, 128, P)
+    else:
+        c = _room(_paged, lens, keep + 16, page, kvd.BF16, lens, 2, 64, page, 2)
+    heads = LR.heads_of(c)
+    to, _, new_lens, _ = _evict(c, _masses(2, heads, 300, 3), keep, 4, 16)
+    t = dict(c.t, page_table=to, seq_lens=new_lens)
+    if latent:
+        d = kvd.LatentCache(c.dtype, 2, c.n_pages, page, to.shape[1], rank=128, rope_dim=P, tensors=t)
+    else:
+        d = kvd.PagedKVCache(c.dtype, 2, c.n_pages, 2, page, to.shape[1], head_dim=64, tensors=t)
+    d.len = keep
+    f, m = R.freqs(P, 10000.0)
+    rope = kvd.rope_table(P)
+    g = _gen(9)
+    positions = torch.tensor(lens, dtype=torch.int32, device=DEV)       # of the next tokens, not their places
+    place = torch.arange(2, device=DEV)
+    for _ in range(3):
+        d.seq_lens += 1
+        d.len = d.len + 1
+        at = (d.seq_lens - 1).long()
+        ids, in_page = to[place, at // page].long(), at % page
+        w = torch.rand(128 if latent else 64, generator=g, device=DEV) + 0.5
+        if latent:
+            down = torch.randn(T, 128 + P, generator=g, device=DEV).bfloat16()
+            wide = torch.randn(T, H, 64 + P, generator=g, device=DEV).bfloat16()
+            q_pe = wide[:, :, 64:].contiguous() if kind != "latent" else wide[:, :, 64:]
+            q = torch.randn(T, H, 128 + P, generator=g, device=DEV).bfloat16()
+            absorbed = q[:, :, :128].clone()
+            k_rot = torch.empty(T, 1, P, device=DEV, dtype=torch.bfloat16)
+            kvd.qk_norm_rope(down[:, 128:][:, None], None, positions, rope, k_rot, None)
+            kvd.qk_norm_rope(q_pe.flatten(0, 1)[:, None], None, positions.repeat_interleave(H), rope,
+                             q[:, :, 128:].flatten(0, 1)[:, None], None)
+            assert torch.equal(q[:, :, :128], absorbed)
+            kvd.latent_append(d, down[:, :128], k_rot[:, 0], _starts([1, 1]), c_weight=w)
+            y, err = R.turned(q_pe, positions, f, m, False)
+            R.assert_within(q[:, :, 128:], y, R.rounding(y, err, q.dtype), "q")
+            y, err = R.turned(down[:, None, :128], positions, None, 1.0, False, w)
+            got = d.rows[ids, in_page]
+            R.assert_within(got[:, :128], y[:, 0], R.rounding(y, err, q.dtype)[:, 0], "latent")
+            y, err = R.turned(down[:, None, 128:], positions, f, m, False)
+            R.assert_within(got[:, 128:], y[:, 0], R.rounding(y, err, q.dtype)[:, 0], "key part")
+        else:
+            qkv = torch.randn(T, H + 4, 64, generator=g, device=DEV).bfloat16()
+            q, k, v = torch.empty_like(qkv[:, :H]), torch.empty_like(qkv[:, :2]), qkv[:, H + 2:]
+            kvd.qk_norm_rope(qkv[:, :H], qkv[:, H:H + 2], positions, rope, q, k, w, w)
+            kvd.paged_append(d, k, v, _starts([1, 1]))
+            y, err = R.turned(qkv[:, H:H + 2], positions, f, m, False, w)
+            R.assert_within(d.k[ids, :, in_page], y, R.rounding(y, err, q.dtype), "key")
+            assert torch.equal(d.v[ids, :, in_page], v)
+        out, lse = _attend(d, q, [1, 1], window=40)                      # the last 40 that stayed
+        want = LR.attn(d, q, [0, 1, 2], d.seq_lens.tolist(), 0.1, 40)
+        LR.assert_close(out, want["out"])
+        LR.assert_close(lse, want["lse"])
+        positions += 1
+    assert d.device_status() == 0
