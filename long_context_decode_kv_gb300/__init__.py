@@ -536,7 +536,9 @@ def rope_table(rot_dim: int, base: float = 10000.0, interleaved: bool = False,
     "linear", "ntk", "yarn" or "bands" (kvd_rope_scaling), with the context's
     stretch `factor`, the trained length orig_len and, for the last two, the
     turns in orig_len below which a channel is stretched in full (low) and above
-    which it is kept (high); 0 and 0 take the usual ones."""
+    which it is kept (high); 0 and 0 take the usual ones.  "yarn" multiplies cosines
+    and sines by 0.1 ln(factor) + 1 (t.mscale); for a model that puts its factor into
+    the softmax scale instead take RopeTable(t.freqs, t.rot_dim, t.interleaved, 1.0)."""
     if scaling not in SCALINGS:
         raise ValueError(f"scaling is one of {sorted(SCALINGS)}")
     words = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)

@@ -10,11 +10,15 @@
 // Measured, 8 sequences of up to 65,536 int8 tokens and 8 heads cut to 16,384: 107 us, of
 // which moving takes 72 (6.4 TB/s, 0.95 of what a copy reaches) and choosing the rest, in
 // passes of 4 us with a meeting of the cluster each (with the keys read four at a time it
-// took 6 more).  4096 tokens of 8 heads to 1024: 13.6 us.
+// took 6 more).  4096 tokens of 8 heads to 1024: 13.6 us.  One sequence of 1,048,576 of 8 int8
+// heads to 4096: 300 us, nearly all of it the choice (8 blocks a row, 64 in all, which read their
+// slices in every pass).
 //
 // move_kernel: a warp looks up 32 rows' places, a lane a row, and copies them 16 bytes a
 // lane, 8 loads in flight.  The rows go to other pages than they come from
-// (which other sequences may share), so no order between the copies matters.
+// (which other sequences may share), so no order between the copies matters.  Latent rows
+// (72 parts of 16 bytes at 576 channels, a lane's row and part counted on the way): 8 sequences
+// of 65,536 to 16,384 98 us with the choice, the moves at 4.3 TB/s.
 #include <cooperative_groups.h>
 
 #include <utility>
@@ -31,7 +35,13 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kCached = 16384;  // weights a block keeps in shared memory
+// Weights a block keeps in shared memory: as many as leave room for two blocks an SM (64 KB
+// beside 33 KB of histograms; a row's 4 or 8 blocks wait for one another between short passes, and
+// a second block fills the waits).  Longer slices are read again in each pass.  With the moves, 64
+// rows cut to a quarter: of 131,072 weights 295 us (8192 weights a block 349, 32,768 376, 49,152
+// 421), of 262,144 584 (688, 754, 845); of 65,536 and 8 rows of 1,048,576 the larger ones are no
+// faster, and 8192 takes 182 us for 130 and 617 for 566.
+constexpr int kCached = 16384;
 constexpr int kBins = 2048;
 
 // Larger weight, larger key; NaN below all.

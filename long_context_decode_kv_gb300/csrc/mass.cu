@@ -9,13 +9,23 @@
 // registers, so that no sum crosses threads, and none is joined between CTAs.
 //
 // One CTA per SM, persistent.  The line of all (sequence, KV head) key tiles of 128 tokens
-// is cut into equal pieces; over its tiles of a head a CTA takes the head's rows in tiles
-// of up to 256 (latent rows, whose queries fill more shared memory: 128), the queries'
-// tile resident and the keys streaming past it, 64 channels a step.  A key's sum lives in
-// `out` between the row tiles, always in the same thread's hands.
+// is cut into pieces of equally many tiles; over its tiles of a head a CTA takes the head's
+// rows in tiles of up to 256 (latent rows, whose queries fill more shared memory: 128), the
+// queries' tile resident and the keys streaming past it, 64 channels a step.  A key's sum lives
+// in `out` between the row tiles, always in the same thread's hands.
 //
-// Measured: single tokens of 32 heads over 8 sequences of 65,536, 8 f16 KV heads, 172 us (6.2
-// TB/s of keys); of 64 heads over 16 of 16,384 latent rows 55 us (5.5 TB/s): HBM.
+// Pieces of equally many tiles are pieces of equal work only where every tile is seen by
+// equally many row tiles: a batch of single tokens, or of chunks without a window.  A chunk's
+// tiles among single tokens', and tiles behind a window, cost their CTA the chunk's row tiles
+// or nothing, and the call takes as long as the busiest CTA.  1024 tokens of 32 heads over 8000
+// int8 tokens alone 77 us; beside 7 single tokens over 8000 each 467 us, beside 31 over 60,000
+// each 9.5 ms (those 32 as single tokens 0.77); 1024 over 60,000 with a window of 4096 454 us.
+//
+// Measured: single tokens of 32 heads over 8 sequences of 65,536, 8 KV heads, f16 172 us (6.2
+// TB/s of keys: HBM), int8 177 us (3.1 TB/s; a tile's way through the turning warps and two
+// places, with the issue slots at 38 %); of 64 heads over 16 of 16,384 latent rows 55 us (5.5 TB/s:
+// HBM).  1000 tokens of 32 heads over 8000 latent rows 918 us: their 71 tiles occupy 71 CTAs, and
+// the keys stream past 250 row tiles of 128 rows.
 //
 // Roles: warps 0-3 and 4-7 take the tiles of even and odd index, a thread a key; warp 8
 // loads by TMA, warp 9 issues the products; int8: warps 10-13 turn codes into f16 or bf16
@@ -992,6 +1002,8 @@ cudaError_t launch_q(const MassArgs &m, cudaStream_t st) {
     // More rows than a tile that stays: the keys stay instead.  With the attention, over 60,000
     // f16 tokens, 8 KV heads: 260 rows a head 169 us against 193 with keys that stream, 512 rows
     // 183 and 178, 2048 604 and 641; the limit at 64 rows instead: 132 rows 122 us against 102.
+    // The rule is the batch's, by its longest run of new tokens: a chunk sends the single tokens
+    // beside it to the kernel whose keys stay, too.
     const bool many = c.head_dim <= 128 && static_cast<int64_t>(m.attn.G) * m.attn.max_new > kMaxRows;
     if (c.dtype == KVD_INT8) {
         if (c.head_dim == 64)

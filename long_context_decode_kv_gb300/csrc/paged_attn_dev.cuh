@@ -31,8 +31,11 @@ struct AttnArgs {  // of a launch
 };
 
 // A row's statistic from the reference m (base 2) and the sum l of its weights 2^(logit - m).
-// References stand below the row's maximum, so l is above 16 where it is not 0, and the
-// logarithm's 2 units of its last place are 2^-21 of the result's.
+// References stand below the row's maximum, so l is above 16 where it is not 0: far from 1,
+// where the fast logarithm is good to 2 units in the last place.  That is an absolute error, as
+// m and log2(l) may cancel: 2^-19 for l below 2^16 (2^-17 for any), times ln 2; the sum, the
+// product and the constant add 2.5 * 2^-24 of |lse|.  As a factor exp(-lse) of a weight it is the
+// same relative error: 2^-19.5, and with the weight's own use of lse 2^-22 of |lse|.
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l > 0.0f || l != l ? (m + __log2f(l)) * 0.69314718056f : -INFINITY;
 }
