@@ -747,7 +747,8 @@ KVD_API size_t kvd_latent_workspace_bytes(const kvd_latent_cache *cache, int32_t
 /*   A row whose lse is NaN spoils the weights that it adds to. */
 /*   Logits, weights and sums are f32, added in a fixed order: repeated calls give */
 /*   the same bits.  Beside its logit's error a weight is off by 2^-19 + |lse| 2^-22 of */
-/*   itself, as lse is a number of 24 bits: 2^-15 at |lse| = 100, 2^-12 at 1000. */
+/*   itself, as lse is a number of 24 bits: 2^-15 at |lse| = 100, 2^-12 at 1000; one */
+/*   below 2^-126 may count as 0. */
 /*   q: [n_tokens, n_heads, head_dim] (latent: rank + rope_dim), the type that the */
 /*   attention call takes; lse: f32 [n_tokens, n_heads]. */
 /*   mass, out: f32 [batch, n_kv_heads, ..], mass_stride and out_stride elements */

@@ -908,8 +908,8 @@ def paged_evict(cache, mass: torch.Tensor, keep: int, page_table_out: torch.Tens
     a cache over the new table and lengths.  Keys keep the rotation of their old positions, so
     later tokens are rotated with qk_norm_rope at positions of the caller's and appended without
     rope; a latent cache's k_pe as k_pe[:, None], its q_pe and q as rows of one head, e.g.
-    q_pe.flatten(0, 1)[:, None] and q[..., rank:].flatten(0, 1)[:, None] (views, with a position
-    a row).  An attention's window counts places in the cache."""
+    q_pe.flatten(0, 1)[:, None] into q.view(-1, 1, rank + rope_dim)[..., rank:] (q contiguous, a
+    position a row).  An attention's window counts places in the cache."""
     kind, heads, _ = _kind(cache)
     if page_table_out.dtype != torch.int32 or page_table_out.dim() != 2 or \
             page_table_out.shape[0] != cache.batch:

@@ -550,7 +550,7 @@ def test_rotated_tokens_behind_an_eviction(kind):
             k_rot = torch.empty(T, 1, P, device=DEV, dtype=torch.bfloat16)
             kvd.qk_norm_rope(down[:, 128:][:, None], None, positions, rope, k_rot, None)
             kvd.qk_norm_rope(q_pe.flatten(0, 1)[:, None], None, positions.repeat_interleave(H), rope,
-                             q[:, :, 128:].flatten(0, 1)[:, None], None)
+                             q.view(-1, 1, 128 + P)[..., 128:], None)
             assert torch.equal(q[:, :, :128], absorbed)
             kvd.latent_append(d, down[:, :128], k_rot[:, 0], _starts([1, 1]), c_weight=w)
             y, err = R.turned(q_pe, positions, f, m, False)
